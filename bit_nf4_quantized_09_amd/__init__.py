@@ -28,6 +28,7 @@ __all__ = [
     "lloyd_codebook", "NF4_OP_CODEBOOK_STATS",
     "NF4_OP_DOUBLE_QUANTIZE", "NF4_OP_LINEAR_FWD", "NF4_OP_LINEAR_BWD", "NF4_OP_LOWRANK_SVD", "NF4_OP_LOFTQ",
     "nf4_lowrank_svd", "loftq_init",
+    "RopePlan", "rope_plan", "rope_fwd", "rope_bwd", "KVCache", "kv_cache", "kv_append", "kv_attention", "head_loss",
 ]
 
 NF4_OK, NF4_ERR_ARG, NF4_ERR_UNSUPPORTED, NF4_ERR_WORKSPACE, NF4_ERR_HIP = range(5)
@@ -701,3 +702,8 @@ def loftq_init(W: torch.Tensor, r: int, alpha: float, omega: torch.Tensor, iters
                             _ptr(q), _ptr(c2), _ptr(mean), _ptr(A), _ptr(B), _ptr(err), _ptr(ws), wsb,
                             _stream(dev)))
     return NF4Weight(codes, q, c2, mean, (int(N), int(K))), A, B, err
+
+
+# The operators around the linears (rotary positions, the paged 8-bit cache, the vocabulary head's loss).
+from .decoder import (KVCache, RopePlan, head_loss, kv_append, kv_attention, kv_cache, rope_bwd, rope_fwd,  # noqa: E402
+                      rope_plan)

@@ -11,7 +11,8 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libqlora_nf4.so")
 PROBE_SOURCE = "hbm_probe.hip"      # the HBM ceiling probes: a library of their own
 PROBE_LIB = os.path.join(OUT_DIR, "libnf4_hbm_probe.so")
-SOURCES = ["api.hip", "codec.hip", "lora.hip", "fused.hip", "gemv.hip", "adamw.hip", "codebook.hip", "lowrank.hip"]
+SOURCES = ["api.hip", "codec.hip", "lora.hip", "fused.hip", "gemv.hip", "adamw.hip", "codebook.hip", "lowrank.hip",
+           "decoder_api.hip", "rope.hip", "kv_append.hip", "kv_attention.hip", "head_loss.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -11,25 +11,30 @@
 
 #include "../../include/qlora_nf4.h"
 #include "launch.h"
+#include "status.h"
 
+using nf4::aligned;
+using nf4::align256;
+using nf4::fail;
+using nf4::hip_status;
 using nf4::Nf4Table;
 using nf4::WeightView;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
 
-nf4_status fail(nf4_status st, const std::string& msg) {
+nf4_status nf4::fail(nf4_status st, const std::string& msg) {
     g_last_error = msg;
     return st;
 }
 
-nf4_status hip_status(hipError_t e, const char* where) {
+nf4_status nf4::hip_status(hipError_t e, const char* where) {
     if (e == hipSuccess) return NF4_OK;
     return fail(NF4_ERR_HIP, std::string(where) + ": " + hipGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+namespace {
 
 // ---------------------------------------------------------------------------
 // NF4 levels ("NF4, derived from normal quantiles", zerotofrontier.app
@@ -108,8 +113,6 @@ const Nf4Table& table() {
     std::call_once(once, [] { t = build_table(); });
     return t;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Limits of the linear products, checked before anything is enqueued.  Buffer descriptors
 // cap a range at 2^31 - 1 bytes and take 32-bit per-lane offsets: the adapter products

@@ -1,0 +1,34 @@
+// paged.h -- places of a batch's tokens in the paged cache, shared by kv_append.hip and
+// kv_attention.hip (internal).
+#pragma once
+
+#include "decoder.h"
+
+namespace nf4 {
+
+// The sequence of packed token t: the last b with starts[b] <= t.  Every lane of the wave
+// gets it; each round reads 64 evenly spaced starts, one per lane (one round up to 64
+// sequences, two up to 4096).
+__device__ __forceinline__ int sequence_of(const int32_t* starts, int seqs, int t, int lane) {
+    int lo = 0, n = seqs;
+    while (n > 1) {
+        const int step = (n + 63) >> 6;
+        const int at = lo + lane * step;
+        const bool before = lane * step < n && starts[at] <= t;
+        int hits = __popcll(__ballot(before));
+        hits = hits < 1 ? 1 : hits;
+        const int next = (hits - 1) * step;
+        lo += next;
+        n = n - next < step ? n - next : step;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Page of the pool that holds positions p .. of a sequence, or -1 if the sequence has none there.
+__device__ __forceinline__ int page_of(const CacheView& c, const BatchView& b, int seq, int page_index) {
+    if (page_index < 0 || page_index >= b.table_width) return -1;
+    const int page = b.table[seq * b.table_stride + page_index];
+    return page >= 0 && page < c.pages ? page : -1;
+}
+
+}  // namespace nf4

@@ -1,0 +1,173 @@
+"""The vocabulary head's loss and gradients on the GPU against float64.
+
+Bounds.  A logit's fp32 sum of exact products is within 2 sqrt(K) 2^-24 sum|x w| of the exact one
+(rounding errors of K additions; the square root for their signs), and so are lse and loss,
+with 2^-21 (|lse| + 1) for the base-2 logarithms.  Gradients: each entry of G is rounded to
+bf16, at most 2^-8 of it, and so are the outputs: 2^-8 |dX| + 2^-8 |G| |W| + the logits' error."""
+import math
+
+import pytest
+import torch
+
+import bit_nf4_quantized_09_amd as nf4
+import decoder_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(M, V, K, seed=0, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    X = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    W = (torch.randn((V, K), generator=g, device="cuda") * (std / math.sqrt(K))).bfloat16()
+    t = torch.randint(0, V, (M,), generator=g, device="cuda")
+    dl = torch.randn(M, generator=g, device="cuda") / M
+    return X, W, t, dl
+
+
+def check(X, W, t, dl, need_dw=True, ignore=-100):
+    loss, dX, dW = nf4.head_loss(X, W, t, dloss=dl, need_dw=need_dw, ignore_index=ignore)
+    only = nf4.head_loss(X, W, t, ignore_index=ignore)
+    wl, wx, ww, G, z = ref.head_loss(X, W, t, dl, ignore)
+    K = X.shape[1]
+    dz = 2 * math.sqrt(K) * 2.0 ** -24 * (X.double().abs() @ W.double().abs().t()).amax(1)
+    tol = 2 * dz + 2.0 ** -21 * (z.abs().amax(1) + 1)
+    assert torch.all((loss.double() - wl).abs() <= tol)
+    assert only[1] is None and only[2] is None and torch.all((only[0].double() - wl).abs() <= tol)
+    slack = 2.0 ** -8 + 2 * float(tol.max())
+    ex = (dX.double() - wx).abs() - (2.0 ** -8 * wx.abs() + slack * (G @ W.double().abs()))
+    assert torch.all(ex <= 1e-30), float(ex.max())
+    if need_dw:
+        ew = (dW.double() - ww).abs() - (2.0 ** -8 * ww.abs() + slack * (G.t() @ X.double().abs()))
+        assert torch.all(ew <= 1e-30), float(ew.max())
+    alone = nf4.head_loss(X, W, t, dloss=dl, ignore_index=ignore)
+    ex = (alone[1].double() - wx).abs() - (2.0 ** -8 * wx.abs() + slack * (G @ W.double().abs()))
+    assert torch.all(ex <= 1e-30), float(ex.max())
+    assert torch.all((alone[0].double() - wl).abs() <= tol)
+    return loss, dX, dW
+
+
+@pytest.mark.parametrize("M,V,K", [(1, 1, 64), (1, 1000, 128), (7, 33, 64), (64, 257, 192), (65, 1023, 512), (255, 300, 320),
+                                   (257, 513, 64), (130, 5001, 1024), (700, 2000, 576)])
+def test_values(M, V, K):
+    check(*inputs(M, V, K, seed=M + V))
+
+
+def test_pieces_of_the_vocabulary():
+    # 4096 tokens and 20000 entries: several pieces, a ragged last one
+    check(*inputs(4096, 20001, 128, seed=5))
+
+
+def test_sharp_logits():
+    X, W, t, dl = inputs(300, 2000, 256, seed=6, std=40.0)          # logits of some 40: few entries count
+    t[::2] = (X.float() @ W.float().t()).argmax(1)[::2]             # half of the targets win
+    check(X, W, t, dl)
+
+
+def test_offset_logits():
+    # all logits near +-300: nothing may overflow
+    for sign in (1, -1):
+        X, W, t, dl = inputs(70, 900, 256, seed=7)
+        X[:, 0], W[:, 0] = 300.0 * sign, 1.0
+        check(X, W, t, dl)
+
+
+def test_growing_logits():
+    # each later part of the vocabulary dominates all before it by far more than bf16's or fp32's range of exponents
+    X, W, t, dl = inputs(520, 40000, 64, seed=8)
+    X[:, 0] = 1.0
+    W[:, 0] = torch.arange(40000, device="cuda").float() / 16
+    t[:260] = 39990
+    check(X, W, t, dl, need_dw=False)
+    W[:, 0] = -W[:, 0].float()
+    check(X, W, t, dl, need_dw=False)
+
+
+def test_ignored_targets():
+    X, W, t, dl = inputs(150, 700, 128, seed=9)
+    t[0], t[1], t[2], t[3] = -100, -1, 700, 2 ** 62
+    t[10:20] = 5
+    loss, dX, dW = check(X, W, t, dl, ignore=5)
+    dead = [0, 1, 2, 3] + list(range(10, 20))
+    assert not loss[dead].any() and not dX[dead].any()
+    t[:] = -100
+    loss, dX, dW = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    assert not loss.any() and not dX.any() and not dW.any()
+    loss, dX, dW = nf4.head_loss(X, W, t, dloss=dl)
+    assert not loss.any() and not dX.any()
+
+
+def test_non_finite_rows_stay_alone():
+    X, W, t, dl = inputs(80, 600, 128, seed=10)
+    good = nf4.head_loss(X, W, t, dloss=dl)
+    X[3, 5], X[77, 0] = float("nan"), float("inf")
+    loss, dX, _ = nf4.head_loss(X, W, t, dloss=dl)
+    keep = torch.ones(80, dtype=torch.bool, device="cuda")
+    keep[[3, 77]] = False
+    assert torch.equal(loss[keep], good[0][keep]) and torch.equal(dX[keep], good[1][keep])
+    assert not torch.isfinite(loss[[3, 77]]).any() and not torch.isfinite(dX[[3, 77]]).all(1).any()
+    dl2 = dl.clone()
+    dl2[9] = float("nan")
+    X, W, t, _ = inputs(80, 600, 128, seed=10)
+    _, dX, _ = nf4.head_loss(X, W, t, dloss=dl2)
+    keep = torch.arange(80, device="cuda") != 9
+    assert torch.equal(dX[keep], good[1][keep]) and torch.isnan(dX[9]).all()
+
+
+def test_equal_factors_lose_nothing():
+    # a mean's factor 1/count is no power of two: it must not round every row alike
+    X, W, t, _ = inputs(384, 3000, 512, seed=11)
+    dl = torch.full((384,), 1 / 367.0, device="cuda")
+    _, dX, dW = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    _, wx, ww, _, _ = ref.head_loss(X, W, t, dl)
+    # roundings of 2^-9 on average of independent sign, in G and in the output
+    for got, want in ((dX, wx), (dW, ww), (nf4.head_loss(X, W, t, dloss=dl)[1], wx)):
+        assert float((got.double() - want).norm() / want.norm()) <= 2.5e-3
+
+
+def test_repeats_and_streams():
+    X, W, t, dl = inputs(333, 4000, 256, seed=12)
+    a = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    s.synchronize()
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+def test_graph_replays():
+    X, W, t, dl = inputs(100, 3000, 128, seed=13)
+    run = lambda: nf4.head_loss(X, W, t, dloss=dl, need_dw=True)  # noqa: E731
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in range(4):
+        X.normal_()
+        t.random_(0, 3000)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(out, run()):
+            assert torch.equal(x, y)
+
+
+def test_nothing():
+    X, W, t, dl = inputs(4, 100, 64)
+    loss, dX, dW = nf4.head_loss(X[:0], W, t[:0], dloss=dl[:0], need_dw=True)
+    assert loss.shape == (0,) and dX.shape == (0, 64) and not dW.any()
+
+
+def test_refused_tensors():
+    X, W, t, dl = inputs(4, 100, 64)
+    for bad in (lambda: nf4.head_loss(X.float(), W, t), lambda: nf4.head_loss(X, W[:, :32], t), lambda: nf4.head_loss(X, W, t.int()),
+                lambda: nf4.head_loss(X, W, t[:2]), lambda: nf4.head_loss(X, W, t, dloss=dl[:2]), lambda: nf4.head_loss(X, W, t, need_dw=True),
+                lambda: nf4.head_loss(X, W, t, dloss=dl.double()), lambda: nf4.head_loss(X.t(), W.t(), t), lambda: nf4.head_loss(X, W.cpu(), t)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(nf4.NF4Error):
+        nf4.head_loss(X[:, :40].contiguous(), W[:, :40].contiguous(), t)
