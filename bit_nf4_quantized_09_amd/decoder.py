@@ -9,6 +9,7 @@ longer than a model was trained on follow the base change and the by-parts inter
 Peng et al., "YaRN" (2023).
 """
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 from typing import Optional
@@ -65,22 +66,53 @@ def _library():
     return _bound
 
 
-def _heads(t: torch.Tensor, name: str, dtypes, tokens: int, dim: int) -> _Heads:
-    """A [tokens, heads, dim] tensor of any token and head strides."""
+# The calls below serve single tokens, where the host's time counts: each tensor is asked
+# once for its shape, strides, type and device, and the stream is taken as a raw handle.
+def _on(t: torch.Tensor, name: str, dtype, dev: int) -> int:
+    """Address of a dense tensor of the given type on device `dev`."""
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the same GPU as the other operands, got %s" % (name, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _device(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
-    if t.dtype not in dtypes:
-        raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or t.shape[1] < 1:
-        raise ValueError("%s must be [%d, heads, %d], got %s" % (name, tokens, dim, tuple(t.shape)))
-    if t.numel() and t.stride(2) != 1:
+    return t.get_device()
+
+
+def _heads(t: torch.Tensor, name: str, dtype, tokens: int, dim: int, dev: int) -> _Heads:
+    """A [tokens, heads, dim] tensor of any token and head strides."""
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the same GPU as the other operands, got %s" % (name, t.device))
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or shape[1] < 1:
+        raise ValueError("%s must be [%d, heads, %d], got %s" % (name, tokens, dim, tuple(shape)))
+    token_stride, head_stride, last = t.stride()
+    if last != 1 and tokens:
         raise ValueError("%s must be dense along its last dimension" % name)
-    token_stride, head_stride = t.stride(0), t.stride(1)
-    if t.shape[1] == 1:
+    heads = shape[1]
+    if heads == 1:                      # the stride of a dimension of one is not looked at
         head_stride = dim
     if tokens <= 1:
-        token_stride = t.shape[1] * head_stride
-    return _Heads(t.data_ptr(), token_stride, head_stride, t.shape[1])
+        token_stride = heads * head_stride
+    return _Heads(t.data_ptr(), token_stride, head_stride, heads)
+
+
+def _fresh_heads(like: torch.Tensor, tokens: int, dim: int):
+    """A new dense tensor of `like`'s shape and type, and its description."""
+    out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    heads = out.shape[1]
+    return out, _Heads(out.data_ptr(), heads * dim, dim, heads)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 # ---------------------------------------------------------------------------
@@ -95,11 +127,11 @@ class RopePlan:
     interleaved: bool = False
     magnitude: float = 1.0
 
-    def _struct(self):
-        _dev(self.freq, "freq", torch.int64)
-        if self.freq.numel() * 2 != self.rotary_dim:
+    def _struct(self, dev):
+        freq = self.freq
+        if freq.numel() * 2 != self.rotary_dim:
             raise ValueError("freq must hold rotary_dim / 2 = %d values" % (self.rotary_dim // 2))
-        return _Rope(self.freq.data_ptr(), self.rotary_dim, int(self.interleaved), self.magnitude)
+        return _Rope(_on(freq, "freq", torch.int64, dev), self.rotary_dim, self.interleaved, self.magnitude)
 
 
 def rope_plan(rotary_dim: int, base: float = 10000.0, *, interleaved: bool = False, scaling: Optional[str] = None,
@@ -142,27 +174,29 @@ def rope_plan(rotary_dim: int, base: float = 10000.0, *, interleaved: bool = Fal
     return RopePlan(freq, rotary_dim, bool(interleaved), magnitude)
 
 
-def _rope(plan, positions, tensors, inplace, backward):
-    L = _library()
-    _dev(positions, "positions", torch.int32)
-    M = positions.numel()
-    given = [("q", tensors[0])] + ([("k", tensors[1])] if tensors[1] is not None else [])
-    dtype, dim = tensors[0].dtype, tensors[0].shape[-1]
-    if dtype not in (torch.float32, torch.bfloat16):
+_Heads2 = _Heads * 2
+
+
+def _rope(plan, positions, q, k, inplace, backward):
+    dev = _device(q, "q")
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("q must be float32 or bfloat16, got %s" % dtype)
-    ins, outs = (_Heads * 2)(), (_Heads * 2)()
-    results = []
-    for i, (name, t) in enumerate(given):
-        ins[i] = _heads(t, name, (dtype,), M, dim)
-        out = t if inplace else torch.empty(t.shape, dtype=dtype, device=t.device)
-        outs[i] = ins[i] if inplace else _heads(out, name, (dtype,), M, dim)
-        results.append(out)
-    _same_device(("freq", plan.freq), ("positions", positions), *given)
-    rope = plan._struct()
-    _check(L.qlora_rope_apply(ctypes.byref(rope), int(backward), _ptr(positions), M, dim,
-                              NF4_BF16 if dtype == torch.bfloat16 else NF4_F32, ins, outs, len(given),
-                              _stream(tensors[0].device)))
-    return tuple(results) if len(results) > 1 else results[0]
+    M, dim = positions.numel(), q.shape[-1]
+    at = _on(positions, "positions", torch.int32, dev)
+    rope = plan._struct(dev)
+    ins = _Heads2(_heads(q, "q", dtype, M, dim, dev))
+    if k is not None:
+        ins[1] = _heads(k, "k", dtype, M, dim, dev)
+    yq, yk, outs = q, k, ins
+    if not inplace:
+        yq, hq = _fresh_heads(q, M, dim)
+        outs = _Heads2(hq)
+        if k is not None:
+            yk, outs[1] = _fresh_heads(k, M, dim)
+    _check(_library().qlora_rope_apply(rope, backward, at, M, dim, NF4_BF16 if dtype is torch.bfloat16 else NF4_F32, ins,
+                                       outs, 1 if k is None else 2, _raw_stream(dev)))
+    return yq if k is None else (yq, yk)
 
 
 def rope_fwd(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Tensor] = None,
@@ -170,13 +204,13 @@ def rope_fwd(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, k: Option
     """Queries, and keys if given, rotated to their positions: q [tokens, heads, dim], k
     [tokens, kv_heads, dim] (fp32 or bf16, the same type; any strides with a dense last
     dimension), positions int32 [tokens].  Returns new dense tensors, or the same ones if `inplace`."""
-    return _rope(plan, positions, (q, k), inplace, False)
+    return _rope(plan, positions, q, k, inplace, 0)
 
 
 def rope_bwd(plan: RopePlan, positions: torch.Tensor, dq: torch.Tensor, dk: Optional[torch.Tensor] = None,
              inplace: bool = False):
     """The gradient of rope_fwd: dq and dk turned back, times the same magnitude."""
-    return _rope(plan, positions, (dq, dk), inplace, True)
+    return _rope(plan, positions, dq, dk, inplace, 1)
 
 
 # ---------------------------------------------------------------------------
@@ -189,15 +223,15 @@ class KVCache:
     codes: torch.Tensor
     scales: torch.Tensor
 
-    def _struct(self):
-        _dev(self.codes, "codes", torch.uint8)
-        _dev(self.scales, "scales", torch.float32)
-        if self.codes.dim() != 5 or self.codes.shape[1] != 2:
-            raise ValueError("codes must be [pages, 2, kv_heads, page_size, head_dim], got %s" % (tuple(self.codes.shape),))
-        if tuple(self.scales.shape) != tuple(self.codes.shape[:3]):
-            raise ValueError("scales must be %s, got %s" % (tuple(self.codes.shape[:3]), tuple(self.scales.shape)))
-        pages, _, kv_heads, page, dim = self.codes.shape
-        return _Cache(self.codes.data_ptr(), self.scales.data_ptr(), pages, kv_heads, page, dim)
+    def _struct(self, dev):
+        codes, scales = self.codes, self.scales
+        shape = codes.shape
+        if len(shape) != 5 or shape[1] != 2:
+            raise ValueError("codes must be [pages, 2, kv_heads, page_size, head_dim], got %s" % (tuple(shape),))
+        if scales.shape != shape[:3]:
+            raise ValueError("scales must be %s, got %s" % (tuple(shape[:3]), tuple(scales.shape)))
+        return _Cache(_on(codes, "codes", torch.uint8, dev), _on(scales, "scales", torch.float32, dev), shape[0], shape[2],
+                      shape[3], shape[4])
 
     def decode(self, dtype=torch.float32) -> torch.Tensor:
         """What the codes stand for, [pages, 2, kv_heads, page_size, head_dim] (for looking at)."""
@@ -210,22 +244,20 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, devi
                    torch.ones((pages, 2, kv_heads), dtype=torch.float32, device=device))
 
 
-def _batch(starts, lengths, table, tokens):
-    for name, t in (("starts", starts), ("lengths", lengths), ("table", table)):
-        if not t.is_cuda:
-            raise ValueError("%s must be a GPU tensor" % name)
-        if t.dtype != torch.int32:
-            raise ValueError("%s must be torch.int32, got %s" % (name, t.dtype))
-    _dev(starts, "starts")
-    _dev(lengths, "lengths")
-    seqs = lengths.numel()
-    if lengths.dim() != 1 or starts.dim() != 1 or starts.numel() != seqs + 1:
-        raise ValueError("lengths must be [seqs] and starts [seqs + 1]")
-    if table.dim() != 2 or table.shape[0] != seqs or (table.numel() and table.stride(1) != 1):
-        raise ValueError("table must be [%d, pages of a sequence], dense along its rows" % seqs)
-    width = table.shape[1]
-    return _Batch(starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), table.stride(0) if seqs > 1 else width, tokens,
-                  seqs, width)
+def _batch(starts, lengths, table, tokens, dev):
+    shape = table.shape
+    if len(shape) != 2:
+        raise ValueError("table must be [seqs, pages of a sequence], got %s" % (tuple(shape),))
+    seqs, width = shape
+    if tuple(lengths.shape) != (seqs,) or tuple(starts.shape) != (seqs + 1,):
+        raise ValueError("lengths must be [%d] and starts [%d], as the table has %d rows" % (seqs, seqs + 1, seqs))
+    stride, last = table.stride()
+    if last != 1 and width > 1:
+        raise ValueError("table must be dense along its rows")
+    if table.dtype != torch.int32 or table.get_device() != dev:
+        raise ValueError("table must be torch.int32 on the same GPU as the other operands, got %s on %s" % (table.dtype, table.device))
+    return _Batch(_on(starts, "starts", torch.int32, dev), _on(lengths, "lengths", torch.int32, dev), table.data_ptr(),
+                  stride if seqs > 1 else width, tokens, seqs, width)
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, lengths: torch.Tensor,
@@ -239,26 +271,26 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Te
       lengths  int32 [seqs]: tokens of each sequence before these (negative: an unused row)
       table    int32 [seqs, pages of a sequence]: the pool's page of each page_size positions
     The caller moves its lengths on by the new tokens after the attention of the same step."""
-    L = _library()
-    c = cache._struct()
-    T = k.shape[0]
-    b = _batch(starts, lengths, table, T)
-    bf16 = (torch.bfloat16,)
-    kh, vh = _heads(k, "k", bf16, T, c.head_dim), _heads(v, "v", bf16, T, c.head_dim)
-    named = [("cache", cache.codes), ("scales", cache.scales), ("k", k), ("v", v), ("starts", starts),
-             ("lengths", lengths), ("table", table), ("q", q)]
-    out = qh = oh = r = None
+    dev = _device(k, "k")
+    c = cache._struct(dev)
+    T, dim = k.shape[0], c.head_dim
+    b = _batch(starts, lengths, table, T, dev)
+    kh, vh = _heads(k, "k", torch.bfloat16, T, dim, dev), _heads(v, "v", torch.bfloat16, T, dim, dev)
+    out = qh = oh = None
     if q is not None:
-        qh = _heads(q, "q", bf16, T, c.head_dim)
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        oh = _heads(out, "q", bf16, T, c.head_dim)
-    if rope is not None:
-        r = rope._struct()
-        named.append(("freq", rope.freq))
-    _same_device(*named)
-    ref = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
-    _check(L.qlora_kv_append(ref(c), ref(b), ref(kh), ref(vh), ref(r), ref(qh), ref(oh), _stream(k.device)))
+        qh = _heads(q, "q", torch.bfloat16, T, dim, dev)
+        out, oh = _fresh_heads(q, T, dim)
+    _check(_library().qlora_kv_append(c, b, kh, vh, None if rope is None else rope._struct(dev), qh, oh, _raw_stream(dev)))
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_ws_bytes(kv_heads, page_size, head_dim, seqs, tokens, heads, max_new, max_length):
+    """Workspace of an attention of these sizes (a plain function of them)."""
+    some = 4096                         # addresses that are checked, not followed
+    c = _Cache(some, some, 1, kv_heads, page_size, head_dim)
+    b = _Batch(some, some, some, 1, tokens, seqs, 1)
+    return _library().qlora_kv_attention_workspace_bytes(c, b, heads, max_new, max_length)
 
 
 def kv_attention(cache: KVCache, q: torch.Tensor, starts: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
@@ -269,22 +301,18 @@ def kv_attention(cache: KVCache, q: torch.Tensor, starts: torch.Tensor, lengths:
     reads kv head h // (heads // kv_heads).  scale: 1/sqrt(head_dim) by default.  max_new (the
     most new tokens of a sequence) and max_length (its most positions, new ones included) size
     the launch: without them it is sized for `tokens` and for the table's width."""
-    L = _library()
-    c = cache._struct()
-    T = q.shape[0]
-    b = _batch(starts, lengths, table, T)
-    qh = _heads(q, "q", (torch.bfloat16,), T, c.head_dim)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    oh = _heads(out, "out", (torch.bfloat16,), T, c.head_dim)
-    _same_device(("cache", cache.codes), ("scales", cache.scales), ("q", q), ("starts", starts), ("lengths", lengths),
-                 ("table", table))
+    dev = _device(q, "q")
+    c = cache._struct(dev)
+    T, dim = q.shape[0], c.head_dim
+    b = _batch(starts, lengths, table, T, dev)
+    qh = _heads(q, "q", torch.bfloat16, T, dim, dev)
+    out, oh = _fresh_heads(q, T, dim)
     max_new = max(1, T) if max_new is None else int(max_new)
     max_length = max(1, b.table_width * c.page_size) if max_length is None else int(max_length)
-    scale = 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale)
-    wsb = L.qlora_kv_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), qh.heads, max_new, max_length)
+    wsb = _attention_ws_bytes(c.kv_heads, c.page_size, dim, b.seqs, T, qh.heads, max_new, max_length)
     ws = _workspace(wsb, q.device)
-    _check(L.qlora_kv_attention(ctypes.byref(c), ctypes.byref(b), ctypes.byref(qh), ctypes.byref(oh), scale, max_new,
-                                max_length, _ptr(ws), wsb, _stream(q.device)))
+    _check(_library().qlora_kv_attention(c, b, qh, oh, dim ** -0.5 if scale is None else float(scale), max_new, max_length,
+                                         None if ws is None else ws.data_ptr(), wsb, _raw_stream(dev)))
     return out
 
 
