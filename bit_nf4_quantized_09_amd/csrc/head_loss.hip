@@ -2,49 +2,75 @@
 //
 //   z = X W^T,  loss = lse(z) - z_y,  G = dloss (softmax(z) - onehot),  dX = G W,  dW = G^T X
 //
-// The vocabulary is taken in pieces.  A first pass computes the logits tile by tile and keeps
-// of each tile only the maximum and the sum of exponentials of every row, the target's logit
-// apart: with S = sum_{v != y} exp(z_v - z_y), loss = log1p(S) and 1 - p_y = S / (1 + S) keep
-// their digits where the target has nearly all of the weight (lse - z_y would cancel).  For the gradient each piece's logits are computed
-// again, turned into G (bf16, a piece of [M][piece], small enough to stay in the last-level
-// cache) in the product's epilogue, and multiplied with the piece of W (dX, accumulated in fp32
-// over the pieces) and with X (dW).  Rounding: logits, maxima, sums and accumulators are fp32;
-// G is rounded to bf16, the type of the matrix instructions' operands and of the outputs; it
-// holds dloss / max|dloss| times p - onehot, and the factor max|dloss| is applied to the fp32
-// sums, so that a mean's 1/count does not round the many nearly equal target entries alike.
+// Loss alone: one product computes the logits tile by tile and keeps of each tile only the
+// maximum and the sum of exponentials of every row, the target apart: with
+// S = sum_{v != y} exp(z_v - z_y), loss = log1p(S) and 1 - p_y = S / (1 + S) keep their digits
+// where the target has nearly all of the weight (lse - z_y would cancel).
 //
-// Products.  256 x 256 output tiles, 8 waves, v_mfma_f32_32x32x16_bf16, contraction in steps
-// of 64 through two LDS stages filled by direct loads.  Both products put the token (or, for
-// dW, vocabulary) index into the accumulator's columns, so that a lane's 16 accumulators of a
-// tile belong to one row of the result: the softmax's sums stay in the lane, and stores take
-// four neighbours of a row at once.
+// Loss and dX: one pass over the vocabulary in pieces, two products a piece, like the forward
+// of an attention whose keys and values are the rows of W.  The first product's epilogue writes
+// E[m][v] = 2^(z - R[m]) in bf16, the target's entry zero, with a running integer reference R[m]
+// (base 2) that starts at the target's logit; the second adds E W to fp32 sums; at the end
+// dX = dloss (sums 2^R / l - (1 - p_y) W_y), the target's row added in fp32.  bf16 has fp32's
+// exponents, so R need not be the maximum: a tile takes a reference of its own only where a
+// logit passes R by more than 2^40, and the join after each piece (k_head_join) then brings the
+// row's other tiles and sums to the new R by exact powers of two.
+//
+// With dW, the contraction runs over tokens and needs normalised weights: the statistics pass,
+// then for each piece the logits again, whose epilogue writes G = dloss / max|dloss| (p - onehot)
+// in bf16 (and transposed), multiplied with W and X; the factor max|dloss| is applied to the
+// fp32 sums, so that a mean's 1/count does not round the many nearly equal target entries alike.
+//
+// Rounding: logits, maxima, sums and accumulators are fp32; E and G are bf16, the type of the
+// matrix instructions' operands and of the outputs.
+//
+// Products.  512 x 128 output tiles, 4 waves, v_mfma_f32_32x32x16_bf16, one wave per SIMD with 256
+// accumulators.  The 512-row operand (X, E, G^T) is private to its wave and comes in fragment order
+// (tile_map.h) straight into registers, two steps ahead; X is packed once per call, E and G^T are
+// written in that order by the logits' epilogue.  The 128-column operand (rows of W, or columns of
+// W or X read transposed) goes through four LDS stages filled by direct loads, three steps ahead.
+// (256 x 256 tiles with both operands in LDS, 8 waves of 128 x 64: LDS reads and writes take as
+// many cycles as the matrix instructions; 940-1000 TFLOP/s.)
 #include "bufio.h"
 #include "decoder.h"
+#include "tile_map.h"
 
 namespace nf4 {
 
-constexpr int HL_T = 256;                 // output tile, both ways
+constexpr int HL_TM = FUSED_TM;           // output tile: 512 rows
+constexpr int HL_TN = FUSED_TN;           // x 128 columns
 constexpr int HL_K = 64;                  // contraction step
-constexpr int HL_STAGE = HL_T * HL_K * 2; // bytes of one operand's stage: 32 KB
+constexpr int HL_STAGE = HL_TN * HL_K * 2;   // an LDS stage: 16 KB
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-// Sixteen bytes per lane from memory into LDS at base + 16 * lane, without passing registers.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, lds_u8* base, uint32_t voff, uint32_t soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)base, 16, (int)voff, (int)soff, 0, 0);
+// A buffer descriptor as plain registers.
+typedef int hl_rsrc __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ hl_rsrc hl_make_rsrc(const void* base, int64_t bytes) {
+    const uint64_t p = (uint64_t)base;
+    return hl_rsrc{(int)(uint32_t)p, (int)((p >> 32) & 0xFFFF), (int)(bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF), 0x00020000};
 }
 
-// Rows of 128 bytes (64 values of the contraction): 16-byte chunk c of row r lies at chunk
-// c ^ g(r), so that 16 neighbouring rows reading one chunk meet all 64 banks once.
-__device__ __forceinline__ int hl_swizzle(int row) { return (row ^ (row >> 3)) & 7; }
-__device__ __forceinline__ int hl_off(int row, int chunk) { return row * 128 + ((chunk ^ hl_swizzle(row)) << 4); }
+// Sixteen bytes per lane from memory into LDS at `at` + 16 * lane, without passing registers.  In
+// assembly, because the compiler makes a transposing LDS read wait for every such load of the
+// builtin's kind, whichever stage it fills (1016 instead of 1200 TFLOP/s in the second product);
+// the loop below waits for a stage itself.  (Nothing else in these kernels uses m0.)  The compiler counts the loads it knows of, so its own
+// waits with these among them are only stricter.
+__device__ __forceinline__ void load_to_lds(hl_rsrc r, uint32_t at, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voff), "s"(r), "s"(soff) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)(p);
+}
 
-// Rows of 512 bytes (256 columns of one contraction value), read transposed: 32-byte segment
-// u of row r lies at u ^ 2 (r & 3), so that the 4 rows x 2 segments of one pass meet all banks.
+// Stage of a direct operand: 128 rows of 128 bytes (64 values of the contraction), 16-byte chunk c of
+// row r at chunk c ^ g(r), so that 16 neighbouring rows reading one chunk meet all 64 banks once.
+__device__ __forceinline__ int hl_swizzle(int row) { return (row ^ (row >> 3)) & 7; }
+
+// Stage of a transposed operand: 64 rows of 256 bytes (128 columns of one contraction value), 32-byte
+// segment u of row r at u ^ 2 (r & 3), so that the 4 rows x 2 segments of one pass meet all banks.
 __device__ __forceinline__ int hl_toff(int row, int col) {
-    return row * 512 + (((col >> 4) ^ ((row & 3) << 1)) << 5) + ((col & 15) << 1);
+    return row * 256 + (((col >> 4) ^ ((row & 3) << 1)) << 5) + ((col & 15) << 1);
 }
 
 typedef short hl_i16x4 __attribute__((ext_vector_type(4)));
@@ -55,302 +81,595 @@ __device__ __forceinline__ uint2 hl_read_tr(const uint8_t* p) {
 }
 
 // Output tile of a workgroup: neighbours in launch order go to different XCDs, so XCD x gets a
-// contiguous run of the tile order (columns of 4 row tiles), whose operands its L2 then shares.
-__device__ __forceinline__ bool hl_tile(int wg, int tiles_a, int tiles_b, int& ta, int& tb) {
-    const int total = tiles_a * tiles_b, q = total / 8, rem = total % 8;
-    const int x = wg % 8, local = wg / 8;
-    const int p = x * q + (x < rem ? x : rem) + local;
+// contiguous run of the tile order (columns of 2 row tiles), whose operands its L2 then shares.
+__device__ __forceinline__ bool hl_tile(int wg, int64_t tiles_m, int64_t tiles_n, int64_t& tm, int64_t& tn) {
+    const int64_t total = tiles_m * tiles_n, q = total / XCDS, rem = total % XCDS;
+    const int64_t x = wg % XCDS, local = wg / XCDS;
     if (local >= q + (x < rem ? 1 : 0)) return false;
-    const int per = 4 * tiles_b, first = p / per * 4;
-    const int g = tiles_a - first < 4 ? tiles_a - first : 4;
-    ta = first + p % per % g;
-    tb = p % per / g;
+    tile_at(x * q + (x < rem ? x : rem) + local, tiles_m, tiles_n, tm, tn);
     return true;
 }
 
+// Bytes of a block in use when `rows` rows of the tile are: 4 KB per 32 rows.
+__device__ __forceinline__ int hl_block_bytes(int64_t rows) {
+    return __builtin_amdgcn_readfirstlane(rows < HL_TM ? (int)((rows + 31) / 32) * 4096 : A_BLOCK_BYTES);
+}
+
+struct HlFrags {
+    uint4 f[4][4];            // [row tile i][substep s]
+};
+
+// The main loop of both products: acc[i][j] += (rows 32 i.. of the wave's 128) x (columns 32 j..),
+// contraction steps first .. last - 1 (at least one).  SWAP: accumulator columns are the 512-row
+// operand's rows.  TRANS: the 128-column operand is read transposed.  `blocks`: the 512-row operand's
+// 64 KB blocks of this row tile, `block_bytes` of each in use (rows past the last are zero and are
+// not fetched); `dma(stage, step, q)`: fills quarter q of a stage with the other operand.
+//
+// A step is 8 regions of 8 matrix instructions.  Region 2 s + half uses rows 2 half, 2 half + 1 of
+// substep s, reloads their fragments for two steps ahead, and (half 0) reads the next substep's column
+// fragments; regions 0-3 also start a quarter each of the stage three steps ahead.  The barrier stands
+// before the last region, whose matrix instructions hide the next step's first LDS reads.  A stage
+// is complete at the barrier before its first read: 36 is below the number of loads that each wave has
+// started since it started that stage's (at least 46).
+template <bool SWAP, bool TRANS, typename Dma>
+__device__ __forceinline__ void hl_loop(f32x16 (&acc)[4][4], const uint8_t* lds, const uint16_t* blocks, int block_bytes, int first, int last,
+                                        int wave, int lane, Dma&& dma) {
+    const int h = lane >> 5, rl = lane & 31;
+    int off[4];               // LDS offset of this lane's column fragments; + 4096 j (direct), + 4096 s (transposed)
+    if constexpr (TRANS) {
+        const int g = lane >> 4, jl = lane & 15;
+        const int row0 = 8 * (g >> 1) + (jl >> 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) off[j] = hl_toff(row0, j * 32 + 16 * (g & 1) + 4 * (jl & 3));
+    } else {
+        // row 32 j + rl, chunk 2 s + h: swizzled by g(rl) ^ 4 (j & 1), so (s, j) and (s ^ 2 (j & 1), 0) share a base
+#pragma unroll
+        for (int s = 0; s < 4; ++s) off[s] = rl * 128 + (((2 * s + h) ^ hl_swizzle(rl)) << 4);
+    }
+    auto read_b = [&](const uint8_t* stage, int j, int s) -> bf16x8 {
+        if constexpr (TRANS) {
+            const uint8_t* p = stage + off[j] + s * 16 * 256;
+            const uint2 lo = hl_read_tr(p), hi = hl_read_tr(p + 4 * 256);
+            return __builtin_bit_cast(bf16x8, make_uint4(lo.x, lo.y, hi.x, hi.y));
+        } else {
+            return *reinterpret_cast<const bf16x8*>(stage + off[s ^ (2 * (j & 1))] + 4096 * j);
+        }
+    };
+    uint32_t a_voff[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a_voff[i] = (uint32_t)(wave * 16384 + 4096 * i + lane * 16);
+    // (past the last step the range is empty and the fragments are zero: an odd number of steps ends with an idle one)
+    auto a_rsrc = [&](int step) {
+        return make_rsrc(blocks + (int64_t)(step < last ? step : first) * (A_BLOCK_BYTES / 2), step < last ? block_bytes : 0);
+    };
+    auto clamp = [&](int step) { return step < last ? step : last - 1; };
+    auto load_all = [&](HlFrags& F, int step) {
+        const __amdgpu_buffer_rsrc_t rs = a_rsrc(step);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) F.f[i][s] = buf_load16(rs, a_voff[i] + 1024 * s, 0);
+    };
+    auto mfma = [&](int i, int j, uint4 af, bf16x8 bf) {
+        const bf16x8 a = __builtin_bit_cast(bf16x8, af);
+        acc[i][j] = SWAP ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf, a, acc[i][j], 0, 0, 0)
+                         : __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, bf, acc[i][j], 0, 0, 0);
+    };
+    bf16x8 fb[2][4];
+    HlFrags fa0, fa1;
+    auto step_body = [&](int it, HlFrags& cur) {
+        const int st = (it - first) & 3;
+        const uint8_t* now = lds + st * HL_STAGE;
+        const uint8_t* next = lds + ((st + 1) & 3) * HL_STAGE;
+        const __amdgpu_buffer_rsrc_t rs = a_rsrc(it + 2);
+        const int ahead = clamp(it + 3);
+#pragma unroll
+        for (int rg = 0; rg < 8; ++rg) {
+            const int s = rg >> 1, half = rg & 1;
+            if (rg == 7) {
+                asm volatile("s_waitcnt vmcnt(36) lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 4; ++j) fb[0][j] = read_b(next, j, 0);
+            } else if (half == 0 && s < 3) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) fb[(s & 1) ^ 1][j] = read_b(now, j, s + 1);
+            }
+            if (rg < 4) dma((st + 3) & 3, ahead, rg);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) mfma(2 * half + (t >> 2), t & 3, cur.f[2 * half + (t >> 2)][s], fb[s & 1][t & 3]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) cur.f[2 * half + q][s] = buf_load16(rs, a_voff[2 * half + q] + 1024 * s, 0);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // matrix
+                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);                       // VALU
+                if ((rg == 7 || (half == 0 && s < 3)) && t < 4)
+                    __builtin_amdgcn_sched_group_barrier(0x100, TRANS ? 2 : 1, 0);      // LDS reads
+                if (t == 2 || t == 5) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // loads
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+#pragma unroll
+    for (int st = 0; st < 3; ++st)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) dma(st, clamp(first + st), q);
+    __builtin_amdgcn_sched_barrier(0);
+    load_all(fa0, first);
+    load_all(fa1, first + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(36)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fb[0][j] = read_b(lds, j, 0);
+    for (int it = first; it < last; it += 2) {
+        step_body(it, fa0);
+        step_body(it + 1, fa1);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // nothing may land in LDS after the workgroup
+}
+
+// X in fragment order (64 KB per 512 rows and 64 values, zeros past row M): one wave per 32 rows and step.
+__global__ __launch_bounds__(256)
+void k_head_pack(const uint16_t* X, int64_t M, int64_t K, uint16_t* out) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t steps = K / HL_K;
+    const int64_t step = blockIdx.x, tm = blockIdx.y >> 2;
+    const int i = (int)(blockIdx.y & 3);
+    const int64_t row = tm * HL_TM + 128 * wave + 32 * i + (lane & 31);
+    uint4* block = reinterpret_cast<uint4*>(out + (tm * steps + step) * (A_BLOCK_BYTES / 2));
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < M) v = *reinterpret_cast<const uint4*>(X + row * K + step * HL_K + (2 * s + (lane >> 5)) * 8);
+        block[1024 * wave + 64 * (4 * i + s) + lane] = v;
+    }
+}
+
 struct HeadArgs {
-    const uint16_t* X;        // [M][K]
+    const uint16_t* Xp;       // X in fragment order
     const uint16_t* W;        // [V][K]
     int64_t M, K, V;
     const int64_t* targets;
     int64_t ignore;
     int64_t v0;               // first vocabulary row of the launch, and
-    int tiles_v, tiles_m;     // its tiles
-    float2* part;             // [tile of v][Mp]: maximum and sum of a row, base 2 (statistics)
-    float* zy;                // [Mp]: target's logit, base 2
-    const float2* rows;       // [Mp]: lse, base 2, and 1 - p of the target (gradient)
-    const float* dloss;
-    uint32_t* top;            // max|dloss| as bits
-    uint16_t* G;              // [Mp][ldg], or null
-    uint16_t* Gt;             // [ldg][Mp], or null
-    int64_t ldg, Mp;
+    int64_t tiles_v, tiles_m; // its tiles (128 vocabulary rows, 512 tokens)
+    float2* part;             // [Mp][tiles of v of the launch]: reference and sum of a row, base 2
+    float* zy;                // [Mp]: target's logit, base 2 (HEAD_STATS: out)
+    const float* ref;         // [Mp]: running reference (HEAD_E)
+    const float4* rows;       // [Mp]: lse, base 2; 1 - p of the target; dloss; the target (as bits, -1: none) (HEAD_GT)
+    const uint32_t* top;      // max|dloss| as bits (HEAD_GT)
+    uint16_t* out;            // E or G^T in fragment order
+    int64_t out_steps;        // blocks of a row tile of `out`
+    int64_t Mp;
 };
 
-// Logits of a 256 (vocabulary) x 256 (tokens) tile; GRAD false: row statistics, true: G.
-template <bool GRAD>
-__global__ __launch_bounds__(512)
+// What the epilogue of the logits' product leaves: row statistics, exponentials against the running
+// reference with their sums, or normalised gradients, transposed.
+enum HeadMode { HEAD_STATS, HEAD_E, HEAD_GT };
+
+__device__ __forceinline__ bool head_live(int64_t target, int64_t V, int64_t ignore) {
+    return target >= 0 && target < V && target != ignore;
+}
+constexpr float HEAD_ROOM = 40.0f;        // binades a logit may pass the running reference by
+// The factor on G, from max|dloss|: at least the smallest normal number, so that its inverse is finite.
+__device__ __forceinline__ float head_scale(const uint32_t* top) { return fmaxf(__uint_as_float(*top), 0x1p-126f); }
+
+// Logits of a tile of 512 tokens x 128 vocabulary rows.
+template <HeadMode MODE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_head_logits(HeadArgs a) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * HL_STAGE];
+    constexpr bool SWAP = MODE != HEAD_GT;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5, rl = lane & 31;
-    int tv, tm;
-    if (!hl_tile(blockIdx.x, a.tiles_v, a.tiles_m, tv, tm)) return;
-    const int64_t v0 = a.v0 + (int64_t)tv * HL_T, m0 = (int64_t)tm * HL_T;
-    if (!GRAD && blockIdx.x == 0 && tid == 0) *a.top = 0;      // for k_head_rows
-    const int wv = wave >> 2, wm = wave & 3;           // 2 x 4 waves of 128 x 64
-    // rows past the end repeat the last one (their results are dropped)
-    uint32_t wof[4], xof[4];
+    int64_t tv, tm;
+    if (!hl_tile(blockIdx.x, a.tiles_m, a.tiles_v, tm, tv)) return;
+    const int64_t v0 = a.v0 + tv * HL_TN, m0 = tm * HL_TM;
+    const int steps = __builtin_amdgcn_readfirstlane((int)(a.K / HL_K));
+    // a wave fills rows 32 wave .. of a stage, 8 rows a load; rows past V repeat the last (dropped later)
+    uint32_t wof[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = wave * 32 + i * 8 + (lane >> 3);
-        const int chunk = (lane & 7) ^ hl_swizzle(row);
-        const int64_t rv = v0 + row < a.V ? row : a.V - 1 - v0, rm = m0 + row < a.M ? row : a.M - 1 - m0;
-        wof[i] = (uint32_t)(rv * a.K * 2) + chunk * 16;
-        xof[i] = (uint32_t)(rm * a.K * 2) + chunk * 16;
+    for (int q = 0; q < 4; ++q) {
+        const int row = wave * 32 + q * 8 + (lane >> 3);
+        const int64_t rv = v0 + row < a.V ? row : a.V - 1 - v0;
+        wof[q] = (uint32_t)(rv * a.K * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
     }
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.W + v0 * a.K, (a.V - v0) * a.K * 2);
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X + m0 * a.K, (a.M - m0) * a.K * 2);
-    auto load = [&](int stage, int step) {
-        lds_u8* base = (lds_u8*)lds + stage * 2 * HL_STAGE + wave * 4096;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            load_to_lds(rw, base + i * 1024, wof[i], (uint32_t)step * 128);
-            load_to_lds(rx, base + HL_STAGE + i * 1024, xof[i], (uint32_t)step * 128);
-        }
-    };
-    f32x16 acc[4][2];
+    const hl_rsrc rw = hl_make_rsrc(a.W + v0 * a.K, (a.V - v0) * a.K * 2);
+    const uint32_t mine = lds_address(lds) + wave * 4096;
+    f32x16 acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
-    const int steps = (int)(a.K / HL_K);
-    load(0, 0);
-    for (int it = 0; it < steps; ++it) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (it + 1 < steps) load((it + 1) & 1, it + 1);
-        const uint8_t* sw = lds + (it & 1) * 2 * HL_STAGE;
-        const uint8_t* sx = sw + HL_STAGE;
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    hl_loop<SWAP, false>(acc, lds, a.Xp + tm * steps * (int64_t)(A_BLOCK_BYTES / 2), hl_block_bytes(a.M - m0), 0, steps, wave, lane,
+                         [&](int stage, int step, int q) {
+                             load_to_lds(rw, mine + stage * HL_STAGE + q * 1024, wof[q], (uint32_t)step * 128);
+                         });
+    if constexpr (MODE == HEAD_GT) {
+        // accumulator (i, j, reg): token 32 i + 8 (reg / 4) + 4 h + reg % 4 of the wave's 128, vocabulary row 32 j + rl.
+        // G^T's block of 512 vocabulary rows and 64 tokens: this tile is wave slice tv % 4 of it.
+        const float inv = 1.0f / head_scale(a.top);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            bf16x8 af[4], bf[2];
+        for (int i = 0; i < 4; ++i) {
+            const int64_t mi = m0 + wave * 128 + i * 32;
+            uint8_t* block = reinterpret_cast<uint8_t*>(a.out) + ((tv >> 2) * a.out_steps + (mi >> 6)) * A_BLOCK_BYTES +
+                             (tv & 3) * 16384 + rl * 16 + 8 * h;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) bf[j] = *reinterpret_cast<const bf16x8*>(sx + hl_off(wm * 64 + j * 32 + rl, 2 * s + h));
+            for (int r4 = 0; r4 < 4; ++r4) {
+                float4 row[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) af[i] = *reinterpret_cast<const bf16x8*>(sw + hl_off(wv * 128 + i * 32 + rl, 2 * s + h));
+                for (int r = 0; r < 4; ++r) row[r] = a.rows[mi + 8 * r4 + 4 * h + r];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[i], bf[j], acc[i][j], 0, 0, 0);
-        }
-    }
-    // accumulator (i, j, reg): vocabulary row 32 i + 8 (reg / 4) + 4 h + reg % 4 of the wave's 128,
-    // token 32 j + rl of its 64
-    const int64_t vw = v0 + wv * 128 + 4 * h;
-    if constexpr (!GRAD) {
-        __syncthreads();
-        float2* join = reinterpret_cast<float2*>(lds);          // [2][256]
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t m = m0 + wm * 64 + j * 32 + rl;
-            const int64_t target = m < a.M ? a.targets[m] : -1;
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t v = vw + i * 32 + 8 * (r >> 2) + (r & 3);
-                    float z = v < a.V ? acc[i][j][r] * LOG2E : -INFINITY;
-                    if (v == target && v < a.V) {
-                        a.zy[m] = z;
-                        z = -INFINITY;
-                    }
-                    acc[i][j][r] = z;
-                    top = fmaxf(top, z);
-                }
-            float sum = 0.0f;
-            const float ref = top > -INFINITY ? top : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(acc[i][j][r] - ref);
-            const float other = __shfl_xor(top, 32), osum = __shfl_xor(sum, 32);
-            const float both = fmaxf(top, other), bref = both > -INFINITY ? both : 0.0f;
-            sum = sum * __builtin_amdgcn_exp2f(top - bref) + osum * __builtin_amdgcn_exp2f(other - bref);
-            if (h == 0) join[wv * 256 + wm * 64 + j * 32 + rl] = make_float2(both, sum);
-        }
-        __syncthreads();
-        if (tid < 256) {
-            const float2 p = join[tid], q = join[256 + tid];
-            const float both = fmaxf(p.x, q.x), ref = both > -INFINITY ? both : 0.0f;
-            const float sum = p.y * __builtin_amdgcn_exp2f(p.x - ref) + q.y * __builtin_amdgcn_exp2f(q.x - ref);
-            a.part[((a.v0 / HL_T) + tv) * a.Mp + m0 + tid] = make_float2(both, sum);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t m = m0 + wm * 64 + j * 32 + rl;
-            int64_t target = m < a.M ? a.targets[m] : -1;
-            const bool live = m < a.M && target >= 0 && target < a.V && target != a.ignore;
-            const float most = __uint_as_float(*a.top);
-            const float g = live ? (most > 0.0f ? a.dloss[m] / most : a.dloss[m]) : 0.0f;
-            const float2 row = live ? a.rows[m] : make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    const int64_t v = vw + i * 32 + 8 * r4;
+                for (int j = 0; j < 4; ++j) {
+                    const int v = (int)v0 + j * 32 + rl;
                     float y[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float p = __builtin_amdgcn_exp2f(acc[i][j][4 * r4 + r] * LOG2E - row.x);
-                        y[r] = live && v + r < a.V ? g * (v + r == target ? -row.y : p) : 0.0f;
+                        const int target = __float_as_int(row[r].w);
+                        const float p = __builtin_amdgcn_exp2f(acc[i][j][4 * r4 + r] * LOG2E - row[r].x);
+                        y[r] = target >= 0 && v < a.V ? row[r].z * inv * (v == target ? -row[r].y : p) : 0.0f;
                     }
-                    const uint2 w = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-                    if (a.G) *reinterpret_cast<uint2*>(a.G + m * a.ldg + (v - a.v0)) = w;
-                    if (a.Gt) {
-                        uint16_t* t = a.Gt + (v - a.v0) * a.Mp + m;
-                        t[0] = (uint16_t)w.x;
-                        t[a.Mp] = (uint16_t)(w.x >> 16);
-                        t[2 * a.Mp] = (uint16_t)w.y;
-                        t[3 * a.Mp] = (uint16_t)(w.y >> 16);
-                    }
+                    *reinterpret_cast<uint2*>(block + 1024 * (4 * j + (i & 1) * 2 + (r4 >> 1)) + 512 * (r4 & 1)) =
+                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
                 }
+            }
         }
+        return;
+    }
+    // accumulator (i, j, reg): token 32 i + rl of the wave's 128, vocabulary row 32 j + 8 (reg / 4) + 4 h + reg % 4
+    const int left = (int)(a.V - v0 < HL_TN ? a.V - v0 : HL_TN) - 4 * h;       // this lane's valid rows end
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + wave * 128 + i * 32 + rl;
+        const int64_t target = m < a.M ? a.targets[m] : -1;
+        const bool live = m < a.M && head_live(target, a.V, a.ignore);
+        const int64_t tl = target - v0 - 4 * h;
+        const int hit = live && tl >= 0 && tl < HL_TN ? (int)tl : -1;          // the target's row, if this lane's
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int v = j * 32 + 8 * (r >> 2) + (r & 3);
+                float z = acc[i][j][r] * LOG2E;
+                if (v == hit) {
+                    if (MODE == HEAD_STATS) a.zy[m] = z;
+                    z = -INFINITY;
+                }
+                z = v < left ? z : -INFINITY;
+                acc[i][j][r] = z;
+                top = fmaxf(top, z);
+            }
+        top = fmaxf(top, __shfl_xor(top, 32));
+        float ref = top > -INFINITY ? top : 0.0f;
+        if (MODE == HEAD_E) {
+            ref = live ? a.ref[m] : 0.0f;
+            if (top > ref + HEAD_ROOM) ref = ceilf(top);      // an integer, like the running one
+        }
+        // E's block of 512 tokens and 64 vocabulary rows
+        uint8_t* block = nullptr;
+        if (MODE == HEAD_E)
+            block = reinterpret_cast<uint8_t*>(a.out) + (tm * a.out_steps + 2 * tv) * A_BLOCK_BYTES + wave * 16384 + i * 4096 +
+                    rl * 16 + 8 * h;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                float y[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    y[r] = __builtin_amdgcn_exp2f(acc[i][j][4 * r4 + r] - ref);
+                    if (MODE == HEAD_E && !live) y[r] = 0.0f;
+                    sum += y[r];
+                }
+                if (MODE == HEAD_E)
+                    *reinterpret_cast<uint2*>(block + (j >> 1) * A_BLOCK_BYTES + 1024 * ((j & 1) * 2 + (r4 >> 1)) + 512 * (r4 & 1)) =
+                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            }
+        sum += __shfl_xor(sum, 32);
+        if (MODE == HEAD_E && !live) ref = 0.0f;
+        if (h == 0) a.part[m * a.tiles_v + tv] = make_float2(MODE == HEAD_E ? ref : top, sum);
     }
 }
 
-// lse, loss and 1 - p of the target of each row from its tiles' statistics, and max|dloss|.
+// A row's loss from its target's logit and the others' log-sum (both base 2): the loss, lse
+// (base 2) and 1 - p of the target.
+struct RowLoss {
+    float loss, lse, rest;
+};
+__device__ __forceinline__ RowLoss row_loss(float z, float others) {
+    const float d = z - others;
+    const float tail = log1pf(exp2f(-fabsf(d)));
+    return RowLoss{d >= 0.0f ? tail : tail - d * LN2, fmaxf(z, others) + tail * LOG2E, 1.0f / (1.0f + exp2f(d))};
+}
+
+// The loss from a row's statistics: one wave per row.
 __global__ __launch_bounds__(256)
-void k_head_rows(const float2* part, const float* zy, const int64_t* targets, int64_t M, int64_t Mp, int64_t V,
-                 int64_t ignore, int tiles, const float* dloss, uint32_t* most, float2* rows, float* loss) {
-    const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+void k_head_rows(const float2* part, const float* zy, const int64_t* targets, int64_t M, int64_t V, int64_t ignore,
+                 int tiles, float* loss) {
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (m >= M) return;
     float top = -INFINITY, sum = 0.0f;
-    for (int t = 0; t < tiles; ++t) {
-        const float2 p = part[t * Mp + m];
-        const float both = fmaxf(top, p.x), ref = both > -INFINITY ? both : 0.0f;
-        sum = sum * __builtin_amdgcn_exp2f(top - ref) + p.y * __builtin_amdgcn_exp2f(p.x - ref);
+    auto join = [&](float t, float s) {
+        const float both = fmaxf(top, t), ref = both > -INFINITY ? both : 0.0f;
+        sum = sum * __builtin_amdgcn_exp2f(top - ref) + s * __builtin_amdgcn_exp2f(t - ref);
         top = both;
+    };
+    for (int t = lane; t < tiles; t += 64) {
+        const float2 p = part[m * tiles + t];
+        join(p.x, p.y);
     }
-    const int64_t target = targets[m];
-    const bool live = target >= 0 && target < V && target != ignore;
-    if (!live) {
-        if (loss) loss[m] = 0.0f;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+        const float t = __shfl_xor(top, x), s = __shfl_xor(sum, x);
+        join(t, s);
+    }
+    if (lane == 0) loss[m] = head_live(targets[m], V, ignore) ? row_loss(zy[m], top + log2f(sum)).loss : 0.0f;
+}
+
+// Target logits (base 2) and the first references, one wave per row; the last workgroup: the largest
+// finite |dloss| of the rows that count.
+__global__ __launch_bounds__(256)
+void k_head_target(const uint16_t* X, const uint16_t* W, int64_t M, int64_t K, int64_t V, const int64_t* targets,
+                   int64_t ignore, float* zy, float* ref, float* total, const float* dloss, uint32_t* top) {
+    const int lane = threadIdx.x & 63;
+    if (blockIdx.x == gridDim.x - 1) {
+        __shared__ float join[4];
+        float most = 0.0f;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < M; i += 256) {
+            const float g = fabsf(dloss[i]);
+            if (g < INFINITY && head_live(targets[i], V, ignore)) most = fmaxf(most, g);
+        }
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
+        if (lane == 0) join[threadIdx.x >> 6] = most;
+        __syncthreads();
+        if (threadIdx.x == 0) *top = __float_as_uint(fmaxf(fmaxf(join[0], join[1]), fmaxf(join[2], join[3])));
         return;
     }
-    const float rest = top + log2f(sum), z = zy[m], d = z - rest;   // the other entries' lse, base 2
-    const float tail = log1pf(exp2f(-fabsf(d)));
-    if (loss) loss[m] = d >= 0.0f ? tail : tail - d * LN2;
-    rows[m] = make_float2(fmaxf(z, rest) + tail * LOG2E, 1.0f / (1.0f + exp2f(d)));
-    if (dloss) {
-        const float g = fabsf(dloss[m]);
-        if (g < INFINITY) atomicMax(most, __float_as_uint(g));      // a maximum: any order gives the same
+    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (m >= M) return;
+    const int64_t target = targets[m];
+    float sum = 0.0f;
+    if (head_live(target, V, ignore)) {
+        const uint4* x = reinterpret_cast<const uint4*>(X + m * K);
+        const uint4* w = reinterpret_cast<const uint4*>(W + target * K);
+        for (int64_t i = lane; i < K / 8; i += 64) {
+            float a[8], b[8];
+            Vec16<uint16_t>::unpack(x[i], a);
+            Vec16<uint16_t>::unpack(w[i], b);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sum = __fmaf_rn(a[u], b[u], sum);
+        }
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
     }
+    if (lane == 0) {
+        zy[m] = sum * LOG2E;
+        ref[m] = rintf(sum * LOG2E);
+        total[m] = 0.0f;
+    }
+}
+
+struct JoinArgs {
+    const float2* part;       // [Mp][tiles] of the piece: reference and sum
+    int tiles;
+    int64_t M, Mp;
+    const int64_t* targets;
+    int64_t ignore, V;
+    uint16_t* E;              // in fragment order,
+    int64_t steps;            // blocks of a row tile
+    float *ref, *total;       // running reference and sum of each row
+    float* factor;            // out: factor on the row's sums so far
+    const float* zy;
+    int last;                 // 1: also the loss and what the gradients need of a row
+    const float* dloss;
+    float* loss;
+    float2* ends;             // out (last): factor on the sums, and on the target's row of W
+    float4* rows;             // out (last): see HeadArgs
+};
+
+// After a piece: each row's new reference and sum, its tiles brought to that reference.  One
+// wave per row (rows that only fill the last tile included).
+__global__ __launch_bounds__(256)
+void k_head_join(JoinArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (m >= a.Mp) return;
+    const int64_t target = m < a.M ? a.targets[m] : -1;
+    if (m >= a.M || !head_live(target, a.V, a.ignore)) {
+        if (lane == 0 && a.last) a.rows[m] = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
+        if (lane == 0 && m < a.M) {
+            a.factor[m] = 1.0f;
+            if (a.last) {
+                if (a.loss) a.loss[m] = 0.0f;
+                a.ends[m] = make_float2(0.0f, 0.0f);
+            }
+        }
+        return;
+    }
+    const float2* part = a.part + m * a.tiles;
+    const float old = a.ref[m];
+    float now = old;
+    for (int t = lane; t < a.tiles; t += 64) now = fmaxf(now, part[t].x);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) now = fmaxf(now, __shfl_xor(now, x));
+    float sum = 0.0f;
+    for (int t0 = 0; t0 < a.tiles; t0 += 64) {
+        const int t = t0 + lane;
+        const float2 p = t < a.tiles ? part[t] : make_float2(now, 0.0f);
+        sum += p.y * (p.x == now ? 1.0f : __builtin_amdgcn_exp2f(p.x - now));
+        // tiles left below the row's new reference are scaled
+        uint64_t todo = __ballot(p.x < now);
+        const int in = (int)(m % HL_TM);
+        uint8_t* blocks = reinterpret_cast<uint8_t*>(a.E) + (m / HL_TM) * a.steps * A_BLOCK_BYTES + (in >> 5) * 4096 + (in & 31) * 16;
+        while (todo) {
+            const int b = __ffsll((unsigned long long)todo) - 1;
+            todo &= todo - 1;
+            const float f = __builtin_amdgcn_exp2f(__shfl(p.x, b) - now);
+            // the row's 128 values of the tile: 8 chunks of 16 bytes, 512 bytes apart, in each of two blocks
+            if (lane < 16) {
+                uint4* e = reinterpret_cast<uint4*>(blocks + (2 * (t0 + b) + (lane >> 3)) * (int64_t)A_BLOCK_BYTES + (lane & 7) * 512);
+                float x[8];
+                Vec16<uint16_t>::unpack(*e, x);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) x[u] *= f;
+                *e = Vec16<uint16_t>::pack(x);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    if (lane != 0) return;
+    const float f = old == now ? 1.0f : __builtin_amdgcn_exp2f(old - now);
+    const float total = a.total[m] * f + sum;
+    a.ref[m] = now;
+    a.total[m] = total;
+    a.factor[m] = f;
+    if (!a.last) return;
+    const float z = a.zy[m], g = a.dloss[m];
+    RowLoss r = row_loss(z, now + log2f(total));
+    if (!(fabsf(z) < INFINITY)) r = RowLoss{NAN, NAN, NAN};
+    if (a.loss) a.loss[m] = r.loss;
+    a.ends[m] = make_float2(g * __builtin_amdgcn_exp2f(now - r.lse), g * r.rest);
+    a.rows[m] = make_float4(r.lse, r.rest, g, __int_as_float((int)target));
 }
 
 struct ProductArgs {
-    const uint16_t* A;        // [rows][lda]: contraction along the row
-    int64_t lda, rows, out_rows;   // rows of A (all readable), rows written
-    const uint16_t* B;        // [P][N]: contraction down the rows
-    int64_t P, N;             // contraction values of B (A has zeros past them), columns
+    const uint16_t* A;        // in fragment order, `a_steps` blocks of each row tile
+    int64_t a_steps, out_rows;
+    const uint16_t* B;        // [P][N]: contraction down the rows (A has zeros past P)
+    int64_t P, N;
     int steps;                // contraction steps of 64: each starts below P
-    int tiles_r, tiles_n;
-    uint16_t* out;            // bf16 [out_rows][N], or null
-    float* sum;               // fp32 [out_rows][N], or null
-    int add;                  // 1: add what `sum` holds
-    const uint32_t* top;      // factor on `out` (fp32 bits)
+    int splits;               // parts of the contraction, each with sums of its own
+    int64_t tiles_r, tiles_n;
+    float* sum;               // fp32 [splits][out_rows][N]
+    const float* factor;      // ADD: factor of each row on what `sum` holds
+    uint16_t* out;            // OUT_DX, OUT_DW: bf16 [out_rows][N] (splits == 1)
+    const uint32_t* top;      // OUT_DW: times head_scale(top)
+    const float2* ends;       // OUT_DX: out[r] = ends[r].x * sums - ends[r].y * W[targets[r]]
+    const uint16_t* W;
+    const int64_t* targets;
+    int64_t V, ignore;
 };
 
-// C[r][n] = sum_p A[r][p] B[p][n], tiles of 256 rows x 256 columns.
-__global__ __launch_bounds__(512)
+// Four values of a finished row of dX; u: the target's row of W there.
+__device__ __forceinline__ uint2 head_dx4(f32x4 y, float2 row, uint2 u) {
+    return make_uint2(pack_bf16x2(row.x * y[0] - row.y * bf16_lo(u.x), row.x * y[1] - row.y * bf16_hi(u.x)),
+                      pack_bf16x2(row.x * y[2] - row.y * bf16_lo(u.y), row.x * y[3] - row.y * bf16_hi(u.y)));
+}
+
+// C[r][n] = sum_p A[r][p] B[p][n], tiles of 512 rows x 128 columns; ADD: on top of what `sum` holds.
+enum ProductOut { OUT_SUM, OUT_DX, OUT_DW };
+template <ProductOut OUT, bool ADD>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_head_product(ProductArgs a) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * HL_STAGE];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5, rl = lane & 31;
-    int tr, tn;
+    const int split = blockIdx.y;
+    int64_t tr, tn;
     if (!hl_tile(blockIdx.x, a.tiles_r, a.tiles_n, tr, tn)) return;
-    const int64_t r0 = (int64_t)tr * HL_T, n0 = (int64_t)tn * HL_T;
-    const int wn = wave >> 2, wr = wave & 3;           // 2 x 4 waves of 128 columns x 64 rows
-    uint32_t aof[4];
-    int brow[4];
-    uint32_t bcol[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = wave * 32 + i * 8 + (lane >> 3);
-        const int64_t ra = r0 + row < a.rows ? row : a.rows - 1 - r0;
-        aof[i] = (uint32_t)(ra * a.lda * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
-        brow[i] = wave * 8 + i * 2 + (lane >> 5);
-        const int q = lane & 31;
-        const int chunk = (((q >> 1) ^ ((brow[i] & 3) << 1)) << 1) | (q & 1);
-        bcol[i] = (uint32_t)(n0 + chunk * 8 < a.N ? chunk * 16 : 0);   // columns past the last: any, dropped
+    const int per = (a.steps + a.splits - 1) / a.splits;
+    const int first = __builtin_amdgcn_readfirstlane(split * per);
+    const int last = __builtin_amdgcn_readfirstlane(first + per < a.steps ? first + per : a.steps);
+    const int64_t r0 = tr * HL_TM, n0 = tn * HL_TN;
+    const uint32_t mine = lds_address(lds) + wave * 4096;
+    // a wave fills rows 16 wave .. of a stage, 4 rows a load; columns past N: any, dropped later
+    uint32_t bcol = 0;
+    {
+        const int q = lane & 15, row = lane >> 4;
+        const int chunk = (((q >> 1) ^ (row << 1)) << 1) | (q & 1);
+        bcol = (uint32_t)(n0 + chunk * 8 < a.N ? chunk * 16 : 0);
     }
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.A + r0 * a.lda, (a.rows - r0) * a.lda * 2);
-    auto load = [&](int stage, int step) {
-        lds_u8* base = (lds_u8*)lds + stage * 2 * HL_STAGE + wave * 4096;
-        const int64_t p0 = (int64_t)step * HL_K;
-        const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.B + p0 * a.N + n0, (a.P - p0) * a.N * 2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            load_to_lds(ra, base + i * 1024, aof[i], (uint32_t)step * 128);
-            // contraction rows past the last repeat it: A is zero there
-            const int64_t row = p0 + brow[i] < a.P ? brow[i] : a.P - 1 - p0;
-            load_to_lds(rb, base + HL_STAGE + i * 1024, (uint32_t)(row * a.N * 2) + bcol[i], 0);
-        }
-    };
-    f32x16 acc[4][2];
+    f32x16 acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
-    const int g = lane >> 4, jl = lane & 15;
-    const int trow = 8 * (g >> 1) + (jl >> 2);
-    int tof[4];
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    if (first < last)
+        hl_loop<true, true>(acc, lds, a.A + tr * a.a_steps * (int64_t)(A_BLOCK_BYTES / 2), hl_block_bytes(a.out_rows - r0), first, last,
+                            wave, lane,
+                            [&](int stage, int step, int q) {
+                                const int64_t p0 = (int64_t)step * HL_K;
+                                const hl_rsrc rb = hl_make_rsrc(a.B + p0 * a.N + n0, (a.P - p0) * a.N * 2);
+                                // contraction rows past the last repeat it: A is zero there
+                                const int row = wave * 16 + q * 4 + (lane >> 4), most = (int)(a.P - p0 < HL_K ? a.P - p0 : HL_K) - 1;
+                                load_to_lds(rb, mine + stage * HL_STAGE + q * 1024,
+                                            (uint32_t)((row < most ? row : most) * (int)a.N * 2) + bcol, 0);
+                            });
+    // accumulator (i, j, reg): row 32 i + rl of the wave's 128, column 32 j + 8 (reg / 4) + 4 h + reg % 4.  Each 32
+    // rows go through the wave's own quarter of LDS (row r's 16-byte chunk c at c ^ r), so that memory is met in
+    // whole rows of 128 columns.
+    __syncthreads();
+    uint8_t* turn = lds + wave * HL_STAGE;
+    float* sums = a.sum + split * a.out_rows * a.N;
+    const int chunk = lane & 31;
+    const int64_t n = n0 + 4 * chunk;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tof[i] = hl_toff(trow, wn * 128 + i * 32 + 16 * (g & 1) + 4 * (jl & 3));
-    load(0, 0);
-    for (int it = 0; it < a.steps; ++it) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (it + 1 < a.steps) load((it + 1) & 1, it + 1);
-        const uint8_t* sa = lds + (it & 1) * 2 * HL_STAGE;
-        const uint8_t* sb = sa + HL_STAGE;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t ri = r0 + wave * 128 + i * 32;
+        if (ri >= a.out_rows) break;
+        // what the rows are joined with is requested before the turn through LDS
+        f32x4 old[16];
+        uint2 wy[16];
+        float2 end[16];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            bf16x8 bf[4], af[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) af[j] = *reinterpret_cast<const bf16x8*>(sa + hl_off(wr * 64 + j * 32 + rl, 2 * s + h));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint2 lo = hl_read_tr(sb + tof[i] + s * 16 * 512);
-                const uint2 hi = hl_read_tr(sb + tof[i] + s * 16 * 512 + 4 * 512);
-                bf[i] = __builtin_bit_cast(bf16x8, make_uint4(lo.x, lo.y, hi.x, hi.y));
+        for (int q = 0; q < 16; ++q) {
+            const int64_t r = ri + 2 * q + h;
+            const bool in = r < a.out_rows && n < a.N;
+            old[q] = f32x4{};
+            wy[q] = make_uint2(0, 0);
+            end[q] = make_float2(0.0f, 0.0f);
+            if (ADD && in) old[q] = *reinterpret_cast<const f32x4*>(sums + r * a.N + n) * a.factor[r];
+            if (OUT == OUT_DX && in) {
+                const int64_t target = a.targets[r];
+                wy[q] = *reinterpret_cast<const uint2*>(a.W + (head_live(target, a.V, a.ignore) ? target * a.N : 0) + n);
+                end[q] = a.ends[r];
             }
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[i], af[j], acc[i][j], 0, 0, 0);
+            for (int r4 = 0; r4 < 4; ++r4)
+                *reinterpret_cast<f32x4*>(turn + rl * 512 + (((8 * j + 2 * r4 + h) ^ rl) << 4)) =
+                    f32x4{acc[i][j][4 * r4], acc[i][j][4 * r4 + 1], acc[i][j][4 * r4 + 2], acc[i][j][4 * r4 + 3]};
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int in = 2 * q + h;
+            const int64_t r = ri + in;
+            f32x4 y = *reinterpret_cast<const f32x4*>(turn + in * 512 + ((chunk ^ in) << 4)) + old[q];
+            if (r >= a.out_rows || n >= a.N) continue;
+            if constexpr (OUT == OUT_SUM) {
+                *reinterpret_cast<f32x4*>(sums + r * a.N + n) = y;
+            } else if constexpr (OUT == OUT_DW) {
+                y *= head_scale(a.top);
+                *reinterpret_cast<uint2*>(a.out + r * a.N + n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            } else {
+                *reinterpret_cast<uint2*>(a.out + r * a.N + n) = head_dx4(y, end[q], wy[q]);
+            }
         }
     }
-    // accumulator (i, j, reg): column 32 i + 8 (reg / 4) + 4 h + reg % 4 of the wave's 128, row 32 j + rl of its 64
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t r = r0 + wr * 64 + j * 32 + rl;
-        if (r >= a.out_rows) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                const int64_t n = n0 + wn * 128 + i * 32 + 8 * r4 + 4 * h;
-                if (n >= a.N) continue;
-                f32x4 y = {acc[i][j][4 * r4], acc[i][j][4 * r4 + 1], acc[i][j][4 * r4 + 2], acc[i][j][4 * r4 + 3]};
-                if (a.add) y += *reinterpret_cast<const f32x4*>(a.sum + r * a.N + n);
-                if (a.out) y *= __uint_as_float(*a.top);
-                if (a.out)
-                    *reinterpret_cast<uint2*>(a.out + r * a.N + n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-                else
-                    *reinterpret_cast<f32x4*>(a.sum + r * a.N + n) = y;
-            }
+}
+
+// dX from the sums of several parts of the contraction: a workgroup per row.
+__global__ __launch_bounds__(256)
+void k_head_finish(ProductArgs a, uint16_t* out) {
+    const int64_t r = blockIdx.x;
+    const float2 row = a.ends[r];
+    const int64_t target = a.targets[r];
+    const uint16_t* w = a.W + (head_live(target, a.V, a.ignore) ? target * a.N : 0);
+    for (int64_t n = threadIdx.x * 4; n < a.N; n += 1024) {
+        f32x4 y = {};
+        for (int s = 0; s < a.splits; ++s) y += *reinterpret_cast<const f32x4*>(a.sum + (s * a.out_rows + r) * a.N + n);
+        *reinterpret_cast<uint2*>(out + r * a.N + n) = head_dx4(y, row, *reinterpret_cast<const uint2*>(w + n));
     }
 }
 
@@ -358,88 +677,146 @@ void k_head_product(ProductArgs a) {
 struct HeadPlan {
     int64_t Mp;               // tokens up to whole tiles
     int64_t tiles;            // vocabulary tiles
-    int64_t piece;            // vocabulary tiles of a piece
-    size_t top, zy, rows, part, G, Gt, sum, bytes;
+    int64_t piece;            // vocabulary tiles of a piece (a multiple of 4: whole row tiles of G^T)
+    int splits;               // parts of dX's contraction
+    size_t top, zy, ref, total, factor, ends, rows, part, Xp, E, sum, bytes;
 };
 
 static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     HeadPlan p{};
-    p.Mp = (M + HL_T - 1) / HL_T * HL_T;
-    p.tiles = (V + HL_T - 1) / HL_T;
-    // a piece of G of at most 64 MB (and its transpose) stays in the 256 MB last-level cache
-    const int64_t most = ((int64_t)64 << 20) / (p.Mp > 0 ? p.Mp * HL_T * 2 : 1);
-    p.piece = most < 1 ? 1 : (most < p.tiles ? most : p.tiles);
+    const bool grad = dx || dw;
+    p.Mp = (M + HL_TM - 1) / HL_TM * HL_TM;
+    p.tiles = (V + HL_TN - 1) / HL_TN;
+    // a piece of E or G^T of at most 128 MB, half of the last-level cache: larger pieces pass over dX's
+    // fp32 sums less often (64 MB: 947 us for 2048 tokens x 32000 x 4096, 128 MB: 903 us)
+    const int64_t most = ((int64_t)128 << 20) / (p.Mp > 0 ? p.Mp * HL_TN * 2 : 1) / 4 * 4;
+    p.piece = most < 4 ? 4 : most;
+    if (p.piece > p.tiles) p.piece = (p.tiles + 3) / 4 * 4;
+    // where dX has too few tiles for the 256 compute units, its contraction is cut into parts
+    // of at least 16 steps
+    p.splits = 1;
+    const int64_t tiles = p.Mp / HL_TM * ((K + HL_TN - 1) / HL_TN), steps = p.piece * (HL_TN / HL_K);
+    while (p.splits < 8 && tiles * p.splits * 2 <= 256 && steps / (p.splits * 2) >= 16) p.splits *= 2;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t was = at;
         at += (n + 255) & ~(size_t)255;
         return was;
     };
+    const size_t row = (size_t)p.Mp * 4;
     p.top = take(4);
-    p.zy = take((size_t)p.Mp * 4);
-    p.rows = take((size_t)p.Mp * sizeof(float2));
-    p.part = take((size_t)p.Mp * p.tiles * sizeof(float2));
-    p.G = take(dx ? (size_t)p.Mp * p.piece * HL_T * 2 : 0);
-    p.Gt = take(dw ? (size_t)p.Mp * p.piece * HL_T * 2 : 0);
-    p.sum = take(dx && p.piece < p.tiles ? (size_t)M * K * 4 : 0);
+    p.zy = take(row);
+    p.ref = take(row);
+    p.total = take(row);
+    p.factor = take(row);
+    p.ends = take(2 * row);
+    p.rows = take(4 * row);
+    p.part = take((size_t)p.Mp * (grad ? p.piece : p.tiles) * sizeof(float2));
+    p.Xp = take((size_t)p.Mp * K * 2);
+    p.E = take(grad ? (size_t)p.Mp * p.piece * HL_TN * 2 : 0);
+    p.sum = take(dx && (p.piece < p.tiles || p.splits > 1) ? (size_t)M * K * 4 * p.splits : 0);
     p.bytes = at;
     return p;
 }
 
 size_t head_loss_ws_bytes(int64_t M, int64_t K, int64_t V, bool dx, bool dw) { return head_plan(M, K, V, dx, dw).bytes; }
 
+static dim3 head_grid(int64_t x, int64_t y, int splits = 1) { return dim3((uint32_t)((x * y + 7) / 8 * 8), (uint32_t)splits); }
+
+template <typename F>
+static void for_pieces(const HeadPlan& p, int64_t V, F&& f) {
+    for (int64_t t0 = 0; t0 < p.tiles; t0 += p.piece) {
+        const int64_t n = p.tiles - t0 < p.piece ? p.tiles - t0 : p.piece;
+        const int64_t v0 = t0 * HL_TN, rows = V - v0 < n * HL_TN ? V - v0 : n * HL_TN;
+        f(v0, n, rows, t0 + n >= p.tiles);
+    }
+}
+
 hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint16_t* W, int64_t V,
                             const int64_t* targets, int64_t ignore, const float* dloss, float* loss, uint16_t* dX,
                             uint16_t* dW, void* ws, hipStream_t s) {
     const HeadPlan p = head_plan(M, K, V, dX != nullptr, dW != nullptr);
     uint8_t* base = (uint8_t*)ws;
-    constexpr int lds = 4 * HL_STAGE;
-    for (const void* f : {(const void*)k_head_logits<false>, (const void*)k_head_logits<true>, (const void*)k_head_product}) {
-        const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-    }
+    const dim3 row_grid((uint32_t)(p.Mp / 4));
     HeadArgs a{};
-    a.X = X;
+    uint16_t* Xp = (uint16_t*)(base + p.Xp);
+    a.Xp = Xp;
     a.W = W;
     a.M = M;
     a.K = K;
     a.V = V;
     a.targets = targets;
     a.ignore = ignore;
-    a.dloss = dloss;
     a.part = (float2*)(base + p.part);
     a.zy = (float*)(base + p.zy);
-    a.rows = (float2*)(base + p.rows);
+    a.ref = (float*)(base + p.ref);
+    a.rows = (float4*)(base + p.rows);
     a.top = (uint32_t*)(base + p.top);
+    a.out = (uint16_t*)(base + p.E);
     a.Mp = p.Mp;
-    a.tiles_m = (int)(p.Mp / HL_T);
-    a.tiles_v = (int)p.tiles;
-    auto grid = [](int64_t x, int64_t y) { return dim3((uint32_t)((x * y + 7) / 8 * 8)); };
-    hipLaunchKernelGGL(k_head_logits<false>, grid(a.tiles_v, a.tiles_m), dim3(512), lds, s, a);
-    hipLaunchKernelGGL(k_head_rows, dim3((uint32_t)((M + 255) / 256)), dim3(256), 0, s, a.part, a.zy, targets, M, p.Mp, V,
-                       ignore, (int)p.tiles, dX || dW ? dloss : nullptr, a.top, (float2*)(base + p.rows), loss);
-    if (!dX && !dW) return hipGetLastError();
-    a.G = dX ? (uint16_t*)(base + p.G) : nullptr;
-    a.Gt = dW ? (uint16_t*)(base + p.Gt) : nullptr;
-    for (int64_t t0 = 0; t0 < p.tiles; t0 += p.piece) {
-        const int64_t n = p.tiles - t0 < p.piece ? p.tiles - t0 : p.piece;
-        const int64_t rows = V - t0 * HL_T < n * HL_T ? V - t0 * HL_T : n * HL_T;   // vocabulary rows of the piece
-        a.v0 = t0 * HL_T;
-        a.tiles_v = (int)n;
-        a.ldg = n * HL_T;
-        hipLaunchKernelGGL(k_head_logits<true>, grid(a.tiles_v, a.tiles_m), dim3(512), lds, s, a);
-        const int tiles_n = (int)((K + HL_T - 1) / HL_T);
-        if (dX) {
-            const bool last = t0 + n >= p.tiles;
-            ProductArgs d{a.G, a.ldg, p.Mp, M, W + a.v0 * K, rows, K, (int)((rows + HL_K - 1) / HL_K), a.tiles_m, tiles_n,
-                          last ? dX : nullptr, (float*)(base + p.sum), t0 > 0 ? 1 : 0, a.top};
-            hipLaunchKernelGGL(k_head_product, grid(d.tiles_r, d.tiles_n), dim3(512), lds, s, d);
-        }
-        if (dW) {
-            ProductArgs d{a.Gt, p.Mp, a.ldg, rows, X, M, K, (int)((M + HL_K - 1) / HL_K), (int)n, tiles_n, dW + a.v0 * K, nullptr, 0, a.top};
-            hipLaunchKernelGGL(k_head_product, grid(d.tiles_r, d.tiles_n), dim3(512), lds, s, d);
-        }
+    a.tiles_m = p.Mp / HL_TM;
+    a.tiles_v = p.tiles;
+    hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(a.tiles_m * 4)), dim3(256), 0, s, X, M, K, Xp);
+    if (!dX && !dW) {
+        hipLaunchKernelGGL(k_head_logits<HEAD_STATS>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(k_head_rows, row_grid, dim3(256), 0, s, a.part, a.zy, targets, M, V, ignore, (int)p.tiles, loss);
+        return hipGetLastError();
     }
+    float* ref = (float*)(base + p.ref);
+    float* total = (float*)(base + p.total);
+    uint32_t* top = (uint32_t*)(base + p.top);
+    ProductArgs d{};
+    d.A = a.out;
+    d.N = K;
+    d.tiles_n = (K + HL_TN - 1) / HL_TN;
+    d.sum = (float*)(base + p.sum);
+    d.factor = (float*)(base + p.factor);
+    d.ends = (float2*)(base + p.ends);
+    d.W = W;
+    d.targets = targets;
+    d.V = V;
+    d.ignore = ignore;
+    d.splits = p.splits;
+    hipLaunchKernelGGL(k_head_target, dim3((uint32_t)((M + 3) / 4 + 1)), dim3(256), 0, s, X, W, M, K, V, targets, ignore, a.zy,
+                       ref, total, dloss, top);
+    for_pieces(p, V, [&](int64_t v0, int64_t n, int64_t rows, bool last) {
+        a.v0 = v0;
+        a.tiles_v = n;
+        a.out_steps = 2 * n;
+        hipLaunchKernelGGL(k_head_logits<HEAD_E>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
+        const JoinArgs j{a.part, (int)n, M, p.Mp, targets, ignore, V, a.out, a.out_steps, ref, total, (float*)(base + p.factor),
+                         a.zy, last ? 1 : 0, dloss, loss, (float2*)(base + p.ends), (float4*)(base + p.rows)};
+        hipLaunchKernelGGL(k_head_join, row_grid, dim3(256), 0, s, j);
+        if (!dX) return;
+        d.a_steps = a.out_steps;
+        d.out_rows = M;
+        d.B = W + v0 * K;
+        d.P = rows;
+        d.steps = (int)((rows + HL_K - 1) / HL_K);
+        d.tiles_r = a.tiles_m;
+        d.out = dX;
+        const bool add = v0 > 0, closes = last && p.splits == 1;
+        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, head_grid(d.tiles_r, d.tiles_n, d.splits), dim3(256), 0, s, d); };
+        if (closes) add ? run(k_head_product<OUT_DX, true>) : run(k_head_product<OUT_DX, false>);
+        else add ? run(k_head_product<OUT_SUM, true>) : run(k_head_product<OUT_SUM, false>);
+    });
+    if (dX && p.splits > 1) hipLaunchKernelGGL(k_head_finish, dim3((uint32_t)M), dim3(256), 0, s, d, dX);
+    if (!dW) return hipGetLastError();
+    d.splits = 1;
+    d.top = top;
+    d.B = X;
+    d.P = M;
+    d.steps = (int)((M + HL_K - 1) / HL_K);
+    d.a_steps = a.out_steps = p.Mp / HL_K;
+    for_pieces(p, V, [&](int64_t v0, int64_t n, int64_t rows, bool) {
+        a.v0 = v0;
+        a.tiles_v = n;
+        hipLaunchKernelGGL(k_head_logits<HEAD_GT>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
+        d.out_rows = rows;
+        d.tiles_r = (n + 3) / 4;
+        d.out = dW + v0 * K;
+        hipLaunchKernelGGL((k_head_product<OUT_DW, false>), head_grid(d.tiles_r, d.tiles_n), dim3(256), 0, s, d);
+    });
     return hipGetLastError();
 }
 
