@@ -33,6 +33,7 @@
 // many cycles as the matrix instructions; 940-1000 TFLOP/s.)
 #include "bufio.h"
 #include "decoder.h"
+#include "lds_dma.h"
 #include "tile_map.h"
 
 namespace nf4 {
@@ -43,25 +44,6 @@ constexpr int HL_K = 64;                  // contraction step
 constexpr int HL_STAGE = HL_TN * HL_K * 2;   // an LDS stage: 16 KB
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-
-// A buffer descriptor as plain registers.
-typedef int hl_rsrc __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ hl_rsrc hl_make_rsrc(const void* base, int64_t bytes) {
-    const uint64_t p = (uint64_t)base;
-    return hl_rsrc{(int)(uint32_t)p, (int)((p >> 32) & 0xFFFF), (int)(bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF), 0x00020000};
-}
-
-// Sixteen bytes per lane from memory into LDS at `at` + 16 * lane, without passing registers.  In
-// assembly, because the compiler makes a transposing LDS read wait for every such load of the
-// builtin's kind, whichever stage it fills (1016 instead of 1200 TFLOP/s in the second product);
-// the loop below waits for a stage itself.  (Nothing else in these kernels uses m0.)  The compiler counts the loads it knows of, so its own
-// waits with these among them are only stricter.
-__device__ __forceinline__ void load_to_lds(hl_rsrc r, uint32_t at, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voff), "s"(r), "s"(soff) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)(p);
-}
 
 // Stage of a direct operand: 128 rows of 128 bytes (64 values of the contraction), 16-byte chunk c of
 // row r at chunk c ^ g(r), so that 16 neighbouring rows reading one chunk meet all 64 banks once.
@@ -278,7 +260,7 @@ void k_head_logits(HeadArgs a) {
         const int64_t rv = v0 + row < a.V ? row : a.V - 1 - v0;
         wof[q] = (uint32_t)(rv * a.K * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
     }
-    const hl_rsrc rw = hl_make_rsrc(a.W + v0 * a.K, (a.V - v0) * a.K * 2);
+    const dma_rsrc rw = make_dma_rsrc(a.W + v0 * a.K, (a.V - v0) * a.K * 2);
     const uint32_t mine = lds_address(lds) + wave * 4096;
     f32x16 acc[4][4];
 #pragma unroll
@@ -599,7 +581,7 @@ void k_head_product(ProductArgs a) {
                             wave, lane,
                             [&](int stage, int step, int q) {
                                 const int64_t p0 = (int64_t)step * HL_K;
-                                const hl_rsrc rb = hl_make_rsrc(a.B + p0 * a.N + n0, (a.P - p0) * a.N * 2);
+                                const dma_rsrc rb = make_dma_rsrc(a.B + p0 * a.N + n0, (a.P - p0) * a.N * 2);
                                 // contraction rows past the last repeat it: A is zero there
                                 const int row = wave * 16 + q * 4 + (lane >> 4), most = (int)(a.P - p0 < HL_K ? a.P - p0 : HL_K) - 1;
                                 load_to_lds(rb, mine + stage * HL_STAGE + q * 1024,

@@ -24,6 +24,7 @@
 // launch.  Bound by HBM: each key and value byte is read once per row tile.
 #include "bufio.h"
 #include "paged.h"
+#include "tile_map.h"
 
 namespace nf4 {
 
@@ -32,6 +33,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int KV_STEP = 32;               // keys of a step
 constexpr int KV_WAVES = 4;
+constexpr int KV_FEW = 32;                // rows of a (sequence, kv head) that count as few
 constexpr float KV_FLOOR = -3e38f;        // reference before any key: finite, so that no inf - inf arises
 constexpr float KV_BIAS = 10.0f;          // weights are at most 2^(KV_BIAS + KV_SLACK) = 2^15 (fp16 reaches 2^16)
 constexpr float KV_SLACK = 5.0f;          // a reference is raised once a score passes it by more than this
@@ -41,12 +43,16 @@ struct AttendArgs {
     BatchView b;
     HeadsView q, out;
     int group;                // query heads per kv head
-    int row_tiles;            // launched row tiles per (sequence, kv head)
+    int row_tiles;            // k_attend_rows: launched row tiles per (sequence, kv head)
+    int blocks;               // k_attend_block: launched blocks of CT row tiles per (sequence, kv head)
     int chunk;                // keys per chunk, a multiple of 4 * KV_STEP
     int splits;               // launched chunks per row tile
-    float scale2;             // scale * log2(e)
-    float* part;              // [token][head][split][D] sums, and
-    float2* sums;             // [token][head][split] reference and denominator (splits > 1)
+    float scale2;             // |scale| * log2(e)
+    uint32_t flip;            // sign bits of a bf16 pair if scale < 0
+    int limit;                // rows of a (sequence, kv head) up to which k_attend_rows takes it (else k_attend_block)
+    int few;                  // k_attend_rows: rows of each up to which they have slots for their chunks' parts
+    float* part;              // [row slot][split][D] sums, and
+    float2* sums;             // [row slot][split] reference and denominator (splits > 1)
 };
 
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint2 w, float scale) {
@@ -65,31 +71,22 @@ __device__ __forceinline__ T scalar_load(const T* p) {
     return *(const __attribute__((address_space(4))) T*)(uintptr_t)p;
 }
 
-// page_of through scalar loads.
-__device__ __forceinline__ int uniform_page_of(const CacheView& c, const BatchView& b, int seq, int page_index) {
-    if (page_index < 0 || page_index >= b.table_width) return -1;
-    const int page = scalar_load(b.table + seq * b.table_stride + page_index);
-    return page >= 0 && page < c.pages ? page : -1;
+// The table's entry for a page index of a sequence, through a scalar load that no branch and no check
+// waits for: where the entry is looked at, page_or_none checks it.
+__device__ __forceinline__ int page_entry(const BatchView& b, int seq, int page_index) {
+    const int last = b.table_width - 1;
+    return scalar_load(b.table + seq * b.table_stride + (page_index < last ? page_index : last));
 }
+__device__ __forceinline__ int page_or_none(const CacheView& c, int entry) { return entry >= 0 && entry < c.pages ? entry : -1; }
 
-// The codes of 16 keys of one kv head from `slot` of a page on, and their values': ranges that
-// end with the last key that counts, so that whatever lies behind it reads as zero.
-struct TileView {
-    __amdgpu_buffer_rsrc_t k, v;
-    float ks, vf;             // key scale; value exponent
+// Scales of a tile as bits.  They are looked at a step after their load was started.
+struct TileScales {
+    uint32_t k, v;
+    int end;                              // keys of the tile that count lie below; 0: none, and the scales are anything
 };
-template <int D>
-__device__ __forceinline__ TileView tile_view(const CacheView& c, int page, int head, int slot, int have) {
-    const int64_t block = (int64_t)(page < 0 ? 0 : page) * 2 * c.heads + head;
-    const int64_t page_bytes = (int64_t)D << c.page_log2;
-    const uint8_t* kb = c.codes + block * page_bytes + slot * D;
-    const int bytes = page < 0 || have <= 0 ? 0 : (have < 16 ? have : 16) * D;
-    TileView t;
-    t.k = make_rsrc(kb, bytes);
-    t.v = make_rsrc(kb + c.heads * page_bytes, bytes);
-    t.ks = scalar_load(c.scales + block);
-    t.vf = (float)((int)((__float_as_uint(scalar_load(c.scales + block + c.heads)) >> 23) & 0xFFu) - 127);
-    return t;
+__device__ __forceinline__ float key_scale(const TileScales& t) { return t.end > 0 ? __uint_as_float(t.k) : 1.0f; }
+__device__ __forceinline__ float value_exponent(const TileScales& t) {
+    return t.end > 0 ? (float)((int)((t.v >> 23) & 0xFFu) - 127) : 0.0f;
 }
 
 // One step's codes of a wave: two tiles of 16 keys.
@@ -97,9 +94,61 @@ template <int D>
 struct StepCodes {
     uint4 k[2][D / 64];                   // [tile][piece]: 16 bytes of the lane's key
     uint32_t v[2][4][D / 64];             // [tile][token 4 g + r]: D / 16 bytes of its values
-    float ks[2], vf[2];
-    int end[2];                           // keys of the tile that count lie below
+    TileScales scale[2];
 };
+
+// The step's codes at key `first` of a sequence whose keys end at `hi`: ranges that end with the last key that
+// counts, so that whatever lies behind it reads as zero; a page outside the pool holds no keys.
+template <int D, int AUX>
+__device__ __forceinline__ void load_step(StepCodes<D>& x, const CacheView& c, int head, int first, int hi, const int* entries,
+                                          uint32_t koff, uint32_t voff) {
+    const int64_t page_bytes = (int64_t)D << c.page_log2;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int at = first + 16 * t, page = page_or_none(c, entries[t]);
+        const int have = page < 0 || hi <= at ? 0 : (hi - at < 16 ? hi - at : 16);
+        const int64_t block = (int64_t)(page < 0 ? 0 : page) * 2 * c.heads + head;
+        const uint8_t* kb = c.codes + block * page_bytes + (at & ((1 << c.page_log2) - 1)) * D;
+        const __amdgpu_buffer_rsrc_t rk = make_rsrc(kb, have * D), rv = make_rsrc(kb + c.heads * page_bytes, have * D);
+        x.scale[t] = TileScales{scalar_load((const uint32_t*)c.scales + block), scalar_load((const uint32_t*)c.scales + block + c.heads),
+                                have > 0 ? hi : 0};
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) x.k[t][p] = buf_load16_as<AUX>(rk, koff + 64 * p);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if constexpr (D == 64) x.v[t][r][0] = buf_load4_as<AUX>(rv, voff + r * D);
+            if constexpr (D == 128) {
+                const uint2 w = buf_load8_as<AUX>(rv, voff + r * D);
+                x.v[t][r][0] = w.x;
+                x.v[t][r][1] = w.y;
+            }
+            if constexpr (D == 256) {
+                const uint4 w = buf_load16_as<AUX>(rv, voff + r * D);
+                x.v[t][r][0] = w.x;
+                x.v[t][r][1] = w.y;
+                x.v[t][r][2] = w.z;
+                x.v[t][r][3] = w.w;
+            }
+        }
+    }
+}
+
+// Values of 8 tokens in the order of the weights: bytes 2 h and 2 h + 1 of dword d.
+template <int D>
+__device__ __forceinline__ void values_of(const uint32_t (&v)[2][4][D / 64], int d, int h, f16x8& v0, f16x8& v1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {             // token pairs
+        const uint32_t w0 = v[j >> 1][2 * (j & 1)][d], w1 = v[j >> 1][2 * (j & 1) + 1][d];
+        // bytes (tok0.b, tok1.b, tok0.b+1, tok1.b+1)
+        const uint32_t pk = __builtin_amdgcn_perm(w1, w0, h ? 0x07030602u : 0x05010400u);
+        const f16x2 lo2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(pk, 1.0f, false);
+        const f16x2 hi2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(pk, 1.0f, true);
+        v0[2 * j] = lo2[0];
+        v0[2 * j + 1] = lo2[1];
+        v1[2 * j] = hi2[0];
+        v1[2 * j + 1] = hi2[1];
+    }
+}
 
 // The state of a tile of 16 columns (query rows) in a wave.
 template <int D>
@@ -108,57 +157,131 @@ struct RowsState {
     float m, l;                           // reference (the same in a column's four lanes), the lane's part of the sum
 };
 
-// The scores y of 32 keys (lane: column col, keys 4 quarter + r of tile t) join the state.
+// The scores of 32 keys (lane: column col, keys 4 quarter + r of tile t; s: products, f: scale) raise the
+// state's reference where they must, and become weights.  vf: exponents of the values; ev: 2^-vf.
 template <int D>
-__device__ __forceinline__ void attend_step(RowsState<D>& st, float* y, const uint32_t (&v)[2][4][D / 64], const float* vf) {
-    constexpr int TILES = D / 16, PIECES = D / 64;
-    float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+__device__ __forceinline__ f16x8 weights_of(RowsState<D>& st, const f32x4* s, const float* f, const float* vf, const float* ev) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)               // f >= 0: the largest product has the largest score
+        top = fmaxf(top, __fmaf_rn(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])), f[t], vf[t]));
     if (__any(top > st.m + KV_SLACK)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float now = fmaxf(st.m, top);
-        const float f = __builtin_amdgcn_exp2f(st.m - now);
+        const float g = __builtin_amdgcn_exp2f(st.m - now);
         st.m = now;
-        st.l *= f;
+        st.l *= g;
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) st.acc[i] *= f;
+        for (int i = 0; i < D / 16; ++i) st.acc[i] *= g;
     }
     f16x8 w;
-    const float ref = st.m - KV_BIAS;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
+        const float shift = vf[t] - (st.m - KV_BIAS);
         float p[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            p[r] = __builtin_amdgcn_exp2f(y[4 * t + r] - ref);
+            p[r] = __builtin_amdgcn_exp2f(__fmaf_rn(s[t][r], f[t], shift));
             w[4 * t + r] = (_Float16)p[r];
         }
-        st.l = __fmaf_rn((p[0] + p[1]) + (p[2] + p[3]), __builtin_amdgcn_exp2f(-vf[t]), st.l);
+        st.l = __fmaf_rn((p[0] + p[1]) + (p[2] + p[3]), ev[t], st.l);
     }
-#pragma unroll
-    for (int d = 0; d < PIECES; ++d)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {             // bytes 2 h and 2 h + 1 of dword d: two dimension tiles
-            f16x8 v0, v1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {         // token pairs
-                const uint32_t w0 = v[j >> 1][2 * (j & 1)][d], w1 = v[j >> 1][2 * (j & 1) + 1][d];
-                // bytes (tok0.b, tok1.b, tok0.b+1, tok1.b+1)
-                const uint32_t pk = __builtin_amdgcn_perm(w1, w0, h ? 0x07030602u : 0x05010400u);
-                const f16x2 lo2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(pk, 1.0f, false);
-                const f16x2 hi2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(pk, 1.0f, true);
-                v0[2 * j] = lo2[0];
-                v0[2 * j + 1] = lo2[1];
-                v1[2 * j] = hi2[0];
-                v1[2 * j + 1] = hi2[1];
-            }
-            st.acc[4 * d + 2 * h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w, st.acc[4 * d + 2 * h], 0, 0, 0);
-            st.acc[4 * d + 2 * h + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w, st.acc[4 * d + 2 * h + 1], 0, 0, 0);
-        }
+    return w;
 }
 
+// A finished row, and a chunk's part of one, from the accumulators of a column's four lanes.
 template <int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 2 : 3)))
+__device__ __forceinline__ void write_row(const f32x4* acc, float total, uint16_t* o, int quarter) {
+    constexpr int TILES = D / 16;
+    const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;      // no key: zeros
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < TILES; i += 4)
+            *reinterpret_cast<uint2*>(o + (4 * quarter + r) * TILES + i) =
+                make_uint2(pack_bf16x2(acc[i][r] * inv, acc[i + 1][r] * inv), pack_bf16x2(acc[i + 2][r] * inv, acc[i + 3][r] * inv));
+}
+template <int D>
+__device__ __forceinline__ void write_part(const f32x4* acc, float m, float total, float* p, float2* sums, int quarter) {
+    constexpr int TILES = D / 16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < TILES; i += 4)
+            *reinterpret_cast<f32x4*>(p + (4 * quarter + r) * TILES + i) = f32x4{acc[i][r], acc[i + 1][r], acc[i + 2][r], acc[i + 3][r]};
+    if (quarter == 0) *sums = make_float2(m, total);
+}
+
+// Products of keys that a column does not see become -inf (a tile that every column sees passes).
+__device__ __forceinline__ f32x4 hide(f32x4 s, int key, int quarter, int low, int position, int end, bool always) {
+    if (key + 15 > low || key + 16 > end || always) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int k = key + 4 * quarter + r;
+            s[r] = k <= position && k < end ? s[r] : -INFINITY;
+        }
+    }
+    return s;
+}
+
+// A negative scale: the queries change sign instead.
+__device__ __forceinline__ bf16x8 query_piece(const uint16_t* p, uint32_t flip) {
+    uint4 w = *reinterpret_cast<const uint4*>(p);
+    w.x ^= flip;
+    w.y ^= flip;
+    w.z ^= flip;
+    w.w ^= flip;
+    return __builtin_bit_cast(bf16x8, w);
+}
+
+// A query row for the 8-bit matrix instructions, in the order of the key pieces: times a power of two
+// that brings its largest value to 128 .. 255, as the sum of two E4M3 numbers, the nearest one and 16 times
+// what that leaves.  8 significant bits are two of 4 (the second has a sign), so this is exact down to
+// 2^-14 of the largest value, and within 2^-23 of it below.  Returns what undoes the power of two.
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+template <int D>
+__device__ __forceinline__ float split_query(const uint16_t* row, int quarter, uint32_t flip, i32x8 (&q1)[D / 128], i32x8 (&q2)[D / 128]) {
+    float x[D / 64][16], top = 0.0f;
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p) {
+        uint4 w[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            w[u] = *reinterpret_cast<const uint4*>(row + 64 * p + 16 * quarter + 8 * u);
+            w[u] = make_uint4(w[u].x ^ flip, w[u].y ^ flip, w[u].z ^ flip, w[u].w ^ flip);
+            Vec16<uint16_t>::unpack(w[u], x[p] + 8 * u);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[p][i]));
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    int e = 0;
+    if (top > 0.0f && top < INFINITY) frexpf(top, &e);            // top = [0.5, 1) 2^e
+    e = e < -110 ? -110 : e;                                      // (both powers stay finite)
+    const float up = __uint_as_float((uint32_t)(127 + (e > 110 ? -102 : 8 - e)) << 23);
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[4], r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = x[p][4 * i + u] * up;
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+            w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) r[u] = (y[u] - e4m3_to_f32((uint32_t)w >> (8 * u) & 0xFFu)) * 16.0f;
+            int v = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
+            v = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], v, true);
+            q1[p >> 1][4 * (p & 1) + i] = w;
+            q2[p >> 1][4 * (p & 1) + i] = v;
+        }
+    return 1.0f / up;
+}
+
+template <int D, int AUX>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 3)))
 void k_attend_rows(AttendArgs a) {
     constexpr int PIECES = D / 64;        // 16-byte pieces of a key per lane; values dwords per token
     constexpr int KSTEPS = D / 32;        // products along the dimensions
@@ -171,13 +294,17 @@ void k_attend_rows(AttendArgs a) {
     const int begin = scalar_load(a.b.starts + seq), fresh = scalar_load(a.b.starts + seq + 1) - begin;
     const int before = scalar_load(a.b.lengths + seq);
     const int rows = fresh * a.group;
+    if (rows > a.limit) return;
     const int reach = a.b.table_width << a.c.page_log2;      // positions the table can hold
-    const int P = 1 << a.c.page_log2;
     __shared__ float sm[KV_WAVES][16], sl[KV_WAVES][16];
     __shared__ f32x4 so[2][TILES][64];
     const uint32_t koff = col * D + 16 * quarter, voff = 4 * quarter * D + col * (D / 16);
 
     for (int tile = tile0; tile * 16 < rows; tile += a.row_tiles) {
+        // a sequence with more rows than were announced has no slots: one workgroup takes all of its chunks
+        const bool whole = a.splits == 1 || rows > a.few;
+        if (whole && split > 0) continue;
+        const int stride = whole ? 1 : a.splits;
         const int row = tile * 16 + col;
         const bool live = row < rows;
         const int token = (live ? row : rows - 1) / a.group;
@@ -196,7 +323,7 @@ void k_attend_rows(AttendArgs a) {
                                  (int64_t)qhead * a.q.head_stride;
 #pragma unroll
             for (int s = 0; s < KSTEPS; ++s)
-                qf[s] = *reinterpret_cast<const bf16x8*>(qp + 64 * (s >> 1) + 16 * quarter + 8 * (s & 1));
+                qf[s] = query_piece(qp + 64 * (s >> 1) + 16 * quarter + 8 * (s & 1), a.flip);
         }
         RowsState<D> st;
 #pragma unroll
@@ -205,7 +332,7 @@ void k_attend_rows(AttendArgs a) {
         st.l = 0.0f;
 
         const int chunks = (keys + a.chunk - 1) / a.chunk;
-        for (int ch = split; ch < chunks; ch += a.splits) {
+        for (int ch = split; ch < chunks; ch += stride) {
             const int lo = ch * a.chunk;
             const int hi = lo + a.chunk < keys ? lo + a.chunk : keys;
             // this wave's steps: keys lo + 32 (wave + 4 i) ..
@@ -218,39 +345,15 @@ void k_attend_rows(AttendArgs a) {
             auto pages = [&](int i) {
                 Pages g;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) g.p[t] = uniform_page_of(a.c, a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
+                for (int t = 0; t < 2; ++t) g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
                 return g;
             };
             auto load = [&](StepCodes<D>& x, int i, const Pages& g) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int at = first_key(i) + 16 * t;
-                    const TileView v = tile_view<D>(a.c, g.p[t], head, at & (P - 1), hi - at);
-                    x.ks[t] = v.ks;
-                    x.vf[t] = v.vf;
-                    x.end[t] = g.p[t] < 0 ? 0 : hi;           // a page outside the pool holds no keys
-#pragma unroll
-                    for (int p = 0; p < PIECES; ++p) x.k[t][p] = buf_load16(v.k, koff + 64 * p, 0);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if constexpr (D == 64) x.v[t][r][0] = buf_load4(v.v, voff + r * D, 0);
-                        if constexpr (D == 128) {
-                            const uint2 w = buf_load8(v.v, voff + r * D, 0);
-                            x.v[t][r][0] = w.x;
-                            x.v[t][r][1] = w.y;
-                        }
-                        if constexpr (D == 256) {
-                            const uint4 w = buf_load16(v.v, voff + r * D, 0);
-                            x.v[t][r][0] = w.x;
-                            x.v[t][r][1] = w.y;
-                            x.v[t][r][2] = w.z;
-                            x.v[t][r][3] = w.w;
-                        }
-                    }
-                }
+                load_step<D, AUX>(x, a.c, head, first_key(i), hi, g.p, koff, voff);
             };
             auto compute = [&](const StepCodes<D>& x, int i) {
-                float y[8];
+                f32x4 sc[2];
+                float f[2], vf[2], ev[2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     f32x4 s = {};
@@ -260,19 +363,21 @@ void k_attend_rows(AttendArgs a) {
                         const bf16x8 kf = codes_to_bf16((u & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), 1.0f);
                         s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[u], s, 0, 0, 0);
                     }
-                    const int key = first_key(i) + 16 * t;
-                    const float f = x.ks[t] * a.scale2;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) y[4 * t + r] = __fmaf_rn(s[r], f, x.vf[t]);
-                    if (key + 15 > low || key + 16 > x.end[t] || past) {     // some column does not see some key
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int k = key + 4 * quarter + r;
-                            y[4 * t + r] = k <= position && k < x.end[t] ? y[4 * t + r] : -INFINITY;
-                        }
-                    }
+                    f[t] = key_scale(x.scale[t]) * a.scale2;
+                    vf[t] = value_exponent(x.scale[t]);
+                    ev[t] = __builtin_amdgcn_exp2f(-vf[t]);
+                    sc[t] = hide(s, first_key(i) + 16 * t, quarter, low, position, x.scale[t].end, past);
                 }
-                attend_step<D>(st, y, x.v, x.vf);
+                const f16x8 w = weights_of<D>(st, sc, f, vf, ev);
+#pragma unroll
+                for (int d = 0; d < PIECES; ++d)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f16x8 v0, v1;
+                        values_of<D>(x.v, d, h, v0, v1);
+                        st.acc[4 * d + 2 * h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w, st.acc[4 * d + 2 * h], 0, 0, 0);
+                        st.acc[4 * d + 2 * h + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w, st.acc[4 * d + 2 * h + 1], 0, 0, 0);
+                    }
             };
             if (steps > 0) {
                 StepCodes<D> x0, x1;
@@ -327,42 +432,213 @@ void k_attend_rows(AttendArgs a) {
         }
         if (wave == 0 && live) {
             const int64_t t = begin + token;
-            if (a.splits == 1) {
-                const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
-                uint16_t* o = (uint16_t*)a.out.data + t * a.out.token_stride + qhead * a.out.head_stride;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int i = 0; i < TILES; i += 4) {
-                        const uint2 w = make_uint2(pack_bf16x2(st.acc[i][r] * inv, st.acc[i + 1][r] * inv),
-                                                   pack_bf16x2(st.acc[i + 2][r] * inv, st.acc[i + 3][r] * inv));
-                        *reinterpret_cast<uint2*>(o + (4 * quarter + r) * TILES + i) = w;
-                    }
+            if (whole) {
+                write_row<D>(st.acc, total, (uint16_t*)a.out.data + t * a.out.token_stride + qhead * a.out.head_stride, quarter);
             } else {
-                const int64_t at = (t * (int64_t)(a.c.heads * a.group) + qhead) * a.splits + split;
-                float* p = a.part + at * D;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int i = 0; i < TILES; i += 4)
-                        *reinterpret_cast<f32x4*>(p + (4 * quarter + r) * TILES + i) =
-                            f32x4{st.acc[i][r], st.acc[i + 1][r], st.acc[i + 2][r], st.acc[i + 3][r]};
-                if (quarter == 0) a.sums[at] = make_float2(top, total);
+                const int64_t at = (((int64_t)seq * a.c.heads + head) * KV_FEW + row) * a.splits + split;
+                write_part<D>(st.acc, top, total, a.part + at * D, a.sums + at, quarter);
             }
         }
     }
 }
 
-// Joins the chunks of each row: W waves per (token, head), D / 4 lanes per chunk.
-template <int D, int W>
+// Rows of a (sequence, kv head) beyond a few: a wave owns CT tiles of 16 rows and reads the codes itself,
+// each decoded once for all of its tiles; no LDS, no barrier.  Scores by 8-bit products (D >= 128): the codes of
+// the keys are the operand as they lie.  The workgroups (single waves) of one (sequence, kv head) run on one XCD,
+// whose L2 holds its keys; those that see most keys start first.
+template <int D, int CT>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2)))
+void k_attend_block(AttendArgs a) {
+    constexpr int KSTEPS = D / 32, TILES = D / 16, PIECES = D / 64;
+    constexpr bool F8 = D >= 128;
+    const int lane = threadIdx.x, col = lane & 15, quarter = lane >> 4;
+    const int pairs = a.b.seqs * a.c.heads;
+    const int local = (int)(blockIdx.x / XCDS), here = (pairs + XCDS - 1) / XCDS;      // of this XCD: workgroup, pairs
+    const int pair = local % here * XCDS + (int)(blockIdx.x % XCDS);
+    if (pair >= pairs) return;
+    const int head = pair % a.c.heads, seq = pair / a.c.heads, split = blockIdx.y;
+    const int begin = scalar_load(a.b.starts + seq), fresh = scalar_load(a.b.starts + seq + 1) - begin;
+    const int before = scalar_load(a.b.lengths + seq);
+    const int rows = fresh * a.group;
+    if (rows <= a.limit) return;
+    const int reach = a.b.table_width << a.c.page_log2;
+    const uint32_t koff = col * D + 16 * quarter, voff = 4 * quarter * D + col * (D / 16);
+    constexpr int BLOCK = CT * 16;
+    const int blocks = (rows + BLOCK - 1) / BLOCK;
+
+    for (int block = blocks - 1 - local / here; block >= 0; block -= a.blocks) {
+        const int row0 = block * BLOCK;
+        const int last_row = row0 + BLOCK <= rows ? row0 + BLOCK - 1 : rows - 1;
+        int keys = before + last_row / a.group + 1;
+        const bool past = keys > reach;
+        keys = past ? reach : keys;
+        bf16x8 qf[F8 ? 1 : CT][KSTEPS];
+        i32x8 q1[CT][F8 ? D / 128 : 1], q2[CT][F8 ? D / 128 : 1];
+        float qs[CT];
+        RowsState<D> st[CT];
+        int position[CT], low[CT];                // of the lane's column; of the tile's first row
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            const int row = row0 + 16 * c + col < rows ? row0 + 16 * c + col : rows - 1;
+            const int token = row / a.group, qhead = head * a.group + row % a.group;
+            position[c] = before + token < reach ? before + token : -1;
+            low[c] = before + (row0 + 16 * c) / a.group;
+            const uint16_t* qp = (const uint16_t*)a.q.data + (int64_t)(begin + token) * a.q.token_stride +
+                                 (int64_t)qhead * a.q.head_stride;
+            if constexpr (!F8) {
+                qs[c] = a.scale2;
+#pragma unroll
+                for (int s = 0; s < KSTEPS; ++s) qf[c][s] = query_piece(qp + 64 * (s >> 1) + 16 * quarter + 8 * (s & 1), a.flip);
+            } else {
+                qs[c] = split_query<D>(qp, quarter, a.flip, q1[c], q2[c]) * a.scale2;
+            }
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) st[c].acc[i] = f32x4{};
+            st[c].m = KV_FLOOR;
+            st[c].l = 0.0f;
+        }
+        const int chunks = (keys + a.chunk - 1) / a.chunk;
+        for (int ch = split; ch < chunks; ch += a.splits) {
+            const int lo = ch * a.chunk, hi = lo + a.chunk < keys ? lo + a.chunk : keys;
+            const int steps = (hi - lo + KV_STEP - 1) / KV_STEP;
+            struct Pages {
+                int p[2];
+            };
+            auto pages = [&](int i) {
+                Pages g;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) g.p[t] = page_entry(a.b, seq, (lo + KV_STEP * i + 16 * t) >> a.c.page_log2);
+                return g;
+            };
+            auto load = [&](StepCodes<D>& x, int i, const Pages& g) {
+                load_step<D, 0>(x, a.c, head, lo + KV_STEP * i, hi, g.p, koff, voff);
+            };
+            auto compute = [&](const StepCodes<D>& x, int i) {
+                const int first = lo + KV_STEP * i;
+                f32x4 sc[CT][2];
+                float ks[2], vf[2], ev[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    ks[t] = key_scale(x.scale[t]);
+                    vf[t] = value_exponent(x.scale[t]);
+                    ev[t] = __builtin_amdgcn_exp2f(-vf[t]);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) sc[c][t] = f32x4{};
+                    if constexpr (!F8) {
+#pragma unroll
+                        for (int u = 0; u < KSTEPS; ++u) {
+                            const uint4 w = x.k[t][u >> 1];
+                            const bf16x8 kf = codes_to_bf16((u & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), 1.0f);
+#pragma unroll
+                            for (int c = 0; c < CT; ++c) sc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[c][u], sc[c][t], 0, 0, 0);
+                        }
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < D / 128; ++b) {
+                            const uint4 w0 = x.k[t][2 * b], w1 = x.k[t][2 * b + 1];
+                            const i32x8 kf = {(int)w0.x, (int)w0.y, (int)w0.z, (int)w0.w, (int)w1.x, (int)w1.y, (int)w1.z, (int)w1.w};
+                            // (formats E4M3; scales 2^0, and 2^-4 for the second part of the queries)
+#pragma unroll
+                            for (int c = 0; c < CT; ++c) {
+                                sc[c][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q1[c][b], sc[c][t], 0, 0, 0, 127, 0, 127);
+                                sc[c][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q2[c][b], sc[c][t], 0, 0, 0, 127, 0, 123);
+                            }
+                        }
+                    }
+                }
+                f16x8 w[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        sc[c][t] = hide(sc[c][t], first + 16 * t, quarter, low[c], position[c], x.scale[t].end, past);
+                    const float f[2] = {ks[0] * qs[c], ks[1] * qs[c]};
+                    w[c] = weights_of<D>(st[c], sc[c], f, vf, ev);
+                }
+#pragma unroll
+                for (int d = 0; d < PIECES; ++d)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f16x8 v0, v1;
+                        values_of<D>(x.v, d, h, v0, v1);
+#pragma unroll
+                        for (int c = 0; c < CT; ++c) {
+                            f32x4 &o0 = st[c].acc[4 * d + 2 * h], &o1 = st[c].acc[4 * d + 2 * h + 1];
+                            o0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w[c], o0, 0, 0, 0);
+                            o1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w[c], o1, 0, 0, 0);
+                        }
+                    }
+            };
+            if (steps > 0) {
+                StepCodes<D> x0, x1;
+                load(x0, 0, pages(0));
+                Pages g1 = pages(1);
+                int i = 0;
+                for (; i + 2 < steps; i += 2) {
+                    const Pages g2 = pages(i + 2);
+                    load(x1, i + 1, g1);
+                    compute(x0, i);
+                    g1 = pages(i + 3);
+                    load(x0, i + 2, g2);
+                    compute(x1, i + 1);
+                }
+                if (i + 1 < steps) {
+                    load(x1, i + 1, g1);
+                    compute(x0, i);
+                    compute(x1, i + 1);
+                } else {
+                    compute(x0, i);
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            float l = st[c].l;
+            l += __shfl_xor(l, 16);
+            l += __shfl_xor(l, 32);
+            const int row = row0 + 16 * c + col;
+            if (row >= rows) continue;
+            const int64_t t = begin + row / a.group;
+            const int qhead = head * a.group + row % a.group;
+            if (a.splits == 1) {
+                write_row<D>(st[c].acc, l, (uint16_t*)a.out.data + t * a.out.token_stride + qhead * a.out.head_stride, quarter);
+            } else {
+                const int64_t at = (t * (int64_t)(a.c.heads * a.group) + qhead) * a.splits + split;
+                write_part<D>(st[c].acc, st[c].m, l, a.part + at * D, a.sums + at, quarter);
+            }
+        }
+    }
+}
+
+// Joins the chunks of each row: W waves per row, D / 4 lanes per chunk.  FEW: the rows of
+// k_attend_rows (slot: sequence, kv head, row), else those of k_attend_block (slot: token, head).
+template <int D, int W, bool FEW>
 __global__ __launch_bounds__(256)
 void k_attend_join(AttendArgs a) {
     constexpr int LANES = D / 4, GROUPS = W * 64 / LANES;     // chunks at a time
     const int in = threadIdx.x % (W * 64), lane = in & 63;
     const int heads = a.c.heads * a.group;
-    const int64_t row = (int64_t)blockIdx.x * (4 / W) + threadIdx.x / (W * 64);
-    const bool on = row < (int64_t)a.b.tokens * heads;
-    const int64_t base = on ? row * a.splits : 0;
+    const int64_t slot = (int64_t)blockIdx.x * (4 / W) + threadIdx.x / (W * 64);
+    int64_t token, qhead;
+    bool on;
+    if constexpr (FEW) {
+        const int64_t pair = slot / a.few, row = slot % a.few;
+        const int seq = (int)(pair / a.c.heads), head = (int)(pair % a.c.heads);
+        on = seq < a.b.seqs;
+        const int begin = on ? a.b.starts[seq] : 0, rows = on ? (a.b.starts[seq + 1] - begin) * a.group : 0;
+        on = on && rows <= a.few && row < rows;
+        token = begin + row / a.group;
+        qhead = head * a.group + row % a.group;
+    } else {
+        token = slot / heads;
+        qhead = slot % heads;
+        on = token < a.b.tokens;
+        if (on && a.limit > 0) {
+            const int seq = sequence_of(a.b.starts, a.b.seqs, (int)token, lane);
+            on = (a.b.starts[seq + 1] - a.b.starts[seq]) * a.group > a.limit;
+        }
+    }
+    const int64_t base = FEW ? ((slot / a.few) * KV_FEW + slot % a.few) * a.splits : slot * a.splits;
     const int splits = on ? a.splits : 0;
     const int group = in / LANES, c = in % LANES;
     // every wave finds the row's reference for itself
@@ -402,56 +678,114 @@ void k_attend_join(AttendArgs a) {
     }
     if (!on || lane >= LANES) return;
     const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
-    uint16_t* out = (uint16_t*)a.out.data + (row / heads) * a.out.token_stride + (row % heads) * a.out.head_stride;
+    uint16_t* out = (uint16_t*)a.out.data + token * a.out.token_stride + qhead * a.out.head_stride;
     *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
 
-struct AttendPlan {
-    int row_tiles, chunk, splits;
-    size_t bytes;
+// One kernel's part of a call: its chunks and where its parts lie.
+struct AttendPart {
+    bool on;
+    int tiles, chunk, splits;             // row tiles (blocks) launched per (sequence, kv head)
+    size_t slots, bytes;                  // row slots; workspace
 };
+struct AttendPlan {
+    AttendPart rows, block;
+};
+constexpr int block_tiles(int dim) { return dim == 64 ? 4 : dim == 128 ? 2 : 1; }     // CT
+constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 
-// Chunks are sized for about 4096 workgroups (some rounds of three or four on each compute unit) at the
-// stated lengths, and of at least 256 keys: a join costs a launch.
+// k_attend_rows reads the keys once per 16 rows and splits them over many workgroups; k_attend_block
+// reads them once per block_rows rows and decodes them once per block_tiles tiles.  A batch whose sequences all bring
+// up to 32 rows per kv head needs the first alone, one of equal longer ones the second alone; any other
+// may hold both kinds, and each kernel takes its own.
+// Chunks: for k_attend_rows about 4096 workgroups (some rounds of three or four on each compute unit) at
+// the stated lengths, of at least 256 keys, for a join costs a launch; for k_attend_block chunks only
+// where there are fewer than 1024 waves, one for each SIMD.
 static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
                               int64_t max_length) {
     AttendPlan p{};
     const int group = heads / c.heads;
-    int64_t tiles = (max_new * group + 15) / 16;
-    const int64_t most = 32768 / c.heads < 512 ? 32768 / c.heads : 512;   // the launch's second dimension is 65535 at most
-    tiles = tiles < 1 ? 1 : (tiles < most ? tiles : most);
-    p.row_tiles = (int)tiles;
-    const int64_t groups = (int64_t)seqs * c.heads * tiles;
-    constexpr int64_t unit = KV_WAVES * KV_STEP;
-    int64_t chunk = (max_length * groups / 4096 + unit - 1) / unit * unit;
-    if (chunk < 256) chunk = 256;
-    if (chunk > (1 << 20)) chunk = 1 << 20;
-    p.chunk = (int)chunk;
-    int64_t splits = (max_length + chunk - 1) / chunk;
-    splits = splits < 1 ? 1 : (splits < 1024 ? splits : 1024);
-    p.splits = (int)splits;
-    p.bytes = splits > 1 ? (size_t)tokens * heads * splits * (c.dim + 2) * sizeof(float) : 0;   // sums, then references
+    const int64_t most_rows = max_new * group;
+    p.rows.on = most_rows <= KV_FEW || tokens != (int64_t)seqs * max_new;
+    p.block.on = most_rows > KV_FEW;
+    auto chunks = [&](AttendPart& q, int64_t groups, int64_t target, int64_t unit, int64_t least, size_t slots) {
+        int64_t chunk = (max_length * groups / target + unit - 1) / unit * unit;
+        chunk = chunk < least ? least : (chunk > (1 << 24) ? 1 << 24 : chunk);
+        const int64_t splits = (max_length + chunk - 1) / chunk;
+        q.chunk = (int)chunk;
+        q.splits = (int)(splits < 1 ? 1 : (splits < 1024 ? splits : 1024));
+        q.slots = slots;
+        q.bytes = q.splits > 1 ? (slots * q.splits * (c.dim + 2) * sizeof(float) + 255) & ~(size_t)255 : 0;
+    };
+    if (p.rows.on) {
+        const int64_t r = most_rows < KV_FEW ? most_rows : KV_FEW;
+        p.rows.tiles = (int)((r + 15) / 16);
+        chunks(p.rows, (int64_t)seqs * c.heads * p.rows.tiles, 4096, KV_WAVES * KV_STEP, 256, (size_t)seqs * c.heads * KV_FEW);
+    }
+    if (p.block.on) {
+        const int64_t rows = block_rows(c.dim);
+        int64_t blocks = (most_rows + rows - 1) / rows;
+        const int64_t pairs = ((int64_t)seqs * c.heads + XCDS - 1) / XCDS * XCDS, most = ((int64_t)1 << 24) / pairs;
+        blocks = blocks < most ? blocks : most;               // (a wave takes several beyond that)
+        p.block.tiles = (int)(blocks < 1 ? 1 : blocks);
+        const int64_t groups = (tokens * heads + rows - 1) / rows;
+        if (groups >= 1024) chunks(p.block, 1, 1, 1, 1 << 24, 0);
+        else chunks(p.block, groups, 1024, KV_STEP, 512, (size_t)tokens * heads);
+    }
     return p;
 }
 
 size_t kv_attention_ws_bytes(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
                              int64_t max_length) {
-    return attend_plan(c, seqs, tokens, heads, max_new, max_length).bytes;
+    const AttendPlan p = attend_plan(c, seqs, tokens, heads, max_new, max_length);
+    return p.rows.bytes + p.block.bytes;
 }
 
 hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const HeadsView& q, const HeadsView& out,
                                float scale, int64_t max_new, int64_t max_length, void* ws, hipStream_t s) {
     const AttendPlan p = attend_plan(c, b.seqs, b.tokens, q.heads, max_new, max_length);
-    AttendArgs a{c, b, q, out, q.heads / c.heads, p.row_tiles, p.chunk, p.splits, scale * 1.4426950408889634f, (float*)ws,
-                 (float2*)((float*)ws + (size_t)b.tokens * q.heads * p.splits * c.dim)};
-    const dim3 grid((uint32_t)p.splits, (uint32_t)(c.heads * p.row_tiles), (uint32_t)b.seqs);
-    const int64_t rows = (int64_t)b.tokens * q.heads;
-    const bool wide = p.splits > 16;      // four waves to a row: its chunks' loads take turns otherwise
+    AttendArgs a{};
+    a.c = c;
+    a.b = b;
+    a.q = q;
+    a.out = out;
+    a.group = q.heads / c.heads;
+    // (not below 2^-70, so that no hidden score meets a factor of zero: a scale of zero still weighs all keys alike)
+    a.scale2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-70f);
+    a.flip = scale < 0.0f ? 0x80008000u : 0u;
+    a.limit = !p.block.on ? 0x7FFFFFFF : p.rows.on ? KV_FEW : 0;
+    auto part = [&](const AttendPart& q, void* at) {
+        a.chunk = q.chunk;
+        a.splits = q.splits;
+        a.part = (float*)at;
+        a.sums = (float2*)((float*)at + q.slots * q.splits * c.dim);
+    };
     auto with = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        hipLaunchKernelGGL(k_attend_rows<D>, grid, dim3(256), 0, s, a);
-        if (p.splits > 1 && wide) hipLaunchKernelGGL((k_attend_join<D, 4>), dim3((uint32_t)rows), dim3(256), 0, s, a);
-        else if (p.splits > 1) hipLaunchKernelGGL((k_attend_join<D, 1>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
+        // W: four waves to a row of many chunks, whose loads would take turns otherwise
+        if (p.block.on) {
+            part(p.block, (uint8_t*)ws + p.rows.bytes);
+            a.blocks = p.block.tiles;
+            const int64_t pairs = ((int64_t)b.seqs * c.heads + XCDS - 1) / XCDS * XCDS;
+            const dim3 grid((uint32_t)(pairs * a.blocks), (uint32_t)a.splits);
+            hipLaunchKernelGGL((k_attend_block<D, block_tiles(D)>), grid, dim3(64), 0, s, a);
+            const int64_t rows = (int64_t)b.tokens * q.heads;
+            if (a.splits > 16) hipLaunchKernelGGL((k_attend_join<D, 4, false>), dim3((uint32_t)rows), dim3(256), 0, s, a);
+            else if (a.splits > 1) hipLaunchKernelGGL((k_attend_join<D, 1, false>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
+        }
+        if (p.rows.on) {
+            part(p.rows, ws);
+            a.row_tiles = p.rows.tiles;
+            const int64_t most = max_new * a.group;
+            a.few = (int)(most < KV_FEW ? most : KV_FEW);
+            // codes that one row tile reads are read once: they need not stay in the caches
+            const dim3 grid((uint32_t)a.splits, (uint32_t)(c.heads * a.row_tiles), (uint32_t)b.seqs);
+            if (a.row_tiles == 1) hipLaunchKernelGGL((k_attend_rows<D, 2>), grid, dim3(256), 0, s, a);
+            else hipLaunchKernelGGL((k_attend_rows<D, 0>), grid, dim3(256), 0, s, a);
+            const int64_t rows = (int64_t)b.seqs * c.heads * a.few;
+            if (a.splits > 16) hipLaunchKernelGGL((k_attend_join<D, 4, true>), dim3((uint32_t)rows), dim3(256), 0, s, a);
+            else if (a.splits > 1) hipLaunchKernelGGL((k_attend_join<D, 1, true>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
+        }
     };
     if (c.dim == 64) with(std::integral_constant<int, 64>{});
     else if (c.dim == 128) with(std::integral_constant<int, 128>{});

@@ -183,6 +183,15 @@ def test_attention_sharp_and_flat_scores():
     check_attention(c, max_new=1, max_length=501)
 
 
+def test_attention_zero_and_negative_scale():
+    c = Case([300, 20], [1, 40], page=16, kv=2, heads=4, dim=64, seed=18)
+    codes, scales = c.host()
+    for scale in (-0.2, 1e-300):             # the second is zero as fp32: every key that is seen weighs the same
+        want, reach = ref.attention(codes, scales, f64(c.q), c.starts, c.lengths, c.table, scale)
+        got = f64(nf4.kv_attention(c.cache, c.q, *c.meta(), scale=scale))
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * reach[..., None])
+
+
 def test_attention_scales_far_apart():
     c = Case([600], [1], page=16, kv=1, heads=2, dim=64, seed=12)
     r = np.random.RandomState(5)
