@@ -144,7 +144,7 @@ nf4_status qlora_kv_append(const qlora_kv_cache* cache, const qlora_kv_batch* ba
                 return fail(NF4_ERR_ARG, "in place needs the same strides");
         }
         // one launch of fewer than 2^24 workgroups
-        const int64_t most = (int64_t)b.tokens * ((c.heads + 3) / 4) + (q_in ? (int64_t)b.tokens + 1024 : 0);
+        const int64_t most = (int64_t)b.tokens * ((c.heads + 3) / 4) + (q_in ? ((int64_t)b.tokens + 4096) * ((qi.heads * (int64_t)c.dim + 2047) / 2048) : 0);
         if (most >= ((int64_t)1 << 24)) return fail(NF4_ERR_UNSUPPORTED, "too many tokens times heads for one call");
         return hip_status(nf4::launch_kv_append(c, b, kv, vv, r, q_in ? &qi : nullptr, q_in ? &qo : nullptr, (hipStream_t)stream),
                           "qlora_kv_append");
