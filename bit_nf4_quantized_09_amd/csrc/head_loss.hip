@@ -31,6 +31,8 @@
 // W or X read transposed) goes through four LDS stages filled by direct loads, three steps ahead.
 // (256 x 256 tiles with both operands in LDS, 8 waves of 128 x 64: LDS reads and writes take as
 // many cycles as the matrix instructions; 940-1000 TFLOP/s.)
+#include <utility>
+
 #include "bufio.h"
 #include "decoder.h"
 #include "lds_dma.h"
@@ -201,7 +203,8 @@ void k_head_pack(const uint16_t* X, int64_t M, int64_t K, uint16_t* out) {
     const int64_t steps = K / HL_K;
     const int64_t step = blockIdx.x, tm = blockIdx.y >> 2;
     const int i = (int)(blockIdx.y & 3);
-    const int64_t row = tm * HL_TM + 128 * wave + 32 * i + (lane & 31);
+    const int64_t row0 = tm * HL_TM + 128 * wave + 32 * i, row = row0 + (lane & 31);
+    if (row0 >= M) return;                // no row of these 32 is in use, and none is read
     uint4* block = reinterpret_cast<uint4*>(out + (tm * steps + step) * (A_BLOCK_BYTES / 2));
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -212,7 +215,8 @@ void k_head_pack(const uint16_t* X, int64_t M, int64_t K, uint16_t* out) {
 }
 
 struct HeadArgs {
-    const uint16_t* Xp;       // X in fragment order
+    const uint16_t* X;        // [M][K], and
+    const uint16_t* Xp;       // in fragment order
     const uint16_t* W;        // [V][K]
     int64_t M, K, V;
     const int64_t* targets;
@@ -239,6 +243,66 @@ __device__ __forceinline__ bool head_live(int64_t target, int64_t V, int64_t ign
 constexpr float HEAD_ROOM = 40.0f;        // binades a logit may pass the running reference by
 // The factor on G, from max|dloss|: at least the smallest normal number, so that its inverse is finite.
 __device__ __forceinline__ float head_scale(const uint32_t* top) { return fmaxf(__uint_as_float(*top), 0x1p-126f); }
+
+// The epilogue of HEAD_STATS and HEAD_E for 32 tokens m0 .. (column rl) and the 32 J vocabulary rows v0 .. of tile
+// tv: z[j][reg] is row 32 j + 8 (reg / 4) + 4 h + reg % 4.
+template <HeadMode MODE, int J>
+__device__ __forceinline__ void head_column(const HeadArgs& a, f32x16* acc, int64_t m0, int64_t v0, int64_t tv, int h, int rl) {
+    const int left = (int)(a.V - v0 < 32 * J ? a.V - v0 : 32 * J) - 4 * h;      // this lane's valid rows end
+    const int64_t m = m0 + rl;
+    const int64_t target = m < a.M ? a.targets[m] : -1;
+    const bool live = m < a.M && head_live(target, a.V, a.ignore);
+    const int64_t tl = target - v0 - 4 * h;
+    const int hit = live && tl >= 0 && tl < 32 * J ? (int)tl : -1;             // the target's row, if this lane's
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int v = j * 32 + 8 * (r >> 2) + (r & 3);
+            float z = acc[j][r] * LOG2E;
+            if (v == hit) {
+                if (MODE == HEAD_STATS) a.zy[m] = z;
+                z = -INFINITY;
+            }
+            z = v < left ? z : -INFINITY;
+            acc[j][r] = z;
+            top = fmaxf(top, z);
+        }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    float ref = top > -INFINITY ? top : 0.0f;
+    if (MODE == HEAD_E) {
+        ref = live ? a.ref[m] : 0.0f;
+        if (top > ref + HEAD_ROOM) ref = ceilf(top);          // an integer, like the running one
+    }
+    // E's blocks of 512 tokens and 64 vocabulary rows: row m's 16-byte chunk of rows v .. v + 7
+    const int in = (int)(m0 % HL_TM);
+    uint8_t* blocks = nullptr;
+    if (MODE == HEAD_E)
+        blocks = reinterpret_cast<uint8_t*>(a.out) + (m0 / HL_TM) * a.out_steps * A_BLOCK_BYTES + (in >> 7) * 16384 + ((in >> 5) & 3) * 4096 +
+                 rl * 16 + 8 * h;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            float y[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                y[r] = __builtin_amdgcn_exp2f(acc[j][4 * r4 + r] - ref);
+                if (MODE == HEAD_E && !live) y[r] = 0.0f;
+                sum += y[r];
+            }
+            if (MODE == HEAD_E) {
+                const int64_t chunk = ((v0 - a.v0) >> 3) + 4 * j + r4;         // of the row's 16-byte chunks
+                *reinterpret_cast<uint2*>(blocks + (chunk >> 3) * A_BLOCK_BYTES + (chunk & 7) * 512) =
+                    make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            }
+        }
+    sum += __shfl_xor(sum, 32);
+    if (MODE == HEAD_E && !live) ref = 0.0f;
+    if (h == 0 && m < a.Mp) a.part[m * a.tiles_v + tv] = make_float2(MODE == HEAD_E ? ref : top, sum);
+}
 
 // Logits of a tile of 512 tokens x 128 vocabulary rows.
 template <HeadMode MODE>
@@ -303,60 +367,80 @@ void k_head_logits(HeadArgs a) {
         return;
     }
     // accumulator (i, j, reg): token 32 i + rl of the wave's 128, vocabulary row 32 j + 8 (reg / 4) + 4 h + reg % 4
-    const int left = (int)(a.V - v0 < HL_TN ? a.V - v0 : HL_TN) - 4 * h;       // this lane's valid rows end
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + wave * 128 + i * 32 + rl;
-        const int64_t target = m < a.M ? a.targets[m] : -1;
-        const bool live = m < a.M && head_live(target, a.V, a.ignore);
-        const int64_t tl = target - v0 - 4 * h;
-        const int hit = live && tl >= 0 && tl < HL_TN ? (int)tl : -1;          // the target's row, if this lane's
-        float top = -INFINITY;
+    for (int i = 0; i < 4; ++i) head_column<MODE, 4>(a, acc[i], m0 + wave * 128 + i * 32, v0, tv, h, rl);
+}
+
+// The logits of up to 64 tokens, whose time is that of reading W: a workgroup takes 128 vocabulary rows, each of its
+// four waves 32 of them, and streams W (whole 128-byte lines of 8 rows a load) and X through six LDS stages, five
+// steps ahead: up to 80 KB of W in flight per compute unit.  Its tiles are 32 rows.  (W straight into registers,
+// 32 rows a load, meets every line four times: 75 us for 33 tokens x 32000 x 4096.)
+constexpr int FEW_TOKENS = 64, FEW_TN = 32, FEW_STAGES = 6;
+constexpr int few_stage(int nt) { return 16384 + 4096 * nt; }            // bytes: W, then X
+template <HeadMode MODE, int NT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
+void k_head_few(HeadArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5, rl = lane & 31;
+    const int64_t b0 = a.v0 + (int64_t)blockIdx.x * 128;
+    const int steps = __builtin_amdgcn_readfirstlane((int)(a.K / HL_K));
+    // a wave fills its own 32 rows of W and 8 NT of X, 8 a load (rows past the end repeat the last: dropped later)
+    uint32_t wof[4], xof[NT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int v = j * 32 + 8 * (r >> 2) + (r & 3);
-                float z = acc[i][j][r] * LOG2E;
-                if (v == hit) {
-                    if (MODE == HEAD_STATS) a.zy[m] = z;
-                    z = -INFINITY;
-                }
-                z = v < left ? z : -INFINITY;
-                acc[i][j][r] = z;
-                top = fmaxf(top, z);
-            }
-        top = fmaxf(top, __shfl_xor(top, 32));
-        float ref = top > -INFINITY ? top : 0.0f;
-        if (MODE == HEAD_E) {
-            ref = live ? a.ref[m] : 0.0f;
-            if (top > ref + HEAD_ROOM) ref = ceilf(top);      // an integer, like the running one
-        }
-        // E's block of 512 tokens and 64 vocabulary rows
-        uint8_t* block = nullptr;
-        if (MODE == HEAD_E)
-            block = reinterpret_cast<uint8_t*>(a.out) + (tm * a.out_steps + 2 * tv) * A_BLOCK_BYTES + wave * 16384 + i * 4096 +
-                    rl * 16 + 8 * h;
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                float y[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    y[r] = __builtin_amdgcn_exp2f(acc[i][j][4 * r4 + r] - ref);
-                    if (MODE == HEAD_E && !live) y[r] = 0.0f;
-                    sum += y[r];
-                }
-                if (MODE == HEAD_E)
-                    *reinterpret_cast<uint2*>(block + (j >> 1) * A_BLOCK_BYTES + 1024 * ((j & 1) * 2 + (r4 >> 1)) + 512 * (r4 & 1)) =
-                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-            }
-        sum += __shfl_xor(sum, 32);
-        if (MODE == HEAD_E && !live) ref = 0.0f;
-        if (h == 0) a.part[m * a.tiles_v + tv] = make_float2(MODE == HEAD_E ? ref : top, sum);
+    for (int q = 0; q < 4; ++q) {
+        const int row = wave * 32 + q * 8 + (lane >> 3);
+        const int64_t rv = b0 + row < a.V ? row : a.V - 1 - b0;
+        wof[q] = (uint32_t)(rv * a.K * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
     }
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+        const int row = (wave * NT + q) * 8 + (lane >> 3);
+        xof[q] = (uint32_t)((row < a.M ? row : a.M - 1) * a.K * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
+    }
+    const dma_rsrc rw = make_dma_rsrc(a.W + b0 * a.K, (a.V - b0) * a.K * 2), rx = make_dma_rsrc(a.X, a.M * a.K * 2);
+    const uint32_t base = lds_address(lds);
+    auto fill = [&](int stage, int step) {
+        const int at = step < steps ? step : steps - 1;
+        const uint32_t to = base + stage * few_stage(NT);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_to_lds<MODE == HEAD_STATS>(rw, to + wave * 4096 + q * 1024, wof[q], (uint32_t)at * 128);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) load_to_lds(rx, to + 16384 + (wave * NT + q) * 1024, xof[q], (uint32_t)at * 128);
+    };
+    f32x16 acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = f32x16{};
+    int off[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) off[s] = rl * 128 + (((2 * s + h) ^ hl_swizzle(rl)) << 4);      // (row 32 i + rl: swizzled by 4 (i & 1) more)
+#pragma unroll
+    for (int i = 0; i < FEW_STAGES - 1; ++i) fill(i, i);
+    int stage = 0, free = FEW_STAGES - 1;
+    for (int it = 0; it < steps; ++it) {
+        // this stage has landed once only the loads of the four after it are out
+        if constexpr (NT == 2) asm volatile("s_waitcnt vmcnt(24) lgkmcnt(0)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        fill(free, it + FEW_STAGES - 1);                                  // the stage that every wave left before the barrier
+        const uint8_t* sw = lds + stage * few_stage(NT);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bf16x8 w = *reinterpret_cast<const bf16x8*>(sw + wave * 4096 + off[s ^ (2 * (wave & 1))]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const bf16x8 x = *reinterpret_cast<const bf16x8*>(sw + 16384 + 4096 * i + off[s ^ (2 * (i & 1))]);
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, acc[i], 0, 0, 0);
+            }
+        }
+        free = stage;
+        stage = stage + 1 < FEW_STAGES ? stage + 1 : 0;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int64_t tv = (int64_t)blockIdx.x * 4 + wave;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) head_column<MODE, 1>(a, &acc[i], 32 * i, b0 + 32 * wave, tv, h, rl);
 }
 
 // A row's loss from its target's logit and the others' log-sum (both base 2): the loss, lse
@@ -377,21 +461,17 @@ void k_head_rows(const float2* part, const float* zy, const int64_t* targets, in
     const int lane = threadIdx.x & 63;
     const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (m >= M) return;
+    const float2* p = part + m * tiles;
     float top = -INFINITY, sum = 0.0f;
-    auto join = [&](float t, float s) {
-        const float both = fmaxf(top, t), ref = both > -INFINITY ? both : 0.0f;
-        sum = sum * __builtin_amdgcn_exp2f(top - ref) + s * __builtin_amdgcn_exp2f(t - ref);
-        top = both;
-    };
-    for (int t = lane; t < tiles; t += 64) {
-        const float2 p = part[m * tiles + t];
-        join(p.x, p.y);
-    }
+#pragma unroll 8
+    for (int t = lane; t < tiles; t += 64) top = fmaxf(top, p[t].x);
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) {
-        const float t = __shfl_xor(top, x), s = __shfl_xor(sum, x);
-        join(t, s);
-    }
+    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+    const float ref = top > -INFINITY ? top : 0.0f;
+#pragma unroll 8
+    for (int t = lane; t < tiles; t += 64) sum += p[t].y * __builtin_amdgcn_exp2f(p[t].x - ref);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
     if (lane == 0) loss[m] = head_live(targets[m], V, ignore) ? row_loss(zy[m], top + log2f(sum)).loss : 0.0f;
 }
 
@@ -442,7 +522,7 @@ void k_head_target(const uint16_t* X, const uint16_t* W, int64_t M, int64_t K, i
 
 struct JoinArgs {
     const float2* part;       // [Mp][tiles] of the piece: reference and sum
-    int tiles;
+    int tiles, width;         // tiles of the piece, their vocabulary rows
     int64_t M, Mp;
     const int64_t* targets;
     int64_t ignore, V;
@@ -496,9 +576,10 @@ void k_head_join(JoinArgs a) {
             const int b = __ffsll((unsigned long long)todo) - 1;
             todo &= todo - 1;
             const float f = __builtin_amdgcn_exp2f(__shfl(p.x, b) - now);
-            // the row's 128 values of the tile: 8 chunks of 16 bytes, 512 bytes apart, in each of two blocks
-            if (lane < 16) {
-                uint4* e = reinterpret_cast<uint4*>(blocks + (2 * (t0 + b) + (lane >> 3)) * (int64_t)A_BLOCK_BYTES + (lane & 7) * 512);
+            // the row's values of the tile, a 16-byte chunk per lane
+            if (lane < a.width / 8) {
+                const int64_t chunk = (int64_t)(t0 + b) * (a.width / 8) + lane;
+                uint4* e = reinterpret_cast<uint4*>(blocks + (chunk >> 3) * A_BLOCK_BYTES + (chunk & 7) * 512);
                 float x[8];
                 Vec16<uint16_t>::unpack(*e, x);
 #pragma unroll
@@ -658,26 +739,29 @@ void k_head_finish(ProductArgs a, uint16_t* out) {
 // Pieces of the vocabulary and the workspace's layout.
 struct HeadPlan {
     int64_t Mp;               // tokens up to whole tiles
-    int64_t tiles;            // vocabulary tiles
-    int64_t piece;            // vocabulary tiles of a piece (a multiple of 4: whole row tiles of G^T)
+    bool few;                 // up to 64 tokens: logits by k_head_few
+    int width;                // vocabulary rows of a tile of the logits
+    int64_t piece;            // vocabulary rows of a piece (a multiple of 512: whole row tiles of G^T)
     int splits;               // parts of dX's contraction
     size_t top, zy, ref, total, factor, ends, rows, part, Xp, E, sum, bytes;
+    // tiles of the logits (few tokens: four to a workgroup)
+    int64_t tiles(int64_t vocabulary) const { return (vocabulary + 127) / 128 * (few ? 4 : 1); }
 };
 
 static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     HeadPlan p{};
     const bool grad = dx || dw;
     p.Mp = (M + HL_TM - 1) / HL_TM * HL_TM;
-    p.tiles = (V + HL_TN - 1) / HL_TN;
+    p.few = M <= FEW_TOKENS;
+    p.width = p.few ? FEW_TN : HL_TN;
     // a piece of E or G^T of at most 128 MB, half of the last-level cache: larger pieces pass over dX's
     // fp32 sums less often (64 MB: 947 us for 2048 tokens x 32000 x 4096, 128 MB: 903 us)
-    const int64_t most = ((int64_t)128 << 20) / (p.Mp > 0 ? p.Mp * HL_TN * 2 : 1) / 4 * 4;
-    p.piece = most < 4 ? 4 : most;
-    if (p.piece > p.tiles) p.piece = (p.tiles + 3) / 4 * 4;
+    const int64_t most = ((int64_t)128 << 20) / (p.Mp > 0 ? p.Mp * 2 : 1) / 512 * 512, all = (V + 511) / 512 * 512;
+    p.piece = most < 512 ? 512 : (most < all ? most : all);
     // where dX has too few tiles for the 256 compute units, its contraction is cut into parts
     // of at least 16 steps
     p.splits = 1;
-    const int64_t tiles = p.Mp / HL_TM * ((K + HL_TN - 1) / HL_TN), steps = p.piece * (HL_TN / HL_K);
+    const int64_t tiles = p.Mp / HL_TM * ((K + HL_TN - 1) / HL_TN), steps = p.piece / HL_K;
     while (p.splits < 8 && tiles * p.splits * 2 <= 256 && steps / (p.splits * 2) >= 16) p.splits *= 2;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -693,10 +777,10 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     p.factor = take(row);
     p.ends = take(2 * row);
     p.rows = take(4 * row);
-    p.part = take((size_t)p.Mp * (grad ? p.piece : p.tiles) * sizeof(float2));
+    p.part = take((size_t)p.Mp * p.tiles(grad && p.piece < V ? p.piece : V) * sizeof(float2));
     p.Xp = take((size_t)p.Mp * K * 2);
-    p.E = take(grad ? (size_t)p.Mp * p.piece * HL_TN * 2 : 0);
-    p.sum = take(dx && (p.piece < p.tiles || p.splits > 1) ? (size_t)M * K * 4 * p.splits : 0);
+    p.E = take(grad ? (size_t)p.Mp * p.piece * 2 : 0);
+    p.sum = take(dx && (p.piece < V || p.splits > 1) ? (size_t)M * K * 4 * p.splits : 0);
     p.bytes = at;
     return p;
 }
@@ -705,13 +789,19 @@ size_t head_loss_ws_bytes(int64_t M, int64_t K, int64_t V, bool dx, bool dw) { r
 
 static dim3 head_grid(int64_t x, int64_t y, int splits = 1) { return dim3((uint32_t)((x * y + 7) / 8 * 8), (uint32_t)splits); }
 
+// f(first vocabulary row, rows, whether it is the last piece)
 template <typename F>
 static void for_pieces(const HeadPlan& p, int64_t V, F&& f) {
-    for (int64_t t0 = 0; t0 < p.tiles; t0 += p.piece) {
-        const int64_t n = p.tiles - t0 < p.piece ? p.tiles - t0 : p.piece;
-        const int64_t v0 = t0 * HL_TN, rows = V - v0 < n * HL_TN ? V - v0 : n * HL_TN;
-        f(v0, n, rows, t0 + n >= p.tiles);
-    }
+    for (int64_t v0 = 0; v0 < V; v0 += p.piece) f(v0, V - v0 < p.piece ? V - v0 : p.piece, v0 + p.piece >= V);
+}
+
+template <HeadMode MODE>
+static void launch_logits(const HeadPlan& p, HeadArgs& a, int64_t rows, hipStream_t s) {
+    a.tiles_v = p.tiles(rows);
+    const dim3 few((uint32_t)(a.tiles_v / 4));
+    if (p.few && a.M <= 32) hipLaunchKernelGGL((k_head_few<MODE, 1>), few, dim3(256), FEW_STAGES * few_stage(1), s, a);
+    else if (p.few) hipLaunchKernelGGL((k_head_few<MODE, 2>), few, dim3(256), FEW_STAGES * few_stage(2), s, a);
+    else hipLaunchKernelGGL(k_head_logits<MODE>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
 }
 
 hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint16_t* W, int64_t V,
@@ -720,8 +810,16 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     const HeadPlan p = head_plan(M, K, V, dX != nullptr, dW != nullptr);
     uint8_t* base = (uint8_t*)ws;
     const dim3 row_grid((uint32_t)(p.Mp / 4));
+    if (p.few) {                          // their LDS is past the 64 KB that a kernel has unasked
+        for (const auto& f : {std::make_pair((const void*)k_head_few<HEAD_STATS, 1>, 1), std::make_pair((const void*)k_head_few<HEAD_STATS, 2>, 2),
+                              std::make_pair((const void*)k_head_few<HEAD_E, 1>, 1), std::make_pair((const void*)k_head_few<HEAD_E, 2>, 2)}) {
+            const hipError_t e = hipFuncSetAttribute(f.first, hipFuncAttributeMaxDynamicSharedMemorySize, FEW_STAGES * few_stage(f.second));
+            if (e != hipSuccess) return e;
+        }
+    }
     HeadArgs a{};
     uint16_t* Xp = (uint16_t*)(base + p.Xp);
+    a.X = X;
     a.Xp = Xp;
     a.W = W;
     a.M = M;
@@ -737,11 +835,11 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     a.out = (uint16_t*)(base + p.E);
     a.Mp = p.Mp;
     a.tiles_m = p.Mp / HL_TM;
-    a.tiles_v = p.tiles;
-    hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(a.tiles_m * 4)), dim3(256), 0, s, X, M, K, Xp);
+    if (!p.few || dW) hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(a.tiles_m * 4)), dim3(256), 0, s, X, M, K, Xp);
     if (!dX && !dW) {
-        hipLaunchKernelGGL(k_head_logits<HEAD_STATS>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
-        hipLaunchKernelGGL(k_head_rows, row_grid, dim3(256), 0, s, a.part, a.zy, targets, M, V, ignore, (int)p.tiles, loss);
+        launch_logits<HEAD_STATS>(p, a, V, s);
+        hipLaunchKernelGGL(k_head_rows, dim3((uint32_t)((M + 3) / 4)), dim3(256), 0, s, a.part, a.zy, targets, M, V, ignore,
+                           (int)a.tiles_v, loss);
         return hipGetLastError();
     }
     float* ref = (float*)(base + p.ref);
@@ -761,12 +859,11 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     d.splits = p.splits;
     hipLaunchKernelGGL(k_head_target, dim3((uint32_t)((M + 3) / 4 + 1)), dim3(256), 0, s, X, W, M, K, V, targets, ignore, a.zy,
                        ref, total, dloss, top);
-    for_pieces(p, V, [&](int64_t v0, int64_t n, int64_t rows, bool last) {
+    for_pieces(p, V, [&](int64_t v0, int64_t rows, bool last) {
         a.v0 = v0;
-        a.tiles_v = n;
-        a.out_steps = 2 * n;
-        hipLaunchKernelGGL(k_head_logits<HEAD_E>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
-        const JoinArgs j{a.part, (int)n, M, p.Mp, targets, ignore, V, a.out, a.out_steps, ref, total, (float*)(base + p.factor),
+        a.out_steps = (rows + HL_TN - 1) / HL_TN * (HL_TN / HL_K);
+        launch_logits<HEAD_E>(p, a, rows, s);
+        const JoinArgs j{a.part, (int)a.tiles_v, p.width, M, p.Mp, targets, ignore, V, a.out, a.out_steps, ref, total, (float*)(base + p.factor),
                          a.zy, last ? 1 : 0, dloss, loss, (float2*)(base + p.ends), (float4*)(base + p.rows)};
         hipLaunchKernelGGL(k_head_join, row_grid, dim3(256), 0, s, j);
         if (!dX) return;
@@ -790,12 +887,12 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     d.P = M;
     d.steps = (int)((M + HL_K - 1) / HL_K);
     d.a_steps = a.out_steps = p.Mp / HL_K;
-    for_pieces(p, V, [&](int64_t v0, int64_t n, int64_t rows, bool) {
+    for_pieces(p, V, [&](int64_t v0, int64_t rows, bool) {
         a.v0 = v0;
-        a.tiles_v = n;
+        a.tiles_v = (rows + HL_TN - 1) / HL_TN;
         hipLaunchKernelGGL(k_head_logits<HEAD_GT>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
         d.out_rows = rows;
-        d.tiles_r = (n + 3) / 4;
+        d.tiles_r = (rows + HL_TM - 1) / HL_TM;
         d.out = dW + v0 * K;
         hipLaunchKernelGGL((k_head_product<OUT_DW, false>), head_grid(d.tiles_r, d.tiles_n), dim3(256), 0, s, d);
     });
