@@ -1,4 +1,4 @@
-"""Compile the gfx950 HIP library libqlora_nf4.so in-tree with hipcc."""
+"""Compile the gfx950 HIP library libqlora_nf4.so in-tree with hipcc, and the binding of decoder.py with g++."""
 import concurrent.futures as cf
 import os
 import subprocess
@@ -10,6 +10,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libqlora_nf4.so")
 PROBE_SOURCE = "hbm_probe.hip"      # the HBM ceiling probes: a library of their own
+BINDING_SOURCE = "decoder_binding.cpp"   # the Python calls of decoder.py: a CPython extension over the library
+BINDING = os.path.join(OUT_DIR, "qlora_decoder_binding.so")
 PROBE_LIB = os.path.join(OUT_DIR, "libnf4_hbm_probe.so")
 SOURCES = ["api.hip", "codec.hip", "lora.hip", "fused.hip", "gemv.hip", "adamw.hip", "codebook.hip", "lowrank.hip",
            "decoder_api.hip", "rope.hip", "kv_append.hip", "kv_attention.hip", "head_loss.hip"]
@@ -36,6 +38,30 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_binding(verbose: bool) -> None:
+    """The CPython extension (torch's headers and libraries; next to the library, which it loads)."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, BINDING_SOURCE), "-o", tmp,
+           "-L" + OUT_DIR, "-lqlora_nf4", "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s" % (BINDING_SOURCE, r.stderr))
+    if r.stderr.strip() and verbose:
+        print(r.stderr, flush=True)
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
@@ -50,6 +76,7 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _build_binding(verbose)
     return LIB
 
 

@@ -8,111 +8,43 @@ Rotary positions: Su et al., "RoFormer" (2021); the scalings "ntk" and "parts" f
 longer than a model was trained on follow the base change and the by-parts interpolation of
 Peng et al., "YaRN" (2023).
 """
-import ctypes
-import functools
+import importlib.util
 import math
+import os
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from . import NF4_BF16, NF4_F32, _check, _dev, _ptr, _same_device, _stream, _workspace, load_library
+from . import NF4_ERR_HIP, NF4Error, lib_path, load_library
 
 __all__ = ["RopePlan", "rope_plan", "rope_fwd", "rope_bwd", "KVCache", "kv_cache", "kv_append", "kv_attention",
            "head_loss"]
 
-_vp, _i64, _i32, _sz, _f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
-
-
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64), ("heads", _i32)]
-
-
-class _Rope(ctypes.Structure):
-    _fields_ = [("freq", _vp), ("rotary_dim", _i32), ("interleaved", _i32), ("magnitude", _f)]
-
-
-class _Cache(ctypes.Structure):
-    _fields_ = [("codes", _vp), ("scales", _vp), ("pages", _i64), ("kv_heads", _i32), ("page_size", _i32),
-                ("head_dim", _i32)]
-
-
-class _Batch(ctypes.Structure):
-    _fields_ = [("starts", _vp), ("lengths", _vp), ("table", _vp), ("table_stride", _i64), ("tokens", _i64),
-                ("seqs", _i32), ("table_width", _i32)]
-
-
 _bound = None
 
 
-def _library():
+def binding_path() -> str:
+    return os.path.join(os.path.dirname(lib_path()), "qlora_decoder_binding.so")
+
+
+def _binding():
+    """The compiled calls (raises NF4Error if they have not been built).  They check each tensor's
+    type, shape, strides and device, allocate outputs and workspaces with torch, and call the library
+    on torch's current stream."""
     global _bound
     if _bound is None:
-        L = load_library()
-        p = ctypes.POINTER
-        L.qlora_rope_apply.restype = ctypes.c_int
-        L.qlora_rope_apply.argtypes = [p(_Rope), _i32, _vp, _i64, _i32, ctypes.c_int, p(_Heads), p(_Heads), _i32, _vp]
-        L.qlora_kv_append.restype = ctypes.c_int
-        L.qlora_kv_append.argtypes = [p(_Cache), p(_Batch), p(_Heads), p(_Heads), p(_Rope), p(_Heads), p(_Heads), _vp]
-        L.qlora_kv_attention_workspace_bytes.restype = _sz
-        L.qlora_kv_attention_workspace_bytes.argtypes = [p(_Cache), p(_Batch), _i32, _i64, _i64]
-        L.qlora_kv_attention.restype = ctypes.c_int
-        L.qlora_kv_attention.argtypes = [p(_Cache), p(_Batch), p(_Heads), p(_Heads), _f, _i64, _i64, _vp, _sz, _vp]
-        L.qlora_head_loss_workspace_bytes.restype = _sz
-        L.qlora_head_loss_workspace_bytes.argtypes = [_i64, _i64, _i64, _i32, _i32]
-        L.qlora_head_loss.restype = ctypes.c_int
-        L.qlora_head_loss.argtypes = [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
-        _bound = L
+        load_library()
+        path = binding_path()
+        if not os.path.exists(path):
+            raise NF4Error(NF4_ERR_HIP, "binding not built (%s); run __graft_entry__.build()" % path)
+        spec = importlib.util.spec_from_file_location("qlora_decoder_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        module.setup(NF4Error, stream or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+        _bound = module
     return _bound
-
-
-# The calls below serve single tokens, where the host's time counts: each tensor is asked
-# once for its shape, strides, type and device, and the stream is taken as a raw handle.
-def _on(t: torch.Tensor, name: str, dtype, dev: int) -> int:
-    """Address of a dense tensor of the given type on device `dev`."""
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.get_device() != dev:
-        raise ValueError("%s must be on the same GPU as the other operands, got %s" % (name, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
-
-
-def _device(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    return t.get_device()
-
-
-def _heads(t: torch.Tensor, name: str, dtype, tokens: int, dim: int, dev: int) -> _Heads:
-    """A [tokens, heads, dim] tensor of any token and head strides."""
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.get_device() != dev:
-        raise ValueError("%s must be on the same GPU as the other operands, got %s" % (name, t.device))
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or shape[1] < 1:
-        raise ValueError("%s must be [%d, heads, %d], got %s" % (name, tokens, dim, tuple(shape)))
-    token_stride, head_stride, last = t.stride()
-    if last != 1 and tokens:
-        raise ValueError("%s must be dense along its last dimension" % name)
-    heads = shape[1]
-    if heads == 1:                      # the stride of a dimension of one is not looked at
-        head_stride = dim
-    if tokens <= 1:
-        token_stride = heads * head_stride
-    return _Heads(t.data_ptr(), token_stride, head_stride, heads)
-
-
-def _fresh_heads(like: torch.Tensor, tokens: int, dim: int):
-    """A new dense tensor of `like`'s shape and type, and its description."""
-    out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    heads = out.shape[1]
-    return out, _Heads(out.data_ptr(), heads * dim, dim, heads)
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 # ---------------------------------------------------------------------------
@@ -126,12 +58,6 @@ class RopePlan:
     rotary_dim: int
     interleaved: bool = False
     magnitude: float = 1.0
-
-    def _struct(self, dev):
-        freq = self.freq
-        if freq.numel() * 2 != self.rotary_dim:
-            raise ValueError("freq must hold rotary_dim / 2 = %d values" % (self.rotary_dim // 2))
-        return _Rope(_on(freq, "freq", torch.int64, dev), self.rotary_dim, self.interleaved, self.magnitude)
 
 
 def rope_plan(rotary_dim: int, base: float = 10000.0, *, interleaved: bool = False, scaling: Optional[str] = None,
@@ -174,43 +100,18 @@ def rope_plan(rotary_dim: int, base: float = 10000.0, *, interleaved: bool = Fal
     return RopePlan(freq, rotary_dim, bool(interleaved), magnitude)
 
 
-_Heads2 = _Heads * 2
-
-
-def _rope(plan, positions, q, k, inplace, backward):
-    dev = _device(q, "q")
-    dtype = q.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
-        raise ValueError("q must be float32 or bfloat16, got %s" % dtype)
-    M, dim = positions.numel(), q.shape[-1]
-    at = _on(positions, "positions", torch.int32, dev)
-    rope = plan._struct(dev)
-    ins = _Heads2(_heads(q, "q", dtype, M, dim, dev))
-    if k is not None:
-        ins[1] = _heads(k, "k", dtype, M, dim, dev)
-    yq, yk, outs = q, k, ins
-    if not inplace:
-        yq, hq = _fresh_heads(q, M, dim)
-        outs = _Heads2(hq)
-        if k is not None:
-            yk, outs[1] = _fresh_heads(k, M, dim)
-    _check(_library().qlora_rope_apply(rope, backward, at, M, dim, NF4_BF16 if dtype is torch.bfloat16 else NF4_F32, ins,
-                                       outs, 1 if k is None else 2, _raw_stream(dev)))
-    return yq if k is None else (yq, yk)
-
-
 def rope_fwd(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Tensor] = None,
              inplace: bool = False):
     """Queries, and keys if given, rotated to their positions: q [tokens, heads, dim], k
     [tokens, kv_heads, dim] (fp32 or bf16, the same type; any strides with a dense last
     dimension), positions int32 [tokens].  Returns new dense tensors, or the same ones if `inplace`."""
-    return _rope(plan, positions, q, k, inplace, 0)
+    return (_bound or _binding()).rope(plan.freq, plan.rotary_dim, plan.interleaved, plan.magnitude, False, positions, q, k, inplace)
 
 
 def rope_bwd(plan: RopePlan, positions: torch.Tensor, dq: torch.Tensor, dk: Optional[torch.Tensor] = None,
              inplace: bool = False):
     """The gradient of rope_fwd: dq and dk turned back, times the same magnitude."""
-    return _rope(plan, positions, dq, dk, inplace, 1)
+    return (_bound or _binding()).rope(plan.freq, plan.rotary_dim, plan.interleaved, plan.magnitude, True, positions, dq, dk, inplace)
 
 
 # ---------------------------------------------------------------------------
@@ -223,16 +124,6 @@ class KVCache:
     codes: torch.Tensor
     scales: torch.Tensor
 
-    def _struct(self, dev):
-        codes, scales = self.codes, self.scales
-        shape = codes.shape
-        if len(shape) != 5 or shape[1] != 2:
-            raise ValueError("codes must be [pages, 2, kv_heads, page_size, head_dim], got %s" % (tuple(shape),))
-        if scales.shape != shape[:3]:
-            raise ValueError("scales must be %s, got %s" % (tuple(shape[:3]), tuple(scales.shape)))
-        return _Cache(_on(codes, "codes", torch.uint8, dev), _on(scales, "scales", torch.float32, dev), shape[0], shape[2],
-                      shape[3], shape[4])
-
     def decode(self, dtype=torch.float32) -> torch.Tensor:
         """What the codes stand for, [pages, 2, kv_heads, page_size, head_dim] (for looking at)."""
         return (self.codes.view(torch.float8_e4m3fn).float() * self.scales[..., None, None]).to(dtype)
@@ -242,22 +133,6 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, devi
     """An empty cache of `pages` pages."""
     return KVCache(torch.zeros((pages, 2, kv_heads, page_size, head_dim), dtype=torch.uint8, device=device),
                    torch.ones((pages, 2, kv_heads), dtype=torch.float32, device=device))
-
-
-def _batch(starts, lengths, table, tokens, dev):
-    shape = table.shape
-    if len(shape) != 2:
-        raise ValueError("table must be [seqs, pages of a sequence], got %s" % (tuple(shape),))
-    seqs, width = shape
-    if tuple(lengths.shape) != (seqs,) or tuple(starts.shape) != (seqs + 1,):
-        raise ValueError("lengths must be [%d] and starts [%d], as the table has %d rows" % (seqs, seqs + 1, seqs))
-    stride, last = table.stride()
-    if last != 1 and width > 1:
-        raise ValueError("table must be dense along its rows")
-    if table.dtype != torch.int32 or table.get_device() != dev:
-        raise ValueError("table must be torch.int32 on the same GPU as the other operands, got %s on %s" % (table.dtype, table.device))
-    return _Batch(_on(starts, "starts", torch.int32, dev), _on(lengths, "lengths", torch.int32, dev), table.data_ptr(),
-                  stride if seqs > 1 else width, tokens, seqs, width)
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, lengths: torch.Tensor,
@@ -271,26 +146,11 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Te
       lengths  int32 [seqs]: tokens of each sequence before these (negative: an unused row)
       table    int32 [seqs, pages of a sequence]: the pool's page of each page_size positions
     The caller moves its lengths on by the new tokens after the attention of the same step."""
-    dev = _device(k, "k")
-    c = cache._struct(dev)
-    T, dim = k.shape[0], c.head_dim
-    b = _batch(starts, lengths, table, T, dev)
-    kh, vh = _heads(k, "k", torch.bfloat16, T, dim, dev), _heads(v, "v", torch.bfloat16, T, dim, dev)
-    out = qh = oh = None
-    if q is not None:
-        qh = _heads(q, "q", torch.bfloat16, T, dim, dev)
-        out, oh = _fresh_heads(q, T, dim)
-    _check(_library().qlora_kv_append(c, b, kh, vh, None if rope is None else rope._struct(dev), qh, oh, _raw_stream(dev)))
-    return out
-
-
-@functools.lru_cache(maxsize=1024)
-def _attention_ws_bytes(kv_heads, page_size, head_dim, seqs, tokens, heads, max_new, max_length):
-    """Workspace of an attention of these sizes (a plain function of them)."""
-    some = 4096                         # addresses that are checked, not followed
-    c = _Cache(some, some, 1, kv_heads, page_size, head_dim)
-    b = _Batch(some, some, some, 1, tokens, seqs, 1)
-    return _library().qlora_kv_attention_workspace_bytes(c, b, heads, max_new, max_length)
+    call = (_bound or _binding()).append
+    if rope is None:
+        return call(cache.codes, cache.scales, k, v, starts, lengths, table, q, None, 0, False, 1.0)
+    return call(cache.codes, cache.scales, k, v, starts, lengths, table, q, rope.freq, rope.rotary_dim, rope.interleaved,
+                rope.magnitude)
 
 
 def kv_attention(cache: KVCache, q: torch.Tensor, starts: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
@@ -301,19 +161,7 @@ def kv_attention(cache: KVCache, q: torch.Tensor, starts: torch.Tensor, lengths:
     reads kv head h // (heads // kv_heads).  scale: 1/sqrt(head_dim) by default.  max_new (the
     most new tokens of a sequence) and max_length (its most positions, new ones included) size
     the launch: without them it is sized for `tokens` and for the table's width."""
-    dev = _device(q, "q")
-    c = cache._struct(dev)
-    T, dim = q.shape[0], c.head_dim
-    b = _batch(starts, lengths, table, T, dev)
-    qh = _heads(q, "q", torch.bfloat16, T, dim, dev)
-    out, oh = _fresh_heads(q, T, dim)
-    max_new = max(1, T) if max_new is None else int(max_new)
-    max_length = max(1, b.table_width * c.page_size) if max_length is None else int(max_length)
-    wsb = _attention_ws_bytes(c.kv_heads, c.page_size, dim, b.seqs, T, qh.heads, max_new, max_length)
-    ws = _workspace(wsb, q.device)
-    _check(_library().qlora_kv_attention(c, b, qh, oh, dim ** -0.5 if scale is None else float(scale), max_new, max_length,
-                                         None if ws is None else ws.data_ptr(), wsb, _raw_stream(dev)))
-    return out
+    return (_bound or _binding()).attention(cache.codes, cache.scales, q, starts, lengths, table, scale, max_new, max_length)
 
 
 # ---------------------------------------------------------------------------
@@ -329,28 +177,4 @@ def head_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, dloss: Op
       dloss    fp32 [M], the gradient of each row's loss (1/count for a mean): with it dX is
                computed in the same call, and dW if need_dw.  A later factor on a row's loss
                multiplies its row of dX."""
-    L = _library()
-    _dev(X, "X", torch.bfloat16)
-    _dev(W, "W", torch.bfloat16)
-    _dev(targets, "targets", torch.int64)
-    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
-        raise ValueError("X must be [M, K] and W [V, K]")
-    M, K = X.shape
-    V = W.shape[0]
-    if tuple(targets.shape) != (M,):
-        raise ValueError("targets must be [%d]" % M)
-    if dloss is not None:
-        _dev(dloss, "dloss", torch.float32)
-        if tuple(dloss.shape) != (M,):
-            raise ValueError("dloss must be [%d]" % M)
-    elif need_dw:
-        raise ValueError("need_dw needs dloss")
-    _same_device(("X", X), ("W", W), ("targets", targets), ("dloss", dloss))
-    loss = torch.empty(M, dtype=torch.float32, device=X.device)
-    dX = torch.empty((M, K), dtype=torch.bfloat16, device=X.device) if dloss is not None else None
-    dW = torch.empty((V, K), dtype=torch.bfloat16, device=X.device) if need_dw else None
-    wsb = L.qlora_head_loss_workspace_bytes(M, K, V, dX is not None, dW is not None)
-    ws = _workspace(wsb, X.device)
-    _check(L.qlora_head_loss(_ptr(X), M, K, _ptr(W), V, _ptr(targets), ignore_index, _ptr(dloss), _ptr(loss), _ptr(dX),
-                             _ptr(dW), _ptr(ws), wsb, _stream(X.device)))
-    return loss, dX, dW
+    return (_bound or _binding()).head_loss(X, W, targets, dloss, need_dw, ignore_index)

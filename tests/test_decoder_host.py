@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import bit_nf4_quantized_09_amd as nf4
-from bit_nf4_quantized_09_amd import decoder as dec
+import decoder_abi as dec
 import decoder_ref as ref
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "qlora_decoder.h")
