@@ -31,8 +31,6 @@
 // W or X read transposed) goes through four LDS stages filled by direct loads, three steps ahead.
 // (256 x 256 tiles with both operands in LDS, 8 waves of 128 x 64: LDS reads and writes take as
 // many cycles as the matrix instructions; 940-1000 TFLOP/s.)
-#include <utility>
-
 #include "bufio.h"
 #include "decoder.h"
 #include "lds_dma.h"
@@ -229,6 +227,7 @@ struct HeadArgs {
     const float4* rows;       // [Mp]: lse, base 2; 1 - p of the target; dloss; the target (as bits, -1: none) (HEAD_GT)
     const uint32_t* top;      // max|dloss| as bits (HEAD_GT)
     uint16_t* out;            // E or G^T in fragment order
+    uint8_t* low;             // the next eight bits of E's values, in the same order, or null (HEAD_E)
     int64_t out_steps;        // blocks of a row tile of `out`
     int64_t Mp;
 };
@@ -243,6 +242,16 @@ __device__ __forceinline__ bool head_live(int64_t target, int64_t V, int64_t ign
 constexpr float HEAD_ROOM = 40.0f;        // binades a logit may pass the running reference by
 // The factor on G, from max|dloss|: at least the smallest normal number, so that its inverse is finite.
 __device__ __forceinline__ float head_scale(const uint32_t* top) { return fmaxf(__uint_as_float(*top), 0x1p-126f); }
+
+// E is kept for dW as bf16 and eight bits more, so that G is rounded once, from a value of 16 bits: the two together
+// are the fp32 value's bits with the last eight rounded away.
+__device__ __forceinline__ uint32_t head_low(float y, uint32_t kept) {
+    const int d = (int)(__float_as_uint(y) - kept + 0x80u) >> 8;
+    return (uint32_t)(d < -128 ? -128 : d > 127 ? 127 : d) & 0xFFu;
+}
+__device__ __forceinline__ float head_both(float kept, uint32_t low) {
+    return kept == 0.0f ? 0.0f : __uint_as_float(__float_as_uint(kept) + ((uint32_t)(int32_t)(int8_t)low << 8));
+}
 
 // The epilogue of HEAD_STATS and HEAD_E for 32 tokens m0 .. (column rl) and the 32 J vocabulary rows v0 .. of tile
 // tv: z[j][reg] is row 32 j + 8 (reg / 4) + 4 h + reg % 4.
@@ -277,10 +286,7 @@ __device__ __forceinline__ void head_column(const HeadArgs& a, f32x16* acc, int6
     }
     // E's blocks of 512 tokens and 64 vocabulary rows: row m's 16-byte chunk of rows v .. v + 7
     const int in = (int)(m0 % HL_TM);
-    uint8_t* blocks = nullptr;
-    if (MODE == HEAD_E)
-        blocks = reinterpret_cast<uint8_t*>(a.out) + (m0 / HL_TM) * a.out_steps * A_BLOCK_BYTES + (in >> 7) * 16384 + ((in >> 5) & 3) * 4096 +
-                 rl * 16 + 8 * h;
+    const int64_t place = MODE == HEAD_E ? (m0 / HL_TM) * a.out_steps * A_BLOCK_BYTES + (in >> 5) * 4096 + rl * 16 + 8 * h : 0;
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -295,8 +301,12 @@ __device__ __forceinline__ void head_column(const HeadArgs& a, f32x16* acc, int6
             }
             if (MODE == HEAD_E) {
                 const int64_t chunk = ((v0 - a.v0) >> 3) + 4 * j + r4;         // of the row's 16-byte chunks
-                *reinterpret_cast<uint2*>(blocks + (chunk >> 3) * A_BLOCK_BYTES + (chunk & 7) * 512) =
-                    make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                const int64_t to = place + (chunk >> 3) * A_BLOCK_BYTES + (chunk & 7) * 512;
+                const uint2 e = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.out) + to) = e;
+                if (a.low)
+                    *reinterpret_cast<uint32_t*>(a.low + to / 2) = head_low(y[0], e.x << 16) | head_low(y[1], e.x & 0xFFFF0000u) << 8 |
+                                                                   head_low(y[2], e.y << 16) << 16 | head_low(y[3], e.y & 0xFFFF0000u) << 24;
             }
         }
     sum += __shfl_xor(sum, 32);
@@ -371,19 +381,45 @@ void k_head_logits(HeadArgs a) {
     for (int i = 0; i < 4; ++i) head_column<MODE, 4>(a, acc[i], m0 + wave * 128 + i * 32, v0, tv, h, rl);
 }
 
-// The logits of up to 64 tokens, whose time is that of reading W: a workgroup takes 128 vocabulary rows, each of its
-// four waves 32 of them, and streams W (whole 128-byte lines of 8 rows a load) and X through six LDS stages, five
-// steps ahead: up to 80 KB of W in flight per compute unit.  Its tiles are 32 rows.  (W straight into registers,
-// 32 rows a load, meets every line four times: 75 us for 33 tokens x 32000 x 4096.)
+// Tiles of 64 tokens, for few tokens and for grids that 512-token tiles leave mostly empty.
+//
+// Logits: a workgroup takes 128 vocabulary rows and 32 NT tokens, each of its four waves 32 of the rows, and streams
+// W (whole 128-byte lines of 8 rows a load) and X through six LDS stages, five steps ahead: up to 80 KB of W in
+// flight per compute unit.  Up to 64 tokens its time is that of reading W, past the caches where nothing
+// reads it again (ONCE).  (W straight into registers, 32 rows a load, meets every line four times: 75 us for
+// 33 tokens x 32000 x 4096, 63 here.)
 constexpr int FEW_TOKENS = 64, FEW_TN = 32, FEW_STAGES = 6;
-constexpr int few_stage(int nt) { return 16384 + 4096 * nt; }            // bytes: W, then X
-template <HeadMode MODE, int NT>
+constexpr int few_stage(int nt) { return 16384 + 4096 * nt; }            // bytes: 128 x 64 or 64 x 128 of W, then X or E
+
+// Tile of a workgroup, the token blocks of one slice of W on one XCD.
+__device__ __forceinline__ bool few_tile(int wg, int64_t blocks, int64_t slices, int64_t& block, int64_t& slice) {
+    const int64_t total = blocks * slices, q = total / XCDS, rem = total % XCDS;
+    const int64_t x = wg % XCDS, local = wg / XCDS;
+    if (local >= q + (x < rem ? 1 : 0)) return false;
+    const int64_t at = x * q + (x < rem ? x : rem) + local;
+    block = at % blocks;
+    slice = at / blocks;
+    return true;
+}
+
+// Waits until only the loads of the four youngest stages of 4 + NT each are out, and meets the other waves.
+template <int NT>
+__device__ __forceinline__ void few_landed() {
+    if constexpr (NT == 2) asm volatile("s_waitcnt vmcnt(24) lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <HeadMode MODE, int NT, bool ONCE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
 void k_head_few(HeadArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5, rl = lane & 31;
-    const int64_t b0 = a.v0 + (int64_t)blockIdx.x * 128;
+    int64_t block, slice;
+    if (!few_tile(blockIdx.x, (a.M + 32 * NT - 1) / (32 * NT), a.tiles_v / 4, block, slice)) return;
+    const int64_t b0 = a.v0 + slice * 128, m0 = block * 32 * NT;
     const int steps = __builtin_amdgcn_readfirstlane((int)(a.K / HL_K));
     // a wave fills its own 32 rows of W and 8 NT of X, 8 a load (rows past the end repeat the last: dropped later)
     uint32_t wof[4], xof[NT];
@@ -396,15 +432,15 @@ void k_head_few(HeadArgs a) {
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
         const int row = (wave * NT + q) * 8 + (lane >> 3);
-        xof[q] = (uint32_t)((row < a.M ? row : a.M - 1) * a.K * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
+        xof[q] = (uint32_t)((m0 + row < a.M ? row : a.M - 1 - m0) * a.K * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
     }
-    const dma_rsrc rw = make_dma_rsrc(a.W + b0 * a.K, (a.V - b0) * a.K * 2), rx = make_dma_rsrc(a.X, a.M * a.K * 2);
+    const dma_rsrc rw = make_dma_rsrc(a.W + b0 * a.K, (a.V - b0) * a.K * 2), rx = make_dma_rsrc(a.X + m0 * a.K, (a.M - m0) * a.K * 2);
     const uint32_t base = lds_address(lds);
     auto fill = [&](int stage, int step) {
         const int at = step < steps ? step : steps - 1;
         const uint32_t to = base + stage * few_stage(NT);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load_to_lds<MODE == HEAD_STATS>(rw, to + wave * 4096 + q * 1024, wof[q], (uint32_t)at * 128);
+        for (int q = 0; q < 4; ++q) load_to_lds<ONCE>(rw, to + wave * 4096 + q * 1024, wof[q], (uint32_t)at * 128);
 #pragma unroll
         for (int q = 0; q < NT; ++q) load_to_lds(rx, to + 16384 + (wave * NT + q) * 1024, xof[q], (uint32_t)at * 128);
     };
@@ -418,11 +454,7 @@ void k_head_few(HeadArgs a) {
     for (int i = 0; i < FEW_STAGES - 1; ++i) fill(i, i);
     int stage = 0, free = FEW_STAGES - 1;
     for (int it = 0; it < steps; ++it) {
-        // this stage has landed once only the loads of the four after it are out
-        if constexpr (NT == 2) asm volatile("s_waitcnt vmcnt(24) lgkmcnt(0)" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        few_landed<NT>();
         fill(free, it + FEW_STAGES - 1);                                  // the stage that every wave left before the barrier
         const uint8_t* sw = lds + stage * few_stage(NT);
 #pragma unroll
@@ -438,9 +470,8 @@ void k_head_few(HeadArgs a) {
         stage = stage + 1 < FEW_STAGES ? stage + 1 : 0;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const int64_t tv = (int64_t)blockIdx.x * 4 + wave;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) head_column<MODE, 1>(a, &acc[i], 32 * i, b0 + 32 * wave, tv, h, rl);
+    for (int i = 0; i < NT; ++i) head_column<MODE, 1>(a, &acc[i], m0 + 32 * i, b0 + 32 * wave, slice * 4 + wave, h, rl);
 }
 
 // A row's loss from its target's logit and the others' log-sum (both base 2): the loss, lse
@@ -528,7 +559,9 @@ struct JoinArgs {
     int64_t ignore, V;
     uint16_t* E;              // in fragment order,
     int64_t steps;            // blocks of a row tile
-    float *ref, *total;       // running reference and sum of each row
+    const float* ref;         // running reference of each row before the piece, and
+    float* next;              // after it (the next piece's, where each keeps its own),
+    float* total;             // running sum
     float* factor;            // out: factor on the row's sums so far
     const float* zy;
     int last;                 // 1: also the loss and what the gradients need of a row
@@ -593,7 +626,7 @@ void k_head_join(JoinArgs a) {
     if (lane != 0) return;
     const float f = old == now ? 1.0f : __builtin_amdgcn_exp2f(old - now);
     const float total = a.total[m] * f + sum;
-    a.ref[m] = now;
+    a.next[m] = now;
     a.total[m] = total;
     a.factor[m] = f;
     if (!a.last) return;
@@ -615,6 +648,7 @@ struct ProductArgs {
     int64_t tiles_r, tiles_n;
     float* sum;               // fp32 [splits][out_rows][N]
     const float* factor;      // ADD: factor of each row on what `sum` holds
+    bool add;                 // ADD, of the tiles of 64 rows
     uint16_t* out;            // OUT_DX, OUT_DW: bf16 [out_rows][N] (splits == 1)
     const uint32_t* top;      // OUT_DW: times head_scale(top)
     const float2* ends;       // OUT_DX: out[r] = ends[r].x * sums - ends[r].y * W[targets[r]]
@@ -722,47 +756,242 @@ void k_head_product(ProductArgs a) {
     }
 }
 
-// dX from the sums of several parts of the contraction: a workgroup per row.
+// The same sums in tiles of 32 NT rows x 128 columns: a step's 64 rows of B go through LDS once, each wave takes 16
+// of them for the whole tile, and the four waves' accumulators are added at the end.
+template <int NT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
+void k_head_few_product(ProductArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5, rl = lane & 31;
+    const int split = blockIdx.y;
+    int64_t block, tn;
+    if (!few_tile(blockIdx.x, a.tiles_r, a.tiles_n, block, tn)) return;
+    const int per = (a.steps + a.splits - 1) / a.splits;
+    const int first = __builtin_amdgcn_readfirstlane(split * per);
+    const int last = __builtin_amdgcn_readfirstlane(first + per < a.steps ? first + per : a.steps);
+    const int64_t r0 = block * 32 * NT, n0 = tn * HL_TN;
+    const uint32_t base = lds_address(lds);
+    uint32_t bcol;
+    int off[4];
+    {
+        const int q = lane & 15, row = lane >> 4;
+        const int chunk = (((q >> 1) ^ (row << 1)) << 1) | (q & 1);
+        bcol = (uint32_t)(n0 + chunk * 8 < a.N ? chunk * 16 : 0);
+        const int g = lane >> 4, jl = lane & 15;
+        const int row0 = 8 * (g >> 1) + (jl >> 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) off[j] = hl_toff(row0, j * 32 + 16 * (g & 1) + 4 * (jl & 3)) + wave * 16 * 256;
+    }
+    // the rows' fragments of a block: 4 KB per 32 rows, 1 KB of them a wave's
+    const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A) + (r0 / HL_TM) * a.a_steps * A_BLOCK_BYTES + (r0 % HL_TM) * 128;
+    auto fill = [&](int stage, int step) {
+        const int at = step < last ? step : last - 1;
+        const uint32_t to = base + stage * few_stage(NT);
+        const int64_t p0 = (int64_t)at * HL_K;
+        const dma_rsrc rb = make_dma_rsrc(a.B + p0 * a.N + n0, (a.P - p0) * a.N * 2);
+        const dma_rsrc ra = make_dma_rsrc(A + at * (int64_t)A_BLOCK_BYTES, 4096 * NT);
+        const int most = (int)(a.P - p0 < HL_K ? a.P - p0 : HL_K) - 1;    // rows past the last repeat it: A is zero there
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int row = wave * 16 + q * 4 + (lane >> 4);
+            load_to_lds(rb, to + wave * 4096 + q * 1024, (uint32_t)((row < most ? row : most) * (int)a.N * 2) + bcol, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) load_to_lds(ra, to + 16384 + i * 4096 + wave * 1024, (uint32_t)(i * 4096 + wave * 1024 + lane * 16), 0);
+    };
+    f32x16 acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    if (first < last) {
+#pragma unroll
+        for (int i = 0; i < FEW_STAGES - 1; ++i) fill(i, first + i);
+        int stage = 0, free = FEW_STAGES - 1;
+        for (int it = first; it < last; ++it) {
+            few_landed<NT>();
+            fill(free, it + FEW_STAGES - 1);
+            const uint8_t* sb = lds + stage * few_stage(NT);
+            bf16x8 x[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) x[i] = *reinterpret_cast<const bf16x8*>(sb + 16384 + i * 4096 + wave * 1024 + lane * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint2 lo = hl_read_tr(sb + off[j]), hi = hl_read_tr(sb + off[j] + 4 * 256);
+                const bf16x8 w = __builtin_bit_cast(bf16x8, make_uint4(lo.x, lo.y, hi.x, hi.y));
+#pragma unroll
+                for (int i = 0; i < NT; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x[i], acc[i][j], 0, 0, 0);
+            }
+            free = stage;
+            stage = stage + 1 < FEW_STAGES ? stage + 1 : 0;
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    // accumulator (i, j, reg): row 32 i + rl, column 32 j + 8 (reg / 4) + 4 h + reg % 4; wave w finishes columns 32 w ..
+    auto cell = [&](int from, int i, int j, int r4) {
+        return reinterpret_cast<f32x4*>(lds + ((((from * NT + i) * 4 + j) * 4 + r4) << 10) + lane * 16);
+    };
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4)
+                *cell(wave, i, j, r4) = f32x4{acc[i][j][4 * r4], acc[i][j][4 * r4 + 1], acc[i][j][4 * r4 + 2], acc[i][j][4 * r4 + 3]};
+    __syncthreads();
+    float* sums = a.sum + split * a.out_rows * a.N;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int64_t r = r0 + 32 * i + rl;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int64_t n = n0 + 32 * wave + 8 * r4 + 4 * h;
+            if (r >= a.out_rows || n >= a.N) continue;
+            f32x4 y = *cell(0, i, wave, r4);
+#pragma unroll
+            for (int from = 1; from < 4; ++from) y += *cell(from, i, wave, r4);
+            f32x4* to = reinterpret_cast<f32x4*>(sums + r * a.N + n);
+            if (a.add) y += *to * a.factor[r];
+            *to = y;
+        }
+    }
+}
+
+// dX from the sums of several parts of the contraction: a thread per four columns.
 __global__ __launch_bounds__(256)
 void k_head_finish(ProductArgs a, uint16_t* out) {
-    const int64_t r = blockIdx.x;
-    const float2 row = a.ends[r];
+    const int64_t r = blockIdx.x, n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    if (n >= a.N) return;
     const int64_t target = a.targets[r];
-    const uint16_t* w = a.W + (head_live(target, a.V, a.ignore) ? target * a.N : 0);
-    for (int64_t n = threadIdx.x * 4; n < a.N; n += 1024) {
-        f32x4 y = {};
-        for (int s = 0; s < a.splits; ++s) y += *reinterpret_cast<const f32x4*>(a.sum + (s * a.out_rows + r) * a.N + n);
-        *reinterpret_cast<uint2*>(out + r * a.N + n) = head_dx4(y, row, *reinterpret_cast<const uint2*>(w + n));
+    const uint2 w = *reinterpret_cast<const uint2*>(a.W + (head_live(target, a.V, a.ignore) ? target * a.N : 0) + n);
+    f32x4 y = {};
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) y += *reinterpret_cast<const f32x4*>(a.sum + (s * a.out_rows + r) * a.N + n);
+    *reinterpret_cast<uint2*>(out + r * a.N + n) = head_dx4(y, a.ends[r], w);
+}
+
+// G^T of a piece from its E: G = dloss / max|dloss| (E 2^(R - lse) - the target's 1 - p), R the reference that the
+// piece ended with.  A lane takes 8 vocabulary entries of a token; eight lanes with eight tokens exchange them for
+// 8 tokens of an entry each.
+struct TurnArgs {
+    const uint16_t* E;        // [tokens / 512][steps_v] blocks, and
+    const uint8_t* low;       // the eight bits more
+    uint16_t* G;              // [vocabulary / 512][steps_m] blocks
+    int64_t steps_v, steps_m; // steps of 64 vocabulary rows, of 64 tokens
+    int64_t v0, V;
+    const float* ref;         // the piece's last references
+    const float4* rows;
+    const uint32_t* top;
+};
+__global__ __launch_bounds__(256)
+void k_head_turn(TurnArgs a) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // a wave: 32 tokens x 64 vocabulary entries, 4 KB on both sides
+    const int64_t step = (int64_t)blockIdx.x * 4 + wave, m0 = (int64_t)blockIdx.y * 32;
+    if (step >= a.steps_v) return;
+    const int64_t m = m0 + (lane & 31);
+    const float4 row = a.rows[m];
+    const int target = __float_as_int(row.w);
+    const float inv = 1.0f / head_scale(a.top), f = target >= 0 ? row.z * inv * __builtin_amdgcn_exp2f(a.ref[m] - row.x) : 0.0f;
+    const float mine = -row.z * inv * row.y;
+    const int64_t in = ((m0 / HL_TM) * a.steps_v + step) * A_BLOCK_BYTES + (m0 % HL_TM) * 128 + lane * 16;
+    uint4 e[4];
+    uint2 low[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        e[s] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.E) + in + s * 1024);
+        low[s] = *reinterpret_cast<const uint2*>(a.low + (in + s * 1024) / 2);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int64_t v = step * HL_K + 16 * s + 8 * (lane >> 5);        // of the piece
+        float y[8];
+        Vec16<uint16_t>::unpack(e[s], y);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            y[u] = f * head_both(y[u], (u < 4 ? low[s].x : low[s].y) >> (8 * (u & 3)));
+            if (a.v0 + v + u == target) y[u] = mine;
+            if (target < 0 || a.v0 + v + u >= a.V) y[u] = 0.0f;
+        }
+        uint4 g = Vec16<uint16_t>::pack(y);
+        // 8 x 8 values of 16 bits across 8 lanes: halves, pairs, and neighbours change places
+        {
+            const bool up = lane & 4;
+            const uint32_t x = __shfl_xor((int)(up ? g.x : g.z), 4), z = __shfl_xor((int)(up ? g.y : g.w), 4);
+            g = up ? make_uint4(x, z, g.z, g.w) : make_uint4(g.x, g.y, x, z);
+        }
+        {
+            const bool up = lane & 2;
+            const uint32_t x = __shfl_xor((int)(up ? g.x : g.y), 2), z = __shfl_xor((int)(up ? g.z : g.w), 2);
+            g = up ? make_uint4(x, g.y, z, g.w) : make_uint4(g.x, x, g.z, z);
+        }
+        {
+            const bool up = lane & 1;
+            auto swap = [&](uint32_t own) {
+                const uint32_t other = __shfl_xor((int)own, 1);
+                return up ? (own & 0xFFFF0000u) | (other >> 16) : (own & 0xFFFFu) | (other << 16);
+            };
+            g = make_uint4(swap(g.x), swap(g.y), swap(g.z), swap(g.w));
+        }
+        // this lane's entry, with the tokens of its eight
+        const int64_t ve = v + (lane & 7);
+        uint8_t* out = reinterpret_cast<uint8_t*>(a.G) + ((ve / HL_TM) * a.steps_m + m0 / HL_K) * A_BLOCK_BYTES + (ve % HL_TM >> 5) * 4096 +
+                       ((m0 & 32) >> 3) * 512 + ((lane & 31) >> 3) * 512 + (ve & 31) * 16;
+        *reinterpret_cast<uint4*>(out) = g;
     }
 }
 
 // Pieces of the vocabulary and the workspace's layout.
 struct HeadPlan {
     int64_t Mp;               // tokens up to whole tiles
-    bool few;                 // up to 64 tokens: logits by k_head_few
+    bool few;                 // logits by k_head_few
     int width;                // vocabulary rows of a tile of the logits
     int64_t piece;            // vocabulary rows of a piece (a multiple of 512: whole row tiles of G^T)
+    int64_t pieces;
+    bool keep;                // every piece's E is kept until dW
+    bool few_dx;              // dX by k_head_few_product
     int splits;               // parts of dX's contraction
-    size_t top, zy, ref, total, factor, ends, rows, part, Xp, E, sum, bytes;
-    // tiles of the logits (few tokens: four to a workgroup)
+    size_t top, zy, ref, total, factor, ends, rows, part, Xp, E, low, G, sum, bytes;
+    int64_t blocks(int64_t M) const { return M <= 32 ? 1 : (M + 63) / 64; }                   // of 64 tokens (one of 32)
+    // tiles of the logits (few: four to a workgroup)
     int64_t tiles(int64_t vocabulary) const { return (vocabulary + 127) / 128 * (few ? 4 : 1); }
+    size_t piece_bytes() const { return (size_t)Mp * piece * 2; }
 };
+
+// The time of a step of a 64-token tile over that of a 512-token tile, which a compute unit holds one of.
+constexpr double FEW_COST = 0.25;
+constexpr int64_t CUS = 256;
 
 static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     HeadPlan p{};
     const bool grad = dx || dw;
     p.Mp = (M + HL_TM - 1) / HL_TM * HL_TM;
-    p.few = M <= FEW_TOKENS;
-    p.width = p.few ? FEW_TN : HL_TN;
     // a piece of E or G^T of at most 128 MB, half of the last-level cache: larger pieces pass over dX's
     // fp32 sums less often (64 MB: 947 us for 2048 tokens x 32000 x 4096, 128 MB: 903 us)
     const int64_t most = ((int64_t)128 << 20) / (p.Mp > 0 ? p.Mp * 2 : 1) / 512 * 512, all = (V + 511) / 512 * 512;
     p.piece = most < 512 ? 512 : (most < all ? most : all);
-    // where dX has too few tiles for the 256 compute units, its contraction is cut into parts
-    // of at least 16 steps
-    p.splits = 1;
-    const int64_t tiles = p.Mp / HL_TM * ((K + HL_TN - 1) / HL_TN), steps = p.piece / HL_K;
-    while (p.splits < 8 && tiles * p.splits * 2 <= 256 && steps / (p.splits * 2) >= 16) p.splits *= 2;
+    p.pieces = V > 0 ? (V + p.piece - 1) / p.piece : 0;
+    // dW from the kept E, up to 1 GB of it, instead of from the logits again
+    p.keep = dw && p.piece_bytes() * p.pieces <= (size_t)1 << 30;
+    // the tiles whose last round over the compute units ends first
+    auto rounds = [](int64_t tiles) { return (double)((tiles + CUS - 1) / CUS); };
+    const int64_t slices = ((grad && p.piece < V ? p.piece : V) + HL_TN - 1) / HL_TN;
+    p.few = M <= FEW_TOKENS || rounds(slices * p.blocks(M)) * FEW_COST < rounds(slices * (p.Mp / HL_TM));
+    p.width = p.few ? FEW_TN : HL_TN;
+    // where dX has too few tiles for the compute units, its contraction is cut into parts
+    const int64_t columns = (K + HL_TN - 1) / HL_TN, steps = p.piece / HL_K;
+    auto cut = [&](int64_t tiles, int64_t least, int most) {
+        int64_t n = tiles > 0 ? CUS / tiles : 1;
+        n = n < steps / least ? n : steps / least;
+        return (int)(n < 1 ? 1 : n < most ? n : most);
+    };
+    const int64_t big = p.Mp / HL_TM * columns, small = p.blocks(M) * columns;
+    const int big_splits = cut(big, 16, 8), few_splits = cut(small, 4, 64);
+    auto cost = [&](int64_t tiles, int splits) { return rounds(tiles * splits) * (double)((steps + splits - 1) / splits); };
+    p.few_dx = M <= FEW_TOKENS || cost(small, few_splits) * FEW_COST < cost(big, big_splits);
+    p.splits = p.few_dx ? few_splits : big_splits;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t was = at;
@@ -772,15 +1001,17 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     const size_t row = (size_t)p.Mp * 4;
     p.top = take(4);
     p.zy = take(row);
-    p.ref = take(row);
+    p.ref = take(row * (p.keep ? p.pieces + 1 : 1));
     p.total = take(row);
     p.factor = take(row);
     p.ends = take(2 * row);
     p.rows = take(4 * row);
     p.part = take((size_t)p.Mp * p.tiles(grad && p.piece < V ? p.piece : V) * sizeof(float2));
     p.Xp = take((size_t)p.Mp * K * 2);
-    p.E = take(grad ? (size_t)p.Mp * p.piece * 2 : 0);
-    p.sum = take(dx && (p.piece < V || p.splits > 1) ? (size_t)M * K * 4 * p.splits : 0);
+    p.E = take(grad ? p.piece_bytes() * (p.keep ? p.pieces : 1) : 0);
+    p.low = take(p.keep ? p.piece_bytes() / 2 * p.pieces : 0);
+    p.G = p.keep ? take(p.piece_bytes()) : p.E;
+    p.sum = take(dx && (p.piece < V || p.splits > 1 || p.few_dx) ? (size_t)M * K * 4 * p.splits : 0);
     p.bytes = at;
     return p;
 }
@@ -795,12 +1026,22 @@ static void for_pieces(const HeadPlan& p, int64_t V, F&& f) {
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) f(v0, V - v0 < p.piece ? V - v0 : p.piece, v0 + p.piece >= V);
 }
 
+// Tiles of 64 tokens use more LDS than the 64 KB that a kernel has unasked.
+template <typename Args>
+static void launch_few(void (*kernel)(Args), int nt, dim3 grid, hipStream_t s, const Args& a) {
+    const int bytes = FEW_STAGES * few_stage(nt);
+    if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess)
+        hipLaunchKernelGGL(kernel, grid, dim3(256), bytes, s, a);       // (an error is met by the caller's hipGetLastError)
+}
+
 template <HeadMode MODE>
 static void launch_logits(const HeadPlan& p, HeadArgs& a, int64_t rows, hipStream_t s) {
     a.tiles_v = p.tiles(rows);
-    const dim3 few((uint32_t)(a.tiles_v / 4));
-    if (p.few && a.M <= 32) hipLaunchKernelGGL((k_head_few<MODE, 1>), few, dim3(256), FEW_STAGES * few_stage(1), s, a);
-    else if (p.few) hipLaunchKernelGGL((k_head_few<MODE, 2>), few, dim3(256), FEW_STAGES * few_stage(2), s, a);
+    const dim3 few = head_grid(a.tiles_v / 4, p.blocks(a.M));
+    constexpr bool once = MODE == HEAD_STATS;
+    if (p.few && a.M <= 32) launch_few(k_head_few<MODE, 1, once>, 1, few, s, a);
+    else if (p.few && a.M <= 64) launch_few(k_head_few<MODE, 2, once>, 2, few, s, a);
+    else if (p.few) launch_few(k_head_few<MODE, 2, false>, 2, few, s, a);
     else hipLaunchKernelGGL(k_head_logits<MODE>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
 }
 
@@ -810,13 +1051,6 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     const HeadPlan p = head_plan(M, K, V, dX != nullptr, dW != nullptr);
     uint8_t* base = (uint8_t*)ws;
     const dim3 row_grid((uint32_t)(p.Mp / 4));
-    if (p.few) {                          // their LDS is past the 64 KB that a kernel has unasked
-        for (const auto& f : {std::make_pair((const void*)k_head_few<HEAD_STATS, 1>, 1), std::make_pair((const void*)k_head_few<HEAD_STATS, 2>, 2),
-                              std::make_pair((const void*)k_head_few<HEAD_E, 1>, 1), std::make_pair((const void*)k_head_few<HEAD_E, 2>, 2)}) {
-            const hipError_t e = hipFuncSetAttribute(f.first, hipFuncAttributeMaxDynamicSharedMemorySize, FEW_STAGES * few_stage(f.second));
-            if (e != hipSuccess) return e;
-        }
-    }
     HeadArgs a{};
     uint16_t* Xp = (uint16_t*)(base + p.Xp);
     a.X = X;
@@ -835,7 +1069,7 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     a.out = (uint16_t*)(base + p.E);
     a.Mp = p.Mp;
     a.tiles_m = p.Mp / HL_TM;
-    if (!p.few || dW) hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(a.tiles_m * 4)), dim3(256), 0, s, X, M, K, Xp);
+    if (!p.few || (dW && !p.keep)) hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(a.tiles_m * 4)), dim3(256), 0, s, X, M, K, Xp);
     if (!dX && !dW) {
         launch_logits<HEAD_STATS>(p, a, V, s);
         hipLaunchKernelGGL(k_head_rows, dim3((uint32_t)((M + 3) / 4)), dim3(256), 0, s, a.part, a.zy, targets, M, V, ignore,
@@ -859,38 +1093,60 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     d.splits = p.splits;
     hipLaunchKernelGGL(k_head_target, dim3((uint32_t)((M + 3) / 4 + 1)), dim3(256), 0, s, X, W, M, K, V, targets, ignore, a.zy,
                        ref, total, dloss, top);
+    const int64_t piece_values = (int64_t)(p.piece_bytes() / 2);
+    int64_t at = 0;                       // the piece, where each has a place of its own
     for_pieces(p, V, [&](int64_t v0, int64_t rows, bool last) {
         a.v0 = v0;
+        a.out = (uint16_t*)(base + p.E) + at * piece_values;
+        a.low = p.keep ? base + p.low + at * piece_values : nullptr;
         a.out_steps = (rows + HL_TN - 1) / HL_TN * (HL_TN / HL_K);
+        a.ref = ref + at * p.Mp;
         launch_logits<HEAD_E>(p, a, rows, s);
-        const JoinArgs j{a.part, (int)a.tiles_v, p.width, M, p.Mp, targets, ignore, V, a.out, a.out_steps, ref, total, (float*)(base + p.factor),
-                         a.zy, last ? 1 : 0, dloss, loss, (float2*)(base + p.ends), (float4*)(base + p.rows)};
+        const JoinArgs j{a.part, (int)a.tiles_v, p.width, M, p.Mp, targets, ignore, V, a.out, a.out_steps, ref + at * p.Mp, ref + (at + p.keep) * p.Mp, total,
+                         (float*)(base + p.factor), a.zy, last ? 1 : 0, dloss, loss, (float2*)(base + p.ends), (float4*)(base + p.rows)};
         hipLaunchKernelGGL(k_head_join, row_grid, dim3(256), 0, s, j);
+        at += p.keep;
         if (!dX) return;
+        d.A = a.out;
         d.a_steps = a.out_steps;
         d.out_rows = M;
         d.B = W + v0 * K;
         d.P = rows;
         d.steps = (int)((rows + HL_K - 1) / HL_K);
-        d.tiles_r = a.tiles_m;
+        d.tiles_r = p.few_dx ? p.blocks(M) : a.tiles_m;
         d.out = dX;
-        const bool add = v0 > 0, closes = last && p.splits == 1;
-        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, head_grid(d.tiles_r, d.tiles_n, d.splits), dim3(256), 0, s, d); };
-        if (closes) add ? run(k_head_product<OUT_DX, true>) : run(k_head_product<OUT_DX, false>);
-        else add ? run(k_head_product<OUT_SUM, true>) : run(k_head_product<OUT_SUM, false>);
+        d.add = v0 > 0;
+        const dim3 grid = head_grid(d.tiles_r, d.tiles_n, d.splits);
+        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, d); };
+        if (p.few_dx && M <= 32) launch_few(k_head_few_product<1>, 1, grid, s, d);
+        else if (p.few_dx) launch_few(k_head_few_product<2>, 2, grid, s, d);
+        else if (last && p.splits == 1) d.add ? run(k_head_product<OUT_DX, true>) : run(k_head_product<OUT_DX, false>);
+        else d.add ? run(k_head_product<OUT_SUM, true>) : run(k_head_product<OUT_SUM, false>);
     });
-    if (dX && p.splits > 1) hipLaunchKernelGGL(k_head_finish, dim3((uint32_t)M), dim3(256), 0, s, d, dX);
+    if (dX && (p.splits > 1 || p.few_dx))
+        hipLaunchKernelGGL(k_head_finish, dim3((uint32_t)M, (uint32_t)((K + 1023) / 1024)), dim3(256), 0, s, d, dX);
     if (!dW) return hipGetLastError();
     d.splits = 1;
     d.top = top;
+    d.A = (uint16_t*)(base + p.G);
     d.B = X;
     d.P = M;
     d.steps = (int)((M + HL_K - 1) / HL_K);
-    d.a_steps = a.out_steps = p.Mp / HL_K;
+    d.a_steps = p.Mp / HL_K;
+    at = 0;
     for_pieces(p, V, [&](int64_t v0, int64_t rows, bool) {
-        a.v0 = v0;
-        a.tiles_v = (rows + HL_TN - 1) / HL_TN;
-        hipLaunchKernelGGL(k_head_logits<HEAD_GT>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
+        if (p.keep) {
+            const TurnArgs t{(uint16_t*)(base + p.E) + at * piece_values, base + p.low + at * piece_values, (uint16_t*)(base + p.G),
+                             (rows + HL_TN - 1) / HL_TN * (HL_TN / HL_K), d.a_steps, v0, V, ref + (at + 1) * p.Mp, a.rows, top};
+            ++at;
+            hipLaunchKernelGGL(k_head_turn, dim3((uint32_t)((t.steps_v + 3) / 4), (uint32_t)(d.steps * 2)), dim3(256), 0, s, t);
+        } else {
+            a.v0 = v0;
+            a.out = (uint16_t*)(base + p.G);
+            a.out_steps = d.a_steps;
+            a.tiles_v = (rows + HL_TN - 1) / HL_TN;
+            hipLaunchKernelGGL(k_head_logits<HEAD_GT>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
+        }
         d.out_rows = rows;
         d.tiles_r = (rows + HL_TM - 1) / HL_TM;
         d.out = dW + v0 * K;

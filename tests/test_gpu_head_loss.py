@@ -52,6 +52,28 @@ def test_values(M, V, K):
     check(*inputs(M, V, K, seed=M + V))
 
 
+@pytest.mark.parametrize("M,V,K", [(2, 1211, 704), (32, 129, 64), (33, 4097, 128), (63, 2000, 1088), (64, 50001, 64), (66, 128, 2048),
+                                   (128, 1322, 6272), (129, 640, 192), (281, 8191, 256), (513, 1025, 4160), (992, 1524, 576)])
+def test_few_tokens_and_small_grids(M, V, K):
+    check(*inputs(M, V, K, seed=M + V + K))
+
+
+def test_gradient_past_what_is_kept():
+    # more than 1 GB of weights: dW from the logits a second time
+    check(*inputs(4096, 131200, 64, seed=15))
+
+
+def test_growing_logits_in_pieces():
+    # the reference moves within and between pieces whose weights are kept for dW
+    X, W, t, dl = inputs(2048, 70000, 64, seed=16)
+    X[:, 0] = 1.0
+    W[:, 0] = torch.arange(70000, device="cuda").float() / 64
+    t[:1024] = 69990
+    check(X, W, t, dl)
+    W[:, 0] = -W[:, 0].float()
+    check(X, W, t, dl)
+
+
 def test_pieces_of_the_vocabulary():
     # 4096 tokens and 20000 entries: several pieces, a ragged last one
     check(*inputs(4096, 20001, 128, seed=5))
