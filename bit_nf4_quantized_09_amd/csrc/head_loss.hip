@@ -388,8 +388,10 @@ void k_head_logits(HeadArgs a) {
 // flight per compute unit.  Up to 64 tokens its time is that of reading W, past the caches where nothing
 // reads it again (ONCE).  (W straight into registers, 32 rows a load, meets every line four times: 75 us for
 // 33 tokens x 32000 x 4096, 63 here.)
-constexpr int FEW_TOKENS = 64, FEW_TN = 32, FEW_STAGES = 6;
+constexpr int FEW_TOKENS = 64, FEW_TN = 32, FEW_STAGES = 3;
 constexpr int few_stage(int nt) { return 16384 + 4096 * nt; }            // bytes: 128 x 64 or 64 x 128 of W, then X or E
+constexpr int FEW_JOIN = 65536;           // the product's sums of 32 rows, of each wave
+constexpr int few_lds(int nt) { return FEW_STAGES * few_stage(nt) > FEW_JOIN ? FEW_STAGES * few_stage(nt) : FEW_JOIN; }
 
 // Tile of a workgroup, the token blocks of one slice of W on one XCD.
 __device__ __forceinline__ bool few_tile(int wg, int64_t blocks, int64_t slices, int64_t& block, int64_t& slice) {
@@ -402,17 +404,17 @@ __device__ __forceinline__ bool few_tile(int wg, int64_t blocks, int64_t slices,
     return true;
 }
 
-// Waits until only the loads of the four youngest stages of 4 + NT each are out, and meets the other waves.
+// Waits until only the 4 + NT loads of the youngest stage are out, and meets the other waves.
 template <int NT>
 __device__ __forceinline__ void few_landed() {
-    if constexpr (NT == 2) asm volatile("s_waitcnt vmcnt(24) lgkmcnt(0)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
+    if constexpr (NT == 2) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
 template <HeadMode MODE, int NT, bool ONCE>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
+__global__ __launch_bounds__(256, 2)
 void k_head_few(HeadArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -759,7 +761,7 @@ void k_head_product(ProductArgs a) {
 // The same sums in tiles of 32 NT rows x 128 columns: a step's 64 rows of B go through LDS once, each wave takes 16
 // of them for the whole tile, and the four waves' accumulators are added at the end.
 template <int NT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
+__global__ __launch_bounds__(256, 2)
 void k_head_few_product(ProductArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -828,30 +830,27 @@ void k_head_few_product(ProductArgs a) {
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    // accumulator (i, j, reg): row 32 i + rl, column 32 j + 8 (reg / 4) + 4 h + reg % 4; wave w finishes columns 32 w ..
-    auto cell = [&](int from, int i, int j, int r4) {
-        return reinterpret_cast<f32x4*>(lds + ((((from * NT + i) * 4 + j) * 4 + r4) << 10) + lane * 16);
-    };
+    // accumulator (i, j, reg): row 32 i + rl, column 32 j + 8 (reg / 4) + 4 h + reg % 4; wave w finishes columns
+    // 32 w .., 32 rows at a time
+    auto cell = [&](int from, int j, int r4) { return reinterpret_cast<f32x4*>(lds + (((from * 4 + j) * 4 + r4) << 10) + lane * 16); };
+    float* sums = a.sum + split * a.out_rows * a.N;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) {
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int r4 = 0; r4 < 4; ++r4)
-                *cell(wave, i, j, r4) = f32x4{acc[i][j][4 * r4], acc[i][j][4 * r4 + 1], acc[i][j][4 * r4 + 2], acc[i][j][4 * r4 + 3]};
-    __syncthreads();
-    float* sums = a.sum + split * a.out_rows * a.N;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
+                *cell(wave, j, r4) = f32x4{acc[i][j][4 * r4], acc[i][j][4 * r4 + 1], acc[i][j][4 * r4 + 2], acc[i][j][4 * r4 + 3]};
+        __syncthreads();
         const int64_t r = r0 + 32 * i + rl;
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
             const int64_t n = n0 + 32 * wave + 8 * r4 + 4 * h;
             if (r >= a.out_rows || n >= a.N) continue;
-            f32x4 y = *cell(0, i, wave, r4);
+            f32x4 y = *cell(0, wave, r4);
 #pragma unroll
-            for (int from = 1; from < 4; ++from) y += *cell(from, i, wave, r4);
+            for (int from = 1; from < 4; ++from) y += *cell(from, wave, r4);
             f32x4* to = reinterpret_cast<f32x4*>(sums + r * a.N + n);
             if (a.add) y += *to * a.factor[r];
             *to = y;
@@ -960,9 +959,14 @@ struct HeadPlan {
     size_t piece_bytes() const { return (size_t)Mp * piece * 2; }
 };
 
-// The time of a step of a 64-token tile over that of a 512-token tile, which a compute unit holds one of.
-constexpr double FEW_COST = 0.25;
 constexpr int64_t CUS = 256;
+// The time of tiles, in units of a 512-token tile's steps: one of them fills a compute unit.  A 64-token tile alone on a
+// compute unit takes 0.42 us a step, two 0.64 to 0.76, and a 512-token tile 1.65.
+static double big_rounds(int64_t tiles) { return (double)((tiles + CUS - 1) / CUS); }
+static double few_rounds(int64_t tiles) {
+    const int64_t rest = tiles % (2 * CUS);
+    return (double)(tiles / (2 * CUS)) * 0.46 + (rest == 0 ? 0.0 : rest <= CUS ? 0.25 : 0.46);
+}
 
 static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     HeadPlan p{};
@@ -976,21 +980,20 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     // dW from the kept E, up to 1 GB of it, instead of from the logits again
     p.keep = dw && p.piece_bytes() * p.pieces <= (size_t)1 << 30;
     // the tiles whose last round over the compute units ends first
-    auto rounds = [](int64_t tiles) { return (double)((tiles + CUS - 1) / CUS); };
     const int64_t slices = ((grad && p.piece < V ? p.piece : V) + HL_TN - 1) / HL_TN;
-    p.few = M <= FEW_TOKENS || rounds(slices * p.blocks(M)) * FEW_COST < rounds(slices * (p.Mp / HL_TM));
+    p.few = M <= FEW_TOKENS || few_rounds(slices * p.blocks(M)) < big_rounds(slices * (p.Mp / HL_TM));
     p.width = p.few ? FEW_TN : HL_TN;
     // where dX has too few tiles for the compute units, its contraction is cut into parts
     const int64_t columns = (K + HL_TN - 1) / HL_TN, steps = p.piece / HL_K;
-    auto cut = [&](int64_t tiles, int64_t least, int most) {
-        int64_t n = tiles > 0 ? CUS / tiles : 1;
+    auto cut = [&](int64_t tiles, int64_t fill, int64_t least, int most) {
+        int64_t n = tiles > 0 ? fill / tiles : 1;
         n = n < steps / least ? n : steps / least;
         return (int)(n < 1 ? 1 : n < most ? n : most);
     };
     const int64_t big = p.Mp / HL_TM * columns, small = p.blocks(M) * columns;
-    const int big_splits = cut(big, 16, 8), few_splits = cut(small, 4, 64);
-    auto cost = [&](int64_t tiles, int splits) { return rounds(tiles * splits) * (double)((steps + splits - 1) / splits); };
-    p.few_dx = M <= FEW_TOKENS || cost(small, few_splits) * FEW_COST < cost(big, big_splits);
+    const int big_splits = cut(big, CUS, 16, 8), few_splits = cut(small, 2 * CUS, 4, 64);
+    auto per = [&](int splits) { return (double)((steps + splits - 1) / splits); };
+    p.few_dx = M <= FEW_TOKENS || few_rounds(small * few_splits) * per(few_splits) < big_rounds(big * big_splits) * per(big_splits);
     p.splits = p.few_dx ? few_splits : big_splits;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -1029,7 +1032,7 @@ static void for_pieces(const HeadPlan& p, int64_t V, F&& f) {
 // Tiles of 64 tokens use more LDS than the 64 KB that a kernel has unasked.
 template <typename Args>
 static void launch_few(void (*kernel)(Args), int nt, dim3 grid, hipStream_t s, const Args& a) {
-    const int bytes = FEW_STAGES * few_stage(nt);
+    const int bytes = few_lds(nt);
     if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess)
         hipLaunchKernelGGL(kernel, grid, dim3(256), bytes, s, a);       // (an error is met by the caller's hipGetLastError)
 }
