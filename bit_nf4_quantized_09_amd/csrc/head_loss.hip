@@ -38,8 +38,8 @@
 
 namespace nf4 {
 
-constexpr int HL_TM = FUSED_TM;           // output tile: 512 rows
-constexpr int HL_TN = FUSED_TN;           // x 128 columns
+constexpr int HL_TM = FUSED_TM;           // rows of a block of the packed operand: 512
+constexpr int HL_TN = FUSED_TN;           // columns of an output tile: 128
 constexpr int HL_K = 64;                  // contraction step
 constexpr int HL_STAGE = HL_TN * HL_K * 2;   // an LDS stage: 16 KB
 constexpr float LOG2E = 1.4426950408889634f;
@@ -73,13 +73,25 @@ __device__ __forceinline__ bool hl_tile(int wg, int64_t tiles_m, int64_t tiles_n
 }
 
 // Bytes of a block in use when `rows` rows of the tile are: 4 KB per 32 rows.
+template <int I>
 __device__ __forceinline__ int hl_block_bytes(int64_t rows) {
-    return __builtin_amdgcn_readfirstlane(rows < HL_TM ? (int)((rows + 31) / 32) * 4096 : A_BLOCK_BYTES);
+    return __builtin_amdgcn_readfirstlane(rows < 128 * I ? (int)((rows + 31) / 32) * 4096 : 16384 * I);
+}
+// A tile's part of the first block of its row tile of 512, of `steps` blocks.
+__device__ __forceinline__ const uint16_t* hl_blocks(const uint16_t* p, int64_t row, int64_t steps) {
+    return p + (row / HL_TM) * steps * (int64_t)(A_BLOCK_BYTES / 2) + (row % HL_TM) * 64;
 }
 
+template <int I>
 struct HlFrags {
-    uint4 f[4][4];            // [row tile i][substep s]
+    uint4 f[I][4];            // [row tile i][substep s]
 };
+
+template <int I>
+__device__ __forceinline__ void hl_landed() {
+    if constexpr (I == 4) asm volatile("s_waitcnt vmcnt(36) lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
+}
 
 // The main loop of both products: acc[i][j] += (rows 32 i.. of the wave's 128) x (columns 32 j..),
 // contraction steps first .. last - 1 (at least one).  SWAP: accumulator columns are the 512-row
@@ -93,8 +105,8 @@ struct HlFrags {
 // before the last region, whose matrix instructions hide the next step's first LDS reads.  A stage
 // is complete at the barrier before its first read: 36 is below the number of loads that each wave has
 // started since it started that stage's (at least 46).
-template <bool SWAP, bool TRANS, typename Dma>
-__device__ __forceinline__ void hl_loop(f32x16 (&acc)[4][4], const uint8_t* lds, const uint16_t* blocks, int block_bytes, int first, int last,
+template <int I, bool SWAP, bool TRANS, typename Dma>
+__device__ __forceinline__ void hl_loop(f32x16 (&acc)[I][4], const uint8_t* lds, const uint16_t* blocks, int block_bytes, int first, int last,
                                         int wave, int lane, Dma&& dma) {
     const int h = lane >> 5, rl = lane & 31;
     int off[4];               // LDS offset of this lane's column fragments; + 4096 j (direct), + 4096 s (transposed)
@@ -117,20 +129,20 @@ __device__ __forceinline__ void hl_loop(f32x16 (&acc)[4][4], const uint8_t* lds,
             return *reinterpret_cast<const bf16x8*>(stage + off[s ^ (2 * (j & 1))] + 4096 * j);
         }
     };
-    uint32_t a_voff[4];
+    uint32_t a_voff[I];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a_voff[i] = (uint32_t)(wave * 16384 + 4096 * i + lane * 16);
+    for (int i = 0; i < I; ++i) a_voff[i] = (uint32_t)((wave * I + i) * 4096 + lane * 16);
     // (past the last step the range is empty and the fragments are zero: an odd number of steps ends with an idle one)
     auto a_rsrc = [&](int step) {
         return make_rsrc(blocks + (int64_t)(step < last ? step : first) * (A_BLOCK_BYTES / 2), step < last ? block_bytes : 0);
     };
     auto clamp = [&](int step) { return step < last ? step : last - 1; };
-    auto load_all = [&](HlFrags& F, int step) {
+    auto load_all = [&](HlFrags<I>& F, int step) {
         const __amdgpu_buffer_rsrc_t rs = a_rsrc(step);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) F.f[i][s] = buf_load16(rs, a_voff[i] + 1024 * s, 0);
+            for (int i = 0; i < I; ++i) F.f[i][s] = buf_load16(rs, a_voff[i] + 1024 * s, 0);
     };
     auto mfma = [&](int i, int j, uint4 af, bf16x8 bf) {
         const bf16x8 a = __builtin_bit_cast(bf16x8, af);
@@ -138,8 +150,8 @@ __device__ __forceinline__ void hl_loop(f32x16 (&acc)[4][4], const uint8_t* lds,
                          : __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, bf, acc[i][j], 0, 0, 0);
     };
     bf16x8 fb[2][4];
-    HlFrags fa0, fa1;
-    auto step_body = [&](int it, HlFrags& cur) {
+    HlFrags<I> fa0, fa1;
+    auto step_body = [&](int it, HlFrags<I>& cur) {
         const int st = (it - first) & 3;
         const uint8_t* now = lds + st * HL_STAGE;
         const uint8_t* next = lds + ((st + 1) & 3) * HL_STAGE;
@@ -149,7 +161,7 @@ __device__ __forceinline__ void hl_loop(f32x16 (&acc)[4][4], const uint8_t* lds,
         for (int rg = 0; rg < 8; ++rg) {
             const int s = rg >> 1, half = rg & 1;
             if (rg == 7) {
-                asm volatile("s_waitcnt vmcnt(36) lgkmcnt(0)" ::: "memory");
+                hl_landed<I>();
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
 #pragma unroll
@@ -160,16 +172,16 @@ __device__ __forceinline__ void hl_loop(f32x16 (&acc)[4][4], const uint8_t* lds,
             }
             if (rg < 4) dma((st + 3) & 3, ahead, rg);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) mfma(2 * half + (t >> 2), t & 3, cur.f[2 * half + (t >> 2)][s], fb[s & 1][t & 3]);
+            for (int t = 0; t < 2 * I; ++t) mfma(I / 2 * half + (t >> 2), t & 3, cur.f[I / 2 * half + (t >> 2)][s], fb[s & 1][t & 3]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) cur.f[2 * half + q][s] = buf_load16(rs, a_voff[2 * half + q] + 1024 * s, 0);
+            for (int q = 0; q < I / 2; ++q) cur.f[I / 2 * half + q][s] = buf_load16(rs, a_voff[I / 2 * half + q] + 1024 * s, 0);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
+            for (int t = 0; t < 2 * I; ++t) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // matrix
-                __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);                       // VALU
+                __builtin_amdgcn_sched_group_barrier(0x002, 8 / I, 0);                   // VALU
                 if ((rg == 7 || (half == 0 && s < 3)) && t < 4)
                     __builtin_amdgcn_sched_group_barrier(0x100, TRANS ? 2 : 1, 0);      // LDS reads
-                if (t == 2 || t == 5) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // loads
+                if (t == 2 || (I == 4 && t == 5)) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // loads
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -182,7 +194,7 @@ __device__ __forceinline__ void hl_loop(f32x16 (&acc)[4][4], const uint8_t* lds,
     load_all(fa0, first);
     load_all(fa1, first + 1);
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(36)" ::: "memory");
+    hl_landed<I>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -315,8 +327,8 @@ __device__ __forceinline__ void head_column(const HeadArgs& a, f32x16* acc, int6
 }
 
 // Logits of a tile of 512 tokens x 128 vocabulary rows.
-template <HeadMode MODE>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <HeadMode MODE, int I>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(I == 4 ? 1 : 2, I == 4 ? 1 : 2)))
 void k_head_logits(HeadArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[4 * HL_STAGE];
     constexpr bool SWAP = MODE != HEAD_GT;
@@ -324,7 +336,7 @@ void k_head_logits(HeadArgs a) {
     const int h = lane >> 5, rl = lane & 31;
     int64_t tv, tm;
     if (!hl_tile(blockIdx.x, a.tiles_m, a.tiles_v, tm, tv)) return;
-    const int64_t v0 = a.v0 + tv * HL_TN, m0 = tm * HL_TM;
+    const int64_t v0 = a.v0 + tv * HL_TN, m0 = tm * 128 * I;
     const int steps = __builtin_amdgcn_readfirstlane((int)(a.K / HL_K));
     // a wave fills rows 32 wave .. of a stage, 8 rows a load; rows past V repeat the last (dropped later)
     uint32_t wof[4];
@@ -336,12 +348,12 @@ void k_head_logits(HeadArgs a) {
     }
     const dma_rsrc rw = make_dma_rsrc(a.W + v0 * a.K, (a.V - v0) * a.K * 2);
     const uint32_t mine = lds_address(lds) + wave * 4096;
-    f32x16 acc[4][4];
+    f32x16 acc[I][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < I; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-    hl_loop<SWAP, false>(acc, lds, a.Xp + tm * steps * (int64_t)(A_BLOCK_BYTES / 2), hl_block_bytes(a.M - m0), 0, steps, wave, lane,
+    hl_loop<I, SWAP, false>(acc, lds, hl_blocks(a.Xp, m0, steps), hl_block_bytes<I>(a.M - m0), 0, steps, wave, lane,
                          [&](int stage, int step, int q) {
                              load_to_lds(rw, mine + stage * HL_STAGE + q * 1024, wof[q], (uint32_t)step * 128);
                          });
@@ -350,8 +362,8 @@ void k_head_logits(HeadArgs a) {
         // G^T's block of 512 vocabulary rows and 64 tokens: this tile is wave slice tv % 4 of it.
         const float inv = 1.0f / head_scale(a.top);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t mi = m0 + wave * 128 + i * 32;
+        for (int i = 0; i < I; ++i) {
+            const int64_t mi = m0 + (wave * I + i) * 32;
             uint8_t* block = reinterpret_cast<uint8_t*>(a.out) + ((tv >> 2) * a.out_steps + (mi >> 6)) * A_BLOCK_BYTES +
                              (tv & 3) * 16384 + rl * 16 + 8 * h;
 #pragma unroll
@@ -378,7 +390,7 @@ void k_head_logits(HeadArgs a) {
     }
     // accumulator (i, j, reg): token 32 i + rl of the wave's 128, vocabulary row 32 j + 8 (reg / 4) + 4 h + reg % 4
 #pragma unroll
-    for (int i = 0; i < 4; ++i) head_column<MODE, 4>(a, acc[i], m0 + wave * 128 + i * 32, v0, tv, h, rl);
+    for (int i = 0; i < I; ++i) head_column<MODE, 4>(a, acc[i], m0 + (wave * I + i) * 32, v0, tv, h, rl);
 }
 
 // Tiles of 64 tokens, for few tokens and for grids that 512-token tiles leave mostly empty.
@@ -667,8 +679,8 @@ __device__ __forceinline__ uint2 head_dx4(f32x4 y, float2 row, uint2 u) {
 
 // C[r][n] = sum_p A[r][p] B[p][n], tiles of 512 rows x 128 columns; ADD: on top of what `sum` holds.
 enum ProductOut { OUT_SUM, OUT_DX, OUT_DW };
-template <ProductOut OUT, bool ADD>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <ProductOut OUT, bool ADD, int I>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(I == 4 ? 1 : 2, I == 4 ? 1 : 2)))
 void k_head_product(ProductArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[4 * HL_STAGE];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -679,7 +691,7 @@ void k_head_product(ProductArgs a) {
     const int per = (a.steps + a.splits - 1) / a.splits;
     const int first = __builtin_amdgcn_readfirstlane(split * per);
     const int last = __builtin_amdgcn_readfirstlane(first + per < a.steps ? first + per : a.steps);
-    const int64_t r0 = tr * HL_TM, n0 = tn * HL_TN;
+    const int64_t r0 = tr * 128 * I, n0 = tn * HL_TN;
     const uint32_t mine = lds_address(lds) + wave * 4096;
     // a wave fills rows 16 wave .. of a stage, 4 rows a load; columns past N: any, dropped later
     uint32_t bcol = 0;
@@ -688,13 +700,13 @@ void k_head_product(ProductArgs a) {
         const int chunk = (((q >> 1) ^ (row << 1)) << 1) | (q & 1);
         bcol = (uint32_t)(n0 + chunk * 8 < a.N ? chunk * 16 : 0);
     }
-    f32x16 acc[4][4];
+    f32x16 acc[I][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < I; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
     if (first < last)
-        hl_loop<true, true>(acc, lds, a.A + tr * a.a_steps * (int64_t)(A_BLOCK_BYTES / 2), hl_block_bytes(a.out_rows - r0), first, last,
+        hl_loop<I, true, true>(acc, lds, hl_blocks(a.A, r0, a.a_steps), hl_block_bytes<I>(a.out_rows - r0), first, last,
                             wave, lane,
                             [&](int stage, int step, int q) {
                                 const int64_t p0 = (int64_t)step * HL_K;
@@ -713,8 +725,8 @@ void k_head_product(ProductArgs a) {
     const int chunk = lane & 31;
     const int64_t n = n0 + 4 * chunk;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t ri = r0 + wave * 128 + i * 32;
+    for (int i = 0; i < I; ++i) {
+        const int64_t ri = r0 + (wave * I + i) * 32;
         if (ri >= a.out_rows) break;
         // what the rows are joined with is requested before the turn through LDS
         f32x4 old[16];
@@ -946,13 +958,14 @@ void k_head_turn(TurnArgs a) {
 struct HeadPlan {
     int64_t Mp;               // tokens up to whole tiles
     bool few;                 // logits by k_head_few
-    int width;                // vocabulary rows of a tile of the logits
+    int width;                // vocabulary rows of a tile of the logits,
+    int64_t rows;             // and its tokens (not few: 256 or 512)
     int64_t piece;            // vocabulary rows of a piece (a multiple of 512: whole row tiles of G^T)
     int64_t pieces;
     bool keep;                // every piece's E is kept until dW
     bool few_dx;              // dX by k_head_few_product
     int splits;               // parts of dX's contraction
-    size_t top, zy, ref, total, factor, ends, rows, part, Xp, E, low, G, sum, bytes;
+    size_t top, zy, ref, total, factor, ends, of_rows, part, Xp, E, low, G, sum, bytes;
     int64_t blocks(int64_t M) const { return M <= 32 ? 1 : (M + 63) / 64; }                   // of 64 tokens (one of 32)
     // tiles of the logits (few: four to a workgroup)
     int64_t tiles(int64_t vocabulary) const { return (vocabulary + 127) / 128 * (few ? 4 : 1); }
@@ -960,13 +973,16 @@ struct HeadPlan {
 };
 
 constexpr int64_t CUS = 256;
-// The time of tiles, in units of a 512-token tile's steps: one of them fills a compute unit.  A 64-token tile alone on a
-// compute unit takes 0.42 us a step, two 0.64 to 0.76, and a 512-token tile 1.65.
-static double big_rounds(int64_t tiles) { return (double)((tiles + CUS - 1) / CUS); }
-static double few_rounds(int64_t tiles) {
+// The time of a product in tiles of 512, 256 and 64 rows, for a step of 64: in units of a 512-row tile's 1.65 us, of
+// which a compute unit holds one.  It holds two of the smaller; two of 256 rows take as long as one of 512 (alone:
+// 0.9 us), two of 64 rows 0.64 to 0.76 us (alone: 0.42 us).
+static double rounds_512(int64_t tiles) { return (double)((tiles + CUS - 1) / CUS); }
+static double rounds_pairs(int64_t tiles, double two, double one) {
     const int64_t rest = tiles % (2 * CUS);
-    return (double)(tiles / (2 * CUS)) * 0.46 + (rest == 0 ? 0.0 : rest <= CUS ? 0.25 : 0.46);
+    return (double)(tiles / (2 * CUS)) * two + (rest == 0 ? 0.0 : rest <= CUS ? one : two);
 }
+static double rounds_256(int64_t tiles) { return rounds_pairs(tiles, 1.0, 0.55); }
+static double rounds_64(int64_t tiles) { return rounds_pairs(tiles, 0.46, 0.25); }
 
 static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     HeadPlan p{};
@@ -981,7 +997,11 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     p.keep = dw && p.piece_bytes() * p.pieces <= (size_t)1 << 30;
     // the tiles whose last round over the compute units ends first
     const int64_t slices = ((grad && p.piece < V ? p.piece : V) + HL_TN - 1) / HL_TN;
-    p.few = M <= FEW_TOKENS || few_rounds(slices * p.blocks(M)) < big_rounds(slices * (p.Mp / HL_TM));
+    const double all_256 = rounds_256(slices * ((M + 255) / 256));
+    p.few = M <= FEW_TOKENS || rounds_64(slices * p.blocks(M)) < all_256;
+    // over many steps 512-row tiles fetch less for their products and have little to hide at the ends (4096 x 16384 x
+    // 8192: 829 and 859 us; 4096 x 32000 x 4096, losses alone: 866 and 818)
+    p.rows = K >= 96 * HL_K && rounds_512(slices * (p.Mp / HL_TM)) <= all_256 ? 512 : 256;
     p.width = p.few ? FEW_TN : HL_TN;
     // where dX has too few tiles for the compute units, its contraction is cut into parts
     const int64_t columns = (K + HL_TN - 1) / HL_TN, steps = p.piece / HL_K;
@@ -993,7 +1013,7 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     const int64_t big = p.Mp / HL_TM * columns, small = p.blocks(M) * columns;
     const int big_splits = cut(big, CUS, 16, 8), few_splits = cut(small, 2 * CUS, 4, 64);
     auto per = [&](int splits) { return (double)((steps + splits - 1) / splits); };
-    p.few_dx = M <= FEW_TOKENS || few_rounds(small * few_splits) * per(few_splits) < big_rounds(big * big_splits) * per(big_splits);
+    p.few_dx = M <= FEW_TOKENS || rounds_64(small * few_splits) * per(few_splits) < rounds_512(big * big_splits) * per(big_splits);
     p.splits = p.few_dx ? few_splits : big_splits;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -1008,7 +1028,7 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     p.total = take(row);
     p.factor = take(row);
     p.ends = take(2 * row);
-    p.rows = take(4 * row);
+    p.of_rows = take(4 * row);
     p.part = take((size_t)p.Mp * p.tiles(grad && p.piece < V ? p.piece : V) * sizeof(float2));
     p.Xp = take((size_t)p.Mp * K * 2);
     p.E = take(grad ? p.piece_bytes() * (p.keep ? p.pieces : 1) : 0);
@@ -1038,6 +1058,14 @@ static void launch_few(void (*kernel)(Args), int nt, dim3 grid, hipStream_t s, c
 }
 
 template <HeadMode MODE>
+static void launch_tiles(int64_t rows, HeadArgs& a, hipStream_t s) {
+    a.tiles_m = (a.M + rows - 1) / rows;
+    const dim3 grid = head_grid(a.tiles_v, a.tiles_m);
+    if (rows == 512) hipLaunchKernelGGL((k_head_logits<MODE, 4>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_head_logits<MODE, 2>), grid, dim3(256), 0, s, a);
+}
+
+template <HeadMode MODE>
 static void launch_logits(const HeadPlan& p, HeadArgs& a, int64_t rows, hipStream_t s) {
     a.tiles_v = p.tiles(rows);
     const dim3 few = head_grid(a.tiles_v / 4, p.blocks(a.M));
@@ -1045,7 +1073,7 @@ static void launch_logits(const HeadPlan& p, HeadArgs& a, int64_t rows, hipStrea
     if (p.few && a.M <= 32) launch_few(k_head_few<MODE, 1, once>, 1, few, s, a);
     else if (p.few && a.M <= 64) launch_few(k_head_few<MODE, 2, once>, 2, few, s, a);
     else if (p.few) launch_few(k_head_few<MODE, 2, false>, 2, few, s, a);
-    else hipLaunchKernelGGL(k_head_logits<MODE>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
+    else launch_tiles<MODE>(p.rows, a, s);
 }
 
 hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint16_t* W, int64_t V,
@@ -1067,12 +1095,11 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     a.part = (float2*)(base + p.part);
     a.zy = (float*)(base + p.zy);
     a.ref = (float*)(base + p.ref);
-    a.rows = (float4*)(base + p.rows);
+    a.rows = (float4*)(base + p.of_rows);
     a.top = (uint32_t*)(base + p.top);
     a.out = (uint16_t*)(base + p.E);
     a.Mp = p.Mp;
-    a.tiles_m = p.Mp / HL_TM;
-    if (!p.few || (dW && !p.keep)) hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(a.tiles_m * 4)), dim3(256), 0, s, X, M, K, Xp);
+    if (!p.few || (dW && !p.keep)) hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(p.Mp / HL_TM * 4)), dim3(256), 0, s, X, M, K, Xp);
     if (!dX && !dW) {
         launch_logits<HEAD_STATS>(p, a, V, s);
         hipLaunchKernelGGL(k_head_rows, dim3((uint32_t)((M + 3) / 4)), dim3(256), 0, s, a.part, a.zy, targets, M, V, ignore,
@@ -1106,7 +1133,7 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
         a.ref = ref + at * p.Mp;
         launch_logits<HEAD_E>(p, a, rows, s);
         const JoinArgs j{a.part, (int)a.tiles_v, p.width, M, p.Mp, targets, ignore, V, a.out, a.out_steps, ref + at * p.Mp, ref + (at + p.keep) * p.Mp, total,
-                         (float*)(base + p.factor), a.zy, last ? 1 : 0, dloss, loss, (float2*)(base + p.ends), (float4*)(base + p.rows)};
+                         (float*)(base + p.factor), a.zy, last ? 1 : 0, dloss, loss, (float2*)(base + p.ends), (float4*)(base + p.of_rows)};
         hipLaunchKernelGGL(k_head_join, row_grid, dim3(256), 0, s, j);
         at += p.keep;
         if (!dX) return;
@@ -1116,15 +1143,15 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
         d.B = W + v0 * K;
         d.P = rows;
         d.steps = (int)((rows + HL_K - 1) / HL_K);
-        d.tiles_r = p.few_dx ? p.blocks(M) : a.tiles_m;
+        d.tiles_r = p.few_dx ? p.blocks(M) : p.Mp / HL_TM;
         d.out = dX;
         d.add = v0 > 0;
         const dim3 grid = head_grid(d.tiles_r, d.tiles_n, d.splits);
         auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, d); };
         if (p.few_dx && M <= 32) launch_few(k_head_few_product<1>, 1, grid, s, d);
         else if (p.few_dx) launch_few(k_head_few_product<2>, 2, grid, s, d);
-        else if (last && p.splits == 1) d.add ? run(k_head_product<OUT_DX, true>) : run(k_head_product<OUT_DX, false>);
-        else d.add ? run(k_head_product<OUT_SUM, true>) : run(k_head_product<OUT_SUM, false>);
+        else if (last && p.splits == 1) d.add ? run(k_head_product<OUT_DX, true, 4>) : run(k_head_product<OUT_DX, false, 4>);
+        else d.add ? run(k_head_product<OUT_SUM, true, 4>) : run(k_head_product<OUT_SUM, false, 4>);
     });
     if (dX && (p.splits > 1 || p.few_dx))
         hipLaunchKernelGGL(k_head_finish, dim3((uint32_t)M, (uint32_t)((K + 1023) / 1024)), dim3(256), 0, s, d, dX);
@@ -1148,12 +1175,17 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
             a.out = (uint16_t*)(base + p.G);
             a.out_steps = d.a_steps;
             a.tiles_v = (rows + HL_TN - 1) / HL_TN;
-            hipLaunchKernelGGL(k_head_logits<HEAD_GT>, head_grid(a.tiles_v, a.tiles_m), dim3(256), 0, s, a);
+            launch_tiles<HEAD_GT>(p.rows, a, s);
         }
         d.out_rows = rows;
-        d.tiles_r = (rows + HL_TM - 1) / HL_TM;
+        // short contractions are mostly ends, which two smaller tiles on a compute unit hide for each other (281 x
+        // 37263 x 5504: 354 and 238 us; 4096 x 32000 x 8192: 1790 and 1840)
+        const int64_t tile = d.steps >= 64 ? 512 : 256;
+        d.tiles_r = (rows + tile - 1) / tile;
         d.out = dW + v0 * K;
-        hipLaunchKernelGGL((k_head_product<OUT_DW, false>), head_grid(d.tiles_r, d.tiles_n), dim3(256), 0, s, d);
+        const dim3 grid = head_grid(d.tiles_r, d.tiles_n);
+        if (tile == 512) hipLaunchKernelGGL((k_head_product<OUT_DW, false, 4>), grid, dim3(256), 0, s, d);
+        else hipLaunchKernelGGL((k_head_product<OUT_DW, false, 2>), grid, dim3(256), 0, s, d);
     });
     return hipGetLastError();
 }
