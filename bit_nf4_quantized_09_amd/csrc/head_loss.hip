@@ -488,6 +488,92 @@ void k_head_few(HeadArgs a) {
     for (int i = 0; i < NT; ++i) head_column<MODE, 1>(a, &acc[i], m0 + 32 * i, b0 + 32 * wave, slice * 4 + wave, h, rl);
 }
 
+// The same for grids that leave most compute units empty: a workgroup takes 32 vocabulary rows and its waves a quarter
+// of the contraction each (steps wave, wave + 4, ..), every wave with stages of its own, joined at the end.
+constexpr int SPLIT_STAGES = 3;
+constexpr int split_stage(int nt) { return 4096 + 4096 * nt; }           // bytes of a wave's: 32 rows of W, then X
+constexpr int split_lds(int nt) { return SPLIT_STAGES * 4 * split_stage(nt); }
+template <HeadMode MODE, int NT>
+__global__ __launch_bounds__(256)
+void k_head_split(HeadArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5, rl = lane & 31;
+    int64_t block, tile;
+    if (!few_tile(blockIdx.x, (a.M + 32 * NT - 1) / (32 * NT), a.tiles_v, block, tile)) return;
+    const int64_t b0 = a.v0 + tile / 4 * 128, m0 = block * 32 * NT;      // (the last slice of 128 has rows, its last tiles may have none)
+    const int steps = __builtin_amdgcn_readfirstlane((int)(a.K / HL_K));
+    uint32_t wof[4], xof[4 * NT];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int row = (int)(tile & 3) * 32 + q * 8 + (lane >> 3);
+        const int64_t rv = b0 + row < a.V ? row : a.V - 1 - b0;
+        wof[q] = (uint32_t)(rv * a.K * 2) + (((lane & 7) ^ hl_swizzle(row & 31)) << 4);
+    }
+#pragma unroll
+    for (int q = 0; q < 4 * NT; ++q) {
+        const int row = q * 8 + (lane >> 3);
+        xof[q] = (uint32_t)((m0 + row < a.M ? row : a.M - 1 - m0) * a.K * 2) + (((lane & 7) ^ hl_swizzle(row)) << 4);
+    }
+    const dma_rsrc rw = make_dma_rsrc(a.W + b0 * a.K, (a.V - b0) * a.K * 2), rx = make_dma_rsrc(a.X + m0 * a.K, (a.M - m0) * a.K * 2);
+    const uint8_t* mine = lds + wave * SPLIT_STAGES * split_stage(NT);
+    const uint32_t base = lds_address(mine);
+    auto fill = [&](int stage, int step) {
+        const int at = step < steps ? step : steps - 1;
+        const uint32_t to = base + stage * split_stage(NT);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_to_lds(rw, to + q * 1024, wof[q], (uint32_t)at * 128);
+#pragma unroll
+        for (int q = 0; q < 4 * NT; ++q) load_to_lds(rx, to + 4096 + q * 1024, xof[q], (uint32_t)at * 128);
+    };
+    f32x16 acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = f32x16{};
+    int off[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) off[s] = rl * 128 + (((2 * s + h) ^ hl_swizzle(rl)) << 4);
+    fill(0, wave);
+    fill(1, wave + 4);
+    int stage = 0, free = 2;
+    for (int it = wave; it < steps; it += 4) {
+        // this stage has landed once only the next one's loads are out
+        if constexpr (NT == 2) asm volatile("s_waitcnt vmcnt(12) lgkmcnt(0)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+        fill(free, it + 8);
+        const uint8_t* sw = mine + stage * split_stage(NT);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bf16x8 w = *reinterpret_cast<const bf16x8*>(sw + off[s]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const bf16x8 x = *reinterpret_cast<const bf16x8*>(sw + 4096 + 4096 * i + off[s ^ (2 * (i & 1))]);
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, acc[i], 0, 0, 0);
+            }
+        }
+        free = stage;
+        stage = stage + 1 < SPLIT_STAGES ? stage + 1 : 0;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    auto cell = [&](int from, int i, int r4) { return reinterpret_cast<f32x4*>(lds + (((from * NT + i) * 4 + r4) << 10) + lane * 16); };
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) *cell(wave, i, r4) = f32x4{acc[i][4 * r4], acc[i][4 * r4 + 1], acc[i][4 * r4 + 2], acc[i][4 * r4 + 3]};
+    __syncthreads();
+    if (wave >= NT) return;
+    f32x16 sum;
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+        f32x4 y = *cell(0, wave, r4);
+#pragma unroll
+        for (int from = 1; from < 4; ++from) y += *cell(from, wave, r4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[4 * r4 + r] = y[r];
+    }
+    head_column<MODE, 1>(a, &sum, m0 + 32 * wave, a.v0 + tile * 32, tile, h, rl);
+}
+
 // A row's loss from its target's logit and the others' log-sum (both base 2): the loss, lse
 // (base 2) and 1 - p of the target.
 struct RowLoss {
@@ -957,7 +1043,8 @@ void k_head_turn(TurnArgs a) {
 // Pieces of the vocabulary and the workspace's layout.
 struct HeadPlan {
     int64_t Mp;               // tokens up to whole tiles
-    bool few;                 // logits by k_head_few
+    bool few;                 // logits by k_head_few, or
+    bool split;               // by k_head_split
     int width;                // vocabulary rows of a tile of the logits,
     int64_t rows;             // and its tokens (not few: 256 or 512)
     int64_t piece;            // vocabulary rows of a piece (a multiple of 512: whole row tiles of G^T)
@@ -999,6 +1086,10 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     const int64_t slices = ((grad && p.piece < V ? p.piece : V) + HL_TN - 1) / HL_TN;
     const double all_256 = rounds_256(slices * ((M + 255) / 256));
     p.few = M <= FEW_TOKENS || rounds_64(slices * p.blocks(M)) < all_256;
+    // a quarter of a tile for each wave's contraction: where four times the tiles still fit the compute units once, or,
+    // of a long contraction, twice (33 tokens x 8000 x 2048: 13.5 and 23.1 us; x 16000 x 6144: 41 and 64; x 16000 x 576:
+    // 16.7 and 15.5)
+    p.split = p.few && slices * p.blocks(M) * 4 <= (K >= 4096 ? 2 * CUS : CUS);
     // over many steps 512-row tiles fetch less for their products and have little to hide at the ends (4096 x 16384 x
     // 8192: 829 and 859 us; 4096 x 32000 x 4096, losses alone: 866 and 818)
     p.rows = K >= 96 * HL_K && rounds_512(slices * (p.Mp / HL_TM)) <= all_256 ? 512 : 256;
@@ -1051,8 +1142,7 @@ static void for_pieces(const HeadPlan& p, int64_t V, F&& f) {
 
 // Tiles of 64 tokens use more LDS than the 64 KB that a kernel has unasked.
 template <typename Args>
-static void launch_few(void (*kernel)(Args), int nt, dim3 grid, hipStream_t s, const Args& a) {
-    const int bytes = few_lds(nt);
+static void launch_few(void (*kernel)(Args), int bytes, dim3 grid, hipStream_t s, const Args& a) {
     if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess)
         hipLaunchKernelGGL(kernel, grid, dim3(256), bytes, s, a);       // (an error is met by the caller's hipGetLastError)
 }
@@ -1070,9 +1160,12 @@ static void launch_logits(const HeadPlan& p, HeadArgs& a, int64_t rows, hipStrea
     a.tiles_v = p.tiles(rows);
     const dim3 few = head_grid(a.tiles_v / 4, p.blocks(a.M));
     constexpr bool once = MODE == HEAD_STATS;
-    if (p.few && a.M <= 32) launch_few(k_head_few<MODE, 1, once>, 1, few, s, a);
-    else if (p.few && a.M <= 64) launch_few(k_head_few<MODE, 2, once>, 2, few, s, a);
-    else if (p.few) launch_few(k_head_few<MODE, 2, false>, 2, few, s, a);
+    const dim3 split = head_grid(a.tiles_v, p.blocks(a.M));
+    if (p.split && a.M <= 32) launch_few(k_head_split<MODE, 1>, split_lds(1), split, s, a);
+    else if (p.split) launch_few(k_head_split<MODE, 2>, split_lds(2), split, s, a);
+    else if (p.few && a.M <= 32) launch_few(k_head_few<MODE, 1, once>, few_lds(1), few, s, a);
+    else if (p.few && a.M <= 64) launch_few(k_head_few<MODE, 2, once>, few_lds(2), few, s, a);
+    else if (p.few) launch_few(k_head_few<MODE, 2, false>, few_lds(2), few, s, a);
     else launch_tiles<MODE>(p.rows, a, s);
 }
 
@@ -1148,8 +1241,8 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
         d.add = v0 > 0;
         const dim3 grid = head_grid(d.tiles_r, d.tiles_n, d.splits);
         auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, d); };
-        if (p.few_dx && M <= 32) launch_few(k_head_few_product<1>, 1, grid, s, d);
-        else if (p.few_dx) launch_few(k_head_few_product<2>, 2, grid, s, d);
+        if (p.few_dx && M <= 32) launch_few(k_head_few_product<1>, few_lds(1), grid, s, d);
+        else if (p.few_dx) launch_few(k_head_few_product<2>, few_lds(2), grid, s, d);
         else if (last && p.splits == 1) d.add ? run(k_head_product<OUT_DX, true, 4>) : run(k_head_product<OUT_DX, false, 4>);
         else d.add ? run(k_head_product<OUT_SUM, true, 4>) : run(k_head_product<OUT_SUM, false, 4>);
     });
