@@ -697,16 +697,21 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // k_attend_rows reads the keys once per 16 rows and splits them over many workgroups; k_attend_block
 // reads them once per block_rows rows and decodes them once per block_tiles tiles.  A batch whose sequences all bring
 // up to 32 rows per kv head needs the first alone, one of equal longer ones the second alone; any other
-// may hold both kinds, and each kernel takes its own.
+// may hold both kinds, and each kernel takes its own, unless there is so little to read that two launches more cost
+// more than the tiles that a few rows leave empty (27 sequences of up to 494 keys and 11 tokens, 8 heads of 64: 36 us
+// with both kernels, 24 with one).
 // Chunks: for k_attend_rows about 4096 workgroups (some rounds of three or four on each compute unit) at
-// the stated lengths, of at least 256 keys, for a join costs a launch; for k_attend_block chunks only
-// where there are fewer than 1024 waves, one for each SIMD.
+// the stated lengths, of at least 256 keys, for a join costs a launch; for k_attend_block chunks only where there are
+// fewer than 1024 waves, one for each SIMD: of 128 keys at least where most of the keys were there before (that
+// batch: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the others (one
+// prompt of 252 behind 1370 keys, 8 heads of 256: 70 us with 128, 49 with 512).
+constexpr int64_t BLOCK_ALONE = 1024 * 512;
 static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
                               int64_t max_length) {
     AttendPlan p{};
     const int group = heads / c.heads;
-    const int64_t most_rows = max_new * group;
-    p.rows.on = most_rows <= KV_FEW || tokens != (int64_t)seqs * max_new;
+    const int64_t most_rows = max_new * group, keys = (int64_t)seqs * c.heads * max_length;
+    p.rows.on = most_rows <= KV_FEW || (tokens != (int64_t)seqs * max_new && keys > BLOCK_ALONE);
     p.block.on = most_rows > KV_FEW;
     auto chunks = [&](AttendPart& q, int64_t groups, int64_t target, int64_t unit, int64_t least, size_t slots) {
         int64_t chunk = (max_length * groups / target + unit - 1) / unit * unit;
@@ -730,7 +735,7 @@ static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int 
         p.block.tiles = (int)(blocks < 1 ? 1 : blocks);
         const int64_t groups = (tokens * heads + rows - 1) / rows;
         if (groups >= 1024) chunks(p.block, 1, 1, 1, 1 << 24, 0);
-        else chunks(p.block, groups, 1024, KV_STEP, 512, (size_t)tokens * heads);
+        else chunks(p.block, groups, 1024, KV_STEP, 16 * max_new <= max_length ? 128 : 512, (size_t)tokens * heads);
     }
     return p;
 }
