@@ -585,25 +585,34 @@ __device__ __forceinline__ RowLoss row_loss(float z, float others) {
     return RowLoss{d >= 0.0f ? tail : tail - d * LN2, fmaxf(z, others) + tail * LOG2E, 1.0f / (1.0f + exp2f(d))};
 }
 
-// The loss from a row's statistics: one wave per row.
+// The loss from a row's statistics: a workgroup per row.
 __global__ __launch_bounds__(256)
-void k_head_rows(const float2* part, const float* zy, const int64_t* targets, int64_t M, int64_t V, int64_t ignore,
-                 int tiles, float* loss) {
-    const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (m >= M) return;
+void k_head_rows(const float2* part, const float* zy, const int64_t* targets, int64_t V, int64_t ignore, int tiles, float* loss) {
+    __shared__ float2 join[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m = blockIdx.x;
     const float2* p = part + m * tiles;
+    // each wave's own reference first
     float top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-    for (int t = lane; t < tiles; t += 64) top = fmaxf(top, p[t].x);
+#pragma unroll 4
+    for (int t = threadIdx.x; t < tiles; t += 256) top = fmaxf(top, p[t].x);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
     const float ref = top > -INFINITY ? top : 0.0f;
-#pragma unroll 8
-    for (int t = lane; t < tiles; t += 64) sum += p[t].y * __builtin_amdgcn_exp2f(p[t].x - ref);
+#pragma unroll 4
+    for (int t = threadIdx.x; t < tiles; t += 256) sum += p[t].y * __builtin_amdgcn_exp2f(p[t].x - ref);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
-    if (lane == 0) loss[m] = head_live(targets[m], V, ignore) ? row_loss(zy[m], top + log2f(sum)).loss : 0.0f;
+    if (lane == 0) join[wave] = make_float2(top, sum);
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, join[w].x);
+    const float all = top > -INFINITY ? top : 0.0f;
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += join[w].y * __builtin_amdgcn_exp2f(join[w].x - all);
+    loss[m] = head_live(targets[m], V, ignore) ? row_loss(zy[m], top + log2f(sum)).loss : 0.0f;
 }
 
 // Target logits (base 2) and the first references, one wave per row; the last workgroup: the largest
@@ -1195,8 +1204,7 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     if (!p.few || (dW && !p.keep)) hipLaunchKernelGGL(k_head_pack, dim3((uint32_t)(K / HL_K), (uint32_t)(p.Mp / HL_TM * 4)), dim3(256), 0, s, X, M, K, Xp);
     if (!dX && !dW) {
         launch_logits<HEAD_STATS>(p, a, V, s);
-        hipLaunchKernelGGL(k_head_rows, dim3((uint32_t)((M + 3) / 4)), dim3(256), 0, s, a.part, a.zy, targets, M, V, ignore,
-                           (int)a.tiles_v, loss);
+        hipLaunchKernelGGL(k_head_rows, dim3((uint32_t)M), dim3(256), 0, s, a.part, a.zy, targets, V, ignore, (int)a.tiles_v, loss);
         return hipGetLastError();
     }
     float* ref = (float*)(base + p.ref);
