@@ -14,7 +14,8 @@
 // workgroup of a page is the one whose span of `span` packed tokens holds the page's first new token.
 // Queries are rotated by further workgroups of the same launch, a wave per token and part of its heads.
 // Bound by HBM for prompts (4 bytes read and 2 written per key/value pair, 4 per query value) and by the
-// chain of dependent loads (starts, length, table, values) for single tokens.
+// chain of dependent loads (starts, length, table, values) for single tokens.  9 prompts of up to 1023 tokens, 32
+// heads of 128, pages of 16 (272 MB): 70 us, 3.9 TB/s; one token of 16 sequences, 64 heads: 7.2 us.
 #include "paged.h"
 
 namespace nf4 {
@@ -335,7 +336,8 @@ hipError_t launch_kv_append(const CacheView& c, const BatchView& b, const HeadsV
     const int mean = b.tokens / b.seqs;
     a.span = mean < 1 ? 1 : (mean < page ? mean : page);
     a.spans = (b.tokens + a.span - 1) / a.span;
-    // four waves share a head's page where its tokens are more than the rounds one wave holds in registers
+    // four waves share a head's page where its tokens are more than the rounds one wave holds in registers (8 prompts of
+    // up to 1000 tokens, 32 heads of 128: pages of 128 80 us, 117 unshared; 9 on pages of 16: 65 unshared, 128 shared)
     const bool split = a.span > 4 * 512 / c.dim;
     a.kv_blocks = a.spans * (split ? c.heads : (c.heads + 3) / 4);
     int q_blocks = 0;

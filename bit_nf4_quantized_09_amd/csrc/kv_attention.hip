@@ -19,9 +19,15 @@
 // A wave's loads of the next step are in flight while it computes one, so a workgroup of four
 // waves keeps 4 steps of 32 keys x 2 D bytes outstanding.
 //
-// Work.  Workgroups of four waves own (sequence, kv head, row tile, chunk of keys); the waves
-// take the chunk's steps in turn and join through LDS, and chunks of one row join in a second
-// launch.  Bound by HBM: each key and value byte is read once per row tile.
+// Work.  Up to 32 rows of a (sequence, kv head), k_attend_rows: workgroups of four waves own
+// (sequence, kv head, row tile, chunk of keys); the waves take the chunk's steps in turn and join
+// through LDS, and chunks of one row join in a second launch.  Bound by HBM, each key and value byte
+// read once per row tile: 24 sequences of up to 4096 keys, 64 heads of 128 (716 MB): 128 us, 5.6 TB/s;
+// two of 120001, 8 kv heads (343 MB): 73 us with the join.  A short sequence is bound by its chain
+// of loads (length, page, codes): 6.5 us for one of 131 keys.
+// More rows, k_attend_block: single waves own (sequence, kv head, 16 CT rows, chunk).  Bound by the
+// vector instructions of the softmax and of decoding values: 3 prompts of up to 1500 tokens behind up to
+// 1100 cached, 32 heads of 128 (74 GFLOP): 131 us, 565 TFLOP/s.
 #include "bufio.h"
 #include "paged.h"
 #include "tile_map.h"
@@ -691,7 +697,9 @@ struct AttendPart {
 struct AttendPlan {
     AttendPart rows, block;
 };
-constexpr int block_tiles(int dim) { return dim == 64 ? 4 : dim == 128 ? 2 : 1; }     // CT
+// (3 prompts of up to 1500 tokens behind 1100 cached, 32 heads of 128: one tile 213 us, two 131, four, past the
+// registers, 570; of 256: one tile 355, two 1281; of 64: two tiles 92, four 96)
+constexpr int block_tiles(int dim) { return dim == 256 ? 1 : 2; }     // CT
 constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 
 // k_attend_rows reads the keys once per 16 rows and splits them over many workgroups; k_attend_block
@@ -700,9 +708,14 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // may hold both kinds, and each kernel takes its own, unless there is so little to read that two launches more cost
 // more than the tiles that a few rows leave empty (27 sequences of up to 494 keys and 11 tokens, 8 heads of 64: 36 us
 // with both kernels, 24 with one).
-// Chunks: for k_attend_rows about 4096 workgroups (some rounds of three or four on each compute unit) at
-// the stated lengths, of at least 256 keys, for a join costs a launch; for k_attend_block chunks only where there are
-// fewer than 1024 waves, one for each SIMD: of 128 keys at least where most of the keys were there before (that
+// (17 to 32 rows by k_attend_block instead: 55 us for 49 with 8 sequences of up to 8000 keys and 4 tokens, 8 groups of
+// 8 heads of 256, 31 for 19 with heads of 64.)
+// Chunks: for k_attend_rows about 4096 workgroups (some rounds of three or four on each compute unit, so that a
+// ragged batch's last chunks end together) at the stated lengths, but chunks of 1024 keys where 1024 workgroups are left
+// then, for a workgroup's start, end and join cost as much as some 200 keys (two sequences of 120001 keys, 8 kv
+// heads: chunks of 512 keys 81 us, 1024 73; of 24 sequences of up to 4096, 64 heads: 1536 keys 132, 768 149, 3072 199),
+// and of at least 256 keys; for k_attend_block chunks only where there are fewer than 1024 waves, one for each SIMD:
+// of 128 keys at least where most of the keys were there before (that
 // batch: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the others (one
 // prompt of 252 behind 1370 keys, 8 heads of 256: 70 us with 128, 49 with 512).
 constexpr int64_t BLOCK_ALONE = 1024 * 512;
@@ -725,7 +738,8 @@ static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int 
     if (p.rows.on) {
         const int64_t r = most_rows < KV_FEW ? most_rows : KV_FEW;
         p.rows.tiles = (int)((r + 15) / 16);
-        chunks(p.rows, (int64_t)seqs * c.heads * p.rows.tiles, 4096, KV_WAVES * KV_STEP, 256, (size_t)seqs * c.heads * KV_FEW);
+        const int64_t groups = (int64_t)seqs * c.heads * p.rows.tiles, wide = keys * p.rows.tiles / 1024;
+        chunks(p.rows, groups, 4096, KV_WAVES * KV_STEP, wide < 256 ? 256 : wide < 1024 ? wide / 128 * 128 : 1024, (size_t)seqs * c.heads * KV_FEW);
     }
     if (p.block.on) {
         const int64_t rows = block_rows(c.dim);
@@ -783,7 +797,7 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             a.row_tiles = p.rows.tiles;
             const int64_t most = max_new * a.group;
             a.few = (int)(most < KV_FEW ? most : KV_FEW);
-            // codes that one row tile reads are read once: they need not stay in the caches
+            // codes that one row tile reads are read once: they need not stay in the caches (716 MB: 132 us, 140 with them)
             const dim3 grid((uint32_t)a.splits, (uint32_t)(c.heads * a.row_tiles), (uint32_t)b.seqs);
             if (a.row_tiles == 1) hipLaunchKernelGGL((k_attend_rows<D, 2>), grid, dim3(256), 0, s, a);
             else hipLaunchKernelGGL((k_attend_rows<D, 0>), grid, dim3(256), 0, s, a);
