@@ -16,21 +16,28 @@
 // logit passes R by more than 2^40, and the join after each piece (k_head_join) then brings the
 // row's other tiles and sums to the new R by exact powers of two.
 //
-// With dW, the contraction runs over tokens and needs normalised weights: the statistics pass,
-// then for each piece the logits again, whose epilogue writes G = dloss / max|dloss| (p - onehot)
-// in bf16 (and transposed), multiplied with W and X; the factor max|dloss| is applied to the
-// fp32 sums, so that a mean's 1/count does not round the many nearly equal target entries alike.
+// With dW, the contraction runs over tokens and needs normalised weights.  Every piece's E is kept,
+// as bf16 and the eight bits that follow (up to 1 GB of bf16), and once l is known k_head_turn makes
+// G = dloss / max|dloss| (p - onehot) of it, in bf16 and transposed, rounded once; the factor
+// max|dloss| is applied to the fp32 sums, so that a mean's 1/count does not round the many nearly
+// equal target entries alike.  Beyond 1 GB each piece's logits are computed again instead
+// (HEAD_GT): a fourth product (4096 tokens x 32000 x 8192: 6.65 ms, 5.35 with E kept).
 //
 // Rounding: logits, maxima, sums and accumulators are fp32; E and G are bf16, the type of the
 // matrix instructions' operands and of the outputs.
 //
-// Products.  512 x 128 output tiles, 4 waves, v_mfma_f32_32x32x16_bf16, one wave per SIMD with 256
-// accumulators.  The 512-row operand (X, E, G^T) is private to its wave and comes in fragment order
-// (tile_map.h) straight into registers, two steps ahead; X is packed once per call, E and G^T are
-// written in that order by the logits' epilogue.  The 128-column operand (rows of W, or columns of
-// W or X read transposed) goes through four LDS stages filled by direct loads, three steps ahead.
+// Products.  Tiles of 512 or 256 rows x 128 columns, 4 waves, v_mfma_f32_32x32x16_bf16: one wave per
+// SIMD with 256 accumulators, or two with 128 that hide each other's ends.  The long operand (X, E, G^T)
+// is private to its wave and comes in fragment order (tile_map.h) straight into registers, two steps
+// ahead; X is packed once per call, E and G^T are written in that order by the logits' epilogue and
+// by k_head_turn.  The 128-column operand (rows of W, or columns of W or X read transposed) goes through
+// four LDS stages filled by direct loads, three steps ahead.  Bound by the matrix instructions at the clock
+// that the card holds under them: 2048 tokens x 32000 x 4096, logits and dX: 490 + 490 us, 1100 TFLOP/s
+// (440 + 415 before the card is warm); 4096 x 32000 x 8192 with dW: 1280, 1250 and 1190 TFLOP/s.
 // (256 x 256 tiles with both operands in LDS, 8 waves of 128 x 64: LDS reads and writes take as
 // many cycles as the matrix instructions; 940-1000 TFLOP/s.)
+// Grids that such tiles leave mostly empty, and up to 64 tokens, whose time is that of reading W, take
+// tiles of 64 tokens (k_head_few, k_head_few_product) or a quarter of a tile a wave (k_head_split).
 #include "bufio.h"
 #include "decoder.h"
 #include "lds_dma.h"
@@ -93,18 +100,18 @@ __device__ __forceinline__ void hl_landed() {
     else asm volatile("s_waitcnt vmcnt(20) lgkmcnt(0)" ::: "memory");
 }
 
-// The main loop of both products: acc[i][j] += (rows 32 i.. of the wave's 128) x (columns 32 j..),
-// contraction steps first .. last - 1 (at least one).  SWAP: accumulator columns are the 512-row
-// operand's rows.  TRANS: the 128-column operand is read transposed.  `blocks`: the 512-row operand's
+// The main loop of both products: acc[i][j] += (rows 32 i.. of the wave's 32 I) x (columns 32 j..),
+// contraction steps first .. last - 1 (at least one).  SWAP: accumulator columns are the long
+// operand's rows.  TRANS: the 128-column operand is read transposed.  `blocks`: the long operand's
 // 64 KB blocks of this row tile, `block_bytes` of each in use (rows past the last are zero and are
 // not fetched); `dma(stage, step, q)`: fills quarter q of a stage with the other operand.
 //
-// A step is 8 regions of 8 matrix instructions.  Region 2 s + half uses rows 2 half, 2 half + 1 of
-// substep s, reloads their fragments for two steps ahead, and (half 0) reads the next substep's column
-// fragments; regions 0-3 also start a quarter each of the stage three steps ahead.  The barrier stands
-// before the last region, whose matrix instructions hide the next step's first LDS reads.  A stage
-// is complete at the barrier before its first read: 36 is below the number of loads that each wave has
-// started since it started that stage's (at least 46).
+// A step is 8 regions of 2 I matrix instructions.  Region 2 s + half uses the rows of one half (I = 4:
+// 2 half, 2 half + 1) of substep s, reloads their fragments for two steps ahead, and (half 0) reads the next
+// substep's column fragments; regions 0-3 also start a quarter each of the stage three steps ahead.  The
+// barrier stands before the last region, whose matrix instructions hide the next step's first LDS reads.  A
+// stage is complete at the barrier before its first read: hl_landed lets fewer loads be out than each wave
+// has started since it started that stage's (36 of at least 46 for I = 4, 20 of at least 26 for I = 2).
 template <int I, bool SWAP, bool TRANS, typename Dma>
 __device__ __forceinline__ void hl_loop(f32x16 (&acc)[I][4], const uint8_t* lds, const uint16_t* blocks, int block_bytes, int first, int last,
                                         int wave, int lane, Dma&& dma) {
@@ -232,7 +239,7 @@ struct HeadArgs {
     const int64_t* targets;
     int64_t ignore;
     int64_t v0;               // first vocabulary row of the launch, and
-    int64_t tiles_v, tiles_m; // its tiles (128 vocabulary rows, 512 tokens)
+    int64_t tiles_v, tiles_m; // its tiles (of 128 or 32 vocabulary rows; of 512 or 256 tokens)
     float2* part;             // [Mp][tiles of v of the launch]: reference and sum of a row, base 2
     float* zy;                // [Mp]: target's logit, base 2 (HEAD_STATS: out)
     const float* ref;         // [Mp]: running reference (HEAD_E)
@@ -326,7 +333,7 @@ __device__ __forceinline__ void head_column(const HeadArgs& a, f32x16* acc, int6
     if (h == 0 && m < a.Mp) a.part[m * a.tiles_v + tv] = make_float2(MODE == HEAD_E ? ref : top, sum);
 }
 
-// Logits of a tile of 512 tokens x 128 vocabulary rows.
+// Logits of a tile of 128 I tokens x 128 vocabulary rows.
 template <HeadMode MODE, int I>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(I == 4 ? 1 : 2, I == 4 ? 1 : 2)))
 void k_head_logits(HeadArgs a) {
@@ -358,7 +365,7 @@ void k_head_logits(HeadArgs a) {
                              load_to_lds(rw, mine + stage * HL_STAGE + q * 1024, wof[q], (uint32_t)step * 128);
                          });
     if constexpr (MODE == HEAD_GT) {
-        // accumulator (i, j, reg): token 32 i + 8 (reg / 4) + 4 h + reg % 4 of the wave's 128, vocabulary row 32 j + rl.
+        // accumulator (i, j, reg): token 32 i + 8 (reg / 4) + 4 h + reg % 4 of the wave's 32 I, vocabulary row 32 j + rl.
         // G^T's block of 512 vocabulary rows and 64 tokens: this tile is wave slice tv % 4 of it.
         const float inv = 1.0f / head_scale(a.top);
 #pragma unroll
@@ -388,7 +395,7 @@ void k_head_logits(HeadArgs a) {
         }
         return;
     }
-    // accumulator (i, j, reg): token 32 i + rl of the wave's 128, vocabulary row 32 j + 8 (reg / 4) + 4 h + reg % 4
+    // accumulator (i, j, reg): token 32 i + rl of the wave's 32 I, vocabulary row 32 j + 8 (reg / 4) + 4 h + reg % 4
 #pragma unroll
     for (int i = 0; i < I; ++i) head_column<MODE, 4>(a, acc[i], m0 + (wave * I + i) * 32, v0, tv, h, rl);
 }
@@ -396,10 +403,10 @@ void k_head_logits(HeadArgs a) {
 // Tiles of 64 tokens, for few tokens and for grids that 512-token tiles leave mostly empty.
 //
 // Logits: a workgroup takes 128 vocabulary rows and 32 NT tokens, each of its four waves 32 of the rows, and streams
-// W (whole 128-byte lines of 8 rows a load) and X through six LDS stages, five steps ahead: up to 80 KB of W in
-// flight per compute unit.  Up to 64 tokens its time is that of reading W, past the caches where nothing
-// reads it again (ONCE).  (W straight into registers, 32 rows a load, meets every line four times: 75 us for
-// 33 tokens x 32000 x 4096, 63 here.)
+// W (whole 128-byte lines of 8 rows a load) and X through three LDS stages, two steps ahead, two workgroups on a
+// compute unit.  (One with six stages: as fast up to 64 tokens, 223 us for 179 on 512 x 32000 x 4096.)  Up to 64
+// tokens its time is that of reading W, past the caches where nothing reads it again (ONCE): 33 tokens x 32000 x
+// 4096: 55 us, 4.8 TB/s.  (W straight into registers, 32 rows a load, meets every line four times: 75 us.)
 constexpr int FEW_TOKENS = 64, FEW_TN = 32, FEW_STAGES = 3;
 constexpr int few_stage(int nt) { return 16384 + 4096 * nt; }            // bytes: 128 x 64 or 64 x 128 of W, then X or E
 constexpr int FEW_JOIN = 65536;           // the product's sums of 32 rows, of each wave
@@ -772,7 +779,7 @@ __device__ __forceinline__ uint2 head_dx4(f32x4 y, float2 row, uint2 u) {
                       pack_bf16x2(row.x * y[2] - row.y * bf16_lo(u.y), row.x * y[3] - row.y * bf16_hi(u.y)));
 }
 
-// C[r][n] = sum_p A[r][p] B[p][n], tiles of 512 rows x 128 columns; ADD: on top of what `sum` holds.
+// C[r][n] = sum_p A[r][p] B[p][n], tiles of 128 I rows x 128 columns; ADD: on top of what `sum` holds.
 enum ProductOut { OUT_SUM, OUT_DX, OUT_DW };
 template <ProductOut OUT, bool ADD, int I>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(I == 4 ? 1 : 2, I == 4 ? 1 : 2)))
@@ -811,7 +818,7 @@ void k_head_product(ProductArgs a) {
                                 load_to_lds(rb, mine + stage * HL_STAGE + q * 1024,
                                             (uint32_t)((row < most ? row : most) * (int)a.N * 2) + bcol, 0);
                             });
-    // accumulator (i, j, reg): row 32 i + rl of the wave's 128, column 32 j + 8 (reg / 4) + 4 h + reg % 4.  Each 32
+    // accumulator (i, j, reg): row 32 i + rl of the wave's 32 I, column 32 j + 8 (reg / 4) + 4 h + reg % 4.  Each 32
     // rows go through the wave's own quarter of LDS (row r's 16-byte chunk c at c ^ r), so that memory is met in
     // whole rows of 128 columns.
     __syncthreads();
