@@ -58,9 +58,19 @@ def test_few_tokens_and_small_grids(M, V, K):
     check(*inputs(M, V, K, seed=M + V + K))
 
 
-def test_gradient_past_what_is_kept():
+@pytest.mark.parametrize("K", [64, 6144])
+def test_gradient_past_what_is_kept(K):
     # more than 1 GB of weights: dW from the logits a second time
-    check(*inputs(4096, 131200, 64, seed=15))
+    check(*inputs(4096, 131200, K, seed=15))
+
+
+def test_long_contractions():
+    check(*inputs(1024, 32000, 6144, seed=17))
+
+
+@pytest.mark.parametrize("M", [9, 50])
+def test_few_tokens_and_pieces_of_the_vocabulary(M):
+    check(*inputs(M, 140001, 64, seed=M))
 
 
 def test_growing_logits_in_pieces():

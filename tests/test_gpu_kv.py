@@ -170,6 +170,15 @@ def test_attention_chunks(dim, kv, heads):
         assert torch.all((a.float() - b.float()).abs() <= 2.0 ** -7 * a.float().abs() + 2.0 ** -10 * 8)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kv,heads", [(1, 2), (2, 16)])
+def test_attention_few_tokens_behind_many_keys(dim, kv, heads):
+    # short chunks, and sequences of a few rows among longer ones; then with a kernel for each kind
+    c = Case([1500, 900, 3, 1111, 700], [33, 20, 40, 1, 0], page=64, kv=kv, heads=heads, dim=dim, seed=dim + kv)
+    check_attention(c, max_new=40, max_length=1533)
+    check_attention(c, max_new=40, max_length=200000)
+
+
 def test_attention_long_split():
     c = Case([40000, 3, 20011], [1, 1, 2], page=64, kv=1, heads=4, dim=128, seed=9)
     check_attention(c, max_new=2, max_length=40001)
