@@ -51,6 +51,7 @@ struct AttendArgs {
     int group;                // query heads per kv head
     int row_tiles;            // k_attend_rows: launched row tiles per (sequence, kv head)
     int blocks;               // k_attend_block: launched blocks of CT row tiles per (sequence, kv head)
+    int ordered;              // k_attend_block: blocks start in the order of their keys
     int chunk;                // keys per chunk, a multiple of 4 * KV_STEP
     int splits;               // launched chunks per row tile
     float scale2;             // |scale| * log2(e)
@@ -448,6 +449,46 @@ void k_attend_rows(AttendArgs a) {
     }
 }
 
+// The block of rank `rank` among those of an XCD's `here` <= 64 (sequence, kv head) pairs, the one with most keys
+// first: the pair's index in x, its block in y (-1: there are not that many).  A lane has a pair; a block's
+// keys are counted in blocks of rows, base + block, and the least count that `rank` blocks do not pass is
+// searched for.
+template <int BLOCK>
+__device__ __forceinline__ int2 block_of_rank(const AttendArgs& a, int here, int rank, int lane) {
+    const int pair = lane * XCDS + (int)(blockIdx.x % XCDS);
+    int blocks = 0, base = 0;
+    if (lane < here && pair < a.b.seqs * a.c.heads) {
+        const int seq = pair / a.c.heads, rows = (a.b.starts[seq + 1] - a.b.starts[seq]) * a.group;
+        blocks = rows <= a.limit ? 0 : (rows + BLOCK - 1) / BLOCK;
+        const int64_t rows_before = (int64_t)a.b.lengths[seq] * a.group / BLOCK;
+        base = rows_before < 0 ? 0 : rows_before < (1 << 28) ? (int)rows_before : 1 << 28;
+    }
+    auto total = [&](int x) {
+        for (int i = 1; i < here; i <<= 1) x += __shfl_xor(x, i);
+        return __builtin_amdgcn_readfirstlane(x);
+    };
+    auto reaching = [&](int t) {              // this lane's blocks with t keys or more
+        const int n = base + blocks - t;
+        return n < 0 ? 0 : n < blocks ? n : blocks;
+    };
+    if (rank >= total(blocks)) return make_int2(0, -1);
+    int low = 0, high = blocks > 0 ? base + blocks : 0;      // rank < count at `low`, not at `high`
+    for (int i = 1; i < here; i <<= 1) high = max(high, __shfl_xor(high, i));
+    high = __builtin_amdgcn_readfirstlane(high);
+    while (high - low > 1) {
+        const int mid = (low + high) >> 1;
+        if (rank < total(reaching(mid))) low = mid;
+        else high = mid;
+    }
+    // among the pairs that have a block of exactly `low`, the one that is as many places on
+    int left = rank - total(reaching(low + 1));
+    const uint64_t have = __ballot(reaching(low) > reaching(low + 1));
+    uint64_t rest = have;
+    for (; left > 0; --left) rest &= rest - 1;
+    const int at = __ffsll((unsigned long long)rest) - 1;
+    return make_int2(at, low - __builtin_amdgcn_readlane(base, at));
+}
+
 // Rows of a (sequence, kv head) beyond a few: a wave owns CT tiles of 16 rows and reads the codes itself,
 // each decoded once for all of its tiles; no LDS, no barrier.  Scores by 8-bit products (D >= 128): the codes of
 // the keys are the operand as they lie.  The workgroups (single waves) of one (sequence, kv head) run on one XCD,
@@ -460,19 +501,28 @@ void k_attend_block(AttendArgs a) {
     const int lane = threadIdx.x, col = lane & 15, quarter = lane >> 4;
     const int pairs = a.b.seqs * a.c.heads;
     const int local = (int)(blockIdx.x / XCDS), here = (pairs + XCDS - 1) / XCDS;      // of this XCD: workgroup, pairs
-    const int pair = local % here * XCDS + (int)(blockIdx.x % XCDS);
-    if (pair >= pairs) return;
-    const int head = pair % a.c.heads, seq = pair / a.c.heads, split = blockIdx.y;
-    const int begin = scalar_load(a.b.starts + seq), fresh = scalar_load(a.b.starts + seq + 1) - begin;
-    const int before = scalar_load(a.b.lengths + seq);
-    const int rows = fresh * a.group;
-    if (rows <= a.limit) return;
+    const int split = blockIdx.y;
     const int reach = a.b.table_width << a.c.page_log2;
     const uint32_t koff = col * D + 16 * quarter, voff = 4 * quarter * D + col * (D / 16);
     constexpr int BLOCK = CT * 16;
-    const int blocks = (rows + BLOCK - 1) / BLOCK;
-
-    for (int block = blocks - 1 - local / here; block >= 0; block -= a.blocks) {
+    for (int rank = local;; rank += here * a.blocks) {
+        int pair = rank % here * XCDS + (int)(blockIdx.x % XCDS), block = 0;
+        if (a.ordered) {
+            const int2 own = block_of_rank<BLOCK>(a, here, rank, lane);
+            if (own.y < 0) return;
+            pair = own.x * XCDS + (int)(blockIdx.x % XCDS);
+            block = own.y;
+        } else if (pair >= pairs) {
+            return;
+        }
+        const int head = pair % a.c.heads, seq = pair / a.c.heads;
+        const int begin = scalar_load(a.b.starts + seq), fresh = scalar_load(a.b.starts + seq + 1) - begin;
+        const int before = scalar_load(a.b.lengths + seq);
+        const int rows = fresh * a.group;
+        if (!a.ordered) {                     // a pair's last block first (every rank of this workgroup is of one pair)
+            block = (rows + BLOCK - 1) / BLOCK - 1 - rank / here;
+            if (block < 0 || rows <= a.limit) return;
+        }
         const int row0 = block * BLOCK;
         const int last_row = row0 + BLOCK <= rows ? row0 + BLOCK - 1 : rows - 1;
         int keys = before + last_row / a.group + 1;
@@ -787,6 +837,9 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             a.blocks = p.block.tiles;
             const int64_t pairs = ((int64_t)b.seqs * c.heads + XCDS - 1) / XCDS * XCDS;
             const dim3 grid((uint32_t)(pairs * a.blocks), (uint32_t)a.splits);
+            // more waves than the 2048 that run at once: those with most keys first, in whichever sequence (a pair for
+            // each lane; beyond some rounds the order of one sequence's blocks is enough)
+            a.ordered = pairs <= 64 * XCDS && pairs * a.blocks > 2048 && pairs * a.blocks <= 8 * 2048;
             hipLaunchKernelGGL((k_attend_block<D, block_tiles(D)>), grid, dim3(64), 0, s, a);
             const int64_t rows = (int64_t)b.tokens * q.heads;
             if (a.splits > 16) hipLaunchKernelGGL((k_attend_join<D, 4, false>), dim3((uint32_t)rows), dim3(256), 0, s, a);
