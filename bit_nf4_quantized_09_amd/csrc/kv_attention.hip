@@ -27,7 +27,7 @@
 // of loads (length, page, codes): 6.5 us for one of 131 keys.
 // More rows, k_attend_block: single waves own (sequence, kv head, 16 CT rows, chunk).  Bound by the
 // vector instructions of the softmax and of decoding values: 3 prompts of up to 1500 tokens behind up to
-// 1100 cached, 32 heads of 128 (74 GFLOP): 131 us, 565 TFLOP/s.
+// 1100 cached, 32 heads of 128 (74 GFLOP): 128 us, 580 TFLOP/s.
 #include "bufio.h"
 #include "paged.h"
 #include "tile_map.h"
@@ -102,41 +102,57 @@ struct StepCodes {
     uint4 k[2][D / 64];                   // [tile][piece]: 16 bytes of the lane's key
     uint32_t v[2][4][D / 64];             // [tile][token 4 g + r]: D / 16 bytes of its values
     TileScales scale[2];
+    __amdgpu_buffer_rsrc_t values[2];
 };
 
 // The step's codes at key `first` of a sequence whose keys end at `hi`: ranges that end with the last key that
-// counts, so that whatever lies behind it reads as zero; a page outside the pool holds no keys.
-template <int D, int AUX>
-__device__ __forceinline__ void load_step(StepCodes<D>& x, const CacheView& c, int head, int first, int hi, const int* entries,
-                                          uint32_t koff, uint32_t voff) {
-    const int64_t page_bytes = (int64_t)D << c.page_log2;
+// counts, so that whatever lies behind it reads as zero; a page outside the pool holds no keys.  WIDE: both
+// tiles are of one page.
+template <int D, int AUX, bool WIDE>
+__device__ __forceinline__ void load_values(StepCodes<D>& x, uint32_t voff) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int at = first + 16 * t, page = page_or_none(c, entries[t]);
-        const int have = page < 0 || hi <= at ? 0 : (hi - at < 16 ? hi - at : 16);
-        const int64_t block = (int64_t)(page < 0 ? 0 : page) * 2 * c.heads + head;
-        const uint8_t* kb = c.codes + block * page_bytes + (at & ((1 << c.page_log2) - 1)) * D;
-        const __amdgpu_buffer_rsrc_t rk = make_rsrc(kb, have * D), rv = make_rsrc(kb + c.heads * page_bytes, have * D);
-        x.scale[t] = TileScales{scalar_load((const uint32_t*)c.scales + block), scalar_load((const uint32_t*)c.scales + block + c.heads),
-                                have > 0 ? hi : 0};
-#pragma unroll
-        for (int p = 0; p < D / 64; ++p) x.k[t][p] = buf_load16_as<AUX>(rk, koff + 64 * p);
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if constexpr (D == 64) x.v[t][r][0] = buf_load4_as<AUX>(rv, voff + r * D);
+            const __amdgpu_buffer_rsrc_t rv = x.values[WIDE ? 0 : t];
+            const uint32_t at = voff + (WIDE ? 16 * t * D : 0) + r * D;
+            if constexpr (D == 64) x.v[t][r][0] = buf_load4_as<AUX>(rv, at);
             if constexpr (D == 128) {
-                const uint2 w = buf_load8_as<AUX>(rv, voff + r * D);
+                const uint2 w = buf_load8_as<AUX>(rv, at);
                 x.v[t][r][0] = w.x;
                 x.v[t][r][1] = w.y;
             }
             if constexpr (D == 256) {
-                const uint4 w = buf_load16_as<AUX>(rv, voff + r * D);
+                const uint4 w = buf_load16_as<AUX>(rv, at);
                 x.v[t][r][0] = w.x;
                 x.v[t][r][1] = w.y;
                 x.v[t][r][2] = w.z;
                 x.v[t][r][3] = w.w;
             }
         }
+}
+template <int D, int AUX, bool WIDE>
+__device__ __forceinline__ void load_keys(StepCodes<D>& x, const CacheView& c, int head, int first, int hi, const int* entries,
+                                          uint32_t koff) {
+    constexpr int KEYS = WIDE ? 32 : 16;
+    const int64_t page_bytes = (int64_t)D << c.page_log2;
+    __amdgpu_buffer_rsrc_t rk;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        if (!WIDE || t == 0) {
+            const int at = first + 16 * t, page = page_or_none(c, entries[t]);
+            const int have = page < 0 || hi <= at ? 0 : (hi - at < KEYS ? hi - at : KEYS);
+            const int64_t block = (int64_t)(page < 0 ? 0 : page) * 2 * c.heads + head;
+            const uint8_t* kb = c.codes + block * page_bytes + (at & ((1 << c.page_log2) - 1)) * D;
+            rk = make_rsrc(kb, have * D);
+            x.values[t] = make_rsrc(kb + c.heads * page_bytes, have * D);
+            x.scale[t] = TileScales{scalar_load((const uint32_t*)c.scales + block), scalar_load((const uint32_t*)c.scales + block + c.heads),
+                                    have > 0 ? hi : 0};
+        } else {
+            x.scale[t] = x.scale[0];
+        }
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) x.k[t][p] = buf_load16_as<AUX>(rk, koff + (WIDE ? 16 * t * D : 0) + 64 * p);
     }
 }
 
@@ -356,7 +372,8 @@ void k_attend_rows(AttendArgs a) {
                 return g;
             };
             auto load = [&](StepCodes<D>& x, int i, const Pages& g) {
-                load_step<D, AUX>(x, a.c, head, first_key(i), hi, g.p, koff, voff);
+                load_keys<D, AUX, false>(x, a.c, head, first_key(i), hi, g.p, koff);
+                load_values<D, AUX, false>(x, voff);
             };
             auto compute = [&](const StepCodes<D>& x, int i) {
                 f32x4 sc[2];
@@ -493,7 +510,7 @@ __device__ __forceinline__ int2 block_of_rank(const AttendArgs& a, int here, int
 // each decoded once for all of its tiles; no LDS, no barrier.  Scores by 8-bit products (D >= 128): the codes of
 // the keys are the operand as they lie.  The workgroups (single waves) of one (sequence, kv head) run on one XCD,
 // whose L2 holds its keys; those that see most keys start first.
-template <int D, int CT>
+template <int D, int CT, bool WIDE>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2)))
 void k_attend_block(AttendArgs a) {
     constexpr int KSTEPS = D / 32, TILES = D / 16, PIECES = D / 64;
@@ -563,12 +580,14 @@ void k_attend_block(AttendArgs a) {
             auto pages = [&](int i) {
                 Pages g;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) g.p[t] = page_entry(a.b, seq, (lo + KV_STEP * i + 16 * t) >> a.c.page_log2);
+                for (int t = 0; t < (WIDE ? 1 : 2); ++t) g.p[t] = page_entry(a.b, seq, (lo + KV_STEP * i + 16 * t) >> a.c.page_log2);
                 return g;
             };
             auto load = [&](StepCodes<D>& x, int i, const Pages& g) {
-                load_step<D, 0>(x, a.c, head, lo + KV_STEP * i, hi, g.p, koff, voff);
+                load_keys<D, 0, WIDE>(x, a.c, head, lo + KV_STEP * i, hi, g.p, koff);
             };
+            // (a step's values are started as it begins, its keys a step before: 16 D / 64 registers fewer)
+            auto values = [&](StepCodes<D>& x) { load_values<D, 0, WIDE>(x, voff); };
             auto compute = [&](const StepCodes<D>& x, int i) {
                 const int first = lo + KV_STEP * i;
                 f32x4 sc[CT][2];
@@ -632,15 +651,19 @@ void k_attend_block(AttendArgs a) {
                 int i = 0;
                 for (; i + 2 < steps; i += 2) {
                     const Pages g2 = pages(i + 2);
+                    values(x0);
                     load(x1, i + 1, g1);
                     compute(x0, i);
                     g1 = pages(i + 3);
+                    values(x1);
                     load(x0, i + 2, g2);
                     compute(x1, i + 1);
                 }
+                values(x0);
                 if (i + 1 < steps) {
                     load(x1, i + 1, g1);
                     compute(x0, i);
+                    values(x1);
                     compute(x1, i + 1);
                 } else {
                     compute(x0, i);
@@ -840,7 +863,10 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             // more waves than the 2048 that run at once: those with most keys first, in whichever sequence (a pair for
             // each lane; beyond some rounds the order of one sequence's blocks is enough)
             a.ordered = pairs <= 64 * XCDS && pairs * a.blocks > 2048 && pairs * a.blocks <= 8 * 2048;
-            hipLaunchKernelGGL((k_attend_block<D, block_tiles(D)>), grid, dim3(64), 0, s, a);
+            // pages of 32 tokens and more hold a whole step: half the address work (3 prompts of up to 1500
+            // tokens, 32 heads of 64: 73 us for 86)
+            if (c.page_log2 >= 5) hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), true>), grid, dim3(64), 0, s, a);
+            else hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), false>), grid, dim3(64), 0, s, a);
             const int64_t rows = (int64_t)b.tokens * q.heads;
             if (a.splits > 16) hipLaunchKernelGGL((k_attend_join<D, 4, false>), dim3((uint32_t)rows), dim3(256), 0, s, a);
             else if (a.splits > 1) hipLaunchKernelGGL((k_attend_join<D, 1, false>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
