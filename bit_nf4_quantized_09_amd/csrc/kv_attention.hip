@@ -786,7 +786,7 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // Chunks: for k_attend_rows about 4096 workgroups (some rounds of three or four on each compute unit, so that a
 // ragged batch's last chunks end together) at the stated lengths, but chunks of 1024 keys where 1024 workgroups are left
 // then, for a workgroup's start, end and join cost as much as some 200 keys (two sequences of 120001 keys, 8 kv
-// heads: chunks of 512 keys 81 us, 1024 73; of 24 sequences of up to 4096, 64 heads: 1536 keys 132, 768 149, 3072 199),
+// heads: chunks of 512 keys 81 us, 1024 73; of 24 sequences of up to 4096, 64 heads: 1536 keys 132 us, half of that 149, twice 199),
 // and of at least 256 keys; for k_attend_block chunks only where there are fewer than 1024 waves, one for each SIMD:
 // of 128 keys at least where most of the keys were there before (that
 // batch: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the others (one
