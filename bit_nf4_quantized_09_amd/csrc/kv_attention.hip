@@ -25,9 +25,9 @@
 // read once per row tile: 24 sequences of up to 4096 keys, 64 heads of 128 (716 MB): 128 us, 5.6 TB/s;
 // two of 120001, 8 kv heads (343 MB): 73 us with the join.  A short sequence is bound by its chain
 // of loads (length, page, codes): 6.5 us for one of 131 keys.
-// More rows, k_attend_block: single waves own (sequence, kv head, 16 CT rows, chunk).  Bound by the
+// More rows, k_attend_block: one, two or four waves own (sequence, kv head, 16 CT rows, chunk).  Bound by the
 // vector instructions of the softmax and of decoding values: 3 prompts of up to 1500 tokens behind up to
-// 1100 cached, 32 heads of 128 (74 GFLOP): 128 us, 580 TFLOP/s.
+// 1100 cached, 32 heads of 128 (74 GFLOP): 126 us, 585 TFLOP/s.
 #include "bufio.h"
 #include "paged.h"
 #include "tile_map.h"
@@ -507,15 +507,16 @@ __device__ __forceinline__ int2 block_of_rank(const AttendArgs& a, int here, int
 }
 
 // Rows of a (sequence, kv head) beyond a few: a wave owns CT tiles of 16 rows and reads the codes itself,
-// each decoded once for all of its tiles; no LDS, no barrier.  Scores by 8-bit products (D >= 128): the codes of
-// the keys are the operand as they lie.  The workgroups (single waves) of one (sequence, kv head) run on one XCD,
-// whose L2 holds its keys; those that see most keys start first.
-template <int D, int CT, bool WIDE>
-__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2)))
+// each decoded once for all of its tiles; no LDS, no barrier, but where W waves share the keys, at the end.  Scores
+// by 8-bit products (D >= 128): the codes of the keys are the operand as they lie.  The workgroups of one (sequence, kv
+// head) run on one XCD, whose L2 holds its keys; those that see most keys start first.
+template <int D, int CT, bool WIDE, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2)))
 void k_attend_block(AttendArgs a) {
     constexpr int KSTEPS = D / 32, TILES = D / 16, PIECES = D / 64;
     constexpr bool F8 = D >= 128;
-    const int lane = threadIdx.x, col = lane & 15, quarter = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = W > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+    const int col = lane & 15, quarter = lane >> 4;
     const int pairs = a.b.seqs * a.c.heads;
     const int local = (int)(blockIdx.x / XCDS), here = (pairs + XCDS - 1) / XCDS;      // of this XCD: workgroup, pairs
     const int split = blockIdx.y;
@@ -573,23 +574,24 @@ void k_attend_block(AttendArgs a) {
         const int chunks = (keys + a.chunk - 1) / a.chunk;
         for (int ch = split; ch < chunks; ch += a.splits) {
             const int lo = ch * a.chunk, hi = lo + a.chunk < keys ? lo + a.chunk : keys;
-            const int steps = (hi - lo + KV_STEP - 1) / KV_STEP;
+            const int steps = ((hi - lo + KV_STEP - 1) / KV_STEP - wave + W - 1) / W;     // of this wave: every W-th
+            auto first_key = [&](int i) { return lo + KV_STEP * (W * i + wave); };
             struct Pages {
                 int p[2];
             };
             auto pages = [&](int i) {
                 Pages g;
 #pragma unroll
-                for (int t = 0; t < (WIDE ? 1 : 2); ++t) g.p[t] = page_entry(a.b, seq, (lo + KV_STEP * i + 16 * t) >> a.c.page_log2);
+                for (int t = 0; t < (WIDE ? 1 : 2); ++t) g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
                 return g;
             };
             auto load = [&](StepCodes<D>& x, int i, const Pages& g) {
-                load_keys<D, 0, WIDE>(x, a.c, head, lo + KV_STEP * i, hi, g.p, koff);
+                load_keys<D, 0, WIDE>(x, a.c, head, first_key(i), hi, g.p, koff);
             };
             // (a step's values are started as it begins, its keys a step before: 16 D / 64 registers fewer)
             auto values = [&](StepCodes<D>& x) { load_values<D, 0, WIDE>(x, voff); };
             auto compute = [&](const StepCodes<D>& x, int i) {
-                const int first = lo + KV_STEP * i;
+                const int first = first_key(i);
                 f32x4 sc[CT][2];
                 float ks[2], vf[2], ev[2];
 #pragma unroll
@@ -669,6 +671,35 @@ void k_attend_block(AttendArgs a) {
                     compute(x0, i);
                 }
             }
+        }
+        if constexpr (W > 1) {                // the first wave adds the others' parts to its own
+            __shared__ f32x4 parts[W - 1][CT][TILES][64];
+            __shared__ float2 ends[W - 1][CT][64];
+            if (wave > 0) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    ends[wave - 1][c][lane] = make_float2(st[c].m, st[c].l);
+#pragma unroll
+                    for (int i = 0; i < TILES; ++i) parts[wave - 1][c][i][lane] = st[c].acc[i];
+                }
+            }
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int w = 0; w < W - 1; ++w) {
+                        const float2 other = ends[w][c][lane];
+                        const float now = fmaxf(st[c].m, other.x);
+                        const float mine = __builtin_amdgcn_exp2f(st[c].m - now), theirs = __builtin_amdgcn_exp2f(other.x - now);
+                        st[c].m = now;
+                        st[c].l = st[c].l * mine + other.y * theirs;
+#pragma unroll
+                        for (int i = 0; i < TILES; ++i) st[c].acc[i] = st[c].acc[i] * mine + parts[w][c][i][lane] * theirs;
+                    }
+            }
+            __syncthreads();                  // the parts have been read before another block's are written
+            if (wave > 0) continue;
         }
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
@@ -766,6 +797,7 @@ struct AttendPart {
     bool on;
     int tiles, chunk, splits;             // row tiles (blocks) launched per (sequence, kv head)
     size_t slots, bytes;                  // row slots; workspace
+    int waves;                            // k_attend_block: waves that share a block's keys
 };
 struct AttendPlan {
     AttendPart rows, block;
@@ -787,10 +819,13 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // ragged batch's last chunks end together) at the stated lengths, but chunks of 1024 keys where 1024 workgroups are left
 // then, for a workgroup's start, end and join cost as much as some 200 keys (two sequences of 120001 keys, 8 kv
 // heads: chunks of 512 keys 81 us, 1024 73; of 24 sequences of up to 4096, 64 heads: 1536 keys 132 us, half of that 149, twice 199),
-// and of at least 256 keys; for k_attend_block chunks only where there are fewer than 1024 waves, one for each SIMD:
-// of 128 keys at least where most of the keys were there before (that
-// batch: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the others (one
-// prompt of 252 behind 1370 keys, 8 heads of 256: 70 us with 128, 49 with 512).
+// and of at least 256 keys.  For k_attend_block, where there are fewer blocks than waves that run at once, two or four
+// waves share a block's keys (4 prompts of up to 534 tokens, 8 heads of 64: 12.5 us, 22.5 alone; 2 of 1277, 16 heads of
+// 128: 31 and 35; but 3 of 1500, 32 heads: 134 and 126, and heads of 256, whose parts are as large as a step's
+// work: 24 and 10 for 3 of 76 tokens), and chunks only where there are still fewer than 1024 waves, one for
+// each SIMD: of 128 keys a wave at least where most of the keys were there before (27 sequences of up to 494 keys
+// and 11 tokens: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the
+// others (one prompt of 252 behind 1370 keys, 8 heads of 256: 70 us with 128, 49 with 512).
 constexpr int64_t BLOCK_ALONE = 1024 * 512;
 static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
                               int64_t max_length) {
@@ -821,8 +856,9 @@ static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int 
         blocks = blocks < most ? blocks : most;               // (a wave takes several beyond that)
         p.block.tiles = (int)(blocks < 1 ? 1 : blocks);
         const int64_t groups = (tokens * heads + rows - 1) / rows;
-        if (groups >= 1024) chunks(p.block, 1, 1, 1, 1 << 24, 0);
-        else chunks(p.block, groups, 1024, KV_STEP, 16 * max_new <= max_length ? 128 : 512, (size_t)tokens * heads);
+        const int waves = p.block.waves = c.dim == 256 || max_length < 256 || groups >= 2048 ? 1 : groups >= 1024 ? 2 : 4;
+        if (groups * waves >= 1024) chunks(p.block, 1, 1, 1, 1 << 24, 0);
+        else chunks(p.block, groups * waves, 1024, KV_STEP, (16 * max_new <= max_length ? 128 : 512) * waves, (size_t)tokens * heads);
     }
     return p;
 }
@@ -862,11 +898,19 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             const dim3 grid((uint32_t)(pairs * a.blocks), (uint32_t)a.splits);
             // more waves than the 2048 that run at once: those with most keys first, in whichever sequence (a pair for
             // each lane; beyond some rounds the order of one sequence's blocks is enough)
-            a.ordered = pairs <= 64 * XCDS && pairs * a.blocks > 2048 && pairs * a.blocks <= 8 * 2048;
+            a.ordered = pairs <= 64 * XCDS && pairs * a.blocks * p.block.waves > 2048 && pairs * a.blocks * p.block.waves <= 8 * 2048;
             // pages of 32 tokens and more hold a whole step: half the address work (3 prompts of up to 1500
             // tokens, 32 heads of 64: 73 us for 86)
-            if (c.page_log2 >= 5) hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), true>), grid, dim3(64), 0, s, a);
-            else hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), false>), grid, dim3(64), 0, s, a);
+            auto run = [&](auto wide, auto waves) {
+                constexpr int W = decltype(waves)::value;
+                hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), decltype(wide)::value, W>), grid, dim3(64 * W), 0, s, a);
+            };
+            auto with_pages = [&](auto waves) { c.page_log2 >= 5 ? run(std::true_type{}, waves) : run(std::false_type{}, waves); };
+            if (p.block.waves == 1) with_pages(std::integral_constant<int, 1>{});
+            if constexpr (D < 256) {
+                if (p.block.waves == 2) with_pages(std::integral_constant<int, 2>{});
+                if (p.block.waves == 4) with_pages(std::integral_constant<int, 4>{});
+            }
             const int64_t rows = (int64_t)b.tokens * q.heads;
             if (a.splits > 16) hipLaunchKernelGGL((k_attend_join<D, 4, false>), dim3((uint32_t)rows), dim3(256), 0, s, a);
             else if (a.splits > 1) hipLaunchKernelGGL((k_attend_join<D, 1, false>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
