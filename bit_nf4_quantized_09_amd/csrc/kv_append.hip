@@ -335,11 +335,16 @@ hipError_t launch_kv_append(const CacheView& c, const BatchView& b, const HeadsV
     const int page = 1 << c.page_log2;
     const int mean = b.tokens / b.seqs;
     a.span = mean < 1 ? 1 : (mean < page ? mean : page);
-    a.spans = (b.tokens + a.span - 1) / a.span;
     // four waves share a head's page where its tokens are more than the rounds one wave holds in registers (8 prompts of
     // up to 1000 tokens, 32 heads of 128: pages of 128 80 us, 117 unshared; 9 on pages of 16: 65 unshared, 128 shared)
     const bool split = a.span > 4 * 512 / c.dim;
-    a.kv_blocks = a.spans * (split ? c.heads : (c.heads + 3) / 4);
+    const int columns = split ? c.heads : (c.heads + 3) / 4;
+    // a span in which two pages begin takes them one after the other: shorter spans, some of them without a page, while
+    // the workgroups fit the compute units twice (3 sequences of up to 125 tokens, 16 heads, pages of 16: 16 us, 11
+    // with spans of 4; but 9 of 1023: 65 and 79)
+    while (a.span > 1 && (int64_t)((b.tokens + a.span / 2 - 1) / (a.span / 2)) * columns <= 512) a.span /= 2;
+    a.spans = (b.tokens + a.span - 1) / a.span;
+    a.kv_blocks = a.spans * columns;
     int q_blocks = 0;
     bool vec = true;
     if (q_in) {
