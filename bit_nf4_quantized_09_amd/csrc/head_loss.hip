@@ -874,7 +874,7 @@ void k_head_product(ProductArgs a) {
 
 // The same sums in tiles of 32 NT rows x 128 columns: a step's 64 rows of B go through LDS once, each wave takes 16
 // of them for the whole tile, and the four waves' accumulators are added at the end.
-template <int NT>
+template <int NT, ProductOut OUT>
 __global__ __launch_bounds__(256, 2)
 void k_head_few_product(ProductArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -965,9 +965,14 @@ void k_head_few_product(ProductArgs a) {
             f32x4 y = *cell(0, wave, r4);
 #pragma unroll
             for (int from = 1; from < 4; ++from) y += *cell(from, wave, r4);
-            f32x4* to = reinterpret_cast<f32x4*>(sums + r * a.N + n);
-            if (a.add) y += *to * a.factor[r];
-            *to = y;
+            if constexpr (OUT == OUT_DW) {
+                y *= head_scale(a.top);
+                *reinterpret_cast<uint2*>(a.out + r * a.N + n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            } else {
+                f32x4* to = reinterpret_cast<f32x4*>(sums + r * a.N + n);
+                if (a.add) y += *to * a.factor[r];
+                *to = y;
+            }
         }
     }
 }
@@ -1256,8 +1261,8 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
         d.add = v0 > 0;
         const dim3 grid = head_grid(d.tiles_r, d.tiles_n, d.splits);
         auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, d); };
-        if (p.few_dx && M <= 32) launch_few(k_head_few_product<1>, few_lds(1), grid, s, d);
-        else if (p.few_dx) launch_few(k_head_few_product<2>, few_lds(2), grid, s, d);
+        if (p.few_dx && M <= 32) launch_few(k_head_few_product<1, OUT_SUM>, few_lds(1), grid, s, d);
+        else if (p.few_dx) launch_few(k_head_few_product<2, OUT_SUM>, few_lds(2), grid, s, d);
         else if (last && p.splits == 1) d.add ? run(k_head_product<OUT_DX, true, 4>) : run(k_head_product<OUT_DX, false, 4>);
         else d.add ? run(k_head_product<OUT_SUM, true, 4>) : run(k_head_product<OUT_SUM, false, 4>);
     });
@@ -1288,11 +1293,14 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
         d.out_rows = rows;
         // short contractions are mostly ends, which two smaller tiles on a compute unit hide for each other (281 x
         // 37263 x 5504: 354 and 238 us; 4096 x 32000 x 8192: 1790 and 1840)
-        const int64_t tile = d.steps >= 64 ? 512 : 256;
+        int64_t tile = d.steps >= 64 ? 512 : 256;
+        const int64_t fine = (rows + 63) / 64;
+        if (rounds_64(fine * d.tiles_n) < (tile == 512 ? rounds_512((rows + 511) / 512 * d.tiles_n) : rounds_256((rows + 255) / 256 * d.tiles_n))) tile = 64;
         d.tiles_r = (rows + tile - 1) / tile;
         d.out = dW + v0 * K;
         const dim3 grid = head_grid(d.tiles_r, d.tiles_n);
-        if (tile == 512) hipLaunchKernelGGL((k_head_product<OUT_DW, false, 4>), grid, dim3(256), 0, s, d);
+        if (tile == 64) launch_few(k_head_few_product<2, OUT_DW>, few_lds(2), grid, s, d);
+        else if (tile == 512) hipLaunchKernelGGL((k_head_product<OUT_DW, false, 4>), grid, dim3(256), 0, s, d);
         else hipLaunchKernelGGL((k_head_product<OUT_DW, false, 2>), grid, dim3(256), 0, s, d);
     });
     return hipGetLastError();
