@@ -118,7 +118,7 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
                               const qlora_heads* out, float scale, int64_t max_new, int64_t max_length,
                               void* workspace, size_t workspace_bytes, void* stream);
 
-/* Softmax cross entropy of a vocabulary head, z = X W^T, without keeping the logits:
+/* Softmax cross entropy of a vocabulary head, z = X W^T, without fp32 logits in memory:
  *   loss[m] = log sum_v exp(z[m][v]) - z[m][targets[m]]
  *   dX = G W,  dW = G^T X,  G[m][v] = dloss[m] (softmax(z[m])[v] - [v == targets[m]])
  * A row whose target is ignore_index or lies outside 0 .. V-1 has loss 0 and no gradient.
@@ -128,7 +128,9 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
  *   dloss    device fp32[M], the gradient of each row's loss; only read when dX or dW is given
  *   loss     out: fp32[M], or NULL
  *   dX       out: bf16 M x K, or NULL;  dW  out: bf16 V x K, or NULL
- *   workspace  qlora_head_loss_workspace_bytes(M, K, V, dX != NULL, dW != NULL), 256-byte aligned */
+ *   workspace  qlora_head_loss_workspace_bytes(M, K, V, dX != NULL, dW != NULL), 256-byte aligned:
+ *              a packed copy of X and pieces of up to 128 MB; with dX fp32 sums of its size; with dW also the
+ *              exponentials, 3 bytes each, while they are up to 2^29 (beyond, the logits are computed twice) */
 size_t qlora_head_loss_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t need_dx, int32_t need_dw);
 nf4_status qlora_head_loss(const void* X, int64_t M, int64_t K, const void* W, int64_t V, const int64_t* targets,
                            int64_t ignore_index, const float* dloss, float* loss, void* dX, void* dW,
