@@ -201,8 +201,8 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
 static nf4_status check_head(int64_t M, int64_t K, int64_t V) {
     if (M < 0 || K < 1 || V < 1) return fail(NF4_ERR_ARG, "M must be >= 0, K and V at least 1");
     if (K % 64 || K >= ((int64_t)1 << 20)) return fail(NF4_ERR_UNSUPPORTED, "K must be a multiple of 64 below 2^20");
-    if (M >= ((int64_t)1 << 22) || V >= ((int64_t)1 << 23) || ((M + 255) / 256) * ((V + 255) / 256) >= ((int64_t)1 << 23))
-        return fail(NF4_ERR_UNSUPPORTED, "M must be below 2^22, V below 2^23, ceil(M/256) * ceil(V/256) below 2^23");
+    if (M >= ((int64_t)1 << 22) || V >= ((int64_t)1 << 23) || ((M + 255) / 256) * ((V + 255) / 256) >= ((int64_t)1 << 23) - 8)
+        return fail(NF4_ERR_UNSUPPORTED, "M must be below 2^22, V below 2^23, ceil(M/256) * ceil(V/256) below 2^23 - 8");
     return NF4_OK;
 }
 
