@@ -179,6 +179,13 @@ def test_attention_few_tokens_behind_many_keys(dim, kv, heads):
     check_attention(c, max_new=40, max_length=200000)
 
 
+@pytest.mark.parametrize("dim,page,counts", [(128, 64, [300, 290, 45, 0]), (64, 16, [310, 200, 90, 3]), (64, 32, [500, 333, 270, 1]),
+                                             (128, 16, [400, 300, 350, 40]), (256, 128, [70, 200, 1, 100])])
+def test_attention_many_blocks(dim, page, counts):
+    # more waves than run at once: blocks of several sequences in the order of their keys, alone and two to a block
+    check_attention(Case([150, 10, 400, 33], counts, page=page, kv=2, heads=64, dim=dim, seed=sum(counts)), max_new=max(counts), max_length=550)
+
+
 def test_attention_long_split():
     c = Case([40000, 3, 20011], [1, 1, 2], page=64, kv=1, heads=4, dim=128, seed=9)
     check_attention(c, max_new=2, max_length=40001)
