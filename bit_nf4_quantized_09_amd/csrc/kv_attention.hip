@@ -819,7 +819,8 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // ragged batch's last chunks end together) at the stated lengths, but chunks of 1024 keys where 1024 workgroups are left
 // then, for a workgroup's start, end and join cost as much as some 200 keys (two sequences of 120001 keys, 8 kv
 // heads: chunks of 512 keys 81 us, 1024 73; of 24 sequences of up to 4096, 64 heads: 1536 keys 132 us, half of that 149, twice 199),
-// and of at least 256 keys.  For k_attend_block, where there are fewer blocks than waves that run at once, two or four
+// and of at least 256 keys; up to 768 keys stay whole, for the join's launch costs more (4 sequences of up to 600 keys,
+// heads of 128: 7.0 us, 8.9 in chunks; of up to 900: 9.0 and 9.0, heads of 256 14.4 and 11.9).  For k_attend_block, where there are fewer blocks than waves that run at once, two or four
 // waves share a block's keys (4 prompts of up to 534 tokens, 8 heads of 64: 12.5 us, 22.5 alone; 2 of 1277, 16 heads of
 // 128: 31 and 35; but 3 of 1500, 32 heads: 134 and 126, and heads of 256, whose parts are as large as a step's
 // work: 24 and 10 for 3 of 76 tokens), and chunks only where there are still fewer than 1024 waves, one for
@@ -847,7 +848,8 @@ static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int 
         const int64_t r = most_rows < KV_FEW ? most_rows : KV_FEW;
         p.rows.tiles = (int)((r + 15) / 16);
         const int64_t groups = (int64_t)seqs * c.heads * p.rows.tiles, wide = keys * p.rows.tiles / 1024;
-        chunks(p.rows, groups, 4096, KV_WAVES * KV_STEP, wide < 256 ? 256 : wide < 1024 ? wide / 128 * 128 : 1024, (size_t)seqs * c.heads * KV_FEW);
+        const int64_t least = max_length <= 768 ? 768 : wide < 256 ? 256 : wide < 1024 ? wide / 128 * 128 : 1024;
+        chunks(p.rows, groups, 4096, KV_WAVES * KV_STEP, least, (size_t)seqs * c.heads * KV_FEW);
     }
     if (p.block.on) {
         const int64_t rows = block_rows(c.dim);
