@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -190,6 +191,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 9, [&]() -> PyObject* {
         const at::Tensor &positions = tensor(a[5], "positions"), &q = tensor(a[6], "q");
         want_gpu(q, "q");
+        const c10::DeviceGuard on(q.device());
         const at::ScalarType type = q.scalar_type();
         if (type != at::kFloat && type != at::kBFloat16) bad(std::string("q must be Float or BFloat16, got ") + type_name(type));
         want_dense(positions, "positions", at::kInt, q);
@@ -230,6 +232,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> PyObject* {
         const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
         want_gpu(k, "k");
+        const c10::DeviceGuard on(k.device());
         const qlora_kv_cache c = cache_of(a[0], a[1], k);
         const int64_t T = k.dim() > 0 ? k.size(0) : 0;
         const qlora_kv_batch b = batch_of(a[4], a[5], a[6], T, k);
@@ -254,6 +257,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 9, [&]() -> PyObject* {
         const at::Tensor& q = tensor(a[2], "q");
         want_gpu(q, "q");
+        const c10::DeviceGuard on(q.device());
         const qlora_kv_cache c = cache_of(a[0], a[1], q);
         const int64_t T = q.dim() > 0 ? q.size(0) : 0;
         const qlora_kv_batch b = batch_of(a[3], a[4], a[5], T, q);
@@ -276,6 +280,7 @@ PyObject* head_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 6, [&]() -> PyObject* {
         const at::Tensor &X = tensor(a[0], "X"), &W = tensor(a[1], "W"), &targets = tensor(a[2], "targets");
         want_gpu(X, "X");
+        const c10::DeviceGuard on(X.device());
         want_dense(X, "X", at::kBFloat16, X);
         want_dense(W, "W", at::kBFloat16, X);
         want_dense(targets, "targets", at::kLong, X);
