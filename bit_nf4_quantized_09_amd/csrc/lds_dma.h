@@ -17,12 +17,17 @@ __device__ __forceinline__ dma_rsrc make_dma_rsrc(const void* base, int64_t byte
 // assembly, because the compiler makes transposing LDS reads wait for every such load of the
 // builtin's kind, whichever part of LDS it fills; the kernels that use it wait for it themselves
 // (s_waitcnt vmcnt).  The compiler counts the loads it knows of, so its own waits with these among
-// them are only stricter.  Nothing else in those kernels uses m0.
+// them are only stricter.  It puts no wait states inside or right before a string of assembly, so
+// the string has its own: the load reads M0, which needs one after the scalar write, and its scalar
+// operands may come from a vector instruction (v_readfirstlane), which needs five.  The scalar write
+// counts as one of these and s_nop 3 as four; they pass behind the matrix instructions in flight.
 // NT: nontemporal, for what is read once.
 template <bool NT = false>
 __device__ __forceinline__ void load_to_lds(dma_rsrc r, uint32_t at, uint32_t voff, uint32_t soff) {
-    if constexpr (NT) asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(at), "v"(voff), "s"(r), "s"(soff) : "memory");
-    else asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voff), "s"(r), "s"(soff) : "memory");
+    if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(at), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voff), "s"(r), "s"(soff) : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)(p);
