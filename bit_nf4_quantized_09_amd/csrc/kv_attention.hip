@@ -282,8 +282,8 @@ __device__ __forceinline__ float split_query(const uint16_t* row, int quarter, u
     top = fmaxf(top, __shfl_xor(top, 32));
     int e = 0;
     if (top > 0.0f && top < INFINITY) frexpf(top, &e);            // top = [0.5, 1) 2^e
-    e = e < -110 ? -110 : e;                                      // (both powers stay finite)
-    const float up = __uint_as_float((uint32_t)(127 + (e > 110 ? -102 : 8 - e)) << 23);
+    e = e < -110 ? -110 : e;                                      // (e <= 128: both powers are finite and normal)
+    const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
 #pragma unroll
     for (int p = 0; p < D / 64; ++p)
 #pragma unroll

@@ -107,6 +107,8 @@ nf4_status qlora_kv_append(const qlora_kv_cache* cache, const qlora_kv_batch* ba
 /* Causal attention of the batch's tokens over the cache, which already holds them:
  *   out[t] = sum_j p_j v_j,  p = softmax_j(scale * q[t] . k_j),  j = 0 .. position of t
  * Head h of the queries reads kv head h / (heads / kv_heads).
+ * Sums of queries times codes are held in fp32 before any scale is applied to them: queries up
+ * to 2^110 in magnitude stay within it at any head size.
  *   q, out      bf16 [tokens][heads][head_dim], rows 16-byte aligned; heads a multiple of kv_heads
  *   max_new     the most new tokens of one sequence (at least 1), and
  *   max_length  the most positions of one sequence, new tokens included: they size the launch.

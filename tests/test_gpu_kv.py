@@ -208,6 +208,18 @@ def test_attention_zero_and_negative_scale():
         assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * reach[..., None])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("counts", [[1], [40]])
+@pytest.mark.parametrize("top", [2.0 ** 109, 2.0 ** 110, 1.9 * 2.0 ** 110])
+def test_attention_of_large_queries(dim, counts, top):
+    # queries near the limit where sums of 256 products with codes of 448 leave fp32, over keys of 2^-45: scores of order 1
+    c = Case([300], counts, page=16, kv=2, heads=4, dim=dim, seed=dim)
+    c.cache.scales[:, 0] = 2.0 ** -50
+    q = c.q.float()
+    c.q = (q / q.abs().amax(-1, keepdim=True) * top).bfloat16()
+    check_attention(c, scale=2.0 ** 45 / top / math.sqrt(dim))
+
+
 def test_attention_scales_far_apart():
     c = Case([600], [1], page=16, kv=1, heads=2, dim=64, seed=12)
     r = np.random.RandomState(5)
