@@ -183,7 +183,7 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
         BatchView b;
         if (!q || !out) return fail(NF4_ERR_ARG, "q or out is NULL");
         if (nf4_status st = check_attention(cache, batch, q->heads, max_new, max_length, c, b)) return st;
-        if (!isfinite(scale)) return fail(NF4_ERR_ARG, "scale must be finite");
+        if (!(fabsf(scale) < 0x1p127f)) return fail(NF4_ERR_ARG, "scale must be below 2^127");
         if (b.tokens == 0) return NF4_OK;
         HeadsView qv, ov;
         if (nf4_status st = check_heads(q, "q", c.dim, 2, true, qv)) return st;

@@ -92,6 +92,13 @@ struct TileScales {
     int end;                              // keys of the tile that count lie below; 0: none, and the scales are anything
 };
 __device__ __forceinline__ float key_scale(const TileScales& t) { return t.end > 0 ? __uint_as_float(t.k) : 1.0f; }
+// The factor from a product to its score is neither zero nor infinite: a hidden product is -inf and has to stay it, and
+// a product of zero has to stay zero.
+__device__ __forceinline__ float score_factor(float f) { return __builtin_amdgcn_fmed3f(f, 0x1p-126f, 0x1.fffffep127f); }
+// A query's part of it, such that the product with any key scale (2^-50 .. 2^50) is so without a look at each step (1.5%
+// of a prompt's time).  Products reach 2^25 where a query is scaled, so scores below the lower end are below 2^-23
+// and those past the upper end are 2^5 apart at least: neither end changes a weight.
+__device__ __forceinline__ float query_factor(float f) { return __builtin_amdgcn_fmed3f(f, 0x1p-98f, 0x1p77f); }
 __device__ __forceinline__ float value_exponent(const TileScales& t) {
     return t.end > 0 ? (float)((int)((t.v >> 23) & 0xFFu) - 127) : 0.0f;
 }
@@ -186,7 +193,7 @@ template <int D>
 __device__ __forceinline__ f16x8 weights_of(RowsState<D>& st, const f32x4* s, const float* f, const float* vf, const float* ev) {
     float top = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)               // f >= 0: the largest product has the largest score
+    for (int t = 0; t < 2; ++t)               // f > 0: the largest product has the largest score
         top = fmaxf(top, __fmaf_rn(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])), f[t], vf[t]));
     if (__any(top > st.m + KV_SLACK)) {
         top = fmaxf(top, __shfl_xor(top, 16));
@@ -387,7 +394,7 @@ void k_attend_rows(AttendArgs a) {
                         const bf16x8 kf = codes_to_bf16((u & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), 1.0f);
                         s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[u], s, 0, 0, 0);
                     }
-                    f[t] = key_scale(x.scale[t]) * a.scale2;
+                    f[t] = score_factor(key_scale(x.scale[t]) * a.scale2);
                     vf[t] = value_exponent(x.scale[t]);
                     ev[t] = __builtin_amdgcn_exp2f(-vf[t]);
                     sc[t] = hide(s, first_key(i) + 16 * t, quarter, low, position, x.scale[t].end, past);
@@ -560,11 +567,11 @@ void k_attend_block(AttendArgs a) {
             const uint16_t* qp = (const uint16_t*)a.q.data + (int64_t)(begin + token) * a.q.token_stride +
                                  (int64_t)qhead * a.q.head_stride;
             if constexpr (!F8) {
-                qs[c] = a.scale2;
+                qs[c] = query_factor(a.scale2);
 #pragma unroll
                 for (int s = 0; s < KSTEPS; ++s) qf[c][s] = query_piece(qp + 64 * (s >> 1) + 16 * quarter + 8 * (s & 1), a.flip);
             } else {
-                qs[c] = split_query<D>(qp, quarter, a.flip, q1[c], q2[c]) * a.scale2;
+                qs[c] = query_factor(split_query<D>(qp, quarter, a.flip, q1[c], q2[c]) * a.scale2);
             }
 #pragma unroll
             for (int i = 0; i < TILES; ++i) st[c].acc[i] = f32x4{};
@@ -880,8 +887,7 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
     a.q = q;
     a.out = out;
     a.group = q.heads / c.heads;
-    // (not below 2^-70, so that no hidden score meets a factor of zero: a scale of zero still weighs all keys alike)
-    a.scale2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-70f);
+    a.scale2 = fabsf(scale) * 1.4426950408889634f;
     a.flip = scale < 0.0f ? 0x80008000u : 0u;
     a.limit = !p.block.on ? 0x7FFFFFFF : p.rows.on ? KV_FEW : 0;
     auto part = [&](const AttendPart& q, void* at) {

@@ -128,6 +128,13 @@ def test_attention_refusals():
     assert attention_status(length=100000, ws=ctypes.c_void_p(4096 + 16), wsb=size) == ARG
 
 
+def test_attention_scale_refusals():
+    for scale in (float("inf"), -float("inf"), 2.0 ** 127, -3e38):
+        assert attention_status(scale=scale) == ARG
+        assert "scale" in nf4.load_library().nf4_last_error().decode()
+    assert attention_status(scale=-1.7e38, length=100000) == WORKSPACE       # below 2^127: the next check is met
+
+
 def loss_status(X=SOME, M=8, K=64, W=SOME, V=100, t=SOME, dl=SOME, loss=SOME, dX=SOME, dW=SOME, ws=SOME, wsb=1 << 40):
     return dec._library().qlora_head_loss(X, M, K, W, V, t, -100, dl, loss, dX, dW, ws, wsb, None)
 

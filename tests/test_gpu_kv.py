@@ -220,6 +220,19 @@ def test_attention_of_large_queries(dim, counts, top):
     check_attention(c, scale=2.0 ** 45 / top / math.sqrt(dim))
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("counts", [[1], [40], [300]])
+@pytest.mark.parametrize("size,scale", [(1e-28, None), (1e-38, None), (1e-7, 0.0), (1.0, 1e-300), (1e-7, 1e-30), (1.0, 1e38)])
+def test_attention_factors_at_the_ends(dim, counts, size, scale):
+    # keys of nothing on pages of the smallest scale, tiny queries, scales of zero, of zero as fp32 and of 2^126: every
+    # key that is seen weighs the same, and none that is not
+    c = Case([300], counts, page=16, kv=2, heads=4, dim=dim, seed=dim)
+    c.cache.codes[:, 0] = 0
+    c.cache.scales[:, 0] = 2.0 ** -50
+    c.q = (c.q.float() * size).bfloat16()
+    check_attention(c, scale=scale)
+
+
 def test_attention_scales_far_apart():
     c = Case([600], [1], page=16, kv=1, heads=2, dim=64, seed=12)
     r = np.random.RandomState(5)
