@@ -255,14 +255,25 @@ __device__ __forceinline__ f32x4 hide(f32x4 s, int key, int quarter, int low, in
     return s;
 }
 
-// A negative scale: the queries change sign instead.
-__device__ __forceinline__ bf16x8 query_piece(const uint16_t* p, uint32_t flip) {
-    uint4 w = *reinterpret_cast<const uint4*>(p);
-    w.x ^= flip;
-    w.y ^= flip;
-    w.z ^= flip;
-    w.w ^= flip;
-    return __builtin_bit_cast(bf16x8, w);
+// A query row as operands of the bf16 products: the lane's dimensions of product s, in the order of the key pieces.  A
+// negative scale changes the queries' sign instead.  An infinity makes every score infinite or NaN, and a row
+// of nothing but -inf would look like one without keys: it becomes a NaN at once.
+template <int D>
+__device__ __forceinline__ void load_query(const uint16_t* row, int quarter, uint32_t flip, bf16x8 (&q)[D / 32]) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        uint4 w = *reinterpret_cast<const uint4*>(row + 64 * (s >> 1) + 16 * quarter + 8 * (s & 1));
+#pragma unroll
+        for (uint32_t x : {w.x, w.y, w.z, w.w}) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x & 0x7FFF7FFFu));
+        w.x ^= flip;
+        w.y ^= flip;
+        w.z ^= flip;
+        w.w ^= flip;
+        q[s] = __builtin_bit_cast(bf16x8, w);
+    }
+    if (top[0] >= 0x7F80 || top[1] >= 0x7F80) q[0][0] = __builtin_bit_cast(__bf16, (unsigned short)0x7FC0);
 }
 
 // A query row for the 8-bit matrix instructions, in the order of the key pieces: times a power of two
@@ -346,14 +357,11 @@ void k_attend_rows(AttendArgs a) {
         int keys = before + last_row / a.group + 1;           // keys the tile's last row sees
         const bool past = keys > reach;
         keys = past ? reach : keys;
-        // queries: the lane's dimensions of MFMA step s, in the order of the key pieces
         bf16x8 qf[KSTEPS];
         {
             const uint16_t* qp = (const uint16_t*)a.q.data + (int64_t)(begin + token) * a.q.token_stride +
                                  (int64_t)qhead * a.q.head_stride;
-#pragma unroll
-            for (int s = 0; s < KSTEPS; ++s)
-                qf[s] = query_piece(qp + 64 * (s >> 1) + 16 * quarter + 8 * (s & 1), a.flip);
+            load_query<D>(qp, quarter, a.flip, qf);
         }
         RowsState<D> st;
 #pragma unroll
@@ -568,8 +576,7 @@ void k_attend_block(AttendArgs a) {
                                  (int64_t)qhead * a.q.head_stride;
             if constexpr (!F8) {
                 qs[c] = query_factor(a.scale2);
-#pragma unroll
-                for (int s = 0; s < KSTEPS; ++s) qf[c][s] = query_piece(qp + 64 * (s >> 1) + 16 * quarter + 8 * (s & 1), a.flip);
+                load_query<D>(qp, quarter, a.flip, qf[c]);
             } else {
                 qs[c] = query_factor(split_query<D>(qp, quarter, a.flip, q1[c], q2[c]) * a.scale2);
             }

@@ -109,6 +109,7 @@ nf4_status qlora_kv_append(const qlora_kv_cache* cache, const qlora_kv_batch* ba
  * Head h of the queries reads kv head h / (heads / kv_heads).
  * Sums of queries times codes are held in fp32 before any scale is applied to them: queries up
  * to 2^110 in magnitude stay within it at any head size.
+ * A query with a non-finite value that sees any key gives NaN.
  *   q, out      bf16 [tokens][heads][head_dim], rows 16-byte aligned; heads a multiple of kv_heads
  *   scale       of any sign, below 2^127 in magnitude (0: every key that is seen weighs the same)
  *   max_new     the most new tokens of one sequence (at least 1), and

@@ -241,6 +241,21 @@ def test_attention_scales_far_apart():
     check_attention(c, max_new=1, max_length=601)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("counts", [[1, 1], [40, 1]])
+@pytest.mark.parametrize("odd", [-math.inf, math.inf, math.nan])
+def test_attention_of_non_finite_queries(dim, counts, odd):
+    # keys of ones: an infinity makes every score the same one.  Such rows are NaN, others untouched
+    c = Case([30, 77], counts, page=16, kv=1, heads=2, dim=dim, seed=dim)
+    c.cache.codes[:, 0] = 0x38
+    clean = nf4.kv_attention(c.cache, c.q, *c.meta())
+    c.q = c.q.clone()
+    c.q[-1, 0, dim - 1] = c.q[:-1, 1, 3] = odd
+    out = nf4.kv_attention(c.cache, c.q, *c.meta())
+    assert torch.isnan(out[-1, 0]).all() and torch.isnan(out[:-1, 1]).all()
+    assert torch.equal(out[-1, 1], clean[-1, 1]) and torch.equal(out[:-1, 0], clean[:-1, 0])
+
+
 def test_attention_hides_what_is_not_there():
     # NaN codes past the end of a sequence, on spare pages and in later tokens' keys
     c = Case([20, 5], [6, 1], page=16, kv=1, heads=2, dim=128, seed=13)
