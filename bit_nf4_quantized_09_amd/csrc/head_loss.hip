@@ -582,11 +582,13 @@ void k_head_split(HeadArgs a) {
 }
 
 // A row's loss from its target's logit and the others' log-sum (both base 2): the loss, lse
-// (base 2) and 1 - p of the target.
+// (base 2) and 1 - p of the target.  A target's logit of -inf has an infinite loss and p = 0; +inf (an overflow) and NaN
+// leave nothing that is known.
 struct RowLoss {
     float loss, lse, rest;
 };
 __device__ __forceinline__ RowLoss row_loss(float z, float others) {
+    if (!(z < INFINITY)) return RowLoss{NAN, NAN, NAN};
     const float d = z - others;
     const float tail = log1pf(exp2f(-fabsf(d)));
     return RowLoss{d >= 0.0f ? tail : tail - d * LN2, fmaxf(z, others) + tail * LOG2E, 1.0f / (1.0f + exp2f(d))};
@@ -662,7 +664,7 @@ void k_head_target(const uint16_t* X, const uint16_t* W, int64_t M, int64_t K, i
     }
     if (lane == 0) {
         zy[m] = sum * LOG2E;
-        ref[m] = rintf(sum * LOG2E);
+        ref[m] = fmaxf(rintf(sum * LOG2E), -0x1.fffffep127f);       // (finite for a logit of -inf: any other raises it)
         total[m] = 0.0f;
     }
 }
@@ -747,8 +749,7 @@ void k_head_join(JoinArgs a) {
     a.factor[m] = f;
     if (!a.last) return;
     const float z = a.zy[m], g = a.dloss[m];
-    RowLoss r = row_loss(z, now + log2f(total));
-    if (!(fabsf(z) < INFINITY)) r = RowLoss{NAN, NAN, NAN};
+    const RowLoss r = row_loss(z, now + log2f(total));
     if (a.loss) a.loss[m] = r.loss;
     a.ends[m] = make_float2(g * __builtin_amdgcn_exp2f(now - r.lse), g * r.rest);
     a.rows[m] = make_float4(r.lse, r.rest, g, __int_as_float((int)target));

@@ -126,6 +126,8 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
  *   loss[m] = log sum_v exp(z[m][v]) - z[m][targets[m]]
  *   dX = G W,  dW = G^T X,  G[m][v] = dloss[m] (softmax(z[m])[v] - [v == targets[m]])
  * A row whose target is ignore_index or lies outside 0 .. V-1 has loss 0 and no gradient.
+ * A target's logit of -inf (an fp32 sum that overflows) has loss +inf; one of +inf, and any
+ * logit of +inf or NaN, has loss NaN; the same with and without gradients.
  *   X        bf16 M x K, W bf16 V x K, both dense; K a multiple of 64, K < 2^20;
  *            0 <= M < 2^22, 1 <= V < 2^23, ceil(M/256) * ceil(V/256) < 2^23 - 8
  *   targets  device int64[M]

@@ -145,6 +145,41 @@ def test_non_finite_rows_stay_alone():
     assert torch.equal(dX[keep], good[1][keep]) and torch.isnan(dX[9]).all()
 
 
+@pytest.mark.parametrize("M,V,K", [(3, 500, 64), (80, 600, 128), (700, 2000, 576), (2048, 40000, 128)])
+@pytest.mark.parametrize("row", [1, 2])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_target_logits(M, V, K, row, sign):
+    # a product of 3e38 and 3e38 overflows fp32; every other logit of that row is zero (row 1) or an ordinary one (row 2).
+    # With and without gradients the row's loss is the same, and the other rows' are what they were
+    X, W, t, dl = inputs(M, V, K, seed=M)
+    W[:, 0] = 0
+    X[1] = 0
+    t[t == t[row]] = (t[row] + 1) % V
+    t[row] = (t[row] - 1) % V
+    W[t[row], 0] = sign * 3e38
+    X[:, 0] = 0
+    good = nf4.head_loss(X, W, t, dloss=dl)
+    X[row, 0] = 3e38
+    alone = nf4.head_loss(X, W, t)[0]
+    loss, dX, dW = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    keep = torch.arange(M, device="cuda") != row
+    for x in (alone, loss):
+        assert torch.isnan(x[row]) if sign > 0 else x[row] == math.inf
+        assert torch.all((x[keep] - good[0][keep]).abs() <= 2.0 ** -20 * (good[0][keep].abs() + 1))
+    assert torch.equal(dX[keep], good[1][keep])
+    if sign > 0:
+        assert torch.isnan(dX[row]).all()
+        return
+    # p of the target is 0: dX = dloss (sum_v p_v W_v - W_y), bounded as in check()
+    z = X.double() @ W.double().t()
+    z[row, t[row]] = -math.inf
+    p = z[row].softmax(0)
+    want = dl[row].double() * (p @ W.double() - W[t[row]].double())
+    slack = 2.0 ** -8 * want.abs() + 2.0 ** -7 * dl[row].double().abs() * (p @ W.double().abs() + W[t[row]].double().abs())
+    assert torch.all((dX[row].double() - want).abs()[1:] <= slack[1:])
+    assert torch.isfinite(dW[:, 1:]).all()
+
+
 def test_equal_factors_lose_nothing():
     # a mean's factor 1/count is no power of two: it must not round every row alike
     X, W, t, _ = inputs(384, 3000, 512, seed=11)
