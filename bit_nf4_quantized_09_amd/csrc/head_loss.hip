@@ -625,10 +625,11 @@ void k_head_rows(const float2* part, const float* zy, const int64_t* targets, in
 }
 
 // Target logits (base 2) and the first references, one wave per row; the last workgroup: the largest
-// finite |dloss| of the rows that count.
+// finite |dloss| of the rows that count.  With `counted`: X with zeros for the rows that do not count, for dW, whose sums over
+// tokens would take a NaN from a row of no weight (0 NaN = NaN).
 __global__ __launch_bounds__(256)
-void k_head_target(const uint16_t* X, const uint16_t* W, int64_t M, int64_t K, int64_t V, const int64_t* targets,
-                   int64_t ignore, float* zy, float* ref, float* total, const float* dloss, uint32_t* top) {
+void k_head_target(const uint16_t* __restrict__ X, const uint16_t* __restrict__ W, int64_t M, int64_t K, int64_t V, const int64_t* targets,
+                   int64_t ignore, float* zy, float* ref, float* total, const float* dloss, uint32_t* top, uint16_t* __restrict__ counted) {
     const int lane = threadIdx.x & 63;
     if (blockIdx.x == gridDim.x - 1) {
         __shared__ float join[4];
@@ -649,18 +650,36 @@ void k_head_target(const uint16_t* X, const uint16_t* W, int64_t M, int64_t K, i
     if (m >= M) return;
     const int64_t target = targets[m];
     float sum = 0.0f;
+    uint4* copy = reinterpret_cast<uint4*>(counted + m * K);
     if (head_live(target, V, ignore)) {
         const uint4* x = reinterpret_cast<const uint4*>(X + m * K);
         const uint4* w = reinterpret_cast<const uint4*>(W + target * K);
-        for (int64_t i = lane; i < K / 8; i += 64) {
-            float a[8], b[8];
-            Vec16<uint16_t>::unpack(x[i], a);
-            Vec16<uint16_t>::unpack(w[i], b);
+        // (four vectors at a time: one by one their loads wait for each other)
+        for (int64_t i0 = lane; i0 < K / 8; i0 += 256) {
+            uint4 xv[4], wv[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) sum = __fmaf_rn(a[u], b[u], sum);
+            for (int j = 0; j < 4; ++j) {
+                const int64_t i = i0 + 64 * j;
+                xv[j] = wv[j] = make_uint4(0, 0, 0, 0);
+                if (i < K / 8) {
+                    xv[j] = x[i];
+                    wv[j] = w[i];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a[8], b[8];
+                if (counted && i0 + 64 * j < K / 8) copy[i0 + 64 * j] = xv[j];
+                Vec16<uint16_t>::unpack(xv[j], a);
+                Vec16<uint16_t>::unpack(wv[j], b);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) sum = __fmaf_rn(a[u], b[u], sum);
+            }
         }
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    } else if (counted) {
+        for (int64_t i = lane; i < K / 8; i += 64) copy[i] = make_uint4(0, 0, 0, 0);
     }
     if (lane == 0) {
         zy[m] = sum * LOG2E;
@@ -774,8 +793,10 @@ struct ProductArgs {
     int64_t V, ignore;
 };
 
-// Four values of a finished row of dX; u: the target's row of W there.
-__device__ __forceinline__ uint2 head_dx4(f32x4 y, float2 row, uint2 u) {
+// Four values of a finished row of dX; u: the target's row of W there.  A row that does not count (live: 0) is zero
+// whatever its sums hold.
+__device__ __forceinline__ uint2 head_dx4(f32x4 y, float2 row, uint2 u, bool live) {
+    if (!live) return make_uint2(0, 0);
     return make_uint2(pack_bf16x2(row.x * y[0] - row.y * bf16_lo(u.x), row.x * y[1] - row.y * bf16_hi(u.x)),
                       pack_bf16x2(row.x * y[2] - row.y * bf16_lo(u.y), row.x * y[3] - row.y * bf16_hi(u.y)));
 }
@@ -835,6 +856,7 @@ void k_head_product(ProductArgs a) {
         f32x4 old[16];
         uint2 wy[16];
         float2 end[16];
+        uint32_t live = 0;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
             const int64_t r = ri + 2 * q + h;
@@ -845,7 +867,9 @@ void k_head_product(ProductArgs a) {
             if (ADD && in) old[q] = *reinterpret_cast<const f32x4*>(sums + r * a.N + n) * a.factor[r];
             if (OUT == OUT_DX && in) {
                 const int64_t target = a.targets[r];
-                wy[q] = *reinterpret_cast<const uint2*>(a.W + (head_live(target, a.V, a.ignore) ? target * a.N : 0) + n);
+                const bool on = head_live(target, a.V, a.ignore);
+                live |= (on ? 1u : 0u) << q;
+                wy[q] = *reinterpret_cast<const uint2*>(a.W + (on ? target * a.N : 0) + n);
                 end[q] = a.ends[r];
             }
         }
@@ -867,7 +891,7 @@ void k_head_product(ProductArgs a) {
                 y *= head_scale(a.top);
                 *reinterpret_cast<uint2*>(a.out + r * a.N + n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
             } else {
-                *reinterpret_cast<uint2*>(a.out + r * a.N + n) = head_dx4(y, end[q], wy[q]);
+                *reinterpret_cast<uint2*>(a.out + r * a.N + n) = head_dx4(y, end[q], wy[q], live >> q & 1);
             }
         }
     }
@@ -984,11 +1008,12 @@ void k_head_finish(ProductArgs a, uint16_t* out) {
     const int64_t r = blockIdx.x, n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
     if (n >= a.N) return;
     const int64_t target = a.targets[r];
-    const uint2 w = *reinterpret_cast<const uint2*>(a.W + (head_live(target, a.V, a.ignore) ? target * a.N : 0) + n);
+    const bool live = head_live(target, a.V, a.ignore);
+    const uint2 w = *reinterpret_cast<const uint2*>(a.W + (live ? target * a.N : 0) + n);
     f32x4 y = {};
 #pragma unroll 8
     for (int s = 0; s < a.splits; ++s) y += *reinterpret_cast<const f32x4*>(a.sum + (s * a.out_rows + r) * a.N + n);
-    *reinterpret_cast<uint2*>(out + r * a.N + n) = head_dx4(y, a.ends[r], w);
+    *reinterpret_cast<uint2*>(out + r * a.N + n) = head_dx4(y, a.ends[r], w, live);
 }
 
 // G^T of a piece from its E: G = dloss / max|dloss| (E 2^(R - lse) - the target's 1 - p), R the reference that the
@@ -1074,7 +1099,7 @@ struct HeadPlan {
     bool keep;                // every piece's E is kept until dW
     bool few_dx;              // dX by k_head_few_product
     int splits;               // parts of dX's contraction
-    size_t top, zy, ref, total, factor, ends, of_rows, part, Xp, E, low, G, sum, bytes;
+    size_t top, zy, ref, total, factor, ends, of_rows, part, Xp, counted, E, low, G, sum, bytes;
     int64_t blocks(int64_t M) const { return M <= 32 ? 1 : (M + 63) / 64; }                   // of 64 tokens (one of 32)
     // tiles of the logits (few: four to a workgroup)
     int64_t tiles(int64_t vocabulary) const { return (vocabulary + 127) / 128 * (few ? 4 : 1); }
@@ -1144,6 +1169,7 @@ static HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool dx, bool dw) {
     p.of_rows = take(4 * row);
     p.part = take((size_t)p.Mp * p.tiles(grad && p.piece < V ? p.piece : V) * sizeof(float2));
     p.Xp = take((size_t)p.Mp * K * 2);
+    p.counted = take(dw ? (size_t)M * K * 2 : 0);
     p.E = take(grad ? p.piece_bytes() * (p.keep ? p.pieces : 1) : 0);
     p.low = take(p.keep ? p.piece_bytes() / 2 * p.pieces : 0);
     p.G = p.keep ? take(p.piece_bytes()) : p.E;
@@ -1223,6 +1249,7 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     float* ref = (float*)(base + p.ref);
     float* total = (float*)(base + p.total);
     uint32_t* top = (uint32_t*)(base + p.top);
+    uint16_t* counted = dW ? (uint16_t*)(base + p.counted) : nullptr;
     ProductArgs d{};
     d.A = a.out;
     d.N = K;
@@ -1236,7 +1263,7 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     d.ignore = ignore;
     d.splits = p.splits;
     hipLaunchKernelGGL(k_head_target, dim3((uint32_t)((M + 3) / 4 + 1)), dim3(256), 0, s, X, W, M, K, V, targets, ignore, a.zy,
-                       ref, total, dloss, top);
+                       ref, total, dloss, top, counted);
     const int64_t piece_values = (int64_t)(p.piece_bytes() / 2);
     int64_t at = 0;                       // the piece, where each has a place of its own
     for_pieces(p, V, [&](int64_t v0, int64_t rows, bool last) {
@@ -1273,7 +1300,7 @@ hipError_t launch_head_loss(const uint16_t* X, int64_t M, int64_t K, const uint1
     d.splits = 1;
     d.top = top;
     d.A = (uint16_t*)(base + p.G);
-    d.B = X;
+    d.B = counted;
     d.P = M;
     d.steps = (int)((M + HL_K - 1) / HL_K);
     d.a_steps = p.Mp / HL_K;

@@ -125,7 +125,8 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
 /* Softmax cross entropy of a vocabulary head, z = X W^T, without fp32 logits in memory:
  *   loss[m] = log sum_v exp(z[m][v]) - z[m][targets[m]]
  *   dX = G W,  dW = G^T X,  G[m][v] = dloss[m] (softmax(z[m])[v] - [v == targets[m]])
- * A row whose target is ignore_index or lies outside 0 .. V-1 has loss 0 and no gradient.
+ * A row whose target is ignore_index or lies outside 0 .. V-1 has loss 0 and no gradient, whatever
+ * X, dloss (and, for its row of dX, W) hold: its row of dX is zero, and dW takes nothing from it.
  * A target's logit of -inf (an fp32 sum that overflows) has loss +inf; one of +inf, and any
  * logit of +inf or NaN, has loss NaN; the same with and without gradients.
  *   X        bf16 M x K, W bf16 V x K, both dense; K a multiple of 64, K < 2^20;
@@ -135,7 +136,8 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
  *   loss     out: fp32[M], or NULL
  *   dX       out: bf16 M x K, or NULL;  dW  out: bf16 V x K, or NULL
  *   workspace  qlora_head_loss_workspace_bytes(M, K, V, dX != NULL, dW != NULL), 256-byte aligned:
- *              a packed copy of X and pieces of up to 128 MB; with dX fp32 sums of its size; with dW also the
+ *              a packed copy of X and pieces of up to 128 MB; with dX fp32 sums of its size; with dW another copy of X
+ *              (its ignored rows zero) and the
  *              exponentials, 3 bytes each, while they are up to 2^29 (beyond, the logits are computed twice) */
 size_t qlora_head_loss_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t need_dx, int32_t need_dw);
 nf4_status qlora_head_loss(const void* X, int64_t M, int64_t K, const void* W, int64_t V, const int64_t* targets,

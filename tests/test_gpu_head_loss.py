@@ -128,6 +128,29 @@ def test_ignored_targets():
     assert not loss.any() and not dX.any()
 
 
+@pytest.mark.parametrize("M,V,K", [(3, 500, 64), (33, 2000, 128), (80, 600, 128), (700, 2000, 576), (2048, 40000, 128),
+                                   (1024, 32000, 6144), (4096, 131200, 64)])
+def test_ignored_rows_hold_anything(M, V, K):
+    # what ignored rows of X and dloss hold changes nothing: not even a bit of the others, nor of dW
+    X, W, t, dl = inputs(M, V, K, seed=M)
+    t[1], t[M - 1] = -100, V
+    want = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    only = nf4.head_loss(X, W, t)[0]
+    X[1], X[M - 1, 5], dl[1], dl[M - 1] = math.nan, math.inf, math.nan, math.inf
+    got = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+    assert torch.equal(nf4.head_loss(X, W, t)[0], only)
+    assert not got[0][[1, M - 1]].any() and not got[1][[1, M - 1]].any()
+    # a row of W that is not finite reaches every row of dX that counts, and no other
+    W[V // 2] = math.nan
+    for need_dw in (True, False):
+        dX = nf4.head_loss(X, W, t, dloss=dl, need_dw=need_dw)[1]
+        dead = torch.zeros(M, dtype=torch.bool, device="cuda")
+        dead[[1, M - 1]] = True
+        assert not dX[dead].any() and torch.isnan(dX[~dead]).all()
+
+
 def test_non_finite_rows_stay_alone():
     X, W, t, dl = inputs(80, 600, 128, seed=10)
     good = nf4.head_loss(X, W, t, dloss=dl)
