@@ -30,16 +30,13 @@
 // 1100 cached, 32 heads of 128 (74 GFLOP): 126 us, 585 TFLOP/s.
 #include "bufio.h"
 #include "paged.h"
-#include "tile_map.h"
+#include "attend_plan.h"
 
 namespace nf4 {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int KV_STEP = 32;               // keys of a step
-constexpr int KV_WAVES = 4;
-constexpr int KV_FEW = 32;                // rows of a (sequence, kv head) that count as few
 constexpr float KV_FLOOR = -3e38f;        // reference before any key: finite, so that no inf - inf arises
 constexpr float KV_BIAS = 10.0f;          // weights are at most 2^(KV_BIAS + KV_SLACK) = 2^15 (fp16 reaches 2^16)
 constexpr float KV_SLACK = 5.0f;          // a reference is raised once a score passes it by more than this
@@ -321,6 +318,9 @@ __device__ __forceinline__ float split_query(const uint16_t* row, int quarter, u
     return 1.0f / up;
 }
 
+// Chunks of `keys` keys (none or fewer: 0), up to 2^31 - 1 of them.
+__device__ __forceinline__ int chunks_of(int keys, int chunk) { return keys > 0 ? (keys - 1) / chunk + 1 : 0; }
+
 template <int D, int AUX>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 3)))
 void k_attend_rows(AttendArgs a) {
@@ -369,10 +369,9 @@ void k_attend_rows(AttendArgs a) {
         st.m = KV_FLOOR;
         st.l = 0.0f;
 
-        const int chunks = (keys + a.chunk - 1) / a.chunk;
+        const int chunks = chunks_of(keys, a.chunk);
         for (int ch = split; ch < chunks; ch += stride) {
-            const int lo = ch * a.chunk;
-            const int hi = lo + a.chunk < keys ? lo + a.chunk : keys;
+            const int lo = ch * a.chunk, hi = keys - lo > a.chunk ? lo + a.chunk : keys;
             // this wave's steps: keys lo + 32 (wave + 4 i) ..
             const int all = (hi - lo + KV_STEP - 1) / KV_STEP;
             const int steps = (all - wave + KV_WAVES - 1) / KV_WAVES;
@@ -585,9 +584,9 @@ void k_attend_block(AttendArgs a) {
             st[c].m = KV_FLOOR;
             st[c].l = 0.0f;
         }
-        const int chunks = (keys + a.chunk - 1) / a.chunk;
+        const int chunks = chunks_of(keys, a.chunk);
         for (int ch = split; ch < chunks; ch += a.splits) {
-            const int lo = ch * a.chunk, hi = lo + a.chunk < keys ? lo + a.chunk : keys;
+            const int lo = ch * a.chunk, hi = keys - lo > a.chunk ? lo + a.chunk : keys;
             const int steps = ((hi - lo + KV_STEP - 1) / KV_STEP - wave + W - 1) / W;     // of this wave: every W-th
             auto first_key = [&](int i) { return lo + KV_STEP * (W * i + wave); };
             struct Pages {
@@ -806,88 +805,19 @@ void k_attend_join(AttendArgs a) {
     *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
 
-// One kernel's part of a call: its chunks and where its parts lie.
-struct AttendPart {
-    bool on;
-    int tiles, chunk, splits;             // row tiles (blocks) launched per (sequence, kv head)
-    size_t slots, bytes;                  // row slots; workspace
-    int waves;                            // k_attend_block: waves that share a block's keys
-};
-struct AttendPlan {
-    AttendPart rows, block;
-};
-// (3 prompts of up to 1500 tokens behind 1100 cached, 32 heads of 128: one tile 213 us, two 131, four, past the
-// registers, 570; of 256: one tile 355, two 1281; of 64: two tiles 92, four 96)
-constexpr int block_tiles(int dim) { return dim == 256 ? 1 : 2; }     // CT
-constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
-
-// k_attend_rows reads the keys once per 16 rows and splits them over many workgroups; k_attend_block
-// reads them once per block_rows rows and decodes them once per block_tiles tiles.  A batch whose sequences all bring
-// up to 32 rows per kv head needs the first alone, one of equal longer ones the second alone; any other
-// may hold both kinds, and each kernel takes its own, unless there is so little to read that two launches more cost
-// more than the tiles that a few rows leave empty (27 sequences of up to 494 keys and 11 tokens, 8 heads of 64: 36 us
-// with both kernels, 24 with one).
-// (17 to 32 rows by k_attend_block instead: 55 us for 49 with 8 sequences of up to 8000 keys and 4 tokens, 8 groups of
-// 8 heads of 256, 31 for 19 with heads of 64.)
-// Chunks: for k_attend_rows about 4096 workgroups (some rounds of three or four on each compute unit, so that a
-// ragged batch's last chunks end together) at the stated lengths, but chunks of 1024 keys where 1024 workgroups are left
-// then, for a workgroup's start, end and join cost as much as some 200 keys (two sequences of 120001 keys, 8 kv
-// heads: chunks of 512 keys 81 us, 1024 73; of 24 sequences of up to 4096, 64 heads: 1536 keys 132 us, half of that 149, twice 199),
-// and of at least 256 keys; up to 768 keys stay whole, for the join's launch costs more (4 sequences of up to 600 keys,
-// heads of 128: 7.0 us, 8.9 in chunks; of up to 900: 9.0 and 9.0, heads of 256 14.4 and 11.9).  For k_attend_block, where there are fewer blocks than waves that run at once, two or four
-// waves share a block's keys (4 prompts of up to 534 tokens, 8 heads of 64: 12.5 us, 22.5 alone; 2 of 1277, 16 heads of
-// 128: 31 and 35; but 3 of 1500, 32 heads: 134 and 126, and heads of 256, whose parts are as large as a step's
-// work: 24 and 10 for 3 of 76 tokens), and chunks only where there are still fewer than 1024 waves, one for
-// each SIMD: of 128 keys a wave at least where most of the keys were there before (27 sequences of up to 494 keys
-// and 11 tokens: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the
-// others (one prompt of 252 behind 1370 keys, 8 heads of 256: 70 us with 128, 49 with 512).
-constexpr int64_t BLOCK_ALONE = 1024 * 512;
-static AttendPlan attend_plan(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
-                              int64_t max_length) {
-    AttendPlan p{};
-    const int group = heads / c.heads;
-    const int64_t most_rows = max_new * group, keys = (int64_t)seqs * c.heads * max_length;
-    p.rows.on = most_rows <= KV_FEW || (tokens != (int64_t)seqs * max_new && keys > BLOCK_ALONE);
-    p.block.on = most_rows > KV_FEW;
-    auto chunks = [&](AttendPart& q, int64_t groups, int64_t target, int64_t unit, int64_t least, size_t slots) {
-        int64_t chunk = (max_length * groups / target + unit - 1) / unit * unit;
-        chunk = chunk < least ? least : (chunk > (1 << 24) ? 1 << 24 : chunk);
-        const int64_t splits = (max_length + chunk - 1) / chunk;
-        q.chunk = (int)chunk;
-        q.splits = (int)(splits < 1 ? 1 : (splits < 1024 ? splits : 1024));
-        q.slots = slots;
-        q.bytes = q.splits > 1 ? (slots * q.splits * (c.dim + 2) * sizeof(float) + 255) & ~(size_t)255 : 0;
-    };
-    if (p.rows.on) {
-        const int64_t r = most_rows < KV_FEW ? most_rows : KV_FEW;
-        p.rows.tiles = (int)((r + 15) / 16);
-        const int64_t groups = (int64_t)seqs * c.heads * p.rows.tiles, wide = keys * p.rows.tiles / 1024;
-        const int64_t least = max_length <= 768 ? 768 : wide < 256 ? 256 : wide < 1024 ? wide / 128 * 128 : 1024;
-        chunks(p.rows, groups, 4096, KV_WAVES * KV_STEP, least, (size_t)seqs * c.heads * KV_FEW);
-    }
-    if (p.block.on) {
-        const int64_t rows = block_rows(c.dim);
-        int64_t blocks = (most_rows + rows - 1) / rows;
-        const int64_t pairs = ((int64_t)seqs * c.heads + XCDS - 1) / XCDS * XCDS, most = ((int64_t)1 << 24) / pairs;
-        blocks = blocks < most ? blocks : most;               // (a wave takes several beyond that)
-        p.block.tiles = (int)(blocks < 1 ? 1 : blocks);
-        const int64_t groups = (tokens * heads + rows - 1) / rows;
-        const int waves = p.block.waves = c.dim == 256 || max_length < 256 || groups >= 2048 ? 1 : groups >= 1024 ? 2 : 4;
-        if (groups * waves >= 1024) chunks(p.block, 1, 1, 1, 1 << 24, 0);
-        else chunks(p.block, groups * waves, 1024, KV_STEP, (16 * max_new <= max_length ? 128 : 512) * waves, (size_t)tokens * heads);
-    }
-    return p;
+static AttendPlan plan_of(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new, int64_t max_length) {
+    return attend_plan(AttendShape{c.dim, c.heads, seqs, tokens, heads, max_new, max_length});
 }
 
 size_t kv_attention_ws_bytes(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
                              int64_t max_length) {
-    const AttendPlan p = attend_plan(c, seqs, tokens, heads, max_new, max_length);
+    const AttendPlan p = plan_of(c, seqs, tokens, heads, max_new, max_length);
     return p.rows.bytes + p.block.bytes;
 }
 
 hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const HeadsView& q, const HeadsView& out,
                                float scale, int64_t max_new, int64_t max_length, void* ws, hipStream_t s) {
-    const AttendPlan p = attend_plan(c, b.seqs, b.tokens, q.heads, max_new, max_length);
+    const AttendPlan p = plan_of(c, b.seqs, b.tokens, q.heads, max_new, max_length);
     AttendArgs a{};
     a.c = c;
     a.b = b;

@@ -191,6 +191,17 @@ def test_attention_long_split():
     check_attention(c, max_new=2, max_length=40001)
 
 
+@pytest.mark.parametrize("counts", [[300, 200], [3, 1]])
+def test_attention_long_reach(counts):
+    # a table of 2^25 positions, nearly all of them absent: with and without a stated length
+    c = Case([0, 100], counts, page=256, kv=4, heads=32, dim=64, seed=21)
+    c.table = np.concatenate([c.table, np.full((2, (1 << 25) // 256 - c.table.shape[1]), -1)], axis=1)
+    a = check_attention(c)
+    b = check_attention(c, max_new=max(counts), max_length=300)
+    assert torch.all((a.float() - b.float()).abs() <= 2.0 ** -7 * a.float().abs() + 2.0 ** -10 * 8)
+    check_attention(c, max_length=2 ** 31 - 1)
+
+
 def test_attention_sharp_and_flat_scores():
     c = Case([500, 500], [1, 1], page=16, kv=2, heads=4, dim=64, seed=11)
     c.q = c.q * 30                                                   # scores of some hundreds: one key wins
