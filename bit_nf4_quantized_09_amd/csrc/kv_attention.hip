@@ -332,9 +332,9 @@ void k_attend_rows(AttendArgs a) {
     const int split = blockIdx.x;
     const int head = blockIdx.y % a.c.heads, tile0 = blockIdx.y / a.c.heads;
     const int seq = blockIdx.z;
-    const int begin = scalar_load(a.b.starts + seq), fresh = scalar_load(a.b.starts + seq + 1) - begin;
-    const int before = scalar_load(a.b.lengths + seq);
-    const int rows = fresh * a.group;
+    const NewTokens fresh = new_tokens(a.b, scalar_load(a.b.starts + seq), scalar_load(a.b.starts + seq + 1));
+    const int before = scalar_load(a.b.lengths + seq), begin = fresh.begin;
+    const int rows = fresh.count * a.group;
     if (rows > a.limit) return;
     const int reach = a.b.table_width << a.c.page_log2;      // positions the table can hold
     __shared__ float sm[KV_WAVES][16], sl[KV_WAVES][16];
@@ -489,7 +489,7 @@ __device__ __forceinline__ int2 block_of_rank(const AttendArgs& a, int here, int
     const int pair = lane * XCDS + (int)(blockIdx.x % XCDS);
     int blocks = 0, base = 0;
     if (lane < here && pair < a.b.seqs * a.c.heads) {
-        const int seq = pair / a.c.heads, rows = (a.b.starts[seq + 1] - a.b.starts[seq]) * a.group;
+        const int seq = pair / a.c.heads, rows = new_tokens(a.b, a.b.starts[seq], a.b.starts[seq + 1]).count * a.group;
         blocks = rows <= a.limit ? 0 : (rows + BLOCK - 1) / BLOCK;
         const int64_t rows_before = (int64_t)a.b.lengths[seq] * a.group / BLOCK;
         base = rows_before < 0 ? 0 : rows_before < (1 << 28) ? (int)rows_before : 1 << 28;
@@ -548,9 +548,9 @@ void k_attend_block(AttendArgs a) {
             return;
         }
         const int head = pair % a.c.heads, seq = pair / a.c.heads;
-        const int begin = scalar_load(a.b.starts + seq), fresh = scalar_load(a.b.starts + seq + 1) - begin;
-        const int before = scalar_load(a.b.lengths + seq);
-        const int rows = fresh * a.group;
+        const NewTokens fresh = new_tokens(a.b, scalar_load(a.b.starts + seq), scalar_load(a.b.starts + seq + 1));
+        const int before = scalar_load(a.b.lengths + seq), begin = fresh.begin;
+        const int rows = fresh.count * a.group;
         if (!a.ordered) {                     // a pair's last block first (every rank of this workgroup is of one pair)
             block = (rows + BLOCK - 1) / BLOCK - 1 - rank / here;
             if (block < 0 || rows <= a.limit) return;
@@ -748,7 +748,8 @@ void k_attend_join(AttendArgs a) {
         const int64_t pair = slot / a.few, row = slot % a.few;
         const int seq = (int)(pair / a.c.heads), head = (int)(pair % a.c.heads);
         on = seq < a.b.seqs;
-        const int begin = on ? a.b.starts[seq] : 0, rows = on ? (a.b.starts[seq + 1] - begin) * a.group : 0;
+        const NewTokens fresh = on ? new_tokens(a.b, a.b.starts[seq], a.b.starts[seq + 1]) : NewTokens{0, 0};
+        const int begin = fresh.begin, rows = fresh.count * a.group;
         on = on && rows <= a.few && row < rows;
         token = begin + row / a.group;
         qhead = head * a.group + row % a.group;
@@ -758,7 +759,7 @@ void k_attend_join(AttendArgs a) {
         on = token < a.b.tokens;
         if (on && a.limit > 0) {
             const int seq = sequence_of(a.b.starts, a.b.seqs, (int)token, lane);
-            on = (a.b.starts[seq + 1] - a.b.starts[seq]) * a.group > a.limit;
+            on = new_tokens(a.b, a.b.starts[seq], a.b.starts[seq + 1]).count * a.group > a.limit;
         }
     }
     const int64_t base = FEW ? ((slot / a.few) * KV_FEW + slot % a.few) * a.splits : slot * a.splits;

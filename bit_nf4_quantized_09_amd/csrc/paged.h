@@ -24,6 +24,17 @@ __device__ __forceinline__ int sequence_of(const int32_t* starts, int seqs, int 
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// The new tokens begin .. begin + count - 1 of a sequence, from its two starts.  Starts are device data that no host check
+// has seen: whatever they say, the tokens are among the batch's.
+struct NewTokens {
+    int begin, count;
+};
+__device__ __forceinline__ NewTokens new_tokens(const BatchView& b, int start, int end) {
+    const int from = start < 0 ? 0 : (start < b.tokens ? start : b.tokens);
+    const int to = end < from ? from : (end < b.tokens ? end : b.tokens);
+    return NewTokens{from, to - from};
+}
+
 // Page of the pool that holds positions p .. of a sequence, or -1 if the sequence has none there.
 __device__ __forceinline__ int page_of(const CacheView& c, const BatchView& b, int seq, int page_index) {
     if (page_index < 0 || page_index >= b.table_width) return -1;

@@ -70,7 +70,8 @@ typedef struct qlora_kv_cache {
  *   lengths  device int32[seqs]: tokens of the sequence before these; token j of the
  *            sequence's new ones has position lengths[b] + j
  *   table    device int32[seqs][table_stride]: page of each page_size positions
- * starts[0] is 0 and starts[seqs] is `tokens`.  A token whose position is negative or past
+ * starts[0] is 0 and starts[seqs] is `tokens` (starts that say otherwise give rows of no meaning,
+ * but nothing outside the batch's tokens is read or written).  A token whose position is negative or past
  * the table's table_width pages is left out: not appended, and its attention is zero (a
  * negative length marks an unused row of a fixed batch).  An entry of the table outside the
  * pool (such as -1) is never followed: tokens there are not appended, and attention passes

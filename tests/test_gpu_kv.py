@@ -4,6 +4,7 @@ Bounds.  Append: scales are exact; a code is within half a step of the exact quo
 it, or 2^-10 among the subnormals) but for the fp32 rotation's 1e-6 of the pair.  Attention:
 scores carry fp32 rounding, at most D 2^-24 sum|q k| scale (below 2^-13 of a weight for the
 sizes here), weights 2^-12 as fp16, outputs 2^-8 of themselves as bf16: 2^-8 |o| + 2^-10 max|v|."""
+import ctypes
 import math
 
 import numpy as np
@@ -11,6 +12,7 @@ import pytest
 import torch
 
 import bit_nf4_quantized_09_amd as nf4
+import decoder_abi as dec
 import decoder_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -291,6 +293,36 @@ def test_attention_rows_that_see_nothing():
     assert not check_attention(c, max_new=5, max_length=11)[1].any()
     c.lengths[3] = 16                                                # past the table
     assert not check_attention(c, max_new=5, max_length=17)[7].any()
+
+
+@pytest.mark.parametrize("dim,heads,tokens", [(128, 4, 6), (128, 16, 70), (64, 32, 70), (256, 8, 40)])
+@pytest.mark.parametrize("wrong", [[2 ** 31 - 1, 2 ** 31 - 1], [-7, 10 ** 6], [-2 ** 31, -1], [3, 2]])
+def test_attention_and_append_of_wrong_starts(dim, heads, tokens, wrong):
+    # the first sequence is in order, the starts behind it are not: nothing but the batch's own rows is written
+    c = Case([50, 20, 9], [tokens - 2, 1, 1], page=16, kv=2, heads=heads, dim=dim, seed=20)
+    want = nf4.kv_attention(c.cache, c.q, *c.meta(), max_new=tokens)
+    c.starts[2:] = wrong
+    starts, lengths, table = c.meta()
+    room = torch.full((tokens + 64, heads, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    view = lambda x, n: dec._Heads(x.data_ptr(), n * dim, dim, n)  # noqa: E731
+    q = c.q.contiguous()
+    cache = dec._Cache(c.cache.codes.data_ptr(), c.cache.scales.data_ptr(), c.cache.codes.shape[0], 2, 16, dim)
+    batch = dec._Batch(starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), table.shape[1], tokens, 3, table.shape[1])
+    by = ctypes.byref
+    for length in (100, 200000):
+        size = dec._library().qlora_kv_attention_workspace_bytes(by(cache), by(batch), heads, tokens, length)
+        ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+        status = dec._library().qlora_kv_attention(by(cache), by(batch), by(view(q, heads)), by(view(room[32:], heads)), dim ** -0.5, tokens,
+                                                   length, (ws.data_ptr() + 255) // 256 * 256, size, torch.cuda.current_stream().cuda_stream)
+        assert status == nf4.NF4_OK
+        torch.cuda.synchronize()
+        assert (room[:32] == 7).all() and (room[32 + tokens:] == 7).all()
+        if wrong[0] < 0 < wrong[1]:
+            continue                                                # (the third sequence lays claim to the first one's tokens)
+        got = room[32:32 + tokens - 2].float()
+        assert torch.all((got - want[:tokens - 2].float()).abs() <= 2.0 ** -7 * got.abs() + 2.0 ** -10 * 8)
+    nf4.kv_append(c.cache, c.k, c.v, starts, lengths, table, rope=nf4.rope_plan(64), q=c.q)
+    torch.cuda.synchronize()
 
 
 def test_attention_of_appended_tokens_and_other_streams():
