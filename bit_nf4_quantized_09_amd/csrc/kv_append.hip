@@ -273,7 +273,7 @@ void k_append(AppendArgs a) {
         const int t = id / a.q_parts, part = id - t * a.q_parts;
         if (t >= a.b.tokens) return;
         const int seq = sequence_of(a.b.starts, a.b.seqs, t, lane);
-        const int position = a.b.lengths[seq] + t - a.b.starts[seq];
+        const int position = position_at(a.b.lengths[seq], t - a.b.starts[seq]);
         float2* cs = table + wave * (D / 2);       // of this wave alone
         rope_fill(a.rope, position, cs, lane, 64);
         __builtin_amdgcn_wave_barrier();
@@ -304,7 +304,7 @@ void k_append(AppendArgs a) {
             end = a.b.starts[seq + 1];
         }
         if (t >= end || t < begin) return;
-        const int position = a.b.lengths[seq] + t - begin;
+        const int position = position_at(a.b.lengths[seq], t - begin);
         if (position < 0) {
             ++t;
             continue;
@@ -313,7 +313,7 @@ void k_append(AppendArgs a) {
         int n = P - slot < end - t ? P - slot : end - t;      // the page's tokens from t on
         n = n < a.b.tokens - t ? n : a.b.tokens - t;
         // another workgroup has the page if an earlier new token lies on it
-        const bool mine = slot == 0 || t == begin || position - 1 < 0 || a.b.lengths[seq] + t - 1 - begin < 0;
+        const bool mine = slot == 0 || t == begin || position_at(position, -1) < 0;
         if (mine) {
             const int page = page_of(a.c, a.b, seq, position >> a.c.page_log2);
             if (page >= 0) append_page<D, INTER, SPLIT>(a, t, n, page, slot, head, on, position, wave, lane, table, join);

@@ -350,11 +350,11 @@ void k_attend_rows(AttendArgs a) {
         const bool live = row < rows;
         const int token = (live ? row : rows - 1) / a.group;
         const int qhead = head * a.group + (live ? row : rows - 1) % a.group;
-        int position = before + token;
+        int position = position_at(before, token);
         if (position >= reach) position = -1;                 // left out: attends to nothing
         const int last_row = tile * 16 + 15 < rows ? tile * 16 + 15 : rows - 1;
-        const int low = before + tile * 16 / a.group;         // the first row's position
-        int keys = before + last_row / a.group + 1;           // keys the tile's last row sees
+        const int low = position_at(before, tile * 16 / a.group);         // the first row's position
+        int keys = position_at(before, last_row / a.group + 1);           // keys the tile's last row sees
         const bool past = keys > reach;
         keys = past ? reach : keys;
         bf16x8 qf[KSTEPS];
@@ -557,7 +557,7 @@ void k_attend_block(AttendArgs a) {
         }
         const int row0 = block * BLOCK;
         const int last_row = row0 + BLOCK <= rows ? row0 + BLOCK - 1 : rows - 1;
-        int keys = before + last_row / a.group + 1;
+        int keys = position_at(before, last_row / a.group + 1);
         const bool past = keys > reach;
         keys = past ? reach : keys;
         bf16x8 qf[F8 ? 1 : CT][KSTEPS];
@@ -569,8 +569,9 @@ void k_attend_block(AttendArgs a) {
         for (int c = 0; c < CT; ++c) {
             const int row = row0 + 16 * c + col < rows ? row0 + 16 * c + col : rows - 1;
             const int token = row / a.group, qhead = head * a.group + row % a.group;
-            position[c] = before + token < reach ? before + token : -1;
-            low[c] = before + (row0 + 16 * c) / a.group;
+            position[c] = position_at(before, token);
+            position[c] = position[c] < reach ? position[c] : -1;
+            low[c] = position_at(before, (row0 + 16 * c) / a.group);
             const uint16_t* qp = (const uint16_t*)a.q.data + (int64_t)(begin + token) * a.q.token_stride +
                                  (int64_t)qhead * a.q.head_stride;
             if constexpr (!F8) {

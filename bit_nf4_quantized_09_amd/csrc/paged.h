@@ -35,6 +35,10 @@ __device__ __forceinline__ NewTokens new_tokens(const BatchView& b, int start, i
     return NewTokens{from, to - from};
 }
 
+// Position of the new token `i` places on from a sequence's length.  A length near 2^31 wraps round to a negative position,
+// which is left out like any negative one (and 2^31 - 256 is past every table).
+__device__ __forceinline__ int position_at(int length, int i) { return (int)((uint32_t)length + (uint32_t)i); }
+
 // Page of the pool that holds positions p .. of a sequence, or -1 if the sequence has none there.
 __device__ __forceinline__ int page_of(const CacheView& c, const BatchView& b, int seq, int page_index) {
     if (page_index < 0 || page_index >= b.table_width) return -1;

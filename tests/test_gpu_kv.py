@@ -325,6 +325,21 @@ def test_attention_and_append_of_wrong_starts(dim, heads, tokens, wrong):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("counts", [[2, 1, 3], [60, 1, 3]])
+def test_lengths_near_their_limit(dim, counts):
+    # lengths that pass 2^31 with their new tokens, or hold no table: left out, and the third sequence is served
+    c = Case([0, 0, 20], counts, page=16, kv=2, heads=6, dim=dim, seed=22)
+    for lengths in ([2 ** 31 - 1, 2 ** 31 - 1, 20], [2 ** 31 - 2, 2 ** 31 - 40, 20], [2 ** 30, -2 ** 31, 20]):
+        c.lengths = np.array(lengths)
+        before = c.cache.codes.clone()
+        check_append(c, with_q=True)
+        gone = c.table[:2][c.table[:2] >= 0]
+        assert torch.equal(c.cache.codes[gone], before[gone])
+        out = check_attention(c, max_new=max(counts), max_length=23)
+        assert not out[:sum(counts[:2])].any() and out[sum(counts[:2]):].any(-1).all()
+
+
 def test_attention_of_appended_tokens_and_other_streams():
     # prompts, then single tokens, on a stream of their own: against float64 attention of the decoded cache
     plan = nf4.rope_plan(128, interleaved=True)
