@@ -19,6 +19,7 @@ struct AttendShape {
     int dim, kv_heads;
     int64_t seqs, tokens, heads, max_new, max_length;
 };
+constexpr int64_t ATTEND_PAIRS = (int64_t)1 << 25;        // (sequence, kv head) pairs of a call at most: one wave each, of 2^32 threads
 
 // One kernel's part of a call: its chunks and where its parts lie.
 struct AttendPart {
@@ -26,6 +27,7 @@ struct AttendPart {
     int tiles, chunk, splits;             // row tiles (blocks) launched per (sequence, kv head)
     size_t slots, bytes;                  // row slots; workspace
     int waves;                            // k_attend_block: waves that share a block's keys
+    int few;                              // k_attend_rows: rows of a (sequence, kv head) that have slots
 };
 struct AttendPlan {
     AttendPart rows, block;
@@ -58,7 +60,8 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 constexpr int64_t BLOCK_ALONE = 1024 * 512;
 inline AttendPlan attend_plan(const AttendShape& a) {
     AttendPlan p{};
-    const int64_t max_new = a.max_new, max_length = a.max_length;
+    // no sequence brings more tokens than the batch (a capacity in its place would launch for rows that are not there)
+    const int64_t max_new = a.max_new < a.tokens ? a.max_new : a.tokens, max_length = a.max_length;
     const int64_t most_rows = max_new * (a.heads / a.kv_heads), keys = a.seqs * a.kv_heads * max_length;
     p.rows.on = most_rows <= KV_FEW || (a.tokens != a.seqs * max_new && keys > BLOCK_ALONE);
     p.block.on = most_rows > KV_FEW;
@@ -73,6 +76,7 @@ inline AttendPlan attend_plan(const AttendShape& a) {
     };
     if (p.rows.on) {
         const int64_t r = most_rows < KV_FEW ? most_rows : KV_FEW;
+        p.rows.few = (int)r;
         p.rows.tiles = (int)((r + 15) / 16);
         const int64_t groups = a.seqs * a.kv_heads * p.rows.tiles, wide = keys * p.rows.tiles / 1024;
         const int64_t least = max_length <= 768 ? 768 : wide < 256 ? 256 : wide < 1024 ? wide / 128 * 128 : 1024;
@@ -81,11 +85,11 @@ inline AttendPlan attend_plan(const AttendShape& a) {
     if (p.block.on) {
         const int64_t rows = block_rows(a.dim);
         int64_t blocks = (most_rows + rows - 1) / rows;
-        const int64_t pairs = (a.seqs * a.kv_heads + XCDS - 1) / XCDS * XCDS, most = ((int64_t)1 << 24) / pairs;
-        blocks = blocks < most ? blocks : most;               // (a wave takes several beyond that)
-        p.block.tiles = (int)(blocks < 1 ? 1 : blocks);
+        const int64_t pairs = (a.seqs * a.kv_heads + XCDS - 1) / XCDS * XCDS, most = (int64_t)1 << 24;      // (waves launched)
         const int64_t groups = (a.tokens * a.heads + rows - 1) / rows;
-        const int waves = p.block.waves = a.dim == 256 || max_length < 256 || groups >= 2048 ? 1 : groups >= 1024 ? 2 : 4;
+        const int waves = p.block.waves = a.dim == 256 || max_length < 256 || groups >= 2048 || 4 * pairs > most ? 1 : groups >= 1024 ? 2 : 4;
+        blocks = blocks < most / (pairs * waves) ? blocks : most / (pairs * waves);      // (a workgroup takes several beyond that)
+        p.block.tiles = (int)(blocks < 1 ? 1 : blocks);
         // one chunk, of whatever length: no row has a slot for a part
         if (groups * waves >= 1024) p.block.chunk = KV_WHOLE, p.block.splits = 1;
         else chunks(p.block, groups * waves, 1024, KV_STEP, (16 * max_new <= max_length ? 128 : 512) * waves, (size_t)(a.tokens * a.heads));

@@ -34,8 +34,7 @@ constexpr int KV_EXP_MIN = -50, KV_EXP_MAX = 50;   // exponents of a page's scal
 hipError_t launch_kv_append(const CacheView& c, const BatchView& b, const HeadsView& k, const HeadsView& v,
                             const RopeView& rope, const HeadsView* q_in, const HeadsView* q_out, hipStream_t s);
 
-size_t kv_attention_ws_bytes(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
-                             int64_t max_length);
+size_t kv_attention_ws_bytes(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length);
 hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const HeadsView& q, const HeadsView& out,
                                float scale, int64_t max_new, int64_t max_length, void* ws, hipStream_t s);
 

@@ -6,6 +6,7 @@
 
 #include "../../include/qlora_decoder.h"
 #include "decoder.h"
+#include "attend_plan.h"
 #include "status.h"
 
 using nf4::aligned;
@@ -158,6 +159,7 @@ static nf4_status check_attention(const qlora_kv_cache* cache, const qlora_kv_ba
     if (heads < 1 || heads > 65536 || heads % c.heads) return fail(NF4_ERR_ARG, "heads must be a multiple of the cache's, 65536 at most");
     if (max_new < 1 || max_length < 1) return fail(NF4_ERR_ARG, "max_new and max_length must be at least 1");
     if (max_new >= MAX_TOKENS || max_length > (int64_t)0x7FFFFFFF) return fail(NF4_ERR_UNSUPPORTED, "max_new or max_length too large");
+    if ((int64_t)b.seqs * c.heads > nf4::ATTEND_PAIRS) return fail(NF4_ERR_UNSUPPORTED, "seqs times kv_heads must not pass 2^25");
     if (max_new * (heads / c.heads) >= ((int64_t)1 << 30)) return fail(NF4_ERR_UNSUPPORTED, "max_new times heads per key head too large");
     return NF4_OK;
 }
@@ -169,7 +171,7 @@ size_t qlora_kv_attention_workspace_bytes(const qlora_kv_cache* cache, const qlo
         CacheView c;
         BatchView b;
         if (nf4_status st = check_attention(cache, batch, heads, max_new, max_length, c, b)) return st;
-        bytes = b.tokens > 0 ? nf4::kv_attention_ws_bytes(c, b.seqs, b.tokens, heads, max_new, max_length) : 0;
+        bytes = b.tokens > 0 ? nf4::kv_attention_ws_bytes(c, b, heads, max_new, max_length) : 0;
         return NF4_OK;
     });
     return bytes;
@@ -190,7 +192,7 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
         if (nf4_status st = check_heads(out, "out", c.dim, 2, true, ov)) return st;
         if (qv.heads != ov.heads) return fail(NF4_ERR_ARG, "q and out have different heads");
         if ((int64_t)b.tokens * qv.heads >= ((int64_t)1 << 26)) return fail(NF4_ERR_UNSUPPORTED, "tokens times heads must be below 2^26");
-        const size_t need = nf4::kv_attention_ws_bytes(c, b.seqs, b.tokens, qv.heads, max_new, max_length);
+        const size_t need = nf4::kv_attention_ws_bytes(c, b, qv.heads, max_new, max_length);
         if (need > 0 && (!workspace || workspace_bytes < need)) return fail(NF4_ERR_WORKSPACE, "workspace missing or too small");
         if (need > 0 && !aligned(workspace, 256)) return fail(NF4_ERR_ARG, "workspace must be 256-byte aligned");
         return hip_status(nf4::launch_kv_attention(c, b, qv, ov, scale, max_new, max_length, workspace, (hipStream_t)stream),

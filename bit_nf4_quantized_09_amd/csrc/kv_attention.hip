@@ -807,19 +807,18 @@ void k_attend_join(AttendArgs a) {
     *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
 
-static AttendPlan plan_of(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new, int64_t max_length) {
-    return attend_plan(AttendShape{c.dim, c.heads, seqs, tokens, heads, max_new, max_length});
+static AttendPlan plan_of(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length) {
+    return attend_plan(AttendShape{c.dim, c.heads, b.seqs, b.tokens, heads, max_new, max_length});
 }
 
-size_t kv_attention_ws_bytes(const CacheView& c, int seqs, int64_t tokens, int heads, int64_t max_new,
-                             int64_t max_length) {
-    const AttendPlan p = plan_of(c, seqs, tokens, heads, max_new, max_length);
+size_t kv_attention_ws_bytes(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length) {
+    const AttendPlan p = plan_of(c, b, heads, max_new, max_length);
     return p.rows.bytes + p.block.bytes;
 }
 
 hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const HeadsView& q, const HeadsView& out,
                                float scale, int64_t max_new, int64_t max_length, void* ws, hipStream_t s) {
-    const AttendPlan p = plan_of(c, b.seqs, b.tokens, q.heads, max_new, max_length);
+    const AttendPlan p = plan_of(c, b, q.heads, max_new, max_length);
     AttendArgs a{};
     a.c = c;
     a.b = b;
@@ -865,8 +864,7 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
         if (p.rows.on) {
             part(p.rows, ws);
             a.row_tiles = p.rows.tiles;
-            const int64_t most = max_new * a.group;
-            a.few = (int)(most < KV_FEW ? most : KV_FEW);
+            a.few = p.rows.few;
             // codes that one row tile reads are read once: they need not stay in the caches (716 MB: 132 us, 140 with them)
             const dim3 grid((uint32_t)a.splits, (uint32_t)(c.heads * a.row_tiles), (uint32_t)b.seqs);
             if (a.row_tiles == 1) hipLaunchKernelGGL((k_attend_rows<D, 2>), grid, dim3(256), 0, s, a);

@@ -113,9 +113,11 @@ nf4_status qlora_kv_append(const qlora_kv_cache* cache, const qlora_kv_batch* ba
  * A query with a non-finite value that sees any key gives NaN.
  *   q, out      bf16 [tokens][heads][head_dim], rows 16-byte aligned; heads a multiple of kv_heads
  *   scale       of any sign, below 2^127 in magnitude (0: every key that is seen weighs the same)
- *   max_new     the most new tokens of one sequence (at least 1), and
+ *   max_new     the most new tokens of one sequence (at least 1; more than `tokens` count as that), and
  *   max_length  the most positions of one sequence, new tokens included: they size the launch.
- *               Larger batches than they say are still computed, only slower.
+ *               Larger batches than they say are still computed, only slower; smaller ones than a
+ *               max_length says cost workgroups without keys.
+ *   seqs times kv_heads is 2^25 at most
  *   workspace   qlora_kv_attention_workspace_bytes of the same sizes, 256-byte aligned */
 size_t qlora_kv_attention_workspace_bytes(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int32_t heads,
                                           int64_t max_new, int64_t max_length);

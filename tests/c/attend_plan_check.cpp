@@ -1,5 +1,6 @@
 // Host check of attention's launches (attend_plan.h) over many sizes: where a row's keys are split between workgroups,
-// every row that a kernel may take has a slot for its parts inside the planned workspace, and chunks hold whole steps.
+// every row that a kernel may take has a slot for its parts inside the planned workspace, and chunks hold whole steps; a
+// launch stays below 2^32 threads along each dimension; and more new tokens than the batch has change nothing.
 // Prints "<sizes> <failures>".
 #include <cstdio>
 #include <initializer_list>
@@ -30,13 +31,22 @@ static void check(const AttendShape& a) {
     const AttendPlan p = attend_plan(a);
     if (!p.rows.on && !p.block.on) fail(a, "no kernel");
     if (p.rows.on) {
-        const int64_t rows = a.max_new * (a.heads / a.kv_heads);
+        const int64_t rows = (a.max_new < a.tokens ? a.max_new : a.tokens) * (a.heads / a.kv_heads);
         check_part(a, p.rows, a.seqs * a.kv_heads * (rows < KV_FEW ? rows : KV_FEW), KV_WAVES * KV_STEP);
     }
     if (p.block.on) {
         check_part(a, p.block, a.tokens * a.heads, KV_STEP);
         if (p.block.waves != 1 && p.block.waves != 2 && p.block.waves != 4) fail(a, "waves");
+        const int64_t pairs = (a.seqs * a.kv_heads + XCDS - 1) / XCDS * XCDS;
+        if (pairs * p.block.tiles * 64 * p.block.waves >= (int64_t)1 << 32) fail(a, "threads of the prompts' kernel");
     }
+    AttendShape held = a;
+    held.max_new = a.max_new < a.tokens ? a.max_new : a.tokens;
+    const AttendPlan h = attend_plan(held);
+    auto same = [](const AttendPart& x, const AttendPart& y) {
+        return x.on == y.on && x.tiles == y.tiles && x.chunk == y.chunk && x.splits == y.splits && x.bytes == y.bytes && x.waves == y.waves && x.few == y.few;
+    };
+    if (!same(p.rows, h.rows) || !same(p.block, h.block)) fail(a, "more new tokens than the batch has");
 }
 
 int main() {
@@ -49,7 +59,7 @@ int main() {
                             for (int64_t length : {int64_t(1), int64_t(700), int64_t(5000), int64_t(131072), int64_t(1) << 24,
                                                    (int64_t(1) << 24) + 1, int64_t(1) << 30, int64_t(0x7FFFFFFF)})
                                 // (what the entry point lets through)
-                                if (tokens * kv * group < (1 << 26) && max_new * group < (1 << 30))
+                                if (tokens * kv * group < (1 << 26) && max_new * group < (1 << 30) && seqs * kv <= ATTEND_PAIRS)
                                     check(AttendShape{dim, kv, seqs, tokens, kv * group, max_new, length});
     printf("%lld %lld\n", (long long)sizes, (long long)bad);
     return 0;

@@ -128,6 +128,15 @@ def test_attention_refusals():
     assert attention_status(length=100000, ws=ctypes.c_void_p(4096 + 16), wsb=size) == ARG
 
 
+def test_attention_plans_for_the_batch_it_has():
+    size = lambda tokens, new: dec._library().qlora_kv_attention_workspace_bytes(  # noqa: E731
+        ctypes.byref(cache()), ctypes.byref(batch(tokens=tokens)), 8, new, 100000)
+    for tokens in (1, 3, 100, 1000):
+        assert size(tokens, tokens) == size(tokens, 1000 * tokens) == size(tokens, (1 << 23) - 1) > 0
+    assert attention_status(c=cache(kv_heads=1024, pages=8), b=batch(seqs=40000), q=heads(n=1024), out=heads(n=1024, data=8192)) == UNSUPPORTED
+    assert "2^25" in nf4.load_library().nf4_last_error().decode()
+
+
 def test_attention_scale_refusals():
     for scale in (float("inf"), -float("inf"), 2.0 ** 127, -3e38):
         assert attention_status(scale=scale) == ARG

@@ -188,6 +188,16 @@ def test_attention_many_blocks(dim, page, counts):
     check_attention(Case([150, 10, 400, 33], counts, page=page, kv=2, heads=64, dim=dim, seed=sum(counts)), max_new=max(counts), max_length=550)
 
 
+@pytest.mark.parametrize("kv,heads", [(8, 8), (8, 64)])
+def test_attention_with_a_capacity_for_max_new(kv, heads):
+    # single tokens, and a stated maximum far past them, as of a server's fixed limits
+    c = Case([300, 7, 64, 1000, 0, 511, 33, 100], [1] * 8, page=64, kv=kv, heads=heads, dim=128, seed=kv + heads)
+    a = check_attention(c, max_new=1, max_length=1024)
+    for new in (8, 4096, 1 << 20, (1 << 23) - 1):
+        b = check_attention(c, max_new=new, max_length=1 << 20)
+        assert torch.all((a.float() - b.float()).abs() <= 2.0 ** -7 * a.float().abs() + 2.0 ** -10 * 8)
+
+
 def test_attention_long_split():
     c = Case([40000, 3, 20011], [1, 1, 2], page=64, kv=1, heads=4, dim=128, seed=9)
     check_attention(c, max_new=2, max_length=40001)
