@@ -318,8 +318,18 @@ __device__ __forceinline__ float split_query(const uint16_t* row, int quarter, u
     return 1.0f / up;
 }
 
-// Chunks of `keys` keys (none or fewer: 0), up to 2^31 - 1 of them.
-__device__ __forceinline__ int chunks_of(int keys, int chunk) { return keys > 0 ? (keys - 1) / chunk + 1 : 0; }
+// Calls f(first key, end) for chunks split, split + splits, .. of `keys` keys (none or fewer: no chunk; up to 2^31 - 1).
+// In 32 bits without sign: splits * chunk is at most max_length + chunk, so nothing passes them, and no division is needed.
+template <typename F>
+__device__ __forceinline__ void for_chunks(int keys, int chunk, int split, int splits, F&& f) {
+    const uint32_t end = keys > 0 ? keys : 0, jump = (uint32_t)splits * (uint32_t)chunk;
+    uint32_t lo = (uint32_t)split * (uint32_t)chunk;
+    while (lo < end) {
+        f((int)lo, (int)(end - lo > (uint32_t)chunk ? lo + chunk : end));
+        if (end - lo <= jump) break;
+        lo += jump;
+    }
+}
 
 template <int D, int AUX>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 3)))
@@ -369,9 +379,7 @@ void k_attend_rows(AttendArgs a) {
         st.m = KV_FLOOR;
         st.l = 0.0f;
 
-        const int chunks = chunks_of(keys, a.chunk);
-        for (int ch = split; ch < chunks; ch += stride) {
-            const int lo = ch * a.chunk, hi = keys - lo > a.chunk ? lo + a.chunk : keys;
+        for_chunks(keys, a.chunk, split, stride, [&](int lo, int hi) {
             // this wave's steps: keys lo + 32 (wave + 4 i) ..
             const int all = (hi - lo + KV_STEP - 1) / KV_STEP;
             const int steps = (all - wave + KV_WAVES - 1) / KV_WAVES;
@@ -438,7 +446,7 @@ void k_attend_rows(AttendArgs a) {
                     compute(x0, i);
                 }
             }
-        }
+        });
         // ---- the waves join: a common reference, then the sums ----
         float l = st.l;
         l += __shfl_xor(l, 16);
@@ -586,9 +594,7 @@ void k_attend_block(AttendArgs a) {
             st[c].m = KV_FLOOR;
             st[c].l = 0.0f;
         }
-        const int chunks = chunks_of(keys, a.chunk);
-        for (int ch = split; ch < chunks; ch += a.splits) {
-            const int lo = ch * a.chunk, hi = keys - lo > a.chunk ? lo + a.chunk : keys;
+        for_chunks(keys, a.chunk, split, a.splits, [&](int lo, int hi) {
             const int steps = ((hi - lo + KV_STEP - 1) / KV_STEP - wave + W - 1) / W;     // of this wave: every W-th
             auto first_key = [&](int i) { return lo + KV_STEP * (W * i + wave); };
             struct Pages {
@@ -686,7 +692,7 @@ void k_attend_block(AttendArgs a) {
                     compute(x0, i);
                 }
             }
-        }
+        });
         if constexpr (W > 1) {                // the first wave adds the others' parts to its own
             __shared__ f32x4 parts[W - 1][CT][TILES][64];
             __shared__ float2 ends[W - 1][CT][64];
