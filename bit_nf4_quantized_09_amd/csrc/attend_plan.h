@@ -80,7 +80,7 @@ inline AttendPlan attend_plan(const AttendShape& a) {
         p.rows.tiles = (int)((r + 15) / 16);
         const int64_t groups = a.seqs * a.kv_heads * p.rows.tiles, wide = keys * p.rows.tiles / 1024;
         const int64_t least = max_length <= 768 ? 768 : wide < 256 ? 256 : wide < 1024 ? wide / 128 * 128 : 1024;
-        chunks(p.rows, groups, 4096, KV_WAVES * KV_STEP, least, (size_t)(a.seqs * a.kv_heads * KV_FEW));
+        chunks(p.rows, groups, 4096, KV_WAVES * KV_STEP, least, (size_t)(a.seqs * a.kv_heads * r));
     }
     if (p.block.on) {
         const int64_t rows = block_rows(a.dim);

@@ -481,7 +481,7 @@ void k_attend_rows(AttendArgs a) {
             if (whole) {
                 write_row<D>(st.acc, total, (uint16_t*)a.out.data + t * a.out.token_stride + qhead * a.out.head_stride, quarter);
             } else {
-                const int64_t at = (((int64_t)seq * a.c.heads + head) * KV_FEW + row) * a.splits + split;
+                const int64_t at = (((int64_t)seq * a.c.heads + head) * a.few + row) * a.splits + split;
                 write_part<D>(st.acc, top, total, a.part + at * D, a.sums + at, quarter);
             }
         }
@@ -770,7 +770,7 @@ void k_attend_join(AttendArgs a) {
             on = new_tokens(a.b, a.b.starts[seq], a.b.starts[seq + 1]).count * a.group > a.limit;
         }
     }
-    const int64_t base = FEW ? ((slot / a.few) * KV_FEW + slot % a.few) * a.splits : slot * a.splits;
+    const int64_t base = slot * a.splits;
     const int splits = on ? a.splits : 0;
     const int group = in / LANES, c = in % LANES;
     // every wave finds the row's reference for itself

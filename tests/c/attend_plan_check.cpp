@@ -1,5 +1,5 @@
 // Host check of attention's launches (attend_plan.h) over many sizes: where a row's keys are split between workgroups,
-// every row that a kernel may take has a slot for its parts inside the planned workspace, and chunks hold whole steps; a
+// every row that a kernel may take has a slot for its parts inside the planned workspace, which holds no more, and chunks hold whole steps; a
 // launch stays below 2^32 threads along each dimension; and more new tokens than the batch has change nothing.
 // Prints "<sizes> <failures>".
 #include <cstdio>
@@ -23,7 +23,9 @@ static void check_part(const AttendShape& a, const AttendPart& q, int64_t slots,
     if (q.tiles < 1) fail(a, "tiles");
     if (q.splits == 1) return;
     if ((int64_t)q.slots < slots) fail(a, "rows without a slot");
-    if (q.bytes < (size_t)slots * q.splits * (a.dim + 2) * 4) fail(a, "workspace");
+    const size_t need = (size_t)slots * q.splits * (a.dim + 2) * 4;
+    if (q.bytes < need) fail(a, "workspace");
+    if (q.bytes >= need + 256) fail(a, "workspace that no row uses");
 }
 
 static void check(const AttendShape& a) {

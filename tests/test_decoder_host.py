@@ -128,6 +128,14 @@ def test_attention_refusals():
     assert attention_status(length=100000, ws=ctypes.c_void_p(4096 + 16), wsb=size) == ARG
 
 
+def test_attention_workspace_holds_the_parts_and_no_more():
+    # 24 single tokens of 64 heads of 128 behind up to 4096 keys: a sum of 128 values and two statistics for each of up to
+    # four chunks of a row
+    size = dec._library().qlora_kv_attention_workspace_bytes(
+        ctypes.byref(cache(kv_heads=64, page_size=64)), ctypes.byref(batch(tokens=24, seqs=24, table_stride=64, table_width=64)), 64, 1, 4096)
+    assert 0 < size <= 24 * 64 * 4 * (128 + 2) * 4 + 256
+
+
 def test_attention_plans_for_the_batch_it_has():
     size = lambda tokens, new: dec._library().qlora_kv_attention_workspace_bytes(  # noqa: E731
         ctypes.byref(cache()), ctypes.byref(batch(tokens=tokens)), 8, new, 100000)
