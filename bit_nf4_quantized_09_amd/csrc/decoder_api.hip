@@ -44,6 +44,14 @@ nf4_status check_heads(const qlora_heads* x, const char* name, int32_t head_dim,
     return NF4_OK;
 }
 
+// Heads that a call writes: rows of different tokens or heads may not share memory.
+nf4_status check_written(const qlora_heads* x, const char* name, int32_t head_dim, int64_t tokens) {
+    const int64_t token = (x->heads - 1) * x->head_stride + head_dim, head = (tokens - 1) * x->token_stride + head_dim;
+    const bool apart = tokens <= 1 || x->token_stride >= token ||                                    // token after token, or
+                       (x->token_stride >= head_dim && (x->heads == 1 || x->head_stride >= head));   // head after head
+    return apart ? NF4_OK : fail(NF4_ERR_ARG, std::string(name) + ": rows that are written overlap");
+}
+
 nf4_status check_rope(const qlora_rope* r, int32_t head_dim, RopeView& v) {
     if (!r) return fail(NF4_ERR_ARG, "rope is NULL");
     if (!r->freq || !aligned(r->freq, 8)) return fail(NF4_ERR_ARG, "freq is NULL or misaligned");
@@ -109,11 +117,13 @@ nf4_status qlora_rope_apply(const qlora_rope* rope, int32_t backward, const int3
             const int elem = dtype == NF4_BF16 ? 2 : 4;
             if (nf4_status st = check_heads(in + i, "in", head_dim, elem, false, x[i])) return st;
             if (nf4_status st = check_heads(out + i, "out", head_dim, elem, false, y[i])) return st;
+            if (nf4_status st = check_written(out + i, "out", head_dim, M)) return st;
             if (x[i].heads != y[i].heads) return fail(NF4_ERR_ARG, "in and out have different heads");
             if (x[i].data == y[i].data && (x[i].token_stride != y[i].token_stride || x[i].head_stride != y[i].head_stride))
                 return fail(NF4_ERR_ARG, "in place needs the same strides");
             heads += x[i].heads;
         }
+        if (count == 2 && y[0].data == y[1].data) return fail(NF4_ERR_ARG, "out: both tensors are the same");
         if (heads > 65536) return fail(NF4_ERR_UNSUPPORTED, "more than 65536 heads");
         return hip_status(nf4::launch_rope(r, positions, M, head_dim, dtype == NF4_BF16, x, y, count, (hipStream_t)stream),
                           "qlora_rope_apply");
@@ -140,6 +150,7 @@ nf4_status qlora_kv_append(const qlora_kv_cache* cache, const qlora_kv_batch* ba
         if (q_in) {
             if (nf4_status st = check_heads(q_in, "q_in", c.dim, 2, true, qi)) return st;
             if (nf4_status st = check_heads(q_out, "q_out", c.dim, 2, true, qo)) return st;
+            if (nf4_status st = check_written(q_out, "q_out", c.dim, b.tokens)) return st;
             if (qi.heads != qo.heads) return fail(NF4_ERR_ARG, "q_in and q_out have different heads");
             if (qi.data == qo.data && (qi.token_stride != qo.token_stride || qi.head_stride != qo.head_stride))
                 return fail(NF4_ERR_ARG, "in place needs the same strides");
@@ -190,6 +201,7 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
         HeadsView qv, ov;
         if (nf4_status st = check_heads(q, "q", c.dim, 2, true, qv)) return st;
         if (nf4_status st = check_heads(out, "out", c.dim, 2, true, ov)) return st;
+        if (nf4_status st = check_written(out, "out", c.dim, b.tokens)) return st;
         if (qv.heads != ov.heads) return fail(NF4_ERR_ARG, "q and out have different heads");
         if ((int64_t)b.tokens * qv.heads >= ((int64_t)1 << 26)) return fail(NF4_ERR_UNSUPPORTED, "tokens times heads must be below 2^26");
         const size_t need = nf4::kv_attention_ws_bytes(c, b, qv.heads, max_new, max_length);

@@ -75,6 +75,20 @@ def test_rope_refusals():
     assert "strides" in nf4.load_library().nf4_last_error().decode()
 
 
+def test_rope_refuses_rows_that_share_memory():
+    for out in (heads(data=8192, token_stride=0), heads(data=8192, token_stride=64), heads(data=8192, token_stride=511),
+                heads(data=8192, token_stride=128, head_stride=511), heads(data=8192, token_stride=0, head_stride=512),
+                heads(n=1, data=8192, token_stride=127)):
+        n = out.heads
+        assert rope_status(ins=heads(n), outs=out) == ARG
+        assert "overlap" in nf4.load_library().nf4_last_error().decode()
+        out.data = 4096
+        assert rope_status(ins=out, outs=out) == ARG                              # in place
+    both = (dec._Heads * 2)(heads(), heads())
+    assert dec._library().qlora_rope_apply(ctypes.byref(dec._Rope(4096, 128, 0, 1.0)), 0, SOME, 4, 128, nf4.NF4_BF16, both, both, 2, None) == ARG
+    assert "same" in nf4.load_library().nf4_last_error().decode()
+
+
 def cache(**kw):
     a = dict(codes=4096, scales=4096, pages=10, kv_heads=4, page_size=16, head_dim=128)
     a.update(kw)
@@ -108,6 +122,13 @@ def test_append_refusals():
     assert append_status(k=heads(token_stride=513)) == ARG and append_status(v=heads(data=4104)) == ARG
     assert append_status(q=heads(n=8)) == ARG and append_status(q=heads(n=8), qo=heads(n=4, data=8192)) == ARG
     assert append_status(rope=dec._Rope(4096, 256, 0, 1.0)) == ARG
+
+
+def test_append_and_attention_refuse_rows_that_share_memory():
+    for out in (heads(n=8, data=8192, token_stride=0), heads(n=8, data=8192, token_stride=512), heads(n=8, data=8192, token_stride=128, head_stride=128)):
+        assert append_status(q=heads(n=8), qo=out) == ARG and "overlap" in nf4.load_library().nf4_last_error().decode()
+        assert attention_status(out=out, length=100000) == ARG and "overlap" in nf4.load_library().nf4_last_error().decode()
+    assert attention_status(out=heads(n=8, data=8192, token_stride=128, head_stride=384), length=100000) == WORKSPACE
 
 
 def attention_status(c=None, b=None, q=None, out=None, scale=0.1, new=1, length=64, ws=None, wsb=0):

@@ -68,6 +68,27 @@ def test_strides_and_in_place(inter, rotary):
         assert rq is q and torch.equal(q, want_q) and torch.equal(k, want_k) and torch.equal(buf[:, 7 * 128:], tail)
 
 
+def test_in_place_refuses_rows_that_share_memory():
+    plan = nf4.rope_plan(64)
+    positions = torch.arange(5, dtype=torch.int32, device="cuda")
+    x = torch.randn((5, 4, 64), device="cuda")
+    keep = x.clone()
+    for bad in (x[:1].expand(5, 4, 64), x.as_strided((5, 4, 64), (128, 64, 1)), x[:, :1].expand(5, 4, 64)):
+        with pytest.raises(nf4.NF4Error):
+            nf4.rope_fwd(plan, positions, bad, inplace=True)
+        with pytest.raises(nf4.NF4Error):
+            nf4.rope_fwd(plan, positions, torch.zeros_like(x), bad, inplace=True)
+    with pytest.raises(nf4.NF4Error):
+        nf4.rope_fwd(plan, positions, x, x, inplace=True)
+    assert torch.equal(x, keep)
+    # what is only read may repeat
+    y = nf4.rope_fwd(plan, positions, x[:1].expand(5, 4, 64))
+    assert torch.equal(y, nf4.rope_fwd(plan, positions, x[:1].expand(5, 4, 64).contiguous()))
+    heads_first = x.transpose(0, 1).contiguous().transpose(0, 1)
+    want = nf4.rope_fwd(plan, positions, x)
+    assert torch.equal(nf4.rope_fwd(plan, positions, heads_first, inplace=True), want) and torch.equal(heads_first, want)
+
+
 def test_extreme_positions_values_and_nothing():
     plan = nf4.rope_plan(128)
     positions = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 10 ** 9], dtype=torch.int32, device="cuda")
