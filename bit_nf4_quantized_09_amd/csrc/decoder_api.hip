@@ -36,7 +36,7 @@ nf4_status check_heads(const qlora_heads* x, const char* name, int32_t head_dim,
     if (!x || !x->data) return fail(NF4_ERR_ARG, n + " is NULL");
     if (x->heads < 1 || x->heads > 65536) return fail(NF4_ERR_ARG, n + ": heads must be 1 .. 65536");
     if (x->token_stride < 0 || x->head_stride < 0) return fail(NF4_ERR_ARG, n + ": negative stride");
-    if (x->heads > 1 && x->head_stride < head_dim) return fail(NF4_ERR_ARG, n + ": heads overlap");
+    if (x->heads > 1 && x->head_stride != 0 && x->head_stride < head_dim) return fail(NF4_ERR_ARG, n + ": heads overlap");
     if (!aligned(x->data, elem)) return fail(NF4_ERR_ARG, n + " is misaligned");
     if (rows16 && (!aligned(x->data, 16) || x->token_stride % 8 || x->head_stride % 8))
         return fail(NF4_ERR_ARG, n + ": rows must be 16-byte aligned");
@@ -49,7 +49,7 @@ nf4_status check_written(const qlora_heads* x, const char* name, int32_t head_di
     const int64_t token = (x->heads - 1) * x->head_stride + head_dim, head = (tokens - 1) * x->token_stride + head_dim;
     const bool apart = tokens <= 1 || x->token_stride >= token ||                                    // token after token, or
                        (x->token_stride >= head_dim && (x->heads == 1 || x->head_stride >= head));   // head after head
-    return apart ? NF4_OK : fail(NF4_ERR_ARG, std::string(name) + ": rows that are written overlap");
+    return apart && (x->heads == 1 || x->head_stride >= head_dim) ? NF4_OK : fail(NF4_ERR_ARG, std::string(name) + ": rows that are written overlap");
 }
 
 nf4_status check_rope(const qlora_rope* r, int32_t head_dim, RopeView& v) {

@@ -17,8 +17,9 @@ extern "C" {
 #endif
 
 /* Per-token heads in memory: [tokens][heads][head_dim], the last dimension dense, the
- * strides in elements (so that q, k and v may be slices of one projection's output).  Where a
- * call writes them, token follows token or head follows head without sharing memory. */
+ * strides in elements (so that q, k and v may be slices of one projection's output).  What is
+ * only read may repeat: a stride of 0 is one head, or token, for all.  Where a call writes them,
+ * token follows token or head follows head without sharing memory. */
 typedef struct qlora_heads {
     void* data;
     int64_t token_stride;

@@ -100,6 +100,19 @@ def test_append(dim, page, rotary, inter):
         assert torch.equal(q, want)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_one_head_for_all(dim):
+    # keys, values and queries whose heads are one: an expanded tensor, as its copies
+    plan = nf4.rope_plan(dim)
+    c, d = (Case([5, 0, 40], [3, 20, 1], page=16, kv=3, heads=6, dim=dim, seed=23) for _ in range(2))
+    q, k, v = (x[:, :1].contiguous() for x in (c.q, c.k, c.v))
+    a = nf4.kv_append(c.cache, k.expand(-1, 3, -1), v.expand(-1, 3, -1), *c.meta(), rope=plan, q=q.expand(-1, 6, -1))
+    b = nf4.kv_append(d.cache, k.repeat(1, 3, 1), v.repeat(1, 3, 1), *d.meta(), rope=plan, q=q.repeat(1, 6, 1))
+    assert torch.equal(a, b) and torch.equal(c.cache.codes, d.cache.codes) and torch.equal(c.cache.scales, d.cache.scales)
+    assert torch.equal(nf4.kv_attention(c.cache, a[:, :1].expand(-1, 6, -1), *c.meta()),
+                       nf4.kv_attention(d.cache, a[:, :1].repeat(1, 6, 1), *d.meta()))
+
+
 def test_append_many_sequences():
     r = np.random.RandomState(1)
     check_append(Case(r.randint(0, 90, 300), r.randint(0, 4, 300), page=32, kv=2, dim=64, seed=4), with_q=False)

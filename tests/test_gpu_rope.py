@@ -81,7 +81,10 @@ def test_in_place_refuses_rows_that_share_memory():
     with pytest.raises(nf4.NF4Error):
         nf4.rope_fwd(plan, positions, x, x, inplace=True)
     assert torch.equal(x, keep)
-    # what is only read may repeat
+    # what is only read may repeat: one head for all, one token for all, one row for both
+    for one in (x[:, :1], x[:1], x[:1, :1]):
+        y = nf4.rope_fwd(plan, positions, one.expand(5, 4, 64))
+        assert torch.equal(y, nf4.rope_fwd(plan, positions, one.expand(5, 4, 64).contiguous()))
     y = nf4.rope_fwd(plan, positions, x[:1].expand(5, 4, 64))
     assert torch.equal(y, nf4.rope_fwd(plan, positions, x[:1].expand(5, 4, 64).contiguous()))
     heads_first = x.transpose(0, 1).contiguous().transpose(0, 1)
