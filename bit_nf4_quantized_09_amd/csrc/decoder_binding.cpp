@@ -118,6 +118,12 @@ at::Tensor fresh_like(const at::Tensor& t, qlora_heads& h) {
     return out;
 }
 
+// A caller's tensor that the call has written through its pointer: its version moves on, so that autograd refuses a
+// backward that saved it before (tensors of inference mode have none).
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 qlora_rope rope_of(PyObject* const* a, const at::Tensor& of) {       // freq, rotary_dim, interleaved, magnitude
     const at::Tensor& freq = tensor(a[0], "freq");
     want_dense(freq, "freq", at::kLong, of);
@@ -213,6 +219,10 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         check(qlora_rope_apply(&r, truth(a[4]) ? 1 : 0, (const int32_t*)positions.data_ptr(), M, (int32_t)dim,
                                type == at::kBFloat16 ? NF4_BF16 : NF4_F32, in, out, two ? 2 : 1, stream_of(q)));
+        if (inplace) {
+            written(yq);
+            if (two) written(yk);
+        }
         if (!two) return wrap(yq);
         PyObject* pq = wrap(yq);
         PyObject* pk = pq ? wrap(yk) : nullptr;
@@ -248,6 +258,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             out = fresh_like(q, oh);
         }
         check(qlora_kv_append(&c, &b, &kh, &vh, turns ? &r : nullptr, queries ? &qh : nullptr, queries ? &oh : nullptr, stream_of(k)));
+        written(tensor(a[0], "codes"));
+        written(tensor(a[1], "scales"));
         return wrap(out);
     });
 }

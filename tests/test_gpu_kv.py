@@ -113,6 +113,16 @@ def test_one_head_for_all(dim):
                        nf4.kv_attention(d.cache, a[:, :1].repeat(1, 6, 1), *d.meta()))
 
 
+def test_append_moves_the_versions():
+    c = Case([5, 0], [3, 1], page=16, kv=2, heads=4, dim=64, seed=24)
+    before = c.cache.codes._version, c.cache.scales._version, c.q._version
+    q = nf4.kv_append(c.cache, c.k, c.v, *c.meta(), q=c.q)
+    assert c.cache.codes._version > before[0] and c.cache.scales._version > before[1] and c.q._version == before[2]
+    keep = c.cache.codes._version
+    nf4.kv_attention(c.cache, q, *c.meta())
+    assert c.cache.codes._version == keep
+
+
 def test_append_many_sequences():
     r = np.random.RandomState(1)
     check_append(Case(r.randint(0, 90, 300), r.randint(0, 4, 300), page=32, kv=2, dim=64, seed=4), with_q=False)

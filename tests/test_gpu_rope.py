@@ -92,6 +92,25 @@ def test_in_place_refuses_rows_that_share_memory():
     assert torch.equal(nf4.rope_fwd(plan, positions, heads_first, inplace=True), want) and torch.equal(heads_first, want)
 
 
+def test_in_place_moves_the_version():
+    plan = nf4.rope_plan(64)
+    positions = torch.arange(5, dtype=torch.int32, device="cuda")
+    w = torch.randn((5, 4, 64), device="cuda", requires_grad=True)
+    x, k = torch.randn((5, 4, 64), device="cuda"), torch.randn((5, 2, 64), device="cuda")
+    y = (w * x).sum()                         # the product's gradient needs x as it is now
+    before = x._version, k._version
+    nf4.rope_fwd(plan, positions, x, k)
+    assert (x._version, k._version) == before
+    nf4.rope_fwd(plan, positions, x, k, inplace=True)
+    assert x._version > before[0] and k._version > before[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        z = x.clone()
+        nf4.rope_fwd(plan, positions, z, inplace=True)
+    nf4.rope_fwd(plan, positions, z, inplace=True)
+
+
 def test_extreme_positions_values_and_nothing():
     plan = nf4.rope_plan(128)
     positions = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 10 ** 9], dtype=torch.int32, device="cuda")
