@@ -143,6 +143,25 @@ def attention(codes, scales, q, starts, lengths, table, scale):
     return out, reach
 
 
+# Relative norm of dW's error over vocabulary rows that are no row's target.  Their G = dloss (p - 0) carries one rounding
+# to bf16 and the output another.  Rounding to 8 significant bits leaves an error of 2^-8 / sqrt(3) of the power of two
+# below (root of the mean square); mantissas spread evenly over the logarithm have a mean square of 1/m of 3 / (8 ln 2), so
+# that is 1.66e-3 of a value, and errors of independent sign keep their relative norm in a sum: sqrt(2) 1.66e-3 =
+# 2.35e-3.  Exponentials kept without their eight further bits add a third: sqrt(3) 1.66e-3 = 2.87e-3.  The limit is between.
+DW_NORM = 2.6e-3
+
+
+def kept_exponentials(E, low="right"):
+    """fp32 exponentials after they were kept as bf16 and eight bits more; low: what happens to these."""
+    top = E.bfloat16().float()
+    bits = ((E.view(torch.int32) - top.view(torch.int32) + 0x80) >> 8).clamp(-128, 127)
+    if low == "zero":
+        return top
+    if low == "misplaced":
+        bits = bits.roll(1, 1)
+    return (top.view(torch.int32) + (bits << 8)).view(torch.float32)
+
+
 def head_loss(X, W, targets, dloss, ignore=-100):
     """loss, dX, dW and |G| in float64 (torch)."""
     x, w = X.double(), W.double()

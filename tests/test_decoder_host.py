@@ -220,6 +220,26 @@ def test_reference_gradient_against_differences():
                 assert abs((of(A + e) - of(A - e)) / 2e-6 - d[i, j]) < 1e-8
 
 
+@pytest.mark.parametrize("M,V,K", [(384, 3000, 64), (33, 4000, 128)])
+def test_the_limit_on_dw_tells_kept_bits_from_lost_ones(M, V, K):
+    # dW as the library makes it: exponentials kept in 24 bits, G and dW rounded to bf16
+    g = torch.Generator().manual_seed(M)
+    X = torch.randn((M, K), generator=g).bfloat16()
+    W = (torch.randn((V, K), generator=g) / math.sqrt(K)).bfloat16()
+    t, dl = torch.randint(0, V // 2, (M,), generator=g), torch.randn(M, generator=g) / M
+    _, _, dW, _, z = ref.head_loss(X, W, t, dl)
+    z = z / math.log(2)
+    R, lse = torch.round(z[torch.arange(M), t]), torch.logsumexp(z * math.log(2), 1) / math.log(2)
+    E = torch.exp2(z - R[:, None]).float()
+    factor = (dl / dl.abs().max()).double() * torch.exp2(R - lse)
+    error = {}
+    for low in ("right", "zero", "misplaced"):
+        G = (ref.kept_exponentials(E, low).double() * factor[:, None]).bfloat16().double()
+        got = (G.t() @ X.double() * dl.abs().max().double()).bfloat16().double()
+        error[low] = float((got - dW)[V // 2:].norm() / dW[V // 2:].norm())
+    assert error["right"] <= ref.DW_NORM < error["zero"] and ref.DW_NORM < error["misplaced"], error
+
+
 def test_reference_rotation_against_differences():
     # the gradient of sum(w . rotate(x)) by differences is rotate-back of w
     theta, mag = ref.theta_of(6, scaling="parts", factor=4.0, original_length=64)

@@ -214,6 +214,21 @@ def test_equal_factors_lose_nothing():
         assert float((got.double() - want).norm() / want.norm()) <= 2.5e-3
 
 
+@pytest.mark.parametrize("M,V,K", [(33, 4000, 512), (64, 20000, 256), (60, 30000, 4096), (384, 3000, 512), (700, 5000, 576),
+                                   (2048, 70000, 64), (1024, 32000, 6144)])
+@pytest.mark.parametrize("jump", [False, True])
+def test_dw_of_rows_without_targets(M, V, K, jump):
+    # few tokens, 64-, 256- and 512-row tiles, one piece and several; with `jump` the second half of the vocabulary passes
+    # the targets' logits by 60, each tile takes a reference of its own, and they are brought together afterwards
+    X, W, t, dl = inputs(M, V, K, seed=3)
+    t %= V // 2
+    if jump:
+        X[:, 0], W[:, 0], W[V // 2:, 0] = 1.0, 0.0, 60.0
+    dW = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)[2][V // 2:, 1:].double()
+    want = ref.head_loss(X, W, t, dl)[2][V // 2:, 1:]
+    assert float((dW - want).norm() / want.norm()) <= ref.DW_NORM
+
+
 def test_repeats_and_streams():
     X, W, t, dl = inputs(333, 4000, 256, seed=12)
     a = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
