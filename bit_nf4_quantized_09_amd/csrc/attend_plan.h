@@ -48,11 +48,11 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // Chunks: for k_attend_rows about 4096 workgroups (some rounds of three or four on each compute unit, so that a
 // ragged batch's last chunks end together) at the stated lengths, but chunks of 1024 keys where 1024 workgroups are left
 // then, for a workgroup's start, end and join cost as much as some 200 keys (two sequences of 120001 keys, 8 kv
-// heads: chunks of 512 keys 81 us, 1024 73; of 24 sequences of up to 4096, 64 heads: 1536 keys 132 us, half of that 149, twice 199),
+// heads: chunks of 512 keys 82 us, 1024 76; of 24 sequences of up to 4096, 64 heads: 1536 keys 128 us, half of that 130, twice 191),
 // and of at least 256 keys; up to 768 keys stay whole, for the join's launch costs more (4 sequences of up to 600 keys,
 // heads of 128: 7.0 us, 8.9 in chunks; of up to 900: 9.0 and 9.0, heads of 256 14.4 and 11.9).  For k_attend_block, where there are fewer blocks than waves that run at once, two or four
 // waves share a block's keys (4 prompts of up to 534 tokens, 8 heads of 64: 12.5 us, 22.5 alone; 2 of 1277, 16 heads of
-// 128: 31 and 35; but 3 of 1500, 32 heads: 134 and 126, and heads of 256, whose parts are as large as a step's
+// 128: 31 and 35; but 3 of 1500, 32 heads: 134 and 127, and heads of 256, whose parts are as large as a step's
 // work: 24 and 10 for 3 of 76 tokens), and chunks only where there are still fewer than 1024 waves, one for
 // each SIMD: of 128 keys a wave at least where most of the keys were there before (27 sequences of up to 494 keys
 // and 11 tokens: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the

@@ -1,4 +1,4 @@
-// head_loss.hip -- softmax cross entropy of a vocabulary head without its logits (gfx950).
+// head_loss.hip -- softmax cross entropy of a vocabulary head, its logits never in memory as such (gfx950).
 //
 //   z = X W^T,  loss = lse(z) - z_y,  G = dloss (softmax(z) - onehot),  dX = G W,  dW = G^T X
 //
@@ -17,11 +17,12 @@
 // row's other tiles and sums to the new R by exact powers of two.
 //
 // With dW, the contraction runs over tokens and needs normalised weights.  Every piece's E is kept,
-// as bf16 and the eight bits that follow (up to 1 GB of bf16), and once l is known k_head_turn makes
+// as bf16 and the eight bits that follow (up to 1 GB of bf16: half as much again as bf16 logits), and once l is known k_head_turn makes
 // G = dloss / max|dloss| (p - onehot) of it, in bf16 and transposed, rounded once; the factor
 // max|dloss| is applied to the fp32 sums, so that a mean's 1/count does not round the many nearly
 // equal target entries alike.  Beyond 1 GB each piece's logits are computed again instead
-// (HEAD_GT): a fourth product (4096 tokens x 32000 x 8192: 6.65 ms, 5.35 with E kept).
+// (HEAD_GT): a fourth product (4096 tokens x 32000 x 8192: 6.65 ms, 5.2 to 5.4 with E kept; x 131200 x 4096,
+// beyond: 14.2 ms).
 //
 // Rounding: logits, maxima, sums and accumulators are fp32; E and G are bf16, the type of the
 // matrix instructions' operands and of the outputs.

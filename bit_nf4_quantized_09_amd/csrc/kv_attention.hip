@@ -6,8 +6,8 @@
 // x + f, and 2^(-f_j) w_j for the denominator: the value scales cost one addition per score.
 // Rounding: keys are exact in bf16 (E4M3 has 4 significant bits, the scale is a power of
 // two), scores, maxima, sums and outputs are fp32, and the weights go into the second
-// product as fp16, scaled to at most 2^15: 11 significant bits down to 2^-29 of the largest,
-// an eighth of bf16's error (the output itself is bf16).
+// product as fp16, the largest between 2^10 and 2^15: 11 significant bits down to 2^-24 of the
+// largest, an eighth of bf16's error (the output itself is bf16).
 //
 // Shape.  A tile is up to 16 rows (query heads of one kv head, of one or more tokens) and a
 // step 32 keys.  Both products are v_mfma_f32_16x16x32 with the keys or the value dimensions
@@ -22,12 +22,15 @@
 // Work.  Up to 32 rows of a (sequence, kv head), k_attend_rows: workgroups of four waves own
 // (sequence, kv head, row tile, chunk of keys); the waves take the chunk's steps in turn and join
 // through LDS, and chunks of one row join in a second launch.  Bound by HBM, each key and value byte
-// read once per row tile: 24 sequences of up to 4096 keys, 64 heads of 128 (716 MB): 128 us, 5.6 TB/s;
-// two of 120001, 8 kv heads (343 MB): 73 us with the join.  A short sequence is bound by its chain
-// of loads (length, page, codes): 6.5 us for one of 131 keys.
-// More rows, k_attend_block: one, two or four waves own (sequence, kv head, 16 CT rows, chunk).  Bound by the
-// vector instructions of the softmax and of decoding values: 3 prompts of up to 1500 tokens behind up to
-// 1100 cached, 32 heads of 128 (74 GFLOP): 126 us, 585 TFLOP/s.
+// read once per row tile: 24 sequences of up to 4096 keys, 64 heads of 128 (716 MB): 126 us, 5.7 TB/s;
+// two of 120001, 8 kv heads (343 MB): 76 us with the join.  A short sequence is bound by its chain
+// of loads (length, page, codes): 6.3 us for one of 131 keys.
+// More rows, k_attend_block: one, two or four waves own (sequence, kv head, 16 CT rows, chunk).  Bound by latency:
+// a wave waits for its own loads, matrix and vector instructions in turn, registers leave room for two waves a
+// SIMD, and blocks of unequal length leave one in the last third of the time.  3 prompts of up to 1500 tokens
+// behind up to 1100 cached, 32 heads of 128 (74 GFLOP): 137 us alone, 127 a call among others, whose blocks fill
+// that third (540 and 585 TFLOP/s); 1.5 of 2 waves resident, vector instructions issued 39% of the time, matrix
+// cores busy 22%.
 #include "bufio.h"
 #include "paged.h"
 #include "attend_plan.h"
@@ -532,7 +535,7 @@ __device__ __forceinline__ int2 block_of_rank(const AttendArgs& a, int here, int
 // each decoded once for all of its tiles; no LDS, no barrier, but where W waves share the keys, at the end.  Scores
 // by 8-bit products (D >= 128): the codes of the keys are the operand as they lie.  The workgroups of one (sequence, kv
 // head) run on one XCD, whose L2 holds its keys; those that see most keys start first.
-// (Heads of 64: three waves a SIMD, 72 us for 3 prompts of up to 1500 tokens behind up to 1100 cached, 32 heads; two 84.)
+// (Heads of 64: three waves a SIMD, 74 us for 3 prompts of up to 1500 tokens behind up to 1100 cached, 32 heads; two 84.)
 template <int D, int CT, bool WIDE, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(D == 64 && W == 1 ? 3 : 2)))
 void k_attend_block(AttendArgs a) {
@@ -853,7 +856,7 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             // each lane; beyond some rounds the order of one sequence's blocks is enough)
             a.ordered = pairs <= 64 * XCDS && pairs * a.blocks * p.block.waves > 2048 && pairs * a.blocks * p.block.waves <= 8 * 2048;
             // pages of 32 tokens and more hold a whole step: half the address work (3 prompts of up to 1500
-            // tokens, 32 heads of 64: 73 us for 86)
+            // tokens, 32 heads of 64: 74 us for 85)
             auto run = [&](auto wide, auto waves) {
                 constexpr int W = decltype(waves)::value;
                 hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), decltype(wide)::value, W>), grid, dim3(64 * W), 0, s, a);
@@ -872,7 +875,7 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             part(p.rows, ws);
             a.row_tiles = p.rows.tiles;
             a.few = p.rows.few;
-            // codes that one row tile reads are read once: they need not stay in the caches (716 MB: 132 us, 140 with them)
+            // codes that one row tile reads are read once: they need not stay in the caches (716 MB: 128 us, 138 with them)
             const dim3 grid((uint32_t)a.splits, (uint32_t)(c.heads * a.row_tiles), (uint32_t)b.seqs);
             if (a.row_tiles == 1) hipLaunchKernelGGL((k_attend_rows<D, 2>), grid, dim3(256), 0, s, a);
             else hipLaunchKernelGGL((k_attend_rows<D, 0>), grid, dim3(256), 0, s, a);

@@ -160,7 +160,8 @@ def kv_attention(cache: KVCache, q: torch.Tensor, starts: torch.Tensor, lengths:
     head_dim].  Arguments as for kv_append (the same lengths: tokens before these); head h
     reads kv head h // (heads // kv_heads).  scale: 1/sqrt(head_dim) by default.  max_new (the
     most new tokens of a sequence) and max_length (its most positions, new ones included) size
-    the launch: without them it is sized for `tokens` and for the table's width."""
+    the launch: without them it is sized for `tokens` and for the table's width, which costs single
+    tokens up to twice the time (24 sequences of up to 4096 keys, 64 heads on 8: 32 us stated, 57 not)."""
     return (_bound or _binding()).attention(cache.codes, cache.scales, q, starts, lengths, table, scale, max_new, max_length)
 
 
@@ -169,11 +170,13 @@ def kv_attention(cache: KVCache, q: torch.Tensor, starts: torch.Tensor, lengths:
 # ---------------------------------------------------------------------------
 def head_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, dloss: Optional[torch.Tensor] = None,
               need_dw: bool = False, ignore_index: int = -100):
-    """Softmax cross entropy of the vocabulary head z = X W^T, without keeping the logits:
-    (loss fp32 [M], dX bf16 [M, K] or None, dW bf16 [V, K] or None).
+    """Softmax cross entropy of the vocabulary head z = X W^T:
+    (loss fp32 [M], dX bf16 [M, K] or None, dW bf16 [V, K] or None).  Loss and dX do not keep the
+    logits; need_dw keeps their exponentials, three bytes each, while they are up to 2^29 (more memory
+    than bf16 logits), and computes the logits twice beyond.
       X        bf16 [M, K], W bf16 [V, K], K a multiple of 64
       targets  int64 [M]; a row whose target is ignore_index, or outside 0 .. V-1, has loss 0
-               and no gradient
+               and no gradient, whatever X and dloss hold there
       dloss    fp32 [M], the gradient of each row's loss (1/count for a mean): with it dX is
                computed in the same call, and dW if need_dw.  A later factor on a row's loss
                multiplies its row of dX."""

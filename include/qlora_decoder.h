@@ -47,7 +47,7 @@ typedef struct qlora_rope {
  *   in, out    `count` (1 or 2) tensors each; out[i] may be in[i] itself (same pointer and
  *              strides), and may not overlap it otherwise.  Any strides; 16-byte aligned
  *              rows take the fast path.
- *   head_dim   1 .. 512;  0 <= M < 2^24 (M == 0 enqueues nothing); up to 65536 heads in all */
+ *   head_dim   2 .. 512;  0 <= M < 2^24 (M == 0 enqueues nothing); up to 65536 heads in all */
 nf4_status qlora_rope_apply(const qlora_rope* rope, int32_t backward, const int32_t* positions, int64_t M,
                             int32_t head_dim, nf4_dtype dtype, const qlora_heads* in, const qlora_heads* out,
                             int32_t count, void* stream);
@@ -140,10 +140,19 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
  *   dloss    device fp32[M], the gradient of each row's loss; only read when dX or dW is given
  *   loss     out: fp32[M], or NULL
  *   dX       out: bf16 M x K, or NULL;  dW  out: bf16 V x K, or NULL
- *   workspace  qlora_head_loss_workspace_bytes(M, K, V, dX != NULL, dW != NULL), 256-byte aligned:
- *              a packed copy of X and pieces of up to 128 MB; with dX fp32 sums of its size; with dW another copy of X
- *              (its ignored rows zero) and the
- *              exponentials, 3 bytes each, while they are up to 2^29 (beyond, the logits are computed twice) */
+ *   workspace  qlora_head_loss_workspace_bytes(M, K, V, dX != NULL, dW != NULL), 256-byte aligned.  With
+ *              m = M up to a multiple of 512, and pieces of the vocabulary of v entries each (multiples of
+ *              512, as many as 2 m v <= 2^27 holds, one at least, and no more than V asks for), it holds
+ *                2 m K                     X in the order of the products,
+ *                8 m ceil(v / 32) or less  statistics of the logits' tiles (without gradients v is V),
+ *                2 m v                     exponentials of a piece, with dX or dW,
+ *                4 M K c                   with dX, fp32 sums: c is 1, or up to 64 where the tiles of dX are so few that
+ *                                          its contraction is cut into as many parts (and 0 where one piece and
+ *                                          one part need none),
+ *                2 M K                     with dW, X with its ignored rows zero,
+ *              and with dW, where 2 m V (whole pieces) is 2^30 at most, every exponential in three bytes and a
+ *              piece of G^T (3 m V + 2 m v in place of 2 m v): more than bf16 logits take.  Beyond, each
+ *              piece's logits are computed a second time instead. */
 size_t qlora_head_loss_workspace_bytes(int64_t M, int64_t K, int64_t V, int32_t need_dx, int32_t need_dw);
 nf4_status qlora_head_loss(const void* X, int64_t M, int64_t K, const void* W, int64_t V, const int64_t* targets,
                            int64_t ignore_index, const float* dloss, float* loss, void* dX, void* dW,

@@ -196,6 +196,23 @@ def test_loss_workspace_does_not_hold_the_logits():
     assert dec._library().qlora_head_loss_workspace_bytes(M, K, V, 1, 0) < M * V * 2 / 4
 
 
+@pytest.mark.parametrize("dx,dw", [(0, 0), (1, 0), (0, 1), (1, 1)])
+@pytest.mark.parametrize("M", [1, 33, 64, 100, 512, 2048, 4096, 5000, 131072, 200000])
+def test_loss_workspace_is_what_the_header_says(M, dx, dw):
+    up = lambda n, to: -(-n // to) * to  # noqa: E731
+    for K in (64, 512, 4096, 8192):
+        for V in (1, 500, 32000, 128256, 131200):
+            m = up(M, 512)
+            v = min(max(512, (1 << 27) // (2 * m) // 512 * 512), up(V, 512))
+            pieces = -(-V // v)
+            kept = dw and 2 * m * v * pieces <= 1 << 30
+            least = 2 * m * K + (2 * m * v if dx or dw else 0) + 2 * M * K * dw + (3 * m * v * pieces if kept else 0)
+            rows = 64 * m + 4 * m * (pieces + 1)                                # statistics of rows
+            most = least + 8 * m * up(-(-min(V, v if dx or dw else V) // 32), 4) + 4 * M * K * 64 * dx + rows + 16 * 256
+            size = dec._library().qlora_head_loss_workspace_bytes(M, K, V, dx, dw)
+            assert least <= size <= most, (M, K, V, dx, dw, least, size, most)
+
+
 def test_tensor_refusals_without_a_gpu():
     plan = nf4.rope_plan(8, device="cpu")
     x = torch.zeros((2, 1, 8))
