@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import bit_nf4_quantized_09_amd as nf4
+import decoder_abi as dec
 import decoder_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -259,6 +260,23 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for x, y in zip(out, run()):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("M,V,K", [(3, 500, 64), (50, 3000, 128), (300, 5001, 576), (2048, 40000, 64), (4096, 131200, 64)])
+def test_each_output_alone(M, V, K):
+    # through the C entry any of the outputs may be left out: the others are the same bits
+    X, W, t, dl = inputs(M, V, K, seed=19)
+    loss, dX, dW = nf4.head_loss(X, W, t, dloss=dl, need_dw=True)
+    for with_loss, with_dx, with_dw in ((1, 1, 0), (0, 1, 0), (1, 0, 1), (0, 0, 1), (0, 1, 1)):
+        size = dec._library().qlora_head_loss_workspace_bytes(M, K, V, with_dx, with_dw)
+        ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+        got = [torch.full_like(x, 7.0) if on else None for x, on in ((loss, with_loss), (dX, with_dx), (dW, with_dw))]
+        at = [None if x is None else x.data_ptr() for x in got]
+        status = dec._library().qlora_head_loss(X.data_ptr(), M, K, W.data_ptr(), V, t.data_ptr(), -100, dl.data_ptr(), *at,
+                                                (ws.data_ptr() + 255) // 256 * 256, size, torch.cuda.current_stream().cuda_stream)
+        assert status == nf4.NF4_OK
+        for x, want in zip(got, (loss, dX, dW)):
+            assert x is None or torch.equal(x, want)
 
 
 def test_nothing():
