@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -211,6 +212,9 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor yq = q, yk;
         if (two) yk = tensor(a[7], "k");
         if (inplace) {
+            // (autograd would not see the rotation and give the gradient of a step without it)
+            if (c10::GradMode::is_enabled() && (yq.requires_grad() || (two && yk.requires_grad())))
+                bad("a tensor that requires grad is not rotated in place while gradients are recorded");
             out[0] = in[0];
             out[1] = in[1];
         } else {

@@ -104,7 +104,8 @@ def rope_fwd(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, k: Option
              inplace: bool = False):
     """Queries, and keys if given, rotated to their positions: q [tokens, heads, dim], k
     [tokens, kv_heads, dim] (fp32 or bf16, the same type; any strides with a dense last
-    dimension), positions int32 [tokens].  Returns new dense tensors, or the same ones if `inplace`."""
+    dimension), positions int32 [tokens].  Returns new dense tensors, or the same ones if `inplace`
+    (not of tensors that autograd records; rows may not share memory)."""
     return (_bound or _binding()).rope(plan.freq, plan.rotary_dim, plan.interleaved, plan.magnitude, False, positions, q, k, inplace)
 
 

@@ -111,6 +111,20 @@ def test_in_place_moves_the_version():
     nf4.rope_fwd(plan, positions, z, inplace=True)
 
 
+def test_in_place_refuses_what_autograd_records():
+    plan = nf4.rope_plan(64)
+    positions = torch.arange(5, dtype=torch.int32, device="cuda")
+    leaf, k = torch.randn((5, 4, 64), device="cuda", requires_grad=True), torch.randn((5, 2, 64), device="cuda")
+    keep = leaf.detach().clone()
+    for q, kk in ((leaf, None), (leaf * 1, None), (k, leaf), (leaf, k)):
+        with pytest.raises(ValueError, match="in place"):
+            nf4.rope_fwd(plan, positions, q, kk, inplace=True)
+    assert torch.equal(leaf, keep)
+    with torch.no_grad():
+        nf4.rope_fwd(plan, positions, leaf, inplace=True)
+    assert torch.equal(leaf, nf4.rope_fwd(plan, positions, keep))
+
+
 def test_extreme_positions_values_and_nothing():
     plan = nf4.rope_plan(128)
     positions = torch.tensor([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 10 ** 9], dtype=torch.int32, device="cuda")
