@@ -29,6 +29,7 @@ __all__ = [
     "NF4_OP_DOUBLE_QUANTIZE", "NF4_OP_LINEAR_FWD", "NF4_OP_LINEAR_BWD", "NF4_OP_LOWRANK_SVD", "NF4_OP_LOFTQ",
     "nf4_lowrank_svd", "loftq_init",
     "RopePlan", "rope_plan", "rope_fwd", "rope_bwd", "KVCache", "kv_cache", "kv_append", "kv_attention", "head_loss",
+    "block_norm_fwd", "block_norm_bwd", "grad_norm", "clip_grads", "shape_logits",
 ]
 
 NF4_OK, NF4_ERR_ARG, NF4_ERR_UNSUPPORTED, NF4_ERR_WORKSPACE, NF4_ERR_HIP = range(5)
@@ -113,6 +114,11 @@ def load_library():
     L.nf4_adamw_step_paged.restype = ctypes.c_int
     L.nf4_adamw_step_paged.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _f, _f, _f, _f, _f, _i64,
                                        _vp, _sz, _vp]
+    L.qlora_adamw_step_scaled.restype = ctypes.c_int
+    L.qlora_adamw_step_scaled.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _f, _f, _f, _f, _f, _i64, _vp, _vp]
+    L.qlora_adamw_step_paged_scaled.restype = ctypes.c_int
+    L.qlora_adamw_step_paged_scaled.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _f, _f, _f, _f, _f, _i64, _vp,
+                                                _vp, _sz, _vp]
     L.nf4_lowrank_svd.restype = ctypes.c_int
     L.nf4_lowrank_svd.argtypes = [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
     L.nf4_loftq_init.restype = ctypes.c_int
@@ -450,11 +456,20 @@ def _check_state(name, t, n, device=None):
         raise ValueError("%s must be a page-locked host tensor" % name)
 
 
+def _check_factor(factor, g):
+    _dev(factor, "factor", torch.float32)
+    if factor.numel() != 1:
+        raise ValueError("factor must be one number")
+    _same_device(("g", g), ("factor", factor))
+
+
 def adamw_step(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, v: torch.Tensor, lr: float,
                step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-               weight_decay: float = 0.0, p_bf16: Optional[torch.Tensor] = None):
+               weight_decay: float = 0.0, p_bf16: Optional[torch.Tensor] = None,
+               factor: Optional[torch.Tensor] = None):
     """One AdamW step in place on fp32 GPU state p, m, v with gradient g (all the same
-    size); writes bf16(p) into p_bf16 when given (the layer's A or B)."""
+    size), times `factor` (a fp32 number on the GPU) when given; writes bf16(p) into p_bf16
+    when given (the layer's A or B)."""
     L = load_library()
     n = p.numel()
     for name, t in (("p", p), ("g", g), ("m", m), ("v", v)):
@@ -463,14 +478,19 @@ def adamw_step(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, v: torch.Tenso
         _dev(p_bf16, "p_bf16", torch.bfloat16)
         if p_bf16.numel() != n:
             raise ValueError("p_bf16 must have %d values" % n)
-    _check(L.nf4_adamw_step(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), n, float(lr), float(beta1),
-                            float(beta2), float(eps), float(weight_decay), int(step), _stream(p.device)))
+    how = (_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), n, float(lr), float(beta1), float(beta2), float(eps),
+           float(weight_decay), int(step))
+    if factor is None:
+        _check(L.nf4_adamw_step(*how, _stream(p.device)))
+    else:
+        _check_factor(factor, g)
+        _check(L.qlora_adamw_step_scaled(*how, _ptr(factor), _stream(p.device)))
 
 
 def adamw_step_paged(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, v: torch.Tensor, lr: float,
                      step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                      weight_decay: float = 0.0, p_bf16: Optional[torch.Tensor] = None,
-                     stage: Optional[torch.Tensor] = None):
+                     stage: Optional[torch.Tensor] = None, factor: Optional[torch.Tensor] = None):
     """adamw_step for state paged out to page-locked host tensors p, m, v; g (and
     p_bf16) on the GPU.  The state streams through `stage` (a GPU uint8 buffer,
     64 MiB by default) in stream order; the host tensors must not be touched until
@@ -487,9 +507,13 @@ def adamw_step_paged(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, v: torch
     if stage is None:
         stage = _workspace(64 << 20, g.device)
     _dev(stage, "stage", torch.uint8)
-    _check(L.nf4_adamw_step_paged(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), n, float(lr),
-                                  float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
-                                  _ptr(stage), stage.numel(), _stream(g.device)))
+    how = (_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), n, float(lr), float(beta1), float(beta2), float(eps),
+           float(weight_decay), int(step))
+    if factor is None:
+        _check(L.nf4_adamw_step_paged(*how, _ptr(stage), stage.numel(), _stream(g.device)))
+    else:
+        _check_factor(factor, g)
+        _check(L.qlora_adamw_step_paged_scaled(*how, _ptr(factor), _ptr(stage), stage.numel(), _stream(g.device)))
 
 
 class PagedAdamW:
@@ -554,11 +578,16 @@ class PagedAdamW:
     def on_host(self, i: int) -> bool:
         return self.state[i]["host"]
 
-    def step(self, grads):
-        """One AdamW step for every parameter; grads are fp32 GPU tensors (dA, dB)."""
+    def step(self, grads, max_norm: Optional[float] = None):
+        """One AdamW step for every parameter; grads are fp32 GPU tensors (dA, dB).  With max_norm the
+        gradients count times min(1, max_norm / their global norm), without being written, and the
+        norm is returned (a fp32 number on the GPU)."""
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError("one gradient per parameter")
+        norm = factor = None
+        if max_norm is not None:
+            norm, factor = _norm_and_factor(grads, float(max_norm))
         self.t += 1
         b1, b2 = self.betas
         for q, g, st in zip(self.params, grads, self.state):
@@ -567,10 +596,11 @@ class PagedAdamW:
                 if self._stage is None:
                     self._stage = _workspace(self._stage_bytes, q.device)
                 adamw_step_paged(st["p"], gq, st["m"], st["v"], self.lr, self.t, b1, b2, self.eps,
-                                 self.weight_decay, p_bf16=q, stage=self._stage)
+                                 self.weight_decay, p_bf16=q, stage=self._stage, factor=factor)
             else:
                 adamw_step(st["p"], gq, st["m"], st["v"], self.lr, self.t, b1, b2, self.eps,
-                           self.weight_decay, p_bf16=q)
+                           self.weight_decay, p_bf16=q, factor=factor)
+        return norm
 
 
 # ---------------------------------------------------------------------------
@@ -704,6 +734,8 @@ def loftq_init(W: torch.Tensor, r: int, alpha: float, omega: torch.Tensor, iters
     return NF4Weight(codes, q, c2, mean, (int(N), int(K))), A, B, err
 
 
-# The operators around the linears (rotary positions, the paged 8-bit cache, the vocabulary head's loss).
-from .decoder import (KVCache, RopePlan, head_loss, kv_append, kv_attention, kv_cache, rope_bwd, rope_fwd,  # noqa: E402
-                      rope_plan)
+# The operators around the linears (rotary positions, the paged 8-bit cache, the vocabulary head's loss, the norms around
+# a block, the gradients' norm, the logits' penalties and masks).
+from .decoder import (KVCache, RopePlan, block_norm_bwd, block_norm_fwd, clip_grads, grad_norm, head_loss,  # noqa: E402
+                      kv_append, kv_attention, kv_cache, norm_and_factor as _norm_and_factor, rope_bwd, rope_fwd, rope_plan,
+                      shape_logits)

@@ -16,7 +16,8 @@ BINDING_SOURCE = "decoder_binding.cpp"   # the Python calls of decoder.py: a CPy
 BINDING = os.path.join(OUT_DIR, "qlora_decoder_binding.so")
 PROBE_LIB = os.path.join(OUT_DIR, "libnf4_hbm_probe.so")
 SOURCES = ["api.hip", "codec.hip", "lora.hip", "fused.hip", "gemv.hip", "adamw.hip", "codebook.hip", "lowrank.hip",
-           "decoder_api.hip", "rope.hip", "kv_append.hip", "kv_attention.hip", "head_loss.hip"]
+           "decoder_api.hip", "rope.hip", "kv_append.hip", "kv_attention.hip", "head_loss.hip",
+           "step_api.hip", "block_norm.hip", "gradients.hip", "logits.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

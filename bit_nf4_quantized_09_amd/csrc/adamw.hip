@@ -13,7 +13,8 @@
 //   v = b2 v + (1 - b2) g g
 //   p = p (1 - lr wd) - (lr / bc1) (m / (sqrt(v) / sqrt(bc2) + eps))
 // with bc1 = 1 - b1^t, bc2 = 1 - b2^t formed on the host in double.  An optional bf16
-// copy of p (round to nearest even) is the operand the layer reads.
+// copy of p (round to nearest even) is the operand the layer reads.  An optional factor
+// (the clipping of the gradients' global norm, formed on the device) multiplies g first.
 //
 // The step is a stream over 28 bytes per parameter (30 with the bf16 copy): bound by HBM.
 #include "launch.h"
@@ -26,6 +27,7 @@ struct AdamwArgs {
     float* m;
     float* v;
     uint16_t* pbf;        // bf16 copy of p, or null
+    const float* factor;  // of g, or null
     int64_t n;
     AdamwScalars k;
 };
@@ -43,6 +45,7 @@ __device__ __forceinline__ void adamw_one(const AdamwScalars& k, float& p, float
 __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
     const int64_t n4 = a.n >> 2;
     const int64_t stride = (int64_t)gridDim.x * 256;
+    const float f = a.factor ? *a.factor : 1.0f;          // (a product with one changes no bit)
     int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     for (; i + stride < n4; i += 2 * stride) {
         const int64_t j = i + stride;
@@ -50,14 +53,14 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
         const float4 g0 = reinterpret_cast<const float4*>(a.g)[i], g1 = reinterpret_cast<const float4*>(a.g)[j];
         float4 m0 = reinterpret_cast<const float4*>(a.m)[i], m1 = reinterpret_cast<const float4*>(a.m)[j];
         float4 v0 = reinterpret_cast<const float4*>(a.v)[i], v1 = reinterpret_cast<const float4*>(a.v)[j];
-        adamw_one(a.k, p0.x, g0.x, m0.x, v0.x);
-        adamw_one(a.k, p0.y, g0.y, m0.y, v0.y);
-        adamw_one(a.k, p0.z, g0.z, m0.z, v0.z);
-        adamw_one(a.k, p0.w, g0.w, m0.w, v0.w);
-        adamw_one(a.k, p1.x, g1.x, m1.x, v1.x);
-        adamw_one(a.k, p1.y, g1.y, m1.y, v1.y);
-        adamw_one(a.k, p1.z, g1.z, m1.z, v1.z);
-        adamw_one(a.k, p1.w, g1.w, m1.w, v1.w);
+        adamw_one(a.k, p0.x, g0.x * f, m0.x, v0.x);
+        adamw_one(a.k, p0.y, g0.y * f, m0.y, v0.y);
+        adamw_one(a.k, p0.z, g0.z * f, m0.z, v0.z);
+        adamw_one(a.k, p0.w, g0.w * f, m0.w, v0.w);
+        adamw_one(a.k, p1.x, g1.x * f, m1.x, v1.x);
+        adamw_one(a.k, p1.y, g1.y * f, m1.y, v1.y);
+        adamw_one(a.k, p1.z, g1.z * f, m1.z, v1.z);
+        adamw_one(a.k, p1.w, g1.w * f, m1.w, v1.w);
         reinterpret_cast<float4*>(a.p)[i] = p0;
         reinterpret_cast<float4*>(a.p)[j] = p1;
         reinterpret_cast<float4*>(a.m)[i] = m0;
@@ -74,10 +77,10 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
         const float4 g0 = reinterpret_cast<const float4*>(a.g)[i];
         float4 m0 = reinterpret_cast<const float4*>(a.m)[i];
         float4 v0 = reinterpret_cast<const float4*>(a.v)[i];
-        adamw_one(a.k, p0.x, g0.x, m0.x, v0.x);
-        adamw_one(a.k, p0.y, g0.y, m0.y, v0.y);
-        adamw_one(a.k, p0.z, g0.z, m0.z, v0.z);
-        adamw_one(a.k, p0.w, g0.w, m0.w, v0.w);
+        adamw_one(a.k, p0.x, g0.x * f, m0.x, v0.x);
+        adamw_one(a.k, p0.y, g0.y * f, m0.y, v0.y);
+        adamw_one(a.k, p0.z, g0.z * f, m0.z, v0.z);
+        adamw_one(a.k, p0.w, g0.w * f, m0.w, v0.w);
         reinterpret_cast<float4*>(a.p)[i] = p0;
         reinterpret_cast<float4*>(a.m)[i] = m0;
         reinterpret_cast<float4*>(a.v)[i] = v0;
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         for (int64_t e = n4 << 2; e < a.n; ++e) {
             float p = a.p[e], m = a.m[e], v = a.v[e];
-            adamw_one(a.k, p, a.g[e], m, v);
+            adamw_one(a.k, p, a.g[e] * f, m, v);
             a.p[e] = p;
             a.m[e] = m;
             a.v[e] = v;
@@ -97,14 +100,14 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a) {
 }
 
 hipError_t launch_adamw(float* p, const float* g, float* m, float* v, uint16_t* pbf, int64_t n,
-                        const AdamwScalars& k, hipStream_t s) {
+                        const AdamwScalars& k, const float* factor, hipStream_t s) {
     if (n == 0) return hipSuccess;
     // up to 16 workgroups per CU, each lane with at least two iterations where n allows
     const int64_t n4 = n >> 2;
     int64_t grid = (n4 + 511) / 512;
     if (grid > 4096) grid = 4096;
     if (grid < 1) grid = 1;
-    AdamwArgs a{p, g, m, v, pbf, n, k};
+    AdamwArgs a{p, g, m, v, pbf, factor, n, k};
     hipLaunchKernelGGL(k_adamw, dim3((unsigned)grid), dim3(256), 0, s, a);
     return hipGetLastError();
 }

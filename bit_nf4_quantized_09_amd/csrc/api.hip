@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/qlora_nf4.h"
+#include "../../include/qlora_step.h"
 #include "launch.h"
 #include "status.h"
 
@@ -688,11 +689,11 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-nf4_status nf4_adamw_step(float* p, const float* g, float* m, float* v, uint16_t* p_bf16, int64_t n,
-                          float lr, float beta1, float beta2, float eps, float weight_decay,
-                          int64_t step, void* stream) {
+nf4_status adamw_step(float* p, const float* g, float* m, float* v, uint16_t* p_bf16, int64_t n,
+                      float lr, float beta1, float beta2, float eps, float weight_decay,
+                      int64_t step, const float* factor, void* stream, const char* name) {
     nf4::AdamwScalars k;
     nf4_status st = adamw_scalars(lr, beta1, beta2, eps, weight_decay, step, k);
     if (st != NF4_OK) return st;
@@ -709,13 +710,13 @@ nf4_status nf4_adamw_step(float* p, const float* g, float* m, float* v, uint16_t
             if (overlaps(bufs[i], b4, bufs[j], b4)) return fail(NF4_ERR_ARG, "p, g, m and v must not overlap");
         if (overlaps(bufs[i], b4, p_bf16, b2)) return fail(NF4_ERR_ARG, "p_bf16 overlaps the state");
     }
-    return hip_status(nf4::launch_adamw(p, g, m, v, p_bf16, n, k, (hipStream_t)stream), "nf4_adamw_step");
+    return hip_status(nf4::launch_adamw(p, g, m, v, p_bf16, n, k, factor, (hipStream_t)stream), name);
 }
 
-nf4_status nf4_adamw_step_paged(float* p_host, const float* g, float* m_host, float* v_host,
-                                uint16_t* p_bf16, int64_t n, float lr, float beta1, float beta2,
-                                float eps, float weight_decay, int64_t step, void* stage,
-                                size_t stage_bytes, void* stream) {
+nf4_status adamw_step_paged(float* p_host, const float* g, float* m_host, float* v_host,
+                            uint16_t* p_bf16, int64_t n, float lr, float beta1, float beta2,
+                            float eps, float weight_decay, int64_t step, const float* factor, void* stage,
+                            size_t stage_bytes, void* stream, const char* name) {
     nf4::AdamwScalars k;
     nf4_status st = adamw_scalars(lr, beta1, beta2, eps, weight_decay, step, k);
     if (st != NF4_OK) return st;
@@ -752,7 +753,7 @@ nf4_status nf4_adamw_step_paged(float* p_host, const float* g, float* m_host, fl
         if (e == hipSuccess) e = hipMemcpyAsync(sp, p_host + c0, nb, hipMemcpyHostToDevice, hs);
         if (e == hipSuccess) e = hipMemcpyAsync(sm, m_host + c0, nb, hipMemcpyHostToDevice, hs);
         if (e == hipSuccess) e = hipMemcpyAsync(sv, v_host + c0, nb, hipMemcpyHostToDevice, hs);
-        if (e == hipSuccess) e = nf4::launch_adamw(sp, g + c0, sm, sv, p_bf16 ? p_bf16 + c0 : nullptr, cn, k, hs);
+        if (e == hipSuccess) e = nf4::launch_adamw(sp, g + c0, sm, sv, p_bf16 ? p_bf16 + c0 : nullptr, cn, k, factor, hs);
         if (e == hipSuccess) e = hipEventRecord(ready[b], hs);
         if (e == hipSuccess) e = hipStreamWaitEvent(out_stream, ready[b], 0);
         if (e == hipSuccess) e = hipMemcpyAsync(p_host + c0, sp, nb, hipMemcpyDeviceToHost, out_stream);
@@ -762,7 +763,45 @@ nf4_status nf4_adamw_step_paged(float* p_host, const float* g, float* m_host, fl
     }
     // the caller's stream completes after every copy-out
     for (int b = 0; b < 2 && b < nchunks && e == hipSuccess; ++b) e = hipStreamWaitEvent(hs, done[b], 0);
-    return hip_status(e, "nf4_adamw_step_paged");
+    return hip_status(e, name);
+}
+
+nf4_status check_factor(const float* factor) {
+    return factor && aligned(factor, 4) ? NF4_OK : fail(NF4_ERR_ARG, "factor is NULL or misaligned");
+}
+
+}  // namespace
+
+extern "C" {
+
+nf4_status nf4_adamw_step(float* p, const float* g, float* m, float* v, uint16_t* p_bf16, int64_t n,
+                          float lr, float beta1, float beta2, float eps, float weight_decay,
+                          int64_t step, void* stream) {
+    return adamw_step(p, g, m, v, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, nullptr, stream, "nf4_adamw_step");
+}
+
+nf4_status nf4_adamw_step_paged(float* p_host, const float* g, float* m_host, float* v_host,
+                                uint16_t* p_bf16, int64_t n, float lr, float beta1, float beta2,
+                                float eps, float weight_decay, int64_t step, void* stage,
+                                size_t stage_bytes, void* stream) {
+    return adamw_step_paged(p_host, g, m_host, v_host, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, nullptr, stage,
+                            stage_bytes, stream, "nf4_adamw_step_paged");
+}
+
+nf4_status qlora_adamw_step_scaled(float* p, const float* g, float* m, float* v, uint16_t* p_bf16, int64_t n,
+                                   float lr, float beta1, float beta2, float eps, float weight_decay,
+                                   int64_t step, const float* factor, void* stream) {
+    if (nf4_status st = check_factor(factor)) return st;
+    return adamw_step(p, g, m, v, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, factor, stream, "qlora_adamw_step_scaled");
+}
+
+nf4_status qlora_adamw_step_paged_scaled(float* p_host, const float* g, float* m_host, float* v_host,
+                                         uint16_t* p_bf16, int64_t n, float lr, float beta1, float beta2,
+                                         float eps, float weight_decay, int64_t step, const float* factor, void* stage,
+                                         size_t stage_bytes, void* stream) {
+    if (nf4_status st = check_factor(factor)) return st;
+    return adamw_step_paged(p_host, g, m_host, v_host, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, factor, stage,
+                            stage_bytes, stream, "qlora_adamw_step_paged_scaled");
 }
 
 }  // extern "C"

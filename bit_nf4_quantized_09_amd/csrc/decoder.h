@@ -34,9 +34,15 @@ constexpr int KV_EXP_MIN = -50, KV_EXP_MAX = 50;   // exponents of a page's scal
 hipError_t launch_kv_append(const CacheView& c, const BatchView& b, const HeadsView& k, const HeadsView& v,
                             const RopeView& rope, const HeadsView* q_in, const HeadsView* q_out, hipStream_t s);
 
-size_t kv_attention_ws_bytes(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length);
+// The keys that a token sees: the last `window` up to its own, and the first `sinks` (window of 0: all up to its own).
+struct AttendWindow {
+    int64_t window, sinks;
+    bool on() const { return window > 0; }
+};
+size_t kv_attention_ws_bytes(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length,
+                             const AttendWindow& w);
 hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const HeadsView& q, const HeadsView& out,
-                               float scale, int64_t max_new, int64_t max_length, void* ws, hipStream_t s);
+                               float scale, int64_t max_new, int64_t max_length, const AttendWindow& w, void* ws, hipStream_t s);
 
 // ---- the vocabulary head's loss --------------------------------------------
 size_t head_loss_ws_bytes(int64_t M, int64_t K, int64_t V, bool dx, bool dw);

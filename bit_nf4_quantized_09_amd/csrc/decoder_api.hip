@@ -1,10 +1,12 @@
-// decoder_api.hip -- the extern "C" entry points declared in include/qlora_decoder.h.
+// decoder_api.hip -- the extern "C" entry points declared in include/qlora_decoder.h, and the attention of
+// include/qlora_step.h.
 //
 // Host side only: arguments are checked before any HIP call, then the kernels of rope.hip,
 // kv_append.hip, kv_attention.hip and head_loss.hip are launched.
 #include <math.h>
 
 #include "../../include/qlora_decoder.h"
+#include "../../include/qlora_step.h"
 #include "decoder.h"
 #include "attend_plan.h"
 #include "status.h"
@@ -175,22 +177,22 @@ static nf4_status check_attention(const qlora_kv_cache* cache, const qlora_kv_ba
     return NF4_OK;
 }
 
-size_t qlora_kv_attention_workspace_bytes(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int32_t heads,
-                                          int64_t max_new, int64_t max_length) {
+static size_t attention_bytes(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int32_t heads, int64_t max_new,
+                              int64_t max_length, const nf4::AttendWindow& w) {
     size_t bytes = 0;
     guarded([&]() -> nf4_status {
         CacheView c;
         BatchView b;
         if (nf4_status st = check_attention(cache, batch, heads, max_new, max_length, c, b)) return st;
-        bytes = b.tokens > 0 ? nf4::kv_attention_ws_bytes(c, b, heads, max_new, max_length) : 0;
+        bytes = b.tokens > 0 ? nf4::kv_attention_ws_bytes(c, b, heads, max_new, max_length, w) : 0;
         return NF4_OK;
     });
     return bytes;
 }
 
-nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch* batch, const qlora_heads* q,
-                              const qlora_heads* out, float scale, int64_t max_new, int64_t max_length,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+static nf4_status attention(const qlora_kv_cache* cache, const qlora_kv_batch* batch, const qlora_heads* q,
+                            const qlora_heads* out, float scale, int64_t max_new, int64_t max_length,
+                            const nf4::AttendWindow& w, void* workspace, size_t workspace_bytes, void* stream, const char* name) {
     return guarded([&]() -> nf4_status {
         CacheView c;
         BatchView b;
@@ -204,12 +206,43 @@ nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch*
         if (nf4_status st = check_written(out, "out", c.dim, b.tokens)) return st;
         if (qv.heads != ov.heads) return fail(NF4_ERR_ARG, "q and out have different heads");
         if ((int64_t)b.tokens * qv.heads >= ((int64_t)1 << 26)) return fail(NF4_ERR_UNSUPPORTED, "tokens times heads must be below 2^26");
-        const size_t need = nf4::kv_attention_ws_bytes(c, b, qv.heads, max_new, max_length);
+        const size_t need = nf4::kv_attention_ws_bytes(c, b, qv.heads, max_new, max_length, w);
         if (need > 0 && (!workspace || workspace_bytes < need)) return fail(NF4_ERR_WORKSPACE, "workspace missing or too small");
         if (need > 0 && !aligned(workspace, 256)) return fail(NF4_ERR_ARG, "workspace must be 256-byte aligned");
-        return hip_status(nf4::launch_kv_attention(c, b, qv, ov, scale, max_new, max_length, workspace, (hipStream_t)stream),
-                          "qlora_kv_attention");
+        return hip_status(nf4::launch_kv_attention(c, b, qv, ov, scale, max_new, max_length, w, workspace, (hipStream_t)stream), name);
     });
+}
+
+static nf4_status check_window(int64_t window, int64_t sinks) {
+    if (window < 1 || window > (int64_t)0x7FFFFFFF) return fail(NF4_ERR_ARG, "window must be 1 .. 2^31 - 1");
+    if (sinks < 0 || sinks > ((int64_t)1 << 30)) return fail(NF4_ERR_ARG, "sinks must be 0 .. 2^30");
+    return NF4_OK;
+}
+
+size_t qlora_kv_attention_workspace_bytes(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int32_t heads,
+                                          int64_t max_new, int64_t max_length) {
+    return attention_bytes(cache, batch, heads, max_new, max_length, nf4::AttendWindow{0, 0});
+}
+
+nf4_status qlora_kv_attention(const qlora_kv_cache* cache, const qlora_kv_batch* batch, const qlora_heads* q,
+                              const qlora_heads* out, float scale, int64_t max_new, int64_t max_length,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    return attention(cache, batch, q, out, scale, max_new, max_length, nf4::AttendWindow{0, 0}, workspace, workspace_bytes, stream,
+                     "qlora_kv_attention");
+}
+
+size_t qlora_kv_attention_window_workspace_bytes(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int32_t heads,
+                                                 int64_t max_new, int64_t max_length, int64_t window, int64_t sinks) {
+    if (guarded([&] { return check_window(window, sinks); }) != NF4_OK) return 0;
+    return attention_bytes(cache, batch, heads, max_new, max_length, nf4::AttendWindow{window, sinks});
+}
+
+nf4_status qlora_kv_attention_window(const qlora_kv_cache* cache, const qlora_kv_batch* batch, const qlora_heads* q,
+                                     const qlora_heads* out, float scale, int64_t max_new, int64_t max_length, int64_t window,
+                                     int64_t sinks, void* workspace, size_t workspace_bytes, void* stream) {
+    if (nf4_status st = guarded([&] { return check_window(window, sinks); })) return st;
+    return attention(cache, batch, q, out, scale, max_new, max_length, nf4::AttendWindow{window, sinks}, workspace, workspace_bytes,
+                     stream, "qlora_kv_attention_window");
 }
 
 static nf4_status check_head(int64_t M, int64_t K, int64_t V) {

@@ -1,5 +1,5 @@
 // decoder_binding.cpp -- the Python calls of the operators around the linears, over the C ABI of
-// include/qlora_decoder.h.
+// include/qlora_decoder.h and include/qlora_step.h.
 //
 // A CPython extension of its own, because a call that serves single tokens lasts as long as its host
 // side: a call that turns q and k of a few tokens took 13.8 us through ctypes and takes 5.5 us here (4.3 us
@@ -18,8 +18,9 @@
 
 #include <cmath>
 #include <string>
+#include <vector>
 
-#include "../../include/qlora_decoder.h"
+#include "../../include/qlora_step.h"
 
 namespace {
 
@@ -268,9 +269,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// codes, scales, q, starts, lengths, table, scale or None, max_new or None, max_length or None
+// codes, scales, q, starts, lengths, table, scale or None, max_new or None, max_length or None, window or None, sinks
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 9, [&]() -> PyObject* {
+    return guarded(n, 11, [&]() -> PyObject* {
         const at::Tensor& q = tensor(a[2], "q");
         want_gpu(q, "q");
         const c10::DeviceGuard on(q.device());
@@ -284,9 +285,16 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t max_length = a[8] == Py_None ? (reach > 1 ? reach : 1) : whole(a[8]);
         qlora_heads oh;
         at::Tensor out = fresh_like(q, oh), keep;
-        const size_t bytes = qlora_kv_attention_workspace_bytes(&c, &b, qh.heads, max_new, max_length);
+        if (a[9] == Py_None) {
+            const size_t bytes = qlora_kv_attention_workspace_bytes(&c, &b, qh.heads, max_new, max_length);
+            void* ws = workspace(bytes, q, keep);
+            check(qlora_kv_attention(&c, &b, &qh, &oh, (float)scale, max_new, max_length, ws, bytes, stream_of(q)));
+            return wrap(out);
+        }
+        const int64_t window = whole(a[9]), sinks = whole(a[10]);
+        const size_t bytes = qlora_kv_attention_window_workspace_bytes(&c, &b, qh.heads, max_new, max_length, window, sinks);
         void* ws = workspace(bytes, q, keep);
-        check(qlora_kv_attention(&c, &b, &qh, &oh, (float)scale, max_new, max_length, ws, bytes, stream_of(q)));
+        check(qlora_kv_attention_window(&c, &b, &qh, &oh, (float)scale, max_new, max_length, window, sinks, ws, bytes, stream_of(q)));
         return wrap(out);
     });
 }
@@ -328,6 +336,300 @@ PyObject* head_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---- the operators of include/qlora_step.h ----
+
+nf4_dtype dtype_of(const at::Tensor& t, const char* name) {
+    const at::ScalarType s = t.scalar_type();
+    if (s != at::kFloat && s != at::kBFloat16) bad(std::string(name) + " must be Float or BFloat16, got " + type_name(s));
+    return s == at::kBFloat16 ? NF4_BF16 : NF4_F32;
+}
+// A tensor that the call writes in place: autograd would not see it.
+void want_unrecorded(const at::Tensor& t, const char* name) {
+    if (c10::GradMode::is_enabled() && t.requires_grad())
+        bad(std::string(name) + " requires grad: it is not written in place while gradients are recorded");
+}
+// A [M, K] tensor of any row stride, on the device of `of`.
+qlora_rows rows_of(const at::Tensor& t, const char* name, at::ScalarType type, int64_t M, int64_t K, const at::Tensor& of) {
+    want_type(t, name, type);
+    want_device(t, name, of);
+    if (t.dim() != 2 || t.size(0) != M || t.size(1) != K)
+        bad(std::string(name) + " must be [" + std::to_string(M) + ", " + std::to_string(K) + "], got " + shape_of(t));
+    if (M > 0 && K > 1 && t.stride(1) != 1) bad(std::string(name) + " must be dense along its last dimension");
+    return qlora_rows{t.data_ptr(), M > 1 ? t.stride(0) : K};
+}
+qlora_rows fresh_rows(const at::Tensor& t) { return qlora_rows{t.data_ptr(), t.size(1)}; }
+
+// pre and post (a weight [K], True: a norm without a weight, None or False: no norm), gate or None, scale, eps
+struct Norm {
+    qlora_block_norm c{};
+    at::ScalarType type = at::kFloat;
+    bool typed = false;
+    void weight(PyObject* o, const char* name, int64_t K, const at::Tensor& of, int32_t& norm, const void*& p) {
+        norm = 0;
+        if (o == Py_None || o == Py_False) return;
+        norm = 1;
+        if (o == Py_True) return;
+        const at::Tensor& t = tensor(o, name);
+        take(t, name);
+        want_dense(t, name, type, of);
+        if (t.dim() != 1 || t.size(0) != K) bad(std::string(name) + " must be [" + std::to_string(K) + "], got " + shape_of(t));
+        p = t.data_ptr();
+    }
+    void take(const at::Tensor& t, const char* name) {
+        c.dtype = dtype_of(t, name);
+        if (typed && t.scalar_type() != type) bad("pre, post and gate must be of one type");
+        type = t.scalar_type();
+        typed = true;
+    }
+    Norm(PyObject* const* a, int64_t M, int64_t K, const at::Tensor& of) {
+        c.dtype = NF4_F32;
+        weight(a[0], "pre", K, of, c.norm_pre, c.pre);
+        weight(a[1], "post", K, of, c.norm_post, c.post);
+        if (a[2] != Py_None) {
+            const at::Tensor& g = tensor(a[2], "gate");
+            take(g, "gate");
+            want_dense(g, "gate", type, of);
+            const bool one = g.dim() == 1;
+            if (g.dim() < 1 || g.dim() > 2 || g.size(g.dim() - 1) != K) bad("gate must be [" + std::to_string(K) + "] or [rows, " + std::to_string(K) + "], got " + shape_of(g));
+            c.gate = g.data_ptr();
+            c.gate_rows = one ? 1 : g.size(0);
+            if (c.gate_rows < 1 || M % c.gate_rows) bad("gate's rows must divide the tokens (" + std::to_string(M) + "), got " + shape_of(g));
+        }
+        c.scale = (float)number(a[3]);
+        c.eps = (float)number(a[4]);
+    }
+};
+const at::Tensor& stream_tensor(PyObject* o, int64_t& M, int64_t& K) {
+    const at::Tensor& h = tensor(o, "h");
+    want_gpu(h, "h");
+    dtype_of(h, "h");
+    if (h.dim() != 2) bad("h must be [tokens, width], got " + shape_of(h));
+    M = h.size(0);
+    K = h.size(1);
+    return h;
+}
+PyObject* tuple_of(std::initializer_list<PyObject*> items) {
+    bool all = true;
+    for (PyObject* o : items) all = all && o;
+    PyObject* t = all ? PyTuple_New((Py_ssize_t)items.size()) : nullptr;
+    Py_ssize_t i = 0;
+    for (PyObject* o : items) {
+        if (t) PyTuple_SET_ITEM(t, i++, o);
+        else Py_XDECREF(o);
+    }
+    if (!t) throw PythonError{};
+    return t;
+}
+
+// h, x or None, pre, post, gate or None, scale, eps, inplace
+PyObject* block_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject* {
+        int64_t M, K;
+        const at::Tensor& h = stream_tensor(a[0], M, K);
+        const c10::DeviceGuard on(h.device());
+        const bool block = a[1] != Py_None, inplace = truth(a[7]);
+        const Norm norm(a + 2, M, K, h);
+        const qlora_rows hv = rows_of(h, "h", h.scalar_type(), M, K, h);
+        qlora_rows xv{}, ov{}, yv{};
+        at::Tensor out, y;
+        if (block) {
+            xv = rows_of(tensor(a[1], "x"), "x", at::kBFloat16, M, K, h);
+            if (inplace) {
+                want_unrecorded(h, "h");
+                out = h;
+                ov = hv;
+            } else {
+                out = at::empty({M, K}, h.options());
+                ov = fresh_rows(out);
+            }
+        }
+        if (norm.c.norm_pre) {
+            y = at::empty({M, K}, h.options().dtype(at::kBFloat16));
+            yv = fresh_rows(y);
+        }
+        check(qlora_block_norm_fwd(&norm.c, M, K, dtype_of(h, "h"), &hv, block ? &xv : nullptr, block ? &ov : nullptr,
+                                   norm.c.norm_pre ? &yv : nullptr, stream_of(h)));
+        if (block && inplace) written(h);
+        if (!block) Py_INCREF(a[0]);
+        return tuple_of({block ? wrap(out) : a[0], wrap(y)});
+    });
+}
+
+// h, dy or None, dh or None, x or None, need_weights, pre, post, gate or None, scale, eps
+PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject* {
+        int64_t M, K;
+        const at::Tensor& h = stream_tensor(a[0], M, K);
+        const c10::DeviceGuard on(h.device());
+        const bool later = a[2] != Py_None, block = a[3] != Py_None, learn = truth(a[4]);
+        const Norm norm(a + 5, M, K, h);
+        if (norm.c.norm_pre != (a[1] != Py_None)) bad(norm.c.norm_pre ? "dy is missing" : "dy is given without a norm (pre)");
+        const qlora_rows hv = rows_of(h, "h", h.scalar_type(), M, K, h);
+        qlora_rows xv{}, yv{}, dv{}, dxv{};
+        if (norm.c.norm_pre) yv = rows_of(tensor(a[1], "dy"), "dy", at::kBFloat16, M, K, h);
+        if (later) dv = rows_of(tensor(a[2], "dh"), "dh", h.scalar_type(), M, K, h);
+        if (block) xv = rows_of(tensor(a[3], "x"), "x", at::kBFloat16, M, K, h);
+        at::Tensor dh = at::empty({M, K}, h.options()), dx, dpre, dpost, dgate, keep;
+        const qlora_rows ov = fresh_rows(dh);
+        const at::TensorOptions f32 = h.options().dtype(at::kFloat);
+        if (block) {
+            dx = at::empty({M, K}, h.options().dtype(at::kBFloat16));
+            dxv = fresh_rows(dx);
+        }
+        if (learn && norm.c.pre) dpre = at::empty({K}, f32);
+        if (learn && norm.c.post) dpost = at::empty({K}, f32);
+        if (learn && norm.c.gate) dgate = at::empty(tensor(a[7], "gate").sizes(), f32);
+        const size_t bytes = qlora_block_norm_bwd_workspace_bytes(M, K, norm.c.gate ? norm.c.gate_rows : 1, dpre.defined(), dpost.defined(), dgate.defined());
+        void* ws = workspace(bytes, h, keep);
+        auto at_or_null = [](const at::Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; };
+        check(qlora_block_norm_bwd(&norm.c, M, K, dtype_of(h, "h"), norm.c.norm_pre ? &hv : nullptr, block ? &xv : nullptr, norm.c.norm_pre ? &yv : nullptr,
+                                   later ? &dv : nullptr, &ov, block ? &dxv : nullptr, at_or_null(dpre), at_or_null(dpost), at_or_null(dgate), ws, bytes,
+                                   stream_of(h)));
+        return tuple_of({wrap(dh), wrap(dx), wrap(dpre), wrap(dpost), wrap(dgate)});
+    });
+}
+
+// Tensors of a list (or another sequence): dense, of one GPU.  Every one is kept by the sequence, which `keep` holds.
+struct Tensors {
+    PyObject* keep;
+    std::vector<qlora_tensor> v;
+    const at::Tensor* first = nullptr;
+    Tensors(PyObject* o, const char* name, const at::Tensor* of) {
+        keep = PySequence_Fast(o, (std::string(name) + " must be a list of tensors").c_str());
+        if (!keep) throw PythonError{};
+        try {
+            const Py_ssize_t n = PySequence_Fast_GET_SIZE(keep);
+            if (n == 0) bad(std::string(name) + " holds no tensor");
+            v.reserve((size_t)n);
+            for (Py_ssize_t i = 0; i < n; ++i) {
+                const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(keep, i), name);
+                if (!first) {
+                    want_gpu(t, name);
+                    first = of ? of : &t;
+                }
+                want_device(t, name, *first);
+                if (!t.is_contiguous()) bad(std::string(name) + " must be contiguous");
+                v.push_back(qlora_tensor{t.data_ptr(), t.numel(), dtype_of(t, name)});
+            }
+        } catch (...) {
+            Py_DECREF(keep);
+            throw;
+        }
+    }
+    Tensors(const Tensors&) = delete;
+    ~Tensors() { Py_DECREF(keep); }
+    template <typename F>
+    void each(F&& f) const {
+        for (Py_ssize_t i = 0; i < (Py_ssize_t)v.size(); ++i) f(THPVariable_Unpack(PySequence_Fast_GET_ITEM(keep, i)));
+    }
+};
+// norm and factor of the tensors, in one small tensor
+at::Tensor norm_of(const Tensors& g, double max_norm) {
+    at::Tensor out = at::empty({2}, g.first->options().dtype(at::kFloat).requires_grad(false)), keep;
+    const size_t bytes = qlora_grad_norm_workspace_bytes(g.v.data(), (int64_t)g.v.size());
+    void* ws = workspace(bytes, out, keep);
+    check(qlora_grad_norm(g.v.data(), (int64_t)g.v.size(), max_norm, out.data_ptr<float>(), out.data_ptr<float>() + 1, ws, bytes,
+                          stream_of(out)));
+    return out;
+}
+
+// grads, max_norm: (norm, factor)
+PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 2, [&]() -> PyObject* {
+        const Tensors g(a[0], "grads", nullptr);
+        const c10::DeviceGuard on(g.first->device());
+        const at::Tensor out = norm_of(g, number(a[1]));
+        return tuple_of({wrap(out.select(0, 0)), wrap(out.select(0, 1))});
+    });
+}
+
+// grads, max_norm, out or None: norm
+PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const Tensors g(a[0], "grads", nullptr);
+        const c10::DeviceGuard on(g.first->device());
+        const Tensors o(a[2] == Py_None ? a[0] : a[2], a[2] == Py_None ? "grads" : "out", g.first);
+        if (o.v.size() != g.v.size()) bad("out must hold as many tensors as grads");
+        o.each([](const at::Tensor& t) { want_unrecorded(t, "a clipped tensor"); });
+        const at::Tensor out = norm_of(g, number(a[1]));
+        check(qlora_grad_scale(g.v.data(), o.v.data(), (int64_t)g.v.size(), out.data_ptr<float>() + 1, stream_of(out)));
+        o.each([](const at::Tensor& t) { written(t); });
+        return wrap(out.select(0, 0));
+    });
+}
+
+// A [rows, width] int32 or fp32 table (a single row is for all): its stride and width.
+const void* table_of(PyObject* o, const char* name, at::ScalarType type, int64_t rows, const at::Tensor& of, int64_t& stride, int64_t& width) {
+    const at::Tensor& t = tensor(o, name);
+    want_type(t, name, type);
+    want_device(t, name, of);
+    if (t.dim() != 2 || (t.size(0) != rows && t.size(0) != 1)) bad(std::string(name) + " must be [" + std::to_string(rows) + " or 1, width], got " + shape_of(t));
+    width = t.size(1);
+    if (rows > 0 && width > 1 && t.stride(1) != 1) bad(std::string(name) + " must be dense along its rows");
+    stride = t.size(0) == 1 ? 0 : t.stride(0);
+    return t.data_ptr();
+}
+const void* row_numbers(PyObject* o, const char* name, at::ScalarType type, int64_t rows, const at::Tensor& of) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    want_dense(t, name, type, of);
+    if (t.dim() != 1 || t.size(0) != rows) bad(std::string(name) + " must be [" + std::to_string(rows) + "], got " + shape_of(t));
+    return t.data_ptr();
+}
+void penalty(PyObject* o, const char* name, int64_t rows, const at::Tensor& of, float& one, const float*& each) {
+    if (THPVariable_Check(o)) each = (const float*)row_numbers(o, name, at::kFloat, rows, of);
+    else one = (float)number(o);
+}
+
+// logits, history, lengths, prompts (or None each), repetition, presence, frequency (numbers or tensors), bias_ids, bias, allowed
+// (or None each), inplace
+PyObject* shape_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject* {
+        const at::Tensor& z = tensor(a[0], "logits");
+        want_gpu(z, "logits");
+        const c10::DeviceGuard on(z.device());
+        const nf4_dtype type = dtype_of(z, "logits");
+        if (z.dim() != 2) bad("logits must be [rows, vocabulary], got " + shape_of(z));
+        const int64_t R = z.size(0), V = z.size(1);
+        const qlora_rows in = rows_of(z, "logits", z.scalar_type(), R, V, z);
+        qlora_logit_rules r{};
+        if (a[1] != Py_None) r.history = (const int32_t*)table_of(a[1], "history", at::kInt, R, z, r.history_stride, r.history_width);
+        if (a[1] == Py_None && (a[2] != Py_None || a[3] != Py_None)) bad("lengths and prompts need the history");
+        r.lengths = (const int32_t*)row_numbers(a[2], "lengths", at::kInt, R, z);
+        r.prompts = (const int32_t*)row_numbers(a[3], "prompts", at::kInt, R, z);
+        penalty(a[4], "repetition", R, z, r.repetition, r.repetitions);
+        penalty(a[5], "presence", R, z, r.presence, r.presences);
+        penalty(a[6], "frequency", R, z, r.frequency, r.frequencies);
+        if ((a[7] != Py_None) != (a[8] != Py_None)) bad("bias_ids and bias go together");
+        if (a[7] != Py_None) {
+            int64_t width = 0;
+            r.bias_ids = (const int32_t*)table_of(a[7], "bias_ids", at::kInt, R, z, r.bias_ids_stride, r.biases);
+            r.bias = (const float*)table_of(a[8], "bias", at::kFloat, R, z, r.bias_stride, width);
+            if (width != r.biases) bad("bias must have as many entries as bias_ids");
+        }
+        if (a[9] != Py_None) {
+            int64_t words = 0;
+            r.allowed = (const int32_t*)table_of(a[9], "allowed", at::kInt, R, z, r.allowed_stride, words);
+            if (words < (V + 31) / 32) bad("allowed must have a bit for every token: " + std::to_string((V + 31) / 32) + " words, got " + shape_of(tensor(a[9], "allowed")));
+        }
+        // (tables without a value have no address)
+        if (r.history_width == 0) r.history = nullptr, r.lengths = r.prompts = nullptr;
+        if (r.biases == 0) r.bias_ids = nullptr, r.bias = nullptr;
+        const bool inplace = truth(a[10]);
+        at::Tensor out = z;
+        qlora_rows to = in;
+        if (inplace) {
+            want_unrecorded(z, "logits");
+        } else {
+            out = at::empty({R, V}, z.options());
+            to = fresh_rows(out);
+        }
+        check(qlora_logits_shape(&r, R, V, type, &in, &to, stream_of(z)));
+        if (inplace) written(z);
+        return wrap(out);
+    });
+}
+
 // the error class, and the function that gives a device's current stream
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 2, [&]() -> PyObject* {
@@ -342,6 +644,9 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define CALL(f) (PyCFunction)(void*)f, METH_FASTCALL
 PyMethodDef methods[] = {{"rope", CALL(rope), nullptr},           {"append", CALL(append), nullptr},
                          {"attention", CALL(attention), nullptr}, {"head_loss", CALL(head_loss), nullptr},
+                         {"block_norm_fwd", CALL(block_norm_fwd), nullptr}, {"block_norm_bwd", CALL(block_norm_bwd), nullptr},
+                         {"grad_norm", CALL(grad_norm), nullptr}, {"clip_grads", CALL(clip_grads), nullptr},
+                         {"shape_logits", CALL(shape_logits), nullptr},
                          {"setup", CALL(setup), nullptr},         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "qlora_decoder_binding", nullptr, -1, methods};
 

@@ -58,6 +58,8 @@ struct AttendArgs {
     uint32_t flip;            // sign bits of a bf16 pair if scale < 0
     int limit;                // rows of a (sequence, kv head) up to which k_attend_rows takes it (else k_attend_block)
     int few;                  // k_attend_rows: rows of each up to which they have slots for their chunks' parts
+    int window, sinks;        // WINDOW: a token sees the last `window` keys up to its own, and the first `sinks`
+    int sink_span;            // sinks up to a whole step
     float* part;              // [row slot][split][D] sums, and
     float2* sums;             // [row slot][split] reference and denominator (splits > 1)
 };
@@ -243,17 +245,43 @@ __device__ __forceinline__ void write_part(const f32x4* acc, float m, float tota
     if (quarter == 0) *sums = make_float2(m, total);
 }
 
-// Products of keys that a column does not see become -inf (a tile that every column sees passes).
-__device__ __forceinline__ f32x4 hide(f32x4 s, int key, int quarter, int low, int position, int end, bool always) {
-    if (key + 15 > low || key + 16 > end || always) {
+// Products of keys that a column does not see become -inf (a tile that every column sees passes).  low, high: positions of
+// the tile's first and last row.
+template <bool WINDOW>
+__device__ __forceinline__ f32x4 hide(f32x4 s, int key, int quarter, int low, int high, int position, int end, bool always,
+                                      const AttendArgs& a) {
+    bool some = key + 15 > low || key + 16 > end || always;
+    if constexpr (WINDOW) some = some || (high - key >= a.window && key + 15 >= a.sinks);
+    if (some) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int k = key + 4 * quarter + r;
-            s[r] = k <= position && k < end ? s[r] : -INFINITY;
+            bool seen = k <= position && k < end;
+            if constexpr (WINDOW) seen = seen && ((uint32_t)position - (uint32_t)k < (uint32_t)a.window || k < a.sinks);
+            s[r] = seen ? s[r] : -INFINITY;
         }
     }
     return s;
 }
+
+// The keys that rows from position `low` on see, side by side: the first ones up to a whole step, then those from the
+// window of `low` on, from a whole step too.  Key f of this row of keys is key f + gap of the sequence past the first ones.
+template <bool WINDOW>
+struct Sight {
+    int gap, span, sinks, start;
+    __device__ __forceinline__ Sight(const AttendArgs& a, int low) : gap(0), span(0), sinks(0), start(0) {
+        if constexpr (WINDOW) {
+            span = a.sink_span;
+            sinks = a.sinks;
+            start = low >= a.window ? low - a.window + 1 : 0;
+            const int from = start / KV_STEP * KV_STEP;
+            gap = from > span ? from - span : 0;
+        }
+    }
+    __device__ __forceinline__ int past(int f) const { return WINDOW && f >= span ? gap : 0; }
+    // Whether no row sees any of the 16 keys: their page may have been given to others.
+    __device__ __forceinline__ bool none(int key) const { return WINDOW && key >= sinks && key + 15 < start; }
+};
 
 // A query row as operands of the bf16 products: the lane's dimensions of product s, in the order of the key pieces.  A
 // negative scale changes the queries' sign instead.  An infinity makes every score infinite or NaN, and a row
@@ -334,7 +362,7 @@ __device__ __forceinline__ void for_chunks(int keys, int chunk, int split, int s
     }
 }
 
-template <int D, int AUX>
+template <int D, int AUX, bool WINDOW>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 3)))
 void k_attend_rows(AttendArgs a) {
     constexpr int PIECES = D / 64;        // 16-byte pieces of a key per lane; values dwords per token
@@ -367,9 +395,12 @@ void k_attend_rows(AttendArgs a) {
         if (position >= reach) position = -1;                 // left out: attends to nothing
         const int last_row = tile * 16 + 15 < rows ? tile * 16 + 15 : rows - 1;
         const int low = position_at(before, tile * 16 / a.group);         // the first row's position
+        const int high = position_at(before, last_row / a.group);         // and the last one's
         int keys = position_at(before, last_row / a.group + 1);           // keys the tile's last row sees
         const bool past = keys > reach;
         keys = past ? reach : keys;
+        const Sight<WINDOW> sight(a, low);
+        keys -= sight.gap;
         bf16x8 qf[KSTEPS];
         {
             const uint16_t* qp = (const uint16_t*)a.q.data + (int64_t)(begin + token) * a.q.token_stride +
@@ -386,18 +417,22 @@ void k_attend_rows(AttendArgs a) {
             // this wave's steps: keys lo + 32 (wave + 4 i) ..
             const int all = (hi - lo + KV_STEP - 1) / KV_STEP;
             const int steps = (all - wave + KV_WAVES - 1) / KV_WAVES;
-            auto first_key = [&](int i) { return lo + KV_STEP * (wave + KV_WAVES * i); };
+            auto place = [&](int i) { return lo + KV_STEP * (wave + KV_WAVES * i); };
+            auto first_key = [&](int i) { return place(i) + sight.past(place(i)); };
             struct Pages {
                 int p[2];
             };
             auto pages = [&](int i) {
                 Pages g;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
+                for (int t = 0; t < 2; ++t) {
+                    g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
+                    if (sight.none(first_key(i) + 16 * t)) g.p[t] = -1;
+                }
                 return g;
             };
             auto load = [&](StepCodes<D>& x, int i, const Pages& g) {
-                load_keys<D, AUX, false>(x, a.c, head, first_key(i), hi, g.p, koff);
+                load_keys<D, AUX, false>(x, a.c, head, first_key(i), hi + sight.past(place(i)), g.p, koff);
                 load_values<D, AUX, false>(x, voff);
             };
             auto compute = [&](const StepCodes<D>& x, int i) {
@@ -415,7 +450,7 @@ void k_attend_rows(AttendArgs a) {
                     f[t] = score_factor(key_scale(x.scale[t]) * a.scale2);
                     vf[t] = value_exponent(x.scale[t]);
                     ev[t] = __builtin_amdgcn_exp2f(-vf[t]);
-                    sc[t] = hide(s, first_key(i) + 16 * t, quarter, low, position, x.scale[t].end, past);
+                    sc[t] = hide<WINDOW>(s, first_key(i) + 16 * t, quarter, low, high, position, x.scale[t].end, past, a);
                 }
                 const f16x8 w = weights_of<D>(st, sc, f, vf, ev);
 #pragma unroll
@@ -536,7 +571,7 @@ __device__ __forceinline__ int2 block_of_rank(const AttendArgs& a, int here, int
 // by 8-bit products (D >= 128): the codes of the keys are the operand as they lie.  The workgroups of one (sequence, kv
 // head) run on one XCD, whose L2 holds its keys; those that see most keys start first.
 // (Heads of 64: three waves a SIMD, 74 us for 3 prompts of up to 1500 tokens behind up to 1100 cached, 32 heads; two 84.)
-template <int D, int CT, bool WIDE, int W>
+template <int D, int CT, bool WIDE, int W, bool WINDOW>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(D == 64 && W == 1 ? 3 : 2)))
 void k_attend_block(AttendArgs a) {
     constexpr int KSTEPS = D / 32, TILES = D / 16, PIECES = D / 64;
@@ -572,11 +607,13 @@ void k_attend_block(AttendArgs a) {
         int keys = position_at(before, last_row / a.group + 1);
         const bool past = keys > reach;
         keys = past ? reach : keys;
+        const Sight<WINDOW> sight(a, position_at(before, row0 / a.group));
+        keys -= sight.gap;
         bf16x8 qf[F8 ? 1 : CT][KSTEPS];
         i32x8 q1[CT][F8 ? D / 128 : 1], q2[CT][F8 ? D / 128 : 1];
         float qs[CT];
         RowsState<D> st[CT];
-        int position[CT], low[CT];                // of the lane's column; of the tile's first row
+        int position[CT], low[CT], high[CT];      // of the lane's column; of the tile's first and last row
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
             const int row = row0 + 16 * c + col < rows ? row0 + 16 * c + col : rows - 1;
@@ -584,6 +621,7 @@ void k_attend_block(AttendArgs a) {
             position[c] = position_at(before, token);
             position[c] = position[c] < reach ? position[c] : -1;
             low[c] = position_at(before, (row0 + 16 * c) / a.group);
+            high[c] = position_at(before, (row0 + 16 * c + 15 < rows ? row0 + 16 * c + 15 : rows - 1) / a.group);
             const uint16_t* qp = (const uint16_t*)a.q.data + (int64_t)(begin + token) * a.q.token_stride +
                                  (int64_t)qhead * a.q.head_stride;
             if constexpr (!F8) {
@@ -599,18 +637,22 @@ void k_attend_block(AttendArgs a) {
         }
         for_chunks(keys, a.chunk, split, a.splits, [&](int lo, int hi) {
             const int steps = ((hi - lo + KV_STEP - 1) / KV_STEP - wave + W - 1) / W;     // of this wave: every W-th
-            auto first_key = [&](int i) { return lo + KV_STEP * (W * i + wave); };
+            auto place = [&](int i) { return lo + KV_STEP * (W * i + wave); };
+            auto first_key = [&](int i) { return place(i) + sight.past(place(i)); };
             struct Pages {
                 int p[2];
             };
             auto pages = [&](int i) {
                 Pages g;
 #pragma unroll
-                for (int t = 0; t < (WIDE ? 1 : 2); ++t) g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
+                for (int t = 0; t < (WIDE ? 1 : 2); ++t) {
+                    g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
+                    if (!WIDE && sight.none(first_key(i) + 16 * t)) g.p[t] = -1;      // (a wide page's step has a key that is seen)
+                }
                 return g;
             };
             auto load = [&](StepCodes<D>& x, int i, const Pages& g) {
-                load_keys<D, 0, WIDE>(x, a.c, head, first_key(i), hi, g.p, koff);
+                load_keys<D, 0, WIDE>(x, a.c, head, first_key(i), hi + sight.past(place(i)), g.p, koff);
             };
             // (a step's values are started as it begins, its keys a step before: 16 D / 64 registers fewer)
             auto values = [&](StepCodes<D>& x) { load_values<D, 0, WIDE>(x, voff); };
@@ -652,7 +694,7 @@ void k_attend_block(AttendArgs a) {
                 for (int c = 0; c < CT; ++c) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        sc[c][t] = hide(sc[c][t], first + 16 * t, quarter, low[c], position[c], x.scale[t].end, past);
+                        sc[c][t] = hide<WINDOW>(sc[c][t], first + 16 * t, quarter, low[c], high[c], position[c], x.scale[t].end, past, a);
                     const float f[2] = {ks[0] * qs[c], ks[1] * qs[c]};
                     w[c] = weights_of<D>(st[c], sc[c], f, vf, ev);
                 }
@@ -817,18 +859,26 @@ void k_attend_join(AttendArgs a) {
     *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
 
-static AttendPlan plan_of(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length) {
+// A window's keys side by side are the sequence as far as the launch is concerned.
+static int64_t sink_span(const AttendWindow& w) { return (w.sinks + KV_STEP - 1) / KV_STEP * KV_STEP; }
+static AttendPlan plan_of(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length, const AttendWindow& w) {
+    if (w.on()) {
+        // (a block's rows and the window's start up to a whole step reach further)
+        const int64_t most = sink_span(w) + w.window + block_rows(c.dim) + KV_STEP;
+        max_length = max_length < most ? max_length : most;
+    }
     return attend_plan(AttendShape{c.dim, c.heads, b.seqs, b.tokens, heads, max_new, max_length});
 }
 
-size_t kv_attention_ws_bytes(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length) {
-    const AttendPlan p = plan_of(c, b, heads, max_new, max_length);
+size_t kv_attention_ws_bytes(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length,
+                             const AttendWindow& w) {
+    const AttendPlan p = plan_of(c, b, heads, max_new, max_length, w);
     return p.rows.bytes + p.block.bytes;
 }
 
 hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const HeadsView& q, const HeadsView& out,
-                               float scale, int64_t max_new, int64_t max_length, void* ws, hipStream_t s) {
-    const AttendPlan p = plan_of(c, b, q.heads, max_new, max_length);
+                               float scale, int64_t max_new, int64_t max_length, const AttendWindow& w, void* ws, hipStream_t s) {
+    const AttendPlan p = plan_of(c, b, q.heads, max_new, max_length, w);
     AttendArgs a{};
     a.c = c;
     a.b = b;
@@ -838,14 +888,20 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
     a.scale2 = fabsf(scale) * 1.4426950408889634f;
     a.flip = scale < 0.0f ? 0x80008000u : 0u;
     a.limit = !p.block.on ? 0x7FFFFFFF : p.rows.on ? KV_FEW : 0;
+    if (w.on()) {
+        a.window = (int)w.window;
+        a.sinks = (int)w.sinks;
+        a.sink_span = (int)sink_span(w);
+    }
     auto part = [&](const AttendPart& q, void* at) {
         a.chunk = q.chunk;
         a.splits = q.splits;
         a.part = (float*)at;
         a.sums = (float2*)((float*)at + q.slots * q.splits * c.dim);
     };
-    auto with = [&](auto dim) {
+    auto with = [&](auto dim, auto window) {
         constexpr int D = decltype(dim)::value;
+        constexpr bool WINDOW = decltype(window)::value;
         // W: four waves to a row of many chunks, whose loads would take turns otherwise
         if (p.block.on) {
             part(p.block, (uint8_t*)ws + p.rows.bytes);
@@ -859,7 +915,7 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             // tokens, 32 heads of 64: 74 us for 85)
             auto run = [&](auto wide, auto waves) {
                 constexpr int W = decltype(waves)::value;
-                hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), decltype(wide)::value, W>), grid, dim3(64 * W), 0, s, a);
+                hipLaunchKernelGGL((k_attend_block<D, block_tiles(D), decltype(wide)::value, W, WINDOW>), grid, dim3(64 * W), 0, s, a);
             };
             auto with_pages = [&](auto waves) { c.page_log2 >= 5 ? run(std::true_type{}, waves) : run(std::false_type{}, waves); };
             if (p.block.waves == 1) with_pages(std::integral_constant<int, 1>{});
@@ -877,16 +933,17 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             a.few = p.rows.few;
             // codes that one row tile reads are read once: they need not stay in the caches (716 MB: 128 us, 138 with them)
             const dim3 grid((uint32_t)a.splits, (uint32_t)(c.heads * a.row_tiles), (uint32_t)b.seqs);
-            if (a.row_tiles == 1) hipLaunchKernelGGL((k_attend_rows<D, 2>), grid, dim3(256), 0, s, a);
-            else hipLaunchKernelGGL((k_attend_rows<D, 0>), grid, dim3(256), 0, s, a);
+            if (a.row_tiles == 1) hipLaunchKernelGGL((k_attend_rows<D, 2, WINDOW>), grid, dim3(256), 0, s, a);
+            else hipLaunchKernelGGL((k_attend_rows<D, 0, WINDOW>), grid, dim3(256), 0, s, a);
             const int64_t rows = (int64_t)b.seqs * c.heads * a.few;
             if (a.splits > 16) hipLaunchKernelGGL((k_attend_join<D, 4, true>), dim3((uint32_t)rows), dim3(256), 0, s, a);
             else if (a.splits > 1) hipLaunchKernelGGL((k_attend_join<D, 1, true>), dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, a);
         }
     };
-    if (c.dim == 64) with(std::integral_constant<int, 64>{});
-    else if (c.dim == 128) with(std::integral_constant<int, 128>{});
-    else with(std::integral_constant<int, 256>{});
+    auto with_window = [&](auto dim) { w.on() ? with(dim, std::true_type{}) : with(dim, std::false_type{}); };
+    if (c.dim == 64) with_window(std::integral_constant<int, 64>{});
+    else if (c.dim == 128) with_window(std::integral_constant<int, 128>{});
+    else with_window(std::integral_constant<int, 256>{});
     return hipGetLastError();
 }
 

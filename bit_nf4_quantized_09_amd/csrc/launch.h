@@ -161,9 +161,10 @@ hipError_t launch_codebook_stats(const void* w, bool w_bf16, int64_t n, const ui
 struct AdamwScalars {
     float b1, omb1, b2, omb2, step_size, inv_sqrt_bc2, eps, decay;
 };
-// p, g, m, v: n fp32 values (16-byte aligned); pbf: bf16 copy of p or null (8-byte aligned).
+// p, g, m, v: n fp32 values (16-byte aligned); pbf: bf16 copy of p or null (8-byte aligned); factor: of g, on the
+// device, or null.
 hipError_t launch_adamw(float* p, const float* g, float* m, float* v, uint16_t* pbf, int64_t n,
-                        const AdamwScalars& k, hipStream_t s);
+                        const AdamwScalars& k, const float* factor, hipStream_t s);
 
 // ---- rank-r truncated SVD (randomized subspace iteration) and LoftQ initialisation ----
 constexpr int LR_MAX = 96;          // sketch width l at most (l >= r)

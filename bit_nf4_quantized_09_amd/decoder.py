@@ -1,8 +1,9 @@
 """The operators around the QLoRA linears of a decoder: rotary positions, a paged key/value
-cache of 8 bits with its append and its attention, and the vocabulary head's softmax cross
-entropy.  Thin binding over ``include/qlora_decoder.h``; the rules of the package hold (GPU
-tensors, the current stream, no fallback, ``ValueError`` for a bad tensor and ``NF4Error``
-for what the library refuses).
+cache of 8 bits with its append and its attention, the vocabulary head's softmax cross
+entropy, the norms around a block, the gradients' norm and clipping, and the penalties and masks
+of logits.  Thin binding over ``include/qlora_decoder.h`` and ``include/qlora_step.h``; the rules
+of the package hold (GPU tensors, the current stream, no fallback, ``ValueError`` for a bad
+tensor and ``NF4Error`` for what the library refuses).
 
 Rotary positions: Su et al., "RoFormer" (2021); the scalings "ntk" and "parts" for contexts
 longer than a model was trained on follow the base change and the by-parts interpolation of
@@ -19,7 +20,7 @@ import torch
 from . import NF4_ERR_HIP, NF4Error, lib_path, load_library
 
 __all__ = ["RopePlan", "rope_plan", "rope_fwd", "rope_bwd", "KVCache", "kv_cache", "kv_append", "kv_attention",
-           "head_loss"]
+           "head_loss", "block_norm_fwd", "block_norm_bwd", "grad_norm", "clip_grads", "shape_logits"]
 
 _bound = None
 
@@ -156,14 +157,17 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Te
 
 def kv_attention(cache: KVCache, q: torch.Tensor, starts: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
                  scale: Optional[float] = None, max_new: Optional[int] = None,
-                 max_length: Optional[int] = None) -> torch.Tensor:
+                 max_length: Optional[int] = None, window: Optional[int] = None, sinks: int = 0) -> torch.Tensor:
     """Causal attention of new tokens, already appended, over the cache: bf16 [tokens, heads,
     head_dim].  Arguments as for kv_append (the same lengths: tokens before these); head h
     reads kv head h // (heads // kv_heads).  scale: 1/sqrt(head_dim) by default.  max_new (the
     most new tokens of a sequence) and max_length (its most positions, new ones included) size
     the launch: without them it is sized for `tokens` and for the table's width, which costs single
-    tokens up to twice the time (24 sequences of up to 4096 keys, 64 heads on 8: 32 us stated, 57 not)."""
-    return (_bound or _binding()).attention(cache.codes, cache.scales, q, starts, lengths, table, scale, max_new, max_length)
+    tokens up to twice the time (24 sequences of up to 4096 keys, 64 heads on 8: 32 us stated, 57 not).
+    window: a token sees the last `window` keys up to its own, and the first `sinks` of its sequence (None: all up
+    to its own).  Pages that no token of the batch sees are not read: they may be given back, their table entries
+    -1 (lengths and positions go on as if they were there)."""
+    return (_bound or _binding()).attention(cache.codes, cache.scales, q, starts, lengths, table, scale, max_new, max_length, window, sinks)
 
 
 # ---------------------------------------------------------------------------
@@ -182,3 +186,79 @@ def head_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, dloss: Op
                computed in the same call, and dW if need_dw.  A later factor on a row's loss
                multiplies its row of dX."""
     return (_bound or _binding()).head_loss(X, W, targets, dloss, need_dw, ignore_index)
+
+
+# ---------------------------------------------------------------------------
+# The norms around a block
+# ---------------------------------------------------------------------------
+def block_norm_fwd(h: torch.Tensor, x: Optional[torch.Tensor] = None, pre=True, post=None,
+                   gate: Optional[torch.Tensor] = None, scale: float = 1.0, eps: float = 1e-6, inplace: bool = False):
+    """From a block's output to the next block's input, in one pass: (the stream after the block, its norm):
+      h' = h + scale * gate * (n(x) post),   y = n(h') pre,   n(a) = a / sqrt(mean(a^2) + eps)
+      h      the stream [tokens, width], fp32 or bf16, any row stride; width up to 32768
+      x      the block's output, bf16 [tokens, width]; None: no block, h' is h itself
+      pre    the weight [width] of the norm before the next block, True for a norm without one, None for no norm (y is None)
+      post   the same for a norm of the block's output; None: x as it is
+      gate   [width], or [rows, width] where each row belongs to tokens / rows neighbouring tokens (a row for each
+             sequence of a batch of equal lengths, or for each token); None: ones
+    pre, post and gate are fp32 or bf16, all of one type.  h' is of the stream's type (h itself is written if `inplace`;
+    not of tensors that autograd records), and y, bf16, is the norm of h' as it was rounded."""
+    return (_bound or _binding()).block_norm_fwd(h, x, pre, post, gate, scale, eps, inplace)
+
+
+def block_norm_bwd(h: torch.Tensor, dy: Optional[torch.Tensor] = None, dh: Optional[torch.Tensor] = None,
+                   x: Optional[torch.Tensor] = None, pre=True, post=None, gate: Optional[torch.Tensor] = None,
+                   scale: float = 1.0, eps: float = 1e-6, need_weights: bool = True):
+    """The gradients of block_norm_fwd: (dh of the stream before the block, dx bf16, dpre, dpost, dgate); None where there is
+    nothing to have one.
+      h      the stream after the block (what block_norm_fwd returned first)
+      dy     the gradient of y, bf16 (with pre)
+      dh     the gradient of the stream after the block from later blocks, of the stream's type; None: zero
+      x, pre, post, gate, scale, eps   as in the forward call
+    dpre, dpost [width] and dgate (the gate's shape) are fp32 sums over the tokens, in a fixed order; need_weights=False
+    (frozen norms) leaves them out."""
+    return (_bound or _binding()).block_norm_bwd(h, dy, dh, x, need_weights, pre, post, gate, scale, eps)
+
+
+# ---------------------------------------------------------------------------
+# The gradients' global norm
+# ---------------------------------------------------------------------------
+def grad_norm(grads) -> torch.Tensor:
+    """The root of the sum of the squares of all values of a list of tensors (fp32 or bf16, dense, of any sizes, on one
+    GPU): a fp32 number on the GPU.  Squares are added in 64 bits, in a fixed order."""
+    return (_bound or _binding()).grad_norm(grads, math.inf)[0]
+
+
+def norm_and_factor(grads, max_norm: float):
+    """grad_norm, and the factor min(1, max_norm / norm) (both fp32 numbers on the GPU), for the optimizer."""
+    return (_bound or _binding()).grad_norm(grads, max_norm)
+
+
+def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
+    """Gradients times min(1, max_norm / norm), in place, or into the tensors of `out` (of the same sizes and types; none
+    may share memory).  Returns the norm before (a fp32 number on the GPU); nothing waits for it.  A norm of infinity or
+    NaN gives the products that the formula says (zeros and NaN)."""
+    return (_bound or _binding()).clip_grads(grads, max_norm, out)
+
+
+# ---------------------------------------------------------------------------
+# Logits before the choice of a token
+# ---------------------------------------------------------------------------
+def shape_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                 prompts: Optional[torch.Tensor] = None, repetition=1.0, presence=0.0, frequency=0.0,
+                 bias_ids: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                 allowed: Optional[torch.Tensor] = None, inplace: bool = False) -> torch.Tensor:
+    """Logits [rows, vocabulary] (fp32 or bf16, any row stride) with, in this order and rounded once:
+      - those of tokens in the row's history divided by `repetition` where positive, multiplied by it elsewhere,
+      - less frequency * count + presence for tokens that are count > 0 times in the history after the prompt,
+      - plus `bias` at `bias_ids` (of an id that is given twice, the last entry counts),
+      - -inf where the bit v % 32 of word v // 32 of `allowed` is 0.
+      history   int32 [rows, width]: a row's tokens so far are its first lengths[row] (None: all), of which
+                the first prompts[row] are the prompt's (None: none); ids outside the vocabulary are passed over
+      repetition, presence, frequency   numbers, or fp32 [rows]
+      bias_ids, bias   int32 and fp32 [rows, biases]; ids outside the vocabulary are unused
+      allowed   int32 [rows, at least vocabulary / 32, rounded up]
+    history, bias_ids, bias and allowed may have a single row for all.  Returns a new dense tensor, or the same one if
+    `inplace` (not of tensors that autograd records)."""
+    return (_bound or _binding()).shape_logits(logits, history, lengths, prompts, repetition, presence, frequency, bias_ids, bias,
+                                               allowed, inplace)

@@ -2,11 +2,12 @@
 
     python examples/small_decoder.py
 
-Random frozen NF4 weights stand in for a trained model's.  Training runs rope_fwd / rope_bwd around plain
-causal attention, head_loss for the loss with its gradient in one call, and PagedAdamW on the adapters.
-Serving appends ragged prompts and then single tokens with kv_append (which rotates queries and keys on the
-way) and attends with kv_attention.  Both read the same weights and adapters, so the answer's loss can be
-compared between them.
+Random frozen NF4 weights stand in for a trained model's.  Training runs block_norm_fwd / block_norm_bwd between
+the blocks, rope_fwd / rope_bwd around plain causal attention, head_loss for the loss with its gradient in one
+call, and PagedAdamW on the adapters, their gradients clipped to a global norm.  Serving appends ragged prompts
+and then single tokens with kv_append (which rotates queries and keys on the way) and attends with kv_attention,
+over everything or a window, whose old pages it gives back; shape_logits keeps an answer from repeating itself.
+Both read the same weights and adapters, so the answer's loss can be compared between them.
 """
 import math
 import os
@@ -48,6 +49,34 @@ class _Rope(torch.autograd.Function):
         return (*nf4.rope_bwd(ctx.plan, ctx.positions, dq.contiguous(), dk.contiguous()), None, None)
 
 
+class _Norm(torch.autograd.Function):
+    """The norm of the stream h."""
+
+    @staticmethod
+    def forward(ctx, h):
+        ctx.save_for_backward(h)
+        return nf4.block_norm_fwd(h)[1]
+
+    @staticmethod
+    def backward(ctx, dy):
+        return nf4.block_norm_bwd(ctx.saved_tensors[0], dy.contiguous())[0]
+
+
+class _BlockNorm(torch.autograd.Function):
+    """The stream after a block, and its norm."""
+
+    @staticmethod
+    def forward(ctx, h, x):
+        h, y = nf4.block_norm_fwd(h, x)
+        ctx.save_for_backward(h, x)
+        return h, y
+
+    @staticmethod
+    def backward(ctx, dh, dy):
+        h, x = ctx.saved_tensors
+        return nf4.block_norm_bwd(h, dy.contiguous(), dh.contiguous(), x)[:2]
+
+
 class _Loss(torch.autograd.Function):
     """The mean loss over the targets that count; its gradient is made in the same call."""
 
@@ -74,10 +103,6 @@ class Linear:
         return _Linear.apply(x, self, self.A, self.B)
 
 
-def norm(x):
-    return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).bfloat16()
-
-
 class Decoder:
     def __init__(self, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
@@ -92,14 +117,15 @@ class Decoder:
 
     def hidden(self, tokens, attend):
         """Tokens [T] through the layers; attend(i, q, k, v) is layer i's attention, positions included."""
-        x = self.table[tokens]
+        h = self.table[tokens]
+        y = _Norm.apply(h)
         for i, layer in enumerate(self.layers):
-            qkv = layer["qkv"](norm(x)).view(-1, HEADS + 2 * KV_HEADS, DIM)
+            qkv = layer["qkv"](y).view(-1, HEADS + 2 * KV_HEADS, DIM)
             q, k, v = qkv[:, :HEADS], qkv[:, HEADS:HEADS + KV_HEADS], qkv[:, HEADS + KV_HEADS:]
-            x = x + layer["out"](attend(i, q, k, v).reshape(-1, HEADS * DIM).contiguous())
-            gate, up = layer["up"](norm(x)).chunk(2, -1)
-            x = x + layer["down"]((torch.nn.functional.silu(gate.float()) * up.float()).bfloat16())
-        return norm(x)
+            h, y = _BlockNorm.apply(h, layer["out"](attend(i, q, k, v).reshape(-1, HEADS * DIM).contiguous()))
+            gate, up = layer["up"](y).chunk(2, -1)
+            h, y = _BlockNorm.apply(h, layer["down"]((torch.nn.functional.silu(gate.float()) * up.float()).bfloat16()))
+        return y
 
 
 def train_loss(model, tokens, targets):
@@ -118,8 +144,8 @@ def train_loss(model, tokens, targets):
     return _Loss.apply(model.hidden(tokens, attend), model.head, targets)
 
 
-def train(model, tokens, targets, steps=20, lr=3e-3, say=lambda *a: None):
-    """Adapter steps on one sequence; returns the losses."""
+def train(model, tokens, targets, steps=20, lr=3e-3, max_norm=10.0, say=lambda *a: None):
+    """Adapter steps on one sequence, the gradients clipped to a norm of max_norm; returns the losses."""
     linears = model.linears()
     opt = nf4.PagedAdamW([p for m in linears for p in (m.A, m.B)], lr=lr)
     model.table.requires_grad_(True)                # so that the first layer's gradient is asked for, like the others'
@@ -127,19 +153,20 @@ def train(model, tokens, targets, steps=20, lr=3e-3, say=lambda *a: None):
     for i in range(steps):
         loss = train_loss(model, tokens, targets)
         loss.backward()
-        opt.step([d for m in linears for d in m.gradients])
+        size = opt.step([d for m in linears for d in m.gradients], max_norm=max_norm)
         losses.append(float(loss.detach()))
-        say("step %2d  loss %.4f" % (i, losses[-1]))
+        say("step %2d  loss %.4f  gradients %.3f" % (i, losses[-1], float(size)))
     model.table.requires_grad_(False)
     model.table.grad = None
     return losses
 
 
 class Server:
-    """Sequences of one model over one paged cache per layer."""
+    """Sequences of one model over one paged cache per layer.  With a window a token attends to the last `window`
+    keys and the first `sinks`, and pages that no later token sees are given back (table entries of -1)."""
 
-    def __init__(self, model, seqs, longest, page=16):
-        self.model = model
+    def __init__(self, model, seqs, longest, page=16, window=None, sinks=4):
+        self.model, self.page, self.window, self.sinks = model, page, window, sinks
         width = -(-longest // page)
         self.caches = [nf4.kv_cache(seqs * width, KV_HEADS, DIM, page) for _ in range(LAYERS)]
         self.pages = torch.randperm(seqs * width, device="cuda").to(torch.int32).view(seqs, width)
@@ -155,20 +182,35 @@ class Server:
 
         def attend(i, q, k, v):
             q = nf4.kv_append(self.caches[i], k, v, starts, self.lengths, self.pages, rope=self.model.plan, q=q)
-            return nf4.kv_attention(self.caches[i], q, starts, self.lengths, self.pages, max_new=max(map(len, new)))
+            return nf4.kv_attention(self.caches[i], q, starts, self.lengths, self.pages, max_new=max(map(len, new)),
+                                    window=self.window, sinks=self.sinks)
 
         with torch.no_grad():
             x = self.model.hidden(tokens, attend)
         self.lengths += starts[1:] - starts[:-1]
+        if self.window is not None:
+            at = torch.arange(self.pages.shape[1], device="cuda") * self.page
+            unseen = (at + self.page <= (self.lengths - self.window + 1)[:, None]) & (at >= self.sinks)
+            self.pages.masked_fill_(unseen, -1)
         return x, starts
 
-    def answer(self, prompts, count):
-        """The next `count` tokens of each prompt, the likeliest each time."""
+    def answer(self, prompts, count, repetition=1.0, allowed=None):
+        """The next `count` tokens of each prompt, the likeliest each time; tokens that were there before are made
+        less likely by `repetition`, and only those of the mask `allowed` are taken."""
         x, starts = self.step(prompts)
         last = x[starts[1:].long() - 1]
         out = [[] for _ in prompts]
+        longest = max(map(len, prompts)) + count
+        history = torch.zeros((len(prompts), longest), dtype=torch.int32)
+        for row, p in zip(history, prompts):
+            row[:len(p)] = torch.tensor(p)
+        history = history.cuda()
         for i in range(count):
-            best = (last.float() @ self.model.head.float().t()).argmax(-1).tolist()
+            lengths = torch.tensor([len(p) + i for p in prompts], dtype=torch.int32, device="cuda")
+            logits = nf4.shape_logits(last.float() @ self.model.head.float().t(), history, lengths, repetition=repetition, allowed=allowed)
+            choice = logits.argmax(-1)
+            history.scatter_(1, lengths.long()[:, None], choice.to(torch.int32)[:, None])
+            best = choice.tolist()
             for row, t in zip(out, best):
                 row.append(t)
             if i + 1 < count:
@@ -197,6 +239,7 @@ def main():
     prompts = [text[:16], text[:40], text[:23]]
     for p, a in zip(prompts, Server(model, 3, 128).answer(prompts, 8)):
         print("after %2d tokens: %s; the text has %s" % (len(p), a, text[len(p):len(p) + 8]))
+    print("from a window of 24: %s" % Server(model, 1, 128, window=24).answer(prompts[:1], 8, repetition=1.3)[0])
 
 
 if __name__ == "__main__":

@@ -1,0 +1,179 @@
+"""The gradients' global norm and clipping on the GPU against float64.
+
+Bounds.  The norm is a sum in 64 bits (n 2^-53 of it at most) and one rounding to fp32; the factor another, so that a
+clipped value is off by 2^-24 for the factor, 2^-24 for the product and, as bf16, 2^-8."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_09_amd as nf4
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def tensors(sizes, types=(F32,), seed=0, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [(torch.randn(n, generator=g, device="cuda") * scale).to(types[i % len(types)]) for i, n in enumerate(sizes)]
+
+
+def exact_norm(gs):
+    return math.sqrt(sum(float(g.double().square().sum()) for g in gs))
+
+
+def check(gs, max_norm, out=None):
+    keep = [g.clone() for g in gs]
+    norm = exact_norm(gs)
+    got = nf4.grad_norm(gs)
+    assert got.dtype == F32 and got.shape == () and abs(float(got) - norm) <= 2.0 ** -23 * norm
+    clipped = nf4.clip_grads(gs, max_norm, out=out)
+    assert torch.equal(clipped, got)
+    f = min(1.0, max_norm / norm) if norm else 1.0
+    for k, g, o in zip(keep, gs, out or gs):
+        if out is not None:
+            assert torch.equal(g, k)
+        want = k.double() * f
+        step = 2.0 ** -22 + (2.0 ** -8 if o.dtype == BF16 else 0)
+        assert o.dtype == k.dtype and torch.all((o.double() - want).abs() <= step * want.abs() + (1e-44 if o.dtype == F32 else 5e-41))
+    return got
+
+
+@pytest.mark.parametrize("sizes", [[1], [7], [8], [2047, 2049], [0, 5, 0, 3], [1] * 700, [100003], [(1 << 22) + 5, 3, 1 << 20], list(range(1, 400))])
+@pytest.mark.parametrize("types", [(F32,), (BF16,), (F32, BF16, BF16)])
+def test_values(sizes, types):
+    check(tensors(sizes, types), 0.3)
+    check(tensors(sizes, types), 1e9)
+    gs = tensors(sizes, types)
+    check(gs, 0.5, [torch.full_like(g, float("nan")) for g in gs])
+
+
+def test_shapes_and_any_alignment():
+    buf = torch.randn(5000, device="cuda")
+    half = torch.randn(5000, device="cuda").bfloat16()
+    gs = [buf[1:13].view(3, 4), buf[14:1001], buf[1003:1004], half[3:2050], half[2051:2060].view(3, 3), buf[4099:4999].view(30, 30)]
+    keep, kept = buf.clone(), half.clone()
+    check(gs, 0.25)
+    inside, of = torch.zeros(5000, dtype=torch.bool), torch.zeros(5000, dtype=torch.bool)
+    for a, b in ((1, 13), (14, 1001), (1003, 1004), (4099, 4999)):
+        inside[a:b] = True
+    for a, b in ((3, 2050), (2051, 2060)):
+        of[a:b] = True
+    assert torch.equal(buf[~inside], keep[~inside]) and torch.equal(half[~of], kept[~of])      # what lies between is left
+
+
+def test_many_tensors_and_repeats():
+    gs = tensors([1 + 37 * i % 5000 for i in range(1300)], (F32, BF16), seed=3)
+    a = nf4.grad_norm(gs)
+    assert torch.equal(nf4.grad_norm(gs), a) and abs(float(a) - exact_norm(gs)) <= 2.0 ** -23 * float(a)
+    check(gs, 1.0)
+
+
+def test_squares_that_fp32_does_not_hold():
+    gs = [torch.full((3000,), 1e30, device="cuda"), torch.full((10,), 1e-30, device="cuda")]
+    check(gs, 1.0)
+    gs = [torch.full((3000,), 1e-30, device="cuda")]
+    check(gs, 1e-31)
+    gs = [torch.full((10,), 3e38, device="cuda")]                       # its norm is past fp32
+    keep = gs[0].clone()
+    assert math.isinf(float(nf4.clip_grads(gs, 1.0)))
+    assert torch.all((gs[0].double() - keep.double() / (3e38 * math.sqrt(10))).abs() <= 1e-6)
+
+
+def test_non_finite_and_zero():
+    gs = tensors([100, 50])
+    gs[1][7] = float("inf")
+    assert math.isinf(float(nf4.clip_grads(gs, 1.0)))
+    assert not gs[0].any() and torch.isnan(gs[1][7]) and int(torch.isnan(gs[1]).sum()) == 1
+    gs = tensors([100, 50])
+    gs[0][0] = float("nan")
+    assert math.isnan(float(nf4.clip_grads(gs, 1.0))) and torch.isnan(gs[1]).all()
+    gs = [torch.zeros(100, device="cuda")]
+    assert float(nf4.clip_grads(gs, 0.0)) == 0 and not gs[0].any()
+    gs = tensors([100])
+    nf4.clip_grads(gs, 0.0)
+    assert not gs[0].any()
+    gs = tensors([100])
+    keep = gs[0].clone()
+    nf4.clip_grads(gs, math.inf)
+    assert torch.equal(gs[0], keep)
+
+
+def test_a_tensor_twice():
+    g = torch.randn(1000, device="cuda")
+    assert abs(float(nf4.grad_norm([g, g])) - math.sqrt(2) * float(g.double().norm())) <= 2.0 ** -22 * float(g.norm()) * 1.5
+    keep = g.clone()
+    for gs, out in (([g, g], None), ([g[:600], g[500:]], None), ([g[:600], torch.zeros(600, device="cuda")], [torch.zeros(600, device="cuda"), g[:600]]),
+                    ([g[:600]], [g[1:601]])):
+        with pytest.raises(nf4.NF4Error, match="overlap"):
+            nf4.clip_grads(gs, 1e-3, out=out)
+    assert torch.equal(g, keep)
+
+
+def test_versions_and_refusals():
+    g = torch.randn(64, device="cuda")
+    version = g._version
+    nf4.grad_norm([g])
+    assert g._version == version
+    nf4.clip_grads([g], 1.0)
+    assert g._version > version
+    for bad in ([], [g.cpu()], [g.half()], [g.view(8, 8).t()], [g, g.cpu()], [g.long()]):
+        with pytest.raises(ValueError):
+            nf4.grad_norm(bad)
+    for bad in ([None], ["g"], 3, g[0]):
+        with pytest.raises(TypeError):
+            nf4.grad_norm(bad)
+    for out in ([], [g[:5]], [g.bfloat16()], [g, g]):
+        with pytest.raises((ValueError, nf4.NF4Error)):
+            nf4.clip_grads([g], 1.0, out=out)
+    for m in (-1.0, float("nan")):
+        with pytest.raises(nf4.NF4Error):
+            nf4.clip_grads([g], m)
+    leaf = torch.randn(64, device="cuda", requires_grad=True)
+    nf4.grad_norm([leaf])
+    with pytest.raises(ValueError):
+        nf4.clip_grads([leaf], 1.0)
+    with torch.no_grad():
+        nf4.clip_grads([leaf], 1.0)
+
+
+@pytest.mark.parametrize("n", [1, 5, 1000, 65537])
+def test_optimizer_step_with_a_factor(n):
+    rand = lambda s: torch.randn(n, generator=torch.Generator().manual_seed(s))  # noqa: E731
+    def state():
+        return [rand(1).cuda(), rand(2).cuda() * 0.1, rand(3).cuda().square() * 0.01]
+    g = rand(4).cuda()
+    for f in (1.0, 0.37, 0.0):
+        factor = torch.tensor(f, device="cuda")
+        a, b = state(), state()
+        half = [torch.empty(n, dtype=BF16, device="cuda") for _ in range(3)]
+        nf4.adamw_step(a[0], g, a[1], a[2], 1e-2, 3, p_bf16=half[0], factor=factor)
+        nf4.adamw_step(b[0], g * f, b[1], b[2], 1e-2, 3, p_bf16=half[1])
+        assert all(torch.equal(u, v) for u, v in zip(a, b)) and torch.equal(half[0], half[1])
+        c = [t.cpu().pin_memory() for t in state()]
+        nf4.adamw_step_paged(c[0], g, c[1], c[2], 1e-2, 3, p_bf16=half[2], factor=factor)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u.cpu(), v) for u, v in zip(a, c)) and torch.equal(half[0], half[2])
+    for bad in (torch.ones(2, device="cuda"), torch.tensor(1.0), torch.ones((), dtype=torch.float64, device="cuda")):
+        with pytest.raises(ValueError):
+            nf4.adamw_step(*state()[:1], g, *state()[1:], 1e-2, 3, factor=bad)
+
+
+@pytest.mark.parametrize("budget", [None, 0, 12 * 3000])
+def test_clipped_optimizer(budget):
+    # the factor reaches device and paged state, and the gradients stay as they are
+    sizes = [(8, 300), (300, 8), (5, 7)]
+    make = lambda: [torch.randn(s, generator=torch.Generator().manual_seed(i)).to("cuda", BF16) for i, s in enumerate(sizes)]  # noqa: E731
+    a, b = make(), make()
+    one, two = nf4.PagedAdamW(a, lr=1e-2, device_budget_bytes=budget), nf4.PagedAdamW(b, lr=1e-2)
+    for step in range(3):
+        gs = [torch.randn(s, generator=torch.Generator().manual_seed(10 * step + i)).cuda() for i, s in enumerate(sizes)]
+        keep = [g.clone() for g in gs]
+        norm = one.step(gs, max_norm=0.3)
+        assert all(torch.equal(u, v) for u, v in zip(gs, keep)) and abs(float(norm) - exact_norm(gs)) <= 2.0 ** -23 * float(norm)
+        nf4.clip_grads(keep, 0.3)
+        assert two.step(keep) is None
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert np.isfinite(float(norm))
