@@ -14,9 +14,11 @@
 //
 // Shape.  Bound by HBM: each operand is read once and each output written once, so a row stays in the
 // registers of the threads that share it (8 values of 16 bytes a thread and operand), one wave up to a width
-// of 1024, else a workgroup.  Workers (a wave or a workgroup) walk along a stretch of rows: the next row's
-// operands are loaded while one is computed, the weights stay in registers, and the sums over tokens of dpre,
-// dpost and dgate are kept there; the workers' sums are added up in a second launch, in a fixed order.
+// of 512, else a workgroup of as many waves as it takes.  Workers (a wave or a workgroup) walk along a stretch of
+// rows: the next row's operands are loaded while one is computed, the weights stay in registers, and the sums over
+// tokens of dpre, dpost and dgate are kept there; the workers' sums are added up in a second launch, in a fixed
+// order.  4096 tokens of width 8192, all bf16: forward 46 us (268 MB, 5.8 TB/s), backward with all sums 84 us
+// (403 MB, 4.8 TB/s) and 5 for the join; 16 tokens of width 4096 3.5 us.
 #include "rows.h"
 #include "step.h"
 
@@ -27,21 +29,16 @@ struct NormArgs {
     RowsView h_out, y;        // written: the stream (or its gradient) and the norm's output (or the block's gradient)
     const void *pre, *post, *gate;
     float *dpre, *dpost, *dgate;      // out, or
-    float *part_pre, *part_post, *part_gate;      // the workers' sums: [worker][K], of gates [worker][2][K]
-    int64_t M, gate_span;     // tokens; tokens of a gate's row
-    int64_t rows;             // of a worker
-    int K;
+    float *part_pre, *part_post, *part_gate;      // the workgroups' sums: [workgroup][K], of gates [worker][2][K]
+    uint32_t M, gate_span;    // tokens; tokens of a gate's row
+    uint32_t rows;            // of a worker
+    uint32_t K;
     bool norm_pre, norm_post;
     float scale, eps, per;    // per: 1 / K
 };
 
 constexpr float NORM_LARGE = 3e38f;
 constexpr float NORM_SHRINK = 0x1p-80f;
-
-// What turns a row into its norm: value * shrink * factor.
-struct Factor {
-    float shrink, factor;
-};
 
 // One row's operands in a thread.
 template <typename S, typename W, int NC, bool BACK>
@@ -53,61 +50,149 @@ struct RowOperands {
     Eight<W> gate[NC];
 };
 
-template <typename S, typename W, int WAVES, int NC, bool BACK>
+// The rows of a worker, and the thread's columns of them.
+template <typename S, typename W, bool GROUP, int NC, bool BACK>
 struct RowOf {
-    static constexpr int THREADS = 64 * WAVES;
+    typedef RowOperands<S, W, NC, BACK> Operands;
     const NormArgs& a;
-    int t;                    // thread among those of the row
-    __device__ __forceinline__ int column(int i) const { return 8 * (t + i * THREADS); }
-    __device__ __forceinline__ void load(RowOperands<S, W, NC, BACK>& r, int64_t row) const {
+    uint32_t t, threads;                  // thread among those of a row
+    uint32_t worker, first, end;          // rows first .. end - 1
+    bool tail;                            // some of the wave's columns are past the row's end
+    uint32_t gate, gate_left;             // of the row loaded next: its gate, and the gate's tokens from it on
+    __device__ __forceinline__ explicit RowOf(const NormArgs& args) : a(args) {
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        t = GROUP ? threadIdx.x : threadIdx.x & 63;
+        threads = GROUP ? blockDim.x : 64;
+        worker = GROUP ? blockIdx.x : blockIdx.x * 4 + wave;
+        tail = 8 * ((GROUP ? 64 * wave : 0) + (NC - 1) * threads + 64) > a.K;
+        const uint64_t from = (uint64_t)worker * a.rows;
+        first = from < a.M ? (uint32_t)from : a.M;
+        end = a.M - first > a.rows ? first + a.rows : a.M;
+        gate = first / a.gate_span;
+        gate_left = a.gate_span - first % a.gate_span;
+    }
+    __device__ __forceinline__ uint32_t column(int i) const { return 8 * (t + i * threads); }
+    // (a row shared by waves is longer than 512 values, one wave's may be shorter than eight)
+    template <typename T>
+    __device__ __forceinline__ Eight<T> start(const T* p, uint32_t c) const {
+        if (!GROUP && a.K < 8) return load_eight(p, c, a.K);
+        return load_late(p, c, a.K);
+    }
+    template <typename T>
+    __device__ __forceinline__ void finish(Eight<T>& e, uint32_t c) const {
+        if (GROUP || a.K >= 8) settle(e, c, a.K);
+    }
+    __device__ __forceinline__ void load(Operands& r, uint32_t row) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = column(i), left = a.K - c;
-            if (!BACK || a.norm_pre) r.h[i] = load_eight((const S*)a.h.data + row * a.h.stride + c, left);
-            if (a.x.data) r.x[i] = load_eight((const uint16_t*)a.x.data + row * a.x.stride + c, left);
-            if (a.gate) r.gate[i] = load_eight((const W*)a.gate + row / a.gate_span * a.K + c, left);
+            const uint32_t c = column(i);
+            if (!BACK || a.norm_pre) r.h[i] = start((const S*)a.h.data + row * a.h.stride, c);
+            if (a.x.data) r.x[i] = start((const uint16_t*)a.x.data + row * a.x.stride, c);
+            if (a.gate) r.gate[i] = start((const W*)a.gate + (uint64_t)gate * a.K, c);
             if constexpr (BACK) {
-                if (a.norm_pre) r.dy[i] = load_eight((const uint16_t*)a.dy.data + row * a.dy.stride + c, left);
-                if (a.dh.data) r.dh[i] = load_eight((const S*)a.dh.data + row * a.dh.stride + c, left);
+                if (a.norm_pre) r.dy[i] = start((const uint16_t*)a.dy.data + row * a.dy.stride, c);
+                if (a.dh.data) r.dh[i] = start((const S*)a.dh.data + row * a.dh.stride, c);
+            }
+        }
+        if (--gate_left == 0) {
+            ++gate;
+            gate_left = a.gate_span;
+        }
+    }
+    // Operands that are not there: zeros, and gates of one.
+    __device__ __forceinline__ void neutral(Operands& r) const {
+        const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            r.h[i] = {};
+            r.x[i] = {};
+            r.gate[i] = pack_eight<W>(one);
+            if constexpr (BACK) {
+                r.dy[i] = {};
+                r.dh[i] = {};
             }
         }
     }
-    // weights of the thread's columns; ones where there are none
-    __device__ __forceinline__ void weights(Eight<W> (&w)[NC], const void* p) const {
-        const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    __device__ __forceinline__ void settle_all(Operands& r) const {
+        if (!tail) return;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) w[i] = p ? load_eight((const W*)p + column(i), a.K - column(i)) : pack_eight<W>(one);
+        for (int i = 0; i < NC; ++i) {
+            const uint32_t c = column(i);
+            if (!BACK || a.norm_pre) finish(r.h[i], c);
+            if (a.x.data) finish(r.x[i], c);
+            if (a.gate) finish(r.gate[i], c);
+            if constexpr (BACK) {
+                if (a.norm_pre) finish(r.dy[i], c);
+                if (a.dh.data) finish(r.dh[i], c);
+            }
+        }
+    }
+    // a weight's values in the thread's columns; ones where there are none
+    __device__ __forceinline__ Eight<W> weight(const void* p, int i) const {
+        const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+        if (!p) return pack_eight<W>(one);
+        Eight<W> e = start((const W*)p, column(i));
+        if (tail) finish(e, column(i));
+        return e;
     }
 };
 
-// The factor of a row's norm from the sum of its squares; `again` sums its squares shrunk.
-template <typename F>
-__device__ __forceinline__ Factor factor_of(float squares, const NormArgs& a, F&& again) {
-    if (__builtin_expect(squares < NORM_LARGE, 1)) return Factor{1.0f, __frsqrt_rn(squares * a.per + a.eps)};
-    return Factor{NORM_SHRINK, __frsqrt_rn(again() * a.per)};       // (infinities and NaN come here too: eps 2^-160 is nothing)
-}
+// Weights of the thread's columns: held in registers for all rows, or, where a thread has several vectors of a row and no
+// registers to spare, read again for each (from the caches).
+template <typename OF, typename W, int NC>
+struct Weights {
+    static constexpr bool HELD = NC == 1;
+    const OF& of;
+    const void* p;
+    Eight<W> w[HELD ? NC : 1];
+    __device__ __forceinline__ Weights(const OF& o, const void* weight) : of(o), p(weight) {
+        if constexpr (HELD)
+#pragma unroll
+            for (int i = 0; i < NC; ++i) w[i] = of.weight(p, i);
+    }
+    __device__ __forceinline__ void get(int i, float (&v)[8]) const {
+        if constexpr (HELD) unpack_eight<W>(w[i], v);
+        else unpack_eight<W>(of.weight(p, i), v);
+    }
+};
 
-template <int WAVES>
-__device__ __forceinline__ int64_t worker_of() {
-    return WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-}
-
-template <typename S, typename W, int WAVES, int NC>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES)
+// GROUP: a row is shared by the waves of a workgroup, else each of four waves has rows of its own.
+template <typename S, typename W, bool GROUP, int NC>
+__global__ __launch_bounds__(GROUP ? 1024 : 256)
 void k_block_norm_fwd(NormArgs a) {
-    __shared__ float shared[2 * WAVES];
+    __shared__ float4 shared[2 * 4];
     int turn = 0;
-    const RowOf<S, W, WAVES, NC, false> of{a, WAVES == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x};
-    const int64_t first = worker_of<WAVES>() * a.rows, end = first + a.rows < a.M ? first + a.rows : a.M;
-    if (first >= end) return;             // (all threads of a barrier's workgroup together)
-    Eight<W> pre[NC], post[NC];
-    RowOperands<S, W, NC, false> next, now;
-    of.load(next, first);
-    of.weights(pre, a.pre);
-    of.weights(post, a.post);
-    for (int64_t row = first; row < end; ++row) {
+    const int waves = blockDim.x >> 6;
+    if constexpr (GROUP) {
+        if (threadIdx.x < 8) shared[threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __syncthreads();
+    }
+    typedef RowOf<S, W, GROUP, NC, false> Of;
+    Of of(a);
+    if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
+    typename Of::Operands next, now;
+    of.neutral(next);
+    of.load(next, of.first);
+    const Weights<Of, W, NC> pre(of, a.pre), post(of, a.post);
+    // 1 / the root of the mean square of a row
+    auto factor = [&](const float (&v)[NC][8]) {
+        auto squares = [&](float shrink) {
+            float q[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[0] = __fmaf_rn(v[i][j] * shrink, v[i][j] * shrink, q[0]);
+            row_sums<GROUP>(q, shared, turn, waves);
+            return q[0];
+        };
+        const float q = squares(1.0f);
+        if (__builtin_expect(q < NORM_LARGE, 1)) return __frsqrt_rn(q * a.per + a.eps);
+        return __frsqrt_rn(squares(NORM_SHRINK) * a.per) * NORM_SHRINK;         // (infinities and NaN come here too)
+    };
+    for (uint32_t row = of.first; row < of.end; ++row) {
         now = next;
-        if (row + 1 < end) of.load(next, row + 1);
+        if (row + 1 < of.end) of.load(next, row + 1);
+        of.settle_all(now);
         float h[NC][8];
 #pragma unroll
         for (int i = 0; i < NC; ++i) unpack_eight<S>(now.h[i], h[i]);
@@ -116,197 +201,184 @@ void k_block_norm_fwd(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) unpack_eight<uint16_t>(now.x[i], p[i]);
             if (a.norm_post) {
-                auto squares = [&](float shrink) {
-                    float q[1] = {0.0f};
-#pragma unroll
-                    for (int i = 0; i < NC; ++i)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) q[0] = __fmaf_rn(p[i][j] * shrink, p[i][j] * shrink, q[0]);
-                    row_sums<WAVES>(q, shared, turn);
-                    return q[0];
-                };
-                const Factor f = factor_of(squares(1.0f), a, [&] { return squares(NORM_SHRINK); });
+                const float f = factor(p);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     float w[8];
-                    unpack_eight<W>(post[i], w);
+                    post.get(i, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) p[i][j] = p[i][j] * f.shrink * f.factor * w[j];
+                    for (int j = 0; j < 8; ++j) p[i][j] = p[i][j] * f * w[j];
                 }
             }
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                float g[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-                if (a.gate) unpack_eight<W>(now.gate[i], g);
+                float g[8];
+                unpack_eight<W>(now.gate[i], g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) h[i][j] += a.scale * g[j] * p[i][j];
                 const Eight<S> e = pack_eight<S>(h[i]);
                 unpack_eight<S>(e, h[i]);
-                const int c = of.column(i);
-                store_eight((S*)a.h_out.data + row * a.h_out.stride + c, a.K - c, e);
+                store_eight((S*)a.h_out.data + row * a.h_out.stride, of.column(i), a.K, e);
             }
         }
         if (a.norm_pre) {
-            auto squares = [&](float shrink) {
-                float q[1] = {0.0f};
-#pragma unroll
-                for (int i = 0; i < NC; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) q[0] = __fmaf_rn(h[i][j] * shrink, h[i][j] * shrink, q[0]);
-                row_sums<WAVES>(q, shared, turn);
-                return q[0];
-            };
-            const Factor f = factor_of(squares(1.0f), a, [&] { return squares(NORM_SHRINK); });
+            const float f = factor(h);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 float w[8];
-                unpack_eight<W>(pre[i], w);
+                pre.get(i, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = h[i][j] * f.shrink * f.factor * w[j];
-                const int c = of.column(i);
-                store_eight((uint16_t*)a.y.data + row * a.y.stride + c, a.K - c, pack_eight<uint16_t>(w));
+                for (int j = 0; j < 8; ++j) w[j] = h[i][j] * f * w[j];
+                store_eight((uint16_t*)a.y.data + row * a.y.stride, of.column(i), a.K, pack_eight<uint16_t>(w));
             }
         }
     }
 }
 
-// LEARN: the sums over tokens are wanted.
-template <typename S, typename W, int WAVES, int NC, bool LEARN>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES)
+// LEARN: the sums over tokens are wanted.  dpost and dgate are both sums of scale d b (b = n(x)): of each gate's tokens
+// that sum is kept, and leaves for both where a gate's tokens end.  One gate for all has one sum, which the join
+// multiplies out; a gate of one token's own has no sum to keep, and dpost's takes the registers.
+// THREADS: of a workgroup at most.  LEARN: 0, 1, or 2 where the gates are the tokens' own.
+template <typename S, typename W, int THREADS, bool GROUP, int NC, int LEARN>
+__global__ __launch_bounds__(THREADS)
 void k_block_norm_bwd(NormArgs a) {
-    __shared__ float shared[2 * 3 * WAVES];
+    __shared__ float4 shared[2 * 3 * 4];
     int turn = 0;
-    const RowOf<S, W, WAVES, NC, true> of{a, WAVES == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x};
-    const int64_t worker = worker_of<WAVES>(), first = worker * a.rows, end = first + a.rows < a.M ? first + a.rows : a.M;
-    if (first >= end) return;
-    Eight<W> pre[NC], post[NC];
-    RowOperands<S, W, NC, true> next, now;
-    of.load(next, first);
-    of.weights(pre, a.pre);
-    of.weights(post, a.post);
-    float spre[NC][8] = {}, spost[NC][8] = {}, sgate[NC][8] = {};
+    const int waves = blockDim.x >> 6;
+    if constexpr (GROUP) {
+        if (threadIdx.x < 24) shared[threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __syncthreads();
+    }
+    typedef RowOf<S, W, GROUP, NC, true> Of;
+    Of of(a);
+    typename Of::Operands next, now;
+    if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
+    of.neutral(next);
+    of.load(next, of.first);
+    const Weights<Of, W, NC> pre(of, a.pre), post(of, a.post);
+    float spre[NC][8] = {}, sover[NC][8] = {};
+    constexpr bool OWN = LEARN == 2;
+    const bool one_gate = a.gate && a.gate_span == a.M;
+    bool posted = false;                          // the worker's sum of dpost is partly in memory
     auto put = [&](float* to, const float (&v)[NC][8]) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = of.column(i);
-            store_eight(to + c, a.K - c, pack_eight<float>(v[i]));
-        }
+        for (int i = 0; i < NC; ++i) store_eight(to, of.column(i), a.K, pack_eight<float>(v[i]));
     };
     // one of the row sums in turn (the shared numbers are laid out for three)
     auto sum = [&](float v) {
         float q[3] = {v, 0.0f, 0.0f};
-        row_sums<WAVES>(q, shared, turn);
+        row_sums<GROUP>(q, shared, turn, waves);
         return q[0];
     };
-    for (int64_t row = first; row < end; ++row) {
+    uint32_t gate = of.first / a.gate_span, gate_first = gate * a.gate_span;        // of the row computed
+    for (uint32_t row = of.first; row < of.end; ++row) {
         now = next;
-        if (row + 1 < end) of.load(next, row + 1);
+        if (row + 1 < of.end) of.load(next, row + 1);
+        of.settle_all(now);
         float d[NC][8], x[NC][8];
-        // ---- through the norm before the next block ----
+        // ---- through the norm before the next block (without one, h' and dy are zero) ----
         float q[3] = {0.0f, 0.0f, 0.0f};          // squares of h', t h', squares of x
-        if (a.norm_pre) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float h[8], t[8], w[8];
+            unpack_eight<S>(now.h[i], h);
+            unpack_eight<uint16_t>(now.dy[i], t);
+            pre.get(i, w);
+            unpack_eight<uint16_t>(now.x[i], x[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                q[0] = __fmaf_rn(h[j], h[j], q[0]);
+                q[1] = __fmaf_rn(t[j] * w[j], h[j], q[1]);
+                q[2] = __fmaf_rn(x[i][j], x[i][j], q[2]);
+            }
+        }
+        row_sums<GROUP>(q, shared, turn, waves);
+        float f, mean;                            // s(h'); the mean of t a
+        if (__builtin_expect(q[0] < NORM_LARGE, 1)) {
+            f = __frsqrt_rn(q[0] * a.per + a.eps);
+        } else {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                float h[8];
+                unpack_eight<S>(now.h[i], h);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v = __fmaf_rn(h[j] * NORM_SHRINK, h[j] * NORM_SHRINK, v);
+            }
+            f = __frsqrt_rn(sum(v) * a.per) * NORM_SHRINK;
+        }
+        mean = q[1] * f * a.per;
+        if (__builtin_expect(!(fabsf(q[1]) < NORM_LARGE), 0)) {           // t h' left fp32: the sum of t a itself
+            float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 float h[8], t[8], w[8];
                 unpack_eight<S>(now.h[i], h);
                 unpack_eight<uint16_t>(now.dy[i], t);
-                unpack_eight<W>(pre[i], w);
+                pre.get(i, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    q[0] = __fmaf_rn(h[j], h[j], q[0]);
-                    q[1] = __fmaf_rn(t[j] * w[j], h[j], q[1]);
-                }
+                for (int j = 0; j < 8; ++j) v = __fmaf_rn(t[j] * w[j], h[j] * f, v);
             }
-        }
-        if (a.x.data) {
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                unpack_eight<uint16_t>(now.x[i], x[i]);
-                if (a.norm_post)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) q[2] = __fmaf_rn(x[i][j], x[i][j], q[2]);
-            }
-        }
-        row_sums<WAVES>(q, shared, turn);
-        Factor f{1.0f, 0.0f}, g{1.0f, 1.0f};
-        float mean = 0.0f;                        // of t a
-        if (a.norm_pre) {
-            f = factor_of(q[0], a, [&] {
-                float v = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    float h[8];
-                    unpack_eight<S>(now.h[i], h);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v = __fmaf_rn(h[j] * NORM_SHRINK, h[j] * NORM_SHRINK, v);
-                }
-                return sum(v);
-            });
-            mean = q[1] * f.factor * a.per;
-            if (__builtin_expect(!(q[0] < NORM_LARGE && fabsf(q[1]) < NORM_LARGE), 0)) {      // t h' left fp32: the sum of t a itself
-                float v = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    float h[8], t[8], w[8];
-                    unpack_eight<S>(now.h[i], h);
-                    unpack_eight<uint16_t>(now.dy[i], t);
-                    unpack_eight<W>(pre[i], w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v = __fmaf_rn(t[j] * w[j], h[j] * f.shrink * f.factor, v);
-                }
-                mean = sum(v) * a.per;
-            }
+            mean = sum(v) * a.per;
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float h[8], t[8], w[8];
-            if (a.dh.data) unpack_eight<S>(now.dh[i], d[i]);
-            else
+            unpack_eight<S>(now.dh[i], d[i]);
+            unpack_eight<S>(now.h[i], h);
+            unpack_eight<uint16_t>(now.dy[i], t);
+            pre.get(i, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[i][j] = 0.0f;
-            if (a.norm_pre) {
-                unpack_eight<S>(now.h[i], h);
-                unpack_eight<uint16_t>(now.dy[i], t);
-                unpack_eight<W>(pre[i], w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float n = h[j] * f.shrink * f.factor;
-                    if (LEARN) spre[i][j] = __fmaf_rn(t[j], n, spre[i][j]);
-                    d[i][j] += (t[j] * w[j] - n * mean) * f.factor * f.shrink;
-                }
+            for (int j = 0; j < 8; ++j) {
+                const float n = h[j] * f;
+                if (LEARN) spre[i][j] = __fmaf_rn(t[j], n, spre[i][j]);
+                d[i][j] = __fmaf_rn(__fmaf_rn(t[j], w[j], -n * mean), f, d[i][j]);
             }
-            const int c = of.column(i);
-            store_eight((S*)a.h_out.data + row * a.h_out.stride + c, a.K - c, pack_eight<S>(d[i]));
+            store_eight((S*)a.h_out.data + row * a.h_out.stride, of.column(i), a.K, pack_eight<S>(d[i]));
         }
         // ---- through the gate and the norm after the block ----
         if (a.y.data) {
+            float g = 1.0f;                       // s(x)
             if (a.norm_post) {
-                g = factor_of(q[2], a, [&] {
+                if (__builtin_expect(q[2] < NORM_LARGE, 1)) {
+                    g = __frsqrt_rn(q[2] * a.per + a.eps);
+                } else {
                     float v = 0.0f;
 #pragma unroll
                     for (int i = 0; i < NC; ++i)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v = __fmaf_rn(x[i][j] * NORM_SHRINK, x[i][j] * NORM_SHRINK, v);
-                    return sum(v);
-                });
+                    g = __frsqrt_rn(sum(v) * a.per) * NORM_SHRINK;
+                }
+            }
+            if constexpr (OWN) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    float w[8], e[8];
+                    unpack_eight<W>(now.gate[i], e);
+                    post.get(i, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float v = a.scale * d[i][j] * (x[i][j] * g);
+                        sover[i][j] = __fmaf_rn(v, e[j], sover[i][j]);
+                        w[j] *= v;
+                    }
+                    if (a.dgate) store_eight(a.dgate + (uint64_t)row * a.K, of.column(i), a.K, pack_eight<float>(w));
+                }
             }
             float over = 0.0f;                    // the sum of u b
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                float w[8], e[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-                if (a.gate) unpack_eight<W>(now.gate[i], e);
-                unpack_eight<W>(post[i], w);
+                float w[8], e[8];
+                unpack_eight<W>(now.gate[i], e);
+                post.get(i, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float b = x[i][j] * g.shrink * g.factor;
-                    const float u = a.scale * e[j] * d[i][j];
-                    if (LEARN) {
-                        spost[i][j] = __fmaf_rn(u, b, spost[i][j]);
-                        sgate[i][j] = __fmaf_rn(a.scale * d[i][j], b * w[j], sgate[i][j]);
-                    }
-                    d[i][j] = u * w[j];
-                    over = __fmaf_rn(d[i][j], b, over);
-                    x[i][j] = b;
+                    x[i][j] *= g;
+                    const float c = a.scale * d[i][j];
+                    if (LEARN && !OWN) sover[i][j] = __fmaf_rn(c, x[i][j], sover[i][j]);
+                    d[i][j] = c * e[j] * w[j];
+                    over = __fmaf_rn(d[i][j], x[i][j], over);
                 }
             }
             if (a.norm_post) {
@@ -314,49 +386,85 @@ void k_block_norm_bwd(NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[i][j] = (d[i][j] - x[i][j] * over) * g.factor * g.shrink;
+                    for (int j = 0; j < 8; ++j) d[i][j] = __fmaf_rn(-x[i][j], over, d[i][j]) * g;
             }
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int c = of.column(i);
-                store_eight((uint16_t*)a.y.data + row * a.y.stride + c, a.K - c, pack_eight<uint16_t>(d[i]));
-            }
-            if (LEARN && a.dgate) {               // a gate's last token here: its sum leaves the registers
-                const int64_t gate = row / a.gate_span, start = gate * a.gate_span;
-                if (row + 1 == end || row + 1 == start + a.gate_span) {
-                    const bool whole = start >= first && start + a.gate_span <= end;
-                    put(whole ? a.dgate + gate * a.K : a.part_gate + (2 * worker + (first / a.gate_span == gate ? 0 : 1)) * a.K, sgate);
+            for (int i = 0; i < NC; ++i) store_eight((uint16_t*)a.y.data + row * a.y.stride, of.column(i), a.K, pack_eight<uint16_t>(d[i]));
+            if (LEARN && !OWN && a.gate && !one_gate && (row + 1 == of.end || row + 1 == gate_first + a.gate_span)) {
+                // a gate's last token here: its sums leave the registers
+                const bool whole = gate_first >= of.first && gate_first + a.gate_span <= of.end;
+                float* to = whole ? a.dgate + (uint64_t)gate * a.K
+                                  : a.part_gate + (2 * (uint64_t)of.worker + (gate_first <= of.first ? 0 : 1)) * a.K;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i)
+                for (int i = 0; i < NC; ++i) {
+                    float w[8], e[8], s[8], was[8] = {};
+                    post.get(i, w);
+                    unpack_eight<W>(now.gate[i], e);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sgate[i][j] = 0.0f;
+                    for (int j = 0; j < 8; ++j) s[j] = sover[i][j] * w[j];
+                    if (a.dgate) store_eight(to, of.column(i), a.K, pack_eight<float>(s));
+                    if (a.dpost) {
+                        float* post_to = (a.part_post ? a.part_post + (uint64_t)of.worker * a.K : a.dpost);
+                        if (posted) unpack_eight<float>(load_eight((const float*)post_to, of.column(i), a.K), was);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) was[j] = __fmaf_rn(sover[i][j], e[j], was[j]);
+                        store_eight(post_to, of.column(i), a.K, pack_eight<float>(was));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sover[i][j] = 0.0f;
                 }
+                posted = true;
             }
+        }
+        if (row + 1 == gate_first + a.gate_span) {
+            ++gate;
+            gate_first += a.gate_span;
         }
     }
     if constexpr (LEARN) {
-        if (a.dpre) put(a.part_pre ? a.part_pre + worker * a.K : a.dpre, spre);
-        if (a.dpost) put(a.part_post ? a.part_post + worker * a.K : a.dpost, spost);
+        if (a.dpre) put(a.part_pre ? a.part_pre + (uint64_t)of.worker * a.K : a.dpre, spre);
+        if (!OWN && one_gate && !a.part_post) {   // one worker
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                float w[8], e[8];
+                post.get(i, w);
+                unpack_eight<W>(of.weight(a.gate, i), e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    w[j] *= sover[i][j];
+                    e[j] *= sover[i][j];
+                }
+                if (a.dgate) store_eight(a.dgate, of.column(i), a.K, pack_eight<float>(w));
+                if (a.dpost) store_eight(a.dpost, of.column(i), a.K, pack_eight<float>(e));
+            }
+        } else if ((a.dpost || (a.dgate && one_gate)) && !posted) {
+            put(a.part_post ? a.part_post + (uint64_t)of.worker * a.K : a.dpost, sover);
+        }
     }
 }
 
-// The workers' sums, added up.  blockIdx.y: 0 of pre, 1 of post, then the gates that more than one worker has a part of.
-// 16 threads hold 4 columns each, 16 others take every 16th worker; their sums are added in order.
+// The workers' sums, added up.  blockIdx.y: 0 of pre, 1 of post (and of the one gate for all), then the gates that more than
+// one worker has a part of.  8 threads hold 4 columns each; 128 such groups take the workers in turn, and
+// their sums are added in a fixed order.
 struct JoinArgs {
     float *dpre, *dpost, *dgate;
     const float *part_pre, *part_post, *part_gate;
+    const void *post, *gate;  // one gate for all: the factors of its sum (null: ones), else null
     int64_t gates, gate_span, rows, workers;
     int K;
+    bool one_gate, weights_bf16;
 };
-__global__ __launch_bounds__(256)
+constexpr int JOIN_COLUMNS = 32;
+__global__ __launch_bounds__(1024)
 void k_block_norm_join(JoinArgs a) {
-    __shared__ float4 sums[16][16];
-    const int lane = threadIdx.x & 15, slice = threadIdx.x >> 4;
-    const int c = blockIdx.x * 64 + lane * 4;
-    auto join = [&](int64_t from, int64_t to, float* out, auto&& row_of) {
+    constexpr int SLICES = 128;
+    __shared__ float4 sums[SLICES][8];
+    const int lane = threadIdx.x & 7, slice = threadIdx.x >> 3;
+    const int c = blockIdx.x * JOIN_COLUMNS + lane * 4;
+    auto join = [&](int64_t from, int64_t to, auto&& row_of, auto&& put) {
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int64_t w = from + slice; w < to; w += 16) {
+        for (int64_t w = from + slice; w < to; w += SLICES) {
             const float* p = row_of(w) + c;
             if (c + 4 <= a.K) {
                 typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
@@ -370,63 +478,69 @@ void k_block_norm_join(JoinArgs a) {
         }
         sums[slice][lane] = s;
         __syncthreads();
-        if (slice == 0) {
+        float* column = reinterpret_cast<float*>(&sums[0][0]) + threadIdx.x % JOIN_COLUMNS;
+        const int part = threadIdx.x / JOIN_COLUMNS, k = blockIdx.x * JOIN_COLUMNS + threadIdx.x % JOIN_COLUMNS;
+        if (part < 8) {
+            float v = 0.0f;
 #pragma unroll
-            for (int i = 1; i < 16; ++i) {
-                const float4 v = sums[i][lane];
-                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-            }
-            const float v[4] = {s.x, s.y, s.z, s.w};
+            for (int i = 0; i < SLICES / 8; ++i) v += column[(part * (SLICES / 8) + i) * JOIN_COLUMNS];
+            column[part * (SLICES / 8) * JOIN_COLUMNS] = v;
+        }
+        __syncthreads();
+        if (part == 0 && k < a.K) {
+            float v = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (c + i < a.K) out[c + i] = v[i];
+            for (int i = 0; i < 8; ++i) v += column[i * (SLICES / 8) * JOIN_COLUMNS];
+            put(k, v);
         }
         __syncthreads();
     };
+    auto weight = [&](const void* p, int k) { return !p ? 1.0f : a.weights_bf16 ? bf16_to_f32(((const uint16_t*)p)[k]) : ((const float*)p)[k]; };
     if (blockIdx.y == 0) {
-        if (a.dpre) join(0, a.workers, a.dpre, [&](int64_t w) { return a.part_pre + w * a.K; });
+        if (a.dpre) join(0, a.workers, [&](int64_t w) { return a.part_pre + w * a.K; }, [&](int k, float v) { a.dpre[k] = v; });
     } else if (blockIdx.y == 1) {
-        if (a.dpost) join(0, a.workers, a.dpost, [&](int64_t w) { return a.part_post + w * a.K; });
-    } else if (a.dgate) {
+        if (a.dpost || (a.dgate && a.one_gate))
+            join(0, a.workers, [&](int64_t w) { return a.part_post + w * a.K; }, [&](int k, float v) {
+                if (a.dpost) a.dpost[k] = v * weight(a.gate, k);
+                if (a.dgate && a.one_gate) a.dgate[k] = v * weight(a.post, k);
+            });
+    } else {
         for (int64_t g = blockIdx.y - 2; g < a.gates; g += gridDim.y - 2) {
             const int64_t start = g * a.gate_span, w0 = start / a.rows, w1 = a.workers > 0 ? (start + a.gate_span - 1) / a.rows : -1;
             if (w0 == w1) continue;       // (that worker has written it)
-            join(w0, w1 + 1, a.dgate + g * a.K, [&](int64_t w) { return a.part_gate + (2 * w + (w * a.rows / a.gate_span == g ? 0 : 1)) * a.K; });
+            join(w0, w1 + 1, [&](int64_t w) { return a.part_gate + (2 * w + (w * a.rows >= start ? 0 : 1)) * a.K; },
+                 [&](int k, float v) { a.dgate[g * a.K + k] = v; });
         }
     }
 }
 
-// Threads that share a row, and the rows that a worker walks along.
+// Threads that share a row, and the rows that a worker walks along.  One vector a thread as far as a workgroup reaches: with
+// two, 512 threads have the registers for the backward pass without spilling, but two waves a SIMD do not cover the sums'
+// waits (gradient of 4096 x 8192: 105.7 us with two, 90.3 with one; of 4000 x 4099, where five waves of two vectors leave
+// SIMDs idle, 95 and 68).
 struct NormShape {
     int waves, chunks;        // waves of a row; times 8 values a thread
     int64_t rows, workers;
+    bool group() const { return waves > 1; }
+    dim3 grid() const { return dim3((uint32_t)(group() ? workers : (workers + 3) / 4)); }
+    dim3 block() const { return dim3(group() ? 64 * waves : 256); }
 };
+// Workers: those that run at once.  Forward, and backward without sums, 32 waves a compute unit, but one workgroup of more
+// than 8 waves (4096 x 8192: 46 us with one a compute unit, 47 with two, 53 with four; 6000 x 256: 7.5 us with all, 13 with
+// a quarter).  With sums over tokens 8 waves, for each worker leaves sums to be joined (gradients of 6000 x 1000: 25 us
+// with 4 workers of two waves a compute unit, 29 with 8; of 4096 x 4096: 45 us with one of eight, 48 with two, 73 with eight).
 static NormShape norm_shape(int64_t M, int64_t K, bool learn) {
     NormShape p{};
-    p.waves = K <= 1024 ? 1 : K <= 2048 ? 4 : K <= 4096 ? 8 : 16;
-    p.chunks = K <= 512 ? 1 : K <= 1024 ? 2 : K <= 8192 ? 1 : K <= 16384 ? 2 : 4;
-    // workers: those that run at once on 256 compute units
-    const int64_t most = p.waves == 1 ? 4096 : p.waves == 4 ? 1024 : 512;
+    p.chunks = K > 16384 ? 4 : K > 8192 ? 2 : 1;
+    p.waves = (int)((K + 512 * p.chunks - 1) / (512 * p.chunks));
+    const int per_unit = p.waves > 8 ? 1 : (learn ? 8 : 32) / p.waves;
+    const int64_t most = 256 * (int64_t)per_unit;
     p.rows = (M + most - 1) / most;
     p.rows = p.rows < 1 ? 1 : p.rows;
     p.workers = (M + p.rows - 1) / p.rows;
-    (void)learn;
     return p;
 }
 
-template <typename F>
-static void with_shape(const NormShape& p, F&& f) {
-#define NF4_SHAPE(w, c) \
-    if (p.waves == w && p.chunks == c) f(std::integral_constant<int, w>{}, std::integral_constant<int, c>{})
-    NF4_SHAPE(1, 1);
-    NF4_SHAPE(1, 2);
-    NF4_SHAPE(4, 1);
-    NF4_SHAPE(8, 1);
-    NF4_SHAPE(16, 1);
-    NF4_SHAPE(16, 2);
-    NF4_SHAPE(16, 4);
-#undef NF4_SHAPE
-}
 template <typename F>
 static void with_types(const BlockNorm& n, F&& f) {
     if (n.stream_bf16) n.weights_bf16 ? f(uint16_t{}, uint16_t{}) : f(uint16_t{}, float{});
@@ -438,10 +552,10 @@ static NormArgs norm_args(const BlockNorm& n, int64_t M, int64_t K, const NormSh
     a.pre = n.pre;
     a.post = n.post;
     a.gate = n.gate;
-    a.M = M;
-    a.K = (int)K;
-    a.gate_span = n.gate ? M / n.gate_rows : M;
-    a.rows = p.rows;
+    a.M = (uint32_t)M;
+    a.K = (uint32_t)K;
+    a.gate_span = (uint32_t)(n.gate ? M / n.gate_rows : M);
+    a.rows = (uint32_t)p.rows;
     a.norm_pre = n.norm_pre;
     a.norm_post = n.norm_post;
     a.scale = n.scale;
@@ -459,34 +573,35 @@ hipError_t launch_block_norm_fwd(const BlockNorm& n, int64_t M, int64_t K, const
     a.h_out = h_out;
     a.y = y;
     with_types(n, [&](auto st, auto wt) {
-        with_shape(p, [&](auto waves, auto chunks) {
-            constexpr int W = decltype(waves)::value;
-            const dim3 grid((uint32_t)(W == 1 ? (p.workers + 3) / 4 : p.workers)), block(W == 1 ? 256 : 64 * W);
-            hipLaunchKernelGGL((k_block_norm_fwd<decltype(st), decltype(wt), W, decltype(chunks)::value>), grid, block, 0, s, a);
-        });
+        auto run = [&](auto group, auto chunks) {
+            hipLaunchKernelGGL((k_block_norm_fwd<decltype(st), decltype(wt), decltype(group)::value, decltype(chunks)::value>), p.grid(), p.block(), 0, s, a);
+        };
+        if (!p.group()) run(std::false_type{}, std::integral_constant<int, 1>{});
+        else if (p.chunks == 1) run(std::true_type{}, std::integral_constant<int, 1>{});
+        else if (p.chunks == 2) run(std::true_type{}, std::integral_constant<int, 2>{});
+        else run(std::true_type{}, std::integral_constant<int, 4>{});
     });
     return hipGetLastError();
 }
 
-// The workers' sums in the workspace: of pre, of post, of gates (two for each worker, where a worker's stretch can end
-// inside a gate's tokens).
+// The workers' sums in the workspace: of pre, of post (or of the one gate), of gates (two for each worker, whose stretch can
+// begin and end inside a gate's tokens).
 struct NormParts {
     size_t pre, post, gate, bytes;
 };
 static NormParts norm_parts(const NormShape& p, int64_t M, int64_t K, int64_t gate_rows, bool dpre, bool dpost, bool dgate) {
     NormParts q{};
     const size_t one = (size_t)p.workers * K * sizeof(float);
-    if (p.workers == 1) return q;
+    if (p.workers <= 1) return q;
     q.pre = 0;
     q.post = q.pre + (dpre ? one : 0);
-    q.gate = q.post + (dpost ? one : 0);
-    q.bytes = q.gate + (dgate && M > gate_rows ? 2 * one : 0);
+    q.gate = q.post + (dpost || (dgate && gate_rows == 1) ? one : 0);
+    q.bytes = q.gate + (dgate && gate_rows > 1 && gate_rows < M ? 2 * one : 0);
     q.bytes = (q.bytes + 255) & ~(size_t)255;
     return q;
 }
 size_t block_norm_ws_bytes(int64_t M, int64_t K, int64_t gate_rows, bool dpre, bool dpost, bool dgate) {
-    const NormShape p = norm_shape(M, K, dpre || dpost || dgate);
-    return norm_parts(p, M, K, gate_rows, dpre, dpost, dgate).bytes;
+    return norm_parts(norm_shape(M, K, dpre || dpost || dgate), M, K, gate_rows, dpre, dpost, dgate).bytes;
 }
 
 hipError_t launch_block_norm_bwd(const BlockNorm& n, int64_t M, int64_t K, const RowsView& h, const RowsView& x,
@@ -513,18 +628,28 @@ hipError_t launch_block_norm_bwd(const BlockNorm& n, int64_t M, int64_t K, const
     }
     if (M > 0)
         with_types(n, [&](auto st, auto wt) {
-            with_shape(p, [&](auto waves, auto chunks) {
-                constexpr int W = decltype(waves)::value, C = decltype(chunks)::value;
-                const dim3 grid((uint32_t)(W == 1 ? (p.workers + 3) / 4 : p.workers)), block(W == 1 ? 256 : 64 * W);
-                if (learn) hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), W, C, true>), grid, block, 0, s, a);
-                else hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), W, C, false>), grid, block, 0, s, a);
-            });
+            auto run = [&](auto threads, auto group, auto chunks) {
+                constexpr int T = decltype(threads)::value, C = decltype(chunks)::value;
+                constexpr bool G = decltype(group)::value;
+                if (learn && n.gate && n.gate_rows == M && M > 1) hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, 2>), p.grid(), p.block(), 0, s, a);
+                else if (learn) hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, 1>), p.grid(), p.block(), 0, s, a);
+                else hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, 0>), p.grid(), p.block(), 0, s, a);
+            };
+            // (a workgroup of 1024 threads has 128 registers a thread: few spills with one vector, more beyond a width of 8192)
+            if (!p.group()) run(std::integral_constant<int, 256>{}, std::false_type{}, std::integral_constant<int, 1>{});
+            else if (p.chunks == 1 && p.waves <= 8) run(std::integral_constant<int, 512>{}, std::true_type{}, std::integral_constant<int, 1>{});
+            else if (p.chunks == 1) run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 1>{});
+            else if (p.chunks == 2) run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 2>{});
+            else run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 4>{});
         });
     if (q.bytes > 0 || (M == 0 && learn)) {
-        const int64_t gates = dgate && M != n.gate_rows ? n.gate_rows : 0;      // (a token's own gate is never shared)
-        const JoinArgs j{dpre, dpost, dgate, a.part_pre, a.part_post, a.part_gate, gates, a.gate_span, p.rows, p.workers, (int)K};
-        const dim3 grid((uint32_t)((K + 63) / 64), (uint32_t)(2 + (gates < 4096 ? gates : 4096)));
-        hipLaunchKernelGGL(k_block_norm_join, grid, dim3(256), 0, s, j);
+        // (a token's own gate is never shared)
+        const bool one = n.gate && n.gate_rows == 1;
+        const int64_t gates = dgate && !one && M != n.gate_rows ? n.gate_rows : 0;
+        const JoinArgs j{dpre, dpost, dgate, a.part_pre, a.part_post, a.part_gate, one ? n.post : nullptr, one ? n.gate : nullptr,
+                         gates, a.gate_span, p.rows, p.workers, (int)K, one, n.weights_bf16};
+        const dim3 grid((uint32_t)((K + JOIN_COLUMNS - 1) / JOIN_COLUMNS), (uint32_t)(2 + (gates < 4096 ? gates : 4096)));
+        hipLaunchKernelGGL(k_block_norm_join, grid, dim3(1024), 0, s, j);
     }
     return hipGetLastError();
 }

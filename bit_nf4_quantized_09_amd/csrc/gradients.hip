@@ -52,8 +52,7 @@ __device__ __forceinline__ double squares_of(const T* p, uint32_t n) {
         Eight<T> e[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t at = (int64_t)i + 256 * 8 * u;
-            e[u] = load_eight(p + at, (int64_t)n - at);
+            e[u] = load_eight(p, i + 256 * 8 * u, n);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -114,17 +113,15 @@ __device__ __forceinline__ void scale_span(const T* in, T* out, uint32_t n, floa
         Eight<T> e[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t at = (int64_t)i + 256 * 8 * u;
-            e[u] = load_eight(in + at, (int64_t)n - at);
+            e[u] = load_eight(in, i + 256 * 8 * u, n);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t at = (int64_t)i + 256 * 8 * u;
             float v[8];
             unpack_eight<T>(e[u], v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= f;
-            store_eight(out + at, (int64_t)n - at, pack_eight<T>(v));
+            store_eight(out, i + 256 * 8 * u, n, pack_eight<T>(v));
         }
     }
 }

@@ -36,7 +36,7 @@ void k_shape_logits(LogitArgs a) {
     const int64_t row = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
     if (row >= a.r.rows) return;
     const int first = blockIdx.x * SLICE, c = first + threadIdx.x * 8, left = a.V - c;
-    const Eight<T> raw = load_eight((const T*)a.in + row * a.in_stride + c, left);
+    const Eight<T> raw = load_eight((const T*)a.in + row * a.in_stride, c, a.V);
     uint32_t may = 0xFFu;
     if (a.r.allowed && left > 0) may = reinterpret_cast<const uint8_t*>(a.r.allowed + row * a.r.allowed_stride)[c >> 3];
     float rep = 1.0f, presence = 0.0f, frequency = 0.0f;
@@ -97,7 +97,7 @@ void k_shape_logits(LogitArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] = may >> j & 1u ? z[j] : -INFINITY;
-    store_eight((T*)a.out + row * a.out_stride + c, left, pack_eight<T>(z));
+    store_eight((T*)a.out + row * a.out_stride, c, a.V, pack_eight<T>(z));
 }
 
 hipError_t launch_shape_logits(const LogitRules& r, bool bf16, const void* in, int64_t in_stride, void* out, int64_t out_stride,
