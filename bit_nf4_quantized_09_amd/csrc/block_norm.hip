@@ -51,7 +51,7 @@ struct RowOperands {
 };
 
 // The rows of a worker, and the thread's columns of them.
-template <typename S, typename W, bool GROUP, int NC, bool BACK>
+template <typename S, typename W, bool GROUP, int NC, bool STREAM, bool BACK>
 struct RowOf {
     typedef RowOperands<S, W, NC, BACK> Operands;
     const NormArgs& a;
@@ -73,10 +73,10 @@ struct RowOf {
     }
     __device__ __forceinline__ uint32_t column(int i) const { return 8 * (t + i * threads); }
     // (a row shared by waves is longer than 512 values, one wave's may be shorter than eight)
-    template <typename T>
+    template <bool ONCE = false, typename T>
     __device__ __forceinline__ Eight<T> start(const T* p, uint32_t c) const {
         if (!GROUP && a.K < 8) return load_eight(p, c, a.K);
-        return load_late(p, c, a.K);
+        return load_late<T, ONCE>(p, c, a.K);
     }
     template <typename T>
     __device__ __forceinline__ void finish(Eight<T>& e, uint32_t c) const {
@@ -86,12 +86,12 @@ struct RowOf {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const uint32_t c = column(i);
-            if (!BACK || a.norm_pre) r.h[i] = start((const S*)a.h.data + row * a.h.stride, c);
-            if (a.x.data) r.x[i] = start((const uint16_t*)a.x.data + row * a.x.stride, c);
+            if (!BACK || a.norm_pre) r.h[i] = start<STREAM>((const S*)a.h.data + row * a.h.stride, c);
+            if (a.x.data) r.x[i] = start<STREAM>((const uint16_t*)a.x.data + row * a.x.stride, c);
             if (a.gate) r.gate[i] = start((const W*)a.gate + (uint64_t)gate * a.K, c);
             if constexpr (BACK) {
-                if (a.norm_pre) r.dy[i] = start((const uint16_t*)a.dy.data + row * a.dy.stride, c);
-                if (a.dh.data) r.dh[i] = start((const S*)a.dh.data + row * a.dh.stride, c);
+                if (a.norm_pre) r.dy[i] = start<STREAM>((const uint16_t*)a.dy.data + row * a.dy.stride, c);
+                if (a.dh.data) r.dh[i] = start<STREAM>((const S*)a.dh.data + row * a.dh.stride, c);
             }
         }
         if (--gate_left == 0) {
@@ -156,8 +156,9 @@ struct Weights {
     }
 };
 
-// GROUP: a row is shared by the waves of a workgroup, else each of four waves has rows of its own.
-template <typename S, typename W, bool GROUP, int NC>
+// GROUP: a row is shared by the waves of a workgroup, else each of four waves has rows of its own.  STREAM: nontemporal
+// loads of what is read once.
+template <typename S, typename W, bool GROUP, int NC, bool STREAM>
 __global__ __launch_bounds__(GROUP ? 1024 : 256)
 void k_block_norm_fwd(NormArgs a) {
     __shared__ float4 shared[2 * 4];
@@ -167,7 +168,7 @@ void k_block_norm_fwd(NormArgs a) {
         if (threadIdx.x < 8) shared[threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         __syncthreads();
     }
-    typedef RowOf<S, W, GROUP, NC, false> Of;
+    typedef RowOf<S, W, GROUP, NC, STREAM, false> Of;
     Of of(a);
     if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
     typename Of::Operands next, now;
@@ -239,7 +240,7 @@ void k_block_norm_fwd(NormArgs a) {
 // that sum is kept, and leaves for both where a gate's tokens end.  One gate for all has one sum, which the join
 // multiplies out; a gate of one token's own has no sum to keep, and dpost's takes the registers.
 // THREADS: of a workgroup at most.  LEARN: 0, 1, or 2 where the gates are the tokens' own.
-template <typename S, typename W, int THREADS, bool GROUP, int NC, int LEARN>
+template <typename S, typename W, int THREADS, bool GROUP, int NC, bool STREAM, int LEARN>
 __global__ __launch_bounds__(THREADS)
 void k_block_norm_bwd(NormArgs a) {
     __shared__ float4 shared[2 * 3 * 4];
@@ -249,7 +250,7 @@ void k_block_norm_bwd(NormArgs a) {
         if (threadIdx.x < 24) shared[threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         __syncthreads();
     }
-    typedef RowOf<S, W, GROUP, NC, true> Of;
+    typedef RowOf<S, W, GROUP, NC, STREAM, true> Of;
     Of of(a);
     typename Of::Operands next, now;
     if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
@@ -547,6 +548,10 @@ static void with_types(const BlockNorm& n, F&& f) {
     else n.weights_bf16 ? f(float{}, uint16_t{}) : f(float{}, float{});
 }
 
+// 32 MB of a bf16 operand and more, in whole lines of 128 bytes: nontemporal loads (4096 x 8192: 47 us forward and 82 backward,
+// 55 and 92 without; rows that begin inside a line, which two workgroups read: 28.0 us backward of 1001 x 2501, 24.6 without).
+static bool streams(int64_t M, int64_t K, const NormShape& p) { return p.group() && p.chunks == 1 && M * K >= (int64_t)1 << 24 && K % 64 == 0; }
+
 static NormArgs norm_args(const BlockNorm& n, int64_t M, int64_t K, const NormShape& p) {
     NormArgs a{};
     a.pre = n.pre;
@@ -573,13 +578,15 @@ hipError_t launch_block_norm_fwd(const BlockNorm& n, int64_t M, int64_t K, const
     a.h_out = h_out;
     a.y = y;
     with_types(n, [&](auto st, auto wt) {
-        auto run = [&](auto group, auto chunks) {
-            hipLaunchKernelGGL((k_block_norm_fwd<decltype(st), decltype(wt), decltype(group)::value, decltype(chunks)::value>), p.grid(), p.block(), 0, s, a);
+        auto run = [&](auto group, auto chunks, auto stream) {
+            hipLaunchKernelGGL((k_block_norm_fwd<decltype(st), decltype(wt), decltype(group)::value, decltype(chunks)::value, decltype(stream)::value>),
+                               p.grid(), p.block(), 0, s, a);
         };
-        if (!p.group()) run(std::false_type{}, std::integral_constant<int, 1>{});
-        else if (p.chunks == 1) run(std::true_type{}, std::integral_constant<int, 1>{});
-        else if (p.chunks == 2) run(std::true_type{}, std::integral_constant<int, 2>{});
-        else run(std::true_type{}, std::integral_constant<int, 4>{});
+        if (!p.group()) run(std::false_type{}, std::integral_constant<int, 1>{}, std::false_type{});
+        else if (streams(M, K, p)) run(std::true_type{}, std::integral_constant<int, 1>{}, std::true_type{});
+        else if (p.chunks == 1) run(std::true_type{}, std::integral_constant<int, 1>{}, std::false_type{});
+        else if (p.chunks == 2) run(std::true_type{}, std::integral_constant<int, 2>{}, std::false_type{});
+        else run(std::true_type{}, std::integral_constant<int, 4>{}, std::false_type{});
     });
     return hipGetLastError();
 }
@@ -628,19 +635,24 @@ hipError_t launch_block_norm_bwd(const BlockNorm& n, int64_t M, int64_t K, const
     }
     if (M > 0)
         with_types(n, [&](auto st, auto wt) {
-            auto run = [&](auto threads, auto group, auto chunks) {
+            auto run = [&](auto threads, auto group, auto chunks, auto stream) {
                 constexpr int T = decltype(threads)::value, C = decltype(chunks)::value;
-                constexpr bool G = decltype(group)::value;
-                if (learn && n.gate && n.gate_rows == M && M > 1) hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, 2>), p.grid(), p.block(), 0, s, a);
-                else if (learn) hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, 1>), p.grid(), p.block(), 0, s, a);
-                else hipLaunchKernelGGL((k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, 0>), p.grid(), p.block(), 0, s, a);
+                constexpr bool G = decltype(group)::value, N = decltype(stream)::value;
+                auto with = [&](auto kernel) { hipLaunchKernelGGL(kernel, p.grid(), p.block(), 0, s, a); };
+                if (learn && n.gate && n.gate_rows == M && M > 1) with(k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, N, 2>);
+                else if (learn) with(k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, N, 1>);
+                else with(k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, N, 0>);
+            };
+            auto one_vector = [&](auto threads) {
+                if (streams(M, K, p)) run(threads, std::true_type{}, std::integral_constant<int, 1>{}, std::true_type{});
+                else run(threads, std::true_type{}, std::integral_constant<int, 1>{}, std::false_type{});
             };
             // (a workgroup of 1024 threads has 128 registers a thread: few spills with one vector, more beyond a width of 8192)
-            if (!p.group()) run(std::integral_constant<int, 256>{}, std::false_type{}, std::integral_constant<int, 1>{});
-            else if (p.chunks == 1 && p.waves <= 8) run(std::integral_constant<int, 512>{}, std::true_type{}, std::integral_constant<int, 1>{});
-            else if (p.chunks == 1) run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 1>{});
-            else if (p.chunks == 2) run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 2>{});
-            else run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 4>{});
+            if (!p.group()) run(std::integral_constant<int, 256>{}, std::false_type{}, std::integral_constant<int, 1>{}, std::false_type{});
+            else if (p.chunks == 1 && p.waves <= 8) one_vector(std::integral_constant<int, 512>{});
+            else if (p.chunks == 1) one_vector(std::integral_constant<int, 1024>{});
+            else if (p.chunks == 2) run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 2>{}, std::false_type{});
+            else run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 4>{}, std::false_type{});
         });
     if (q.bytes > 0 || (M == 0 && learn)) {
         // (a token's own gate is never shared)

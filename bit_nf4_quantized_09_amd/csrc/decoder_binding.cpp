@@ -551,10 +551,14 @@ PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensors o(a[2] == Py_None ? a[0] : a[2], a[2] == Py_None ? "grads" : "out", g.first);
         if (o.v.size() != g.v.size()) bad("out must hold as many tensors as grads");
         o.each([](const at::Tensor& t) { want_unrecorded(t, "a clipped tensor"); });
-        const at::Tensor out = norm_of(g, number(a[1]));
-        check(qlora_grad_scale(g.v.data(), o.v.data(), (int64_t)g.v.size(), out.data_ptr<float>() + 1, stream_of(out)));
+        const double max_norm = number(a[1]);
+        const at::Tensor norm = at::empty({}, g.first->options().dtype(at::kFloat).requires_grad(false));
+        at::Tensor keep;
+        const size_t bytes = qlora_grad_clip_workspace_bytes(g.v.data(), (int64_t)g.v.size());
+        void* ws = workspace(bytes, norm, keep);
+        check(qlora_grad_clip(g.v.data(), o.v.data(), (int64_t)g.v.size(), max_norm, norm.data_ptr<float>(), ws, bytes, stream_of(norm)));
         o.each([](const at::Tensor& t) { written(t); });
-        return wrap(out.select(0, 0));
+        return wrap(norm);
     });
 }
 

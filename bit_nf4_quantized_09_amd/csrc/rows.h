@@ -34,12 +34,16 @@ template <typename T>
 __device__ __forceinline__ uintptr_t at_value(const T* row, uint32_t at) {
     return (uintptr_t)row + at * (uint32_t)sizeof(T);
 }
-template <typename T>
+// STREAM: a nontemporal load, for what is read once.
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ Eight<T> load_whole(uintptr_t p) {
     Eight<T> e;
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-        e.w[i] = __builtin_bit_cast(uint4, *((const NF4_GLOBAL typename Loose<T>::type*)p + i));
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) {
+        const NF4_GLOBAL typename Loose<T>::type* at = (const NF4_GLOBAL typename Loose<T>::type*)p + i;
+        if constexpr (STREAM) e.w[i] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(at));
+        else e.w[i] = __builtin_bit_cast(uint4, *at);
+    }
     return e;
 }
 // The values a place on (down) or back, a zero behind.
@@ -94,9 +98,9 @@ __device__ __forceinline__ void store_eight(T* row, uint32_t at, uint32_t n, Eig
 // load_eight in two parts for rows of eight values and more, so that nothing waits where the load is started: load_late
 // reads eight values that are all there (the row's last ones past its end), settle moves them to their places once they
 // are needed.
-template <typename T>
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ Eight<T> load_late(const T* row, uint32_t at, uint32_t n) {
-    return load_whole<T>(at_value(row, at + 8 <= n ? at : n - 8));
+    return load_whole<T, STREAM>(at_value(row, at + 8 <= n ? at : n - 8));
 }
 template <typename T>
 __device__ __forceinline__ void settle(Eight<T>& e, uint32_t at, uint32_t n) {

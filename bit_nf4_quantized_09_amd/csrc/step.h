@@ -35,7 +35,9 @@ struct Gradient {
 };
 size_t grad_norm_ws_bytes(const Gradient* g, int64_t count);
 hipError_t launch_grad_norm(const Gradient* g, int64_t count, double max_norm, float* norm, float* factor, void* ws, hipStream_t s);
-hipError_t launch_grad_scale(const Gradient* g, const Gradient* out, int64_t count, const float* factor, hipStream_t s);
+// norm and factor as above (factor is not always written); ws: of the norm.
+hipError_t launch_grad_clip(const Gradient* g, const Gradient* out, int64_t count, double max_norm, float* norm, float* factor,
+                            void* ws, hipStream_t s);
 
 // ---- logits before the choice of a token -----------------------------------
 struct LogitRules {

@@ -196,7 +196,7 @@ nf4_status qlora_grad_norm(const qlora_tensor* grads, int64_t count, double max_
         std::vector<Gradient> g;
         if (nf4_status st = gradients_of(grads, count, "grads", g)) return st;
         if (!norm || !aligned(norm, 4) || !aligned(factor, 4)) return fail(NF4_ERR_ARG, "norm is NULL, or norm or factor misaligned");
-        if (factor && !(max_norm >= 0.0f)) return fail(NF4_ERR_ARG, "max_norm must not be negative");
+        if (factor && !(max_norm >= 0.0)) return fail(NF4_ERR_ARG, "max_norm must not be negative");
         const size_t need = nf4::grad_norm_ws_bytes(g.data(), count);
         if (need > 0 && (!workspace || workspace_bytes < need)) return fail(NF4_ERR_WORKSPACE, "workspace missing or too small");
         if (need > 0 && !aligned(workspace, 256)) return fail(NF4_ERR_ARG, "workspace must be 256-byte aligned");
@@ -204,17 +204,35 @@ nf4_status qlora_grad_norm(const qlora_tensor* grads, int64_t count, double max_
     });
 }
 
-nf4_status qlora_grad_scale(const qlora_tensor* grads, const qlora_tensor* out, int64_t count, const float* factor, void* stream) {
+// (the norm's sums, and a place for the factor)
+size_t qlora_grad_clip_workspace_bytes(const qlora_tensor* grads, int64_t count) {
+    size_t bytes = 0;
+    guarded([&]() -> nf4_status {
+        std::vector<Gradient> g;
+        if (nf4_status st = gradients_of(grads, count, "grads", g)) return st;
+        bytes = nf4::grad_norm_ws_bytes(g.data(), count) + 256;
+        return NF4_OK;
+    });
+    return bytes;
+}
+
+nf4_status qlora_grad_clip(const qlora_tensor* grads, const qlora_tensor* out, int64_t count, double max_norm, float* norm,
+                           void* workspace, size_t workspace_bytes, void* stream) {
     return guarded([&]() -> nf4_status {
         std::vector<Gradient> g, o;
         if (nf4_status st = gradients_of(grads, count, "grads", g)) return st;
         if (nf4_status st = gradients_of(out, count, "out", o)) return st;
-        if (!factor || !aligned(factor, 4)) return fail(NF4_ERR_ARG, "factor is NULL or misaligned");
+        if (!norm || !aligned(norm, 4)) return fail(NF4_ERR_ARG, "norm is NULL or misaligned");
+        if (!(max_norm >= 0.0)) return fail(NF4_ERR_ARG, "max_norm must not be negative");
         for (int64_t i = 0; i < count; ++i)
             if (g[(size_t)i].n != o[(size_t)i].n || g[(size_t)i].bf16 != o[(size_t)i].bf16)
                 return fail(NF4_ERR_ARG, "grads and out have different sizes or types");
         if (written_overlap(g, o)) return fail(NF4_ERR_ARG, "a tensor that is written overlaps another (or is given twice)");
-        return hip_status(nf4::launch_grad_scale(g.data(), o.data(), count, factor, (hipStream_t)stream), "qlora_grad_scale");
+        const size_t sums = nf4::grad_norm_ws_bytes(g.data(), count);
+        if (!workspace || workspace_bytes < sums + 256) return fail(NF4_ERR_WORKSPACE, "workspace missing or too small");
+        if (!aligned(workspace, 256)) return fail(NF4_ERR_ARG, "workspace must be 256-byte aligned");
+        return hip_status(nf4::launch_grad_clip(g.data(), o.data(), count, max_norm, norm, (float*)((uint8_t*)workspace + sums), workspace,
+                                                (hipStream_t)stream), "qlora_grad_clip");
     });
 }
 

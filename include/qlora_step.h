@@ -89,9 +89,12 @@ size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* grads, int64_t count)
 nf4_status qlora_grad_norm(const qlora_tensor* grads, int64_t count, double max_norm, float* norm, float* factor,
                            void* workspace, size_t workspace_bytes, void* stream);
 
-/* out[i] = factor * grads[i], each product rounded to the tensor's type.  factor: device fp32.  out[i] may be grads[i]
- * itself (nothing is written then where the factor is 1); tensors that are written may not overlap any other. */
-nf4_status qlora_grad_scale(const qlora_tensor* grads, const qlora_tensor* out, int64_t count, const float* factor, void* stream);
+/* out[i] = factor * grads[i], each product rounded to the tensor's type, and the norm before.  out[i] may be grads[i]
+ * itself (nothing is written then where the factor is 1); tensors that are written may not overlap any other.
+ *   workspace     qlora_grad_clip_workspace_bytes of the same tensors, 256-byte aligned */
+size_t qlora_grad_clip_workspace_bytes(const qlora_tensor* grads, int64_t count);
+nf4_status qlora_grad_clip(const qlora_tensor* grads, const qlora_tensor* out, int64_t count, double max_norm, float* norm,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* nf4_adamw_step and nf4_adamw_step_paged with the gradient times a factor (device fp32, of qlora_grad_norm), which is
  * rounded to fp32 before the step; with a factor of 1 they give the same bits as those. */

@@ -39,8 +39,10 @@ def library():
     L.qlora_grad_norm_workspace_bytes.argtypes = [p(Tensor), _i64]
     L.qlora_grad_norm.restype = ctypes.c_int
     L.qlora_grad_norm.argtypes = [p(Tensor), _i64, ctypes.c_double, _vp, _vp, _vp, _sz, _vp]
-    L.qlora_grad_scale.restype = ctypes.c_int
-    L.qlora_grad_scale.argtypes = [p(Tensor), p(Tensor), _i64, _vp, _vp]
+    L.qlora_grad_clip_workspace_bytes.restype = _sz
+    L.qlora_grad_clip_workspace_bytes.argtypes = [p(Tensor), _i64]
+    L.qlora_grad_clip.restype = ctypes.c_int
+    L.qlora_grad_clip.argtypes = [p(Tensor), p(Tensor), _i64, ctypes.c_double, _vp, _vp, _sz, _vp]
     L.qlora_kv_attention_window_workspace_bytes.restype = _sz
     L.qlora_kv_attention_window_workspace_bytes.argtypes = [p(dec._Cache), p(dec._Batch), _i32, _i64, _i64, _i64, _i64]
     L.qlora_kv_attention_window.restype = ctypes.c_int

@@ -30,9 +30,9 @@ def test_declared_symbols_are_exported():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(qlora_\w+)\s*\(", text)))
     assert names == ["qlora_adamw_step_paged_scaled", "qlora_adamw_step_scaled", "qlora_block_norm_bwd",
-                     "qlora_block_norm_bwd_workspace_bytes", "qlora_block_norm_fwd", "qlora_grad_norm",
-                     "qlora_grad_norm_workspace_bytes", "qlora_grad_scale", "qlora_kv_attention_window",
-                     "qlora_kv_attention_window_workspace_bytes", "qlora_logits_shape"]
+                     "qlora_block_norm_bwd_workspace_bytes", "qlora_block_norm_fwd", "qlora_grad_clip",
+                     "qlora_grad_clip_workspace_bytes", "qlora_grad_norm", "qlora_grad_norm_workspace_bytes",
+                     "qlora_kv_attention_window", "qlora_kv_attention_window_workspace_bytes", "qlora_logits_shape"]
     for n in names:
         assert hasattr(nf4.load_library(), n)
 
@@ -114,10 +114,14 @@ def test_gradient_refusals():
     assert norm_of(ws=None) == WORKSPACE and norm_of(b=size - 1) == WORKSPACE and norm_of(ws=4100) == ARG
     for bad in ((None, 5, F32), (4098, 5, F32), (4097, 5, BF16), (SOME, -1, F32), (SOME, 5, 3), (SOME, (1 << 40) + 1, F32)):
         assert norm_of(tensors(bad), 1) == ARG and L.qlora_grad_norm_workspace_bytes(tensors(bad), 1) == 0
-    scale = lambda g, o, f=SOME: L.qlora_grad_scale(g, o, len(o), f, None)  # noqa: E731
+    scale = lambda g, o, m=1.0, out=SOME, ws=SOME, b=1 << 20: L.qlora_grad_clip(g, o, len(o), m, out, ws, b, None)  # noqa: E731
     a, b = (4 << 20, 100, F32), (8 << 20, 50, BF16)
-    assert scale(tensors(a), tensors(a), None) == ARG and scale(tensors(a), tensors((8 << 20, 99, F32))) == ARG
-    assert scale(tensors(a), tensors((8 << 20, 100, BF16))) == ARG
+    assert scale(tensors(a), tensors((8 << 20, 99, F32))) == ARG and scale(tensors(a), tensors((8 << 20, 100, BF16))) == ARG
+    assert scale(tensors(a), tensors(a), out=None) == ARG and scale(tensors(a), tensors(a), out=4097) == ARG
+    assert scale(tensors(a), tensors(a), m=-1.0) == ARG and scale(tensors(a), tensors(a), m=float("nan")) == ARG
+    size = L.qlora_grad_clip_workspace_bytes(tensors(a), 1)
+    assert scale(tensors(a), tensors(a), ws=None) == WORKSPACE and scale(tensors(a), tensors(a), b=size - 1) == WORKSPACE
+    assert scale(tensors(a), tensors(a), ws=4100) == ARG
     inside = ((4 << 20) + 4, 10, F32)
     far = (12 << 20, 10, F32)
     for g, o in (((a, a), (a, a)), ((a, inside), (a, inside)), ((a, far), (a, inside)), ((a, inside), (a, far)), ((a,), (((4 << 20) - 4, 100, F32),)),
