@@ -18,6 +18,7 @@ constexpr int KV_WHOLE = 1 << 30;         // the longest chunk (a longer sequenc
 struct AttendShape {
     int dim, kv_heads;
     int64_t seqs, tokens, heads, max_new, max_length;
+    bool window = false;                  // max_length is a window's keys, which most sequences fill
 };
 constexpr int64_t ATTEND_PAIRS = (int64_t)1 << 25;        // (sequence, kv head) pairs of a call at most: one wave each, of 2^32 threads
 
@@ -57,6 +58,26 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // each SIMD: of 128 keys a wave at least where most of the keys were there before (27 sequences of up to 494 keys
 // and 11 tokens: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the
 // others (one prompt of 252 behind 1370 keys, 8 heads of 256: 70 us with 128, 49 with 512).
+// A window makes the sequences equally long, so that workgroups come in rounds: window_splits takes the chunks, all of one
+// size, for which an estimate is least: rounds of three workgroups on a compute unit (one with heads of 256), each as
+// long as a wave's steps take one after the other (1.1 us) or the round's bytes at 6 TB/s, and 5 us for a join.  24
+// sequences, window of 4096, 64 heads on 8: 39 us with one round of four chunks, 48 with one and a half of six; window of
+// 1024: 14 us with whole windows, 20 to 22 with two chunks.  (Eight waves to a workgroup instead of chunks: no faster, one
+// sequence, window of 1000: 13.3 us, 11.8 with chunks.)
+inline int64_t window_splits(const AttendShape& a, int64_t groups) {
+    const int64_t most = a.max_length / (KV_WAVES * KV_STEP) < 64 ? a.max_length / (KV_WAVES * KV_STEP) : 64;
+    const int64_t at_once = 256 * (a.dim == 256 ? 1 : 3);
+    int64_t best = 1;
+    double least = 0;
+    for (int64_t s = 1; s <= most || s == 1; ++s) {
+        const int64_t steps = (a.max_length + s * KV_STEP - 1) / (s * KV_STEP), workgroups = groups * s;
+        const double wave = 1.1 * (double)((steps + KV_WAVES - 1) / KV_WAVES);
+        const double bytes = (double)(workgroups < at_once ? workgroups : at_once) * (double)steps * (KV_STEP * 2.0) * a.dim / 6e6;
+        const double cost = (double)((workgroups + at_once - 1) / at_once) * (wave > bytes ? wave : bytes) + (s > 1 ? 5.0 : 0.0);
+        if (s == 1 || cost < least) best = s, least = cost;
+    }
+    return best;
+}
 constexpr int64_t BLOCK_ALONE = 1024 * 512;
 inline AttendPlan attend_plan(const AttendShape& a) {
     AttendPlan p{};
@@ -65,8 +86,8 @@ inline AttendPlan attend_plan(const AttendShape& a) {
     const int64_t most_rows = max_new * (a.heads / a.kv_heads), keys = a.seqs * a.kv_heads * max_length;
     p.rows.on = most_rows <= KV_FEW || (a.tokens != a.seqs * max_new && keys > BLOCK_ALONE);
     p.block.on = most_rows > KV_FEW;
-    auto chunks = [&](AttendPart& q, int64_t groups, int64_t target, int64_t unit, int64_t least, size_t slots) {
-        int64_t chunk = (max_length * groups / target + unit - 1) / unit * unit;
+    auto chunks = [&](AttendPart& q, int64_t keys, int64_t unit, int64_t least, size_t slots) {
+        int64_t chunk = (keys + unit - 1) / unit * unit;
         chunk = chunk < least ? least : (chunk > KV_WHOLE ? KV_WHOLE : chunk);
         const int64_t splits = (max_length + chunk - 1) / chunk;
         q.chunk = (int)chunk;
@@ -80,7 +101,13 @@ inline AttendPlan attend_plan(const AttendShape& a) {
         p.rows.tiles = (int)((r + 15) / 16);
         const int64_t groups = a.seqs * a.kv_heads * p.rows.tiles, wide = keys * p.rows.tiles / 1024;
         const int64_t least = max_length <= 768 ? 768 : wide < 256 ? 256 : wide < 1024 ? wide / 128 * 128 : 1024;
-        chunks(p.rows, groups, 4096, KV_WAVES * KV_STEP, least, (size_t)(a.seqs * a.kv_heads * r));
+        const size_t slots = (size_t)(a.seqs * a.kv_heads * r);
+        if (a.window) {
+            const int64_t s = window_splits(a, groups);
+            chunks(p.rows, (max_length + s - 1) / s, KV_STEP, KV_STEP, slots);
+        } else {
+            chunks(p.rows, max_length * groups / 4096, KV_WAVES * KV_STEP, least, slots);
+        }
     }
     if (p.block.on) {
         const int64_t rows = block_rows(a.dim);
@@ -92,7 +119,7 @@ inline AttendPlan attend_plan(const AttendShape& a) {
         p.block.tiles = (int)(blocks < 1 ? 1 : blocks);
         // one chunk, of whatever length: no row has a slot for a part
         if (groups * waves >= 1024) p.block.chunk = KV_WHOLE, p.block.splits = 1;
-        else chunks(p.block, groups * waves, 1024, KV_STEP, (16 * max_new <= max_length ? 128 : 512) * waves, (size_t)(a.tokens * a.heads));
+        else chunks(p.block, max_length * groups * waves / 1024, KV_STEP, (16 * max_new <= max_length ? 128 : 512) * waves, (size_t)(a.tokens * a.heads));
     }
     return p;
 }

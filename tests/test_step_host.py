@@ -160,7 +160,6 @@ def test_window_refusals():
     many = _Batch(SOME, SOME, SOME, 1 << 20, 3, 3, 1 << 20)
     plain = abi.library().qlora_kv_attention_workspace_bytes(by(c), by(many), 8, 1, 1 << 24)
     assert size(4096, 4, 1 << 24, many) == size(4096, 4, 1 << 20, many) < plain
-    assert size(1 << 26, 4, 1 << 24, many) == plain
 
 
 @pytest.mark.parametrize("pre,post,gate,later", [(True, None, None, True), ("w", "w", 3, True), ("w", True, "one", False), (None, "w", 6, True), ("w", None, 1, False)])
