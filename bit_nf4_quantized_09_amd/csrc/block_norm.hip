@@ -526,15 +526,17 @@ struct NormShape {
     dim3 grid() const { return dim3((uint32_t)(group() ? workers : (workers + 3) / 4)); }
     dim3 block() const { return dim3(group() ? 64 * waves : 256); }
 };
-// Workers: those that run at once.  Forward, and backward without sums, 32 waves a compute unit, but one workgroup of more
-// than 8 waves (4096 x 8192: 46 us with one a compute unit, 47 with two, 53 with four; 6000 x 256: 7.5 us with all, 13 with
-// a quarter).  With sums over tokens 8 waves, for each worker leaves sums to be joined (gradients of 6000 x 1000: 25 us
-// with 4 workers of two waves a compute unit, 29 with 8; of 4096 x 4096: 45 us with one of eight, 48 with two, 73 with eight).
-static NormShape norm_shape(int64_t M, int64_t K, bool learn) {
+// Workers: those that run at once.  `at_once` waves a compute unit, but one workgroup of more than 8 waves (forward 4096 x
+// 8192: 46 us with one a compute unit, 47 with two, 53 with four).  Forward 32 (6000 x 256: 7.5 us, 13 with a quarter of them);
+// backward, which has fewer waves at once, 16 (1001 x 2501: 12.6 us with 2 or 3 workgroups, 15.8 with 6); with sums over tokens
+// 8, for each worker leaves sums to be joined (gradients of 6000 x 1000: 25 us with 4 workers of two waves a compute unit,
+// 29 with 8; of 4096 x 4096: 45 us with one of eight, 48 with two, 73 with eight).
+constexpr int FORWARD = 32, BACKWARD = 16, WITH_SUMS = 8;
+static NormShape norm_shape(int64_t M, int64_t K, int at_once) {
     NormShape p{};
     p.chunks = K > 16384 ? 4 : K > 8192 ? 2 : 1;
     p.waves = (int)((K + 512 * p.chunks - 1) / (512 * p.chunks));
-    const int per_unit = p.waves > 8 ? 1 : (learn ? 8 : 32) / p.waves;
+    const int per_unit = p.waves > 8 ? 1 : at_once / p.waves;
     const int64_t most = 256 * (int64_t)per_unit;
     p.rows = (M + most - 1) / most;
     p.rows = p.rows < 1 ? 1 : p.rows;
@@ -571,7 +573,7 @@ static NormArgs norm_args(const BlockNorm& n, int64_t M, int64_t K, const NormSh
 
 hipError_t launch_block_norm_fwd(const BlockNorm& n, int64_t M, int64_t K, const RowsView& h, const RowsView& x,
                                  const RowsView& h_out, const RowsView& y, hipStream_t s) {
-    const NormShape p = norm_shape(M, K, false);
+    const NormShape p = norm_shape(M, K, FORWARD);
     NormArgs a = norm_args(n, M, K, p);
     a.h = h;
     a.x = x;
@@ -608,14 +610,14 @@ static NormParts norm_parts(const NormShape& p, int64_t M, int64_t K, int64_t ga
     return q;
 }
 size_t block_norm_ws_bytes(int64_t M, int64_t K, int64_t gate_rows, bool dpre, bool dpost, bool dgate) {
-    return norm_parts(norm_shape(M, K, dpre || dpost || dgate), M, K, gate_rows, dpre, dpost, dgate).bytes;
+    return norm_parts(norm_shape(M, K, WITH_SUMS), M, K, gate_rows, dpre, dpost, dgate).bytes;
 }
 
 hipError_t launch_block_norm_bwd(const BlockNorm& n, int64_t M, int64_t K, const RowsView& h, const RowsView& x,
                                  const RowsView& dy, const RowsView& dh, const RowsView& dh_out, const RowsView& dx,
                                  float* dpre, float* dpost, float* dgate, void* ws, hipStream_t s) {
     const bool learn = dpre || dpost || dgate;
-    const NormShape p = norm_shape(M, K, learn);
+    const NormShape p = norm_shape(M, K, learn ? WITH_SUMS : BACKWARD);
     NormArgs a = norm_args(n, M, K, p);
     a.h = h;
     a.x = x;

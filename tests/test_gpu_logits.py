@@ -81,6 +81,22 @@ def test_large_batches(dtype):
 def test_long_histories():
     Case(3, 50, history=20000).check()                              # counts of some hundreds
     Case(1, 40000, history=50000, each=True).check()
+    Case(2, 30001, history=2000, biases=500, grammar=True).check()
+    Case(2, 20001, history=40000, biases=70, grammar=True, each=True).check()
+    Case(2, 3000, history=5, biases=70000).check()                   # more biases than tokens
+
+
+@pytest.mark.parametrize("width", [1000, 32767, 32768, 70000])
+def test_one_token_alone(width):
+    # every count there is, beside the last entry of the biases
+    z = torch.zeros((1, 3), device="cuda")
+    history = torch.ones((1, width), dtype=torch.int32, device="cuda")
+    ids = torch.ones((1, 65535), dtype=torch.int32, device="cuda")
+    for count in (65535, 100):
+        got = nf4.shape_logits(z, history, frequency=2.0, presence=0.5, bias_ids=ids[:, :count], bias=torch.arange(count, device="cuda")[None].float())
+        assert got.tolist() == [[0.0, count - 1 - 2.0 * width - 0.5, 0.0]]
+    got = nf4.shape_logits(z - 1, history, prompts=torch.tensor([width], dtype=torch.int32, device="cuda"), repetition=3.0, frequency=2.0)
+    assert got.tolist() == [[-1.0, -3.0, -1.0]]
 
 
 def test_many_rows():
