@@ -17,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -495,6 +496,7 @@ struct Tensors {
     std::vector<qlora_tensor> v;
     const at::Tensor* first = nullptr;
     Tensors(PyObject* o, const char* name, const at::Tensor* of) {
+        if (THPVariable_Check(o)) throw BadType{std::string(name) + " must be a list of tensors"};
         keep = PySequence_Fast(o, (std::string(name) + " must be a list of tensors").c_str());
         if (!keep) throw PythonError{};
         try {
@@ -548,7 +550,9 @@ PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 3, [&]() -> PyObject* {
         const Tensors g(a[0], "grads", nullptr);
         const c10::DeviceGuard on(g.first->device());
-        const Tensors o(a[2] == Py_None ? a[0] : a[2], a[2] == Py_None ? "grads" : "out", g.first);
+        std::optional<Tensors> other;
+        if (a[2] != Py_None) other.emplace(a[2], "out", g.first);
+        const Tensors& o = other ? *other : g;
         if (o.v.size() != g.v.size()) bad("out must hold as many tensors as grads");
         o.each([](const at::Tensor& t) { want_unrecorded(t, "a clipped tensor"); });
         const double max_norm = number(a[1]);

@@ -417,8 +417,9 @@ void k_attend_rows(AttendArgs a) {
             // this wave's steps: keys lo + 32 (wave + 4 i) ..
             const int all = (hi - lo + KV_STEP - 1) / KV_STEP;
             const int steps = (all - wave + KV_WAVES - 1) / KV_WAVES;
-            auto place = [&](int i) { return lo + KV_STEP * (wave + KV_WAVES * i); };
-            auto first_key = [&](int i) { return place(i) + sight.past(place(i)); };
+            // (without sign: the page of a step past the last one is asked for too)
+            auto place = [&](int i) { return (int)((uint32_t)lo + KV_STEP * (uint32_t)(wave + KV_WAVES * i)); };
+            auto first_key = [&](int i) { return (int)((uint32_t)place(i) + (uint32_t)sight.past(place(i))); };
             struct Pages {
                 int p[2];
             };
@@ -426,7 +427,7 @@ void k_attend_rows(AttendArgs a) {
                 Pages g;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
+                    g.p[t] = page_entry(a.b, seq, (int)((uint32_t)(first_key(i) + 16 * t) >> a.c.page_log2));
                     if (sight.none(first_key(i) + 16 * t)) g.p[t] = -1;
                 }
                 return g;
@@ -637,8 +638,8 @@ void k_attend_block(AttendArgs a) {
         }
         for_chunks(keys, a.chunk, split, a.splits, [&](int lo, int hi) {
             const int steps = ((hi - lo + KV_STEP - 1) / KV_STEP - wave + W - 1) / W;     // of this wave: every W-th
-            auto place = [&](int i) { return lo + KV_STEP * (W * i + wave); };
-            auto first_key = [&](int i) { return place(i) + sight.past(place(i)); };
+            auto place = [&](int i) { return (int)((uint32_t)lo + KV_STEP * (uint32_t)(W * i + wave)); };
+            auto first_key = [&](int i) { return (int)((uint32_t)place(i) + (uint32_t)sight.past(place(i))); };
             struct Pages {
                 int p[2];
             };
@@ -646,7 +647,7 @@ void k_attend_block(AttendArgs a) {
                 Pages g;
 #pragma unroll
                 for (int t = 0; t < (WIDE ? 1 : 2); ++t) {
-                    g.p[t] = page_entry(a.b, seq, (first_key(i) + 16 * t) >> a.c.page_log2);
+                    g.p[t] = page_entry(a.b, seq, (int)((uint32_t)(first_key(i) + 16 * t) >> a.c.page_log2));
                     if (!WIDE && sight.none(first_key(i) + 16 * t)) g.p[t] = -1;      // (a wide page's step has a key that is seen)
                 }
                 return g;

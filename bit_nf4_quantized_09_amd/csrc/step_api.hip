@@ -54,7 +54,7 @@ nf4_status check_norm(const qlora_block_norm* n, int64_t M, int64_t K, nf4_dtype
     if (!known(stream_dtype) || !known(n->dtype)) return fail(NF4_ERR_ARG, "types must be NF4_F32 or NF4_BF16");
     if (M < 0 || M > (int64_t)0x7FFFFFFF) return fail(NF4_ERR_UNSUPPORTED, "M must be 0 .. 2^31 - 1");
     if (K < 1 || K > nf4::NORM_MAX_WIDTH) return fail(NF4_ERR_UNSUPPORTED, "K must be 1 .. 32768");
-    if (!(n->eps > 0.0f) || !isfinite(n->eps)) return fail(NF4_ERR_ARG, "eps must be positive and finite");
+    if (!(n->eps >= 0x1p-126f) || !isfinite(n->eps)) return fail(NF4_ERR_ARG, "eps must be at least 2^-126 and finite");
     if (!isfinite(n->scale)) return fail(NF4_ERR_ARG, "scale must be finite");
     if (n->pre && !n->norm_pre) return fail(NF4_ERR_ARG, "pre is given without a norm before the next block");
     if (n->post && !n->norm_post) return fail(NF4_ERR_ARG, "post is given without a norm after the block");

@@ -32,7 +32,7 @@ typedef struct qlora_rows {
  *   gate       device [gate_rows][K], or NULL for ones: row i belongs to the i-th M / gate_rows tokens (1: one gate for
  *              all; M: each token's own); gate_rows divides M
  *   dtype      of pre, post and gate
- *   scale      finite;  eps  positive and finite */
+ *   scale      finite;  eps  2^-126 at least, and finite */
 typedef struct qlora_block_norm {
     const void* pre;
     const void* post;
@@ -150,8 +150,8 @@ typedef struct qlora_logit_rules {
 } qlora_logit_rules;
 
 /* logits and out: fp32 or bf16 [rows][V], rounded once; out may be the logits themselves (same pointer and stride).
- * 0 <= rows < 2^24, 1 <= V < 2^28; history_width and biases below 2^31.  repetition must be positive where it is given
- * as a number. */
+ * 0 <= rows < 2^24, 1 <= V < 2^28; history_width and biases up to 2^31 - 2.  A repetition must be positive; one given as a
+ * number is checked. */
 nf4_status qlora_logits_shape(const qlora_logit_rules* rules, int64_t rows, int64_t V, nf4_dtype dtype,
                               const qlora_rows* logits, const qlora_rows* out, void* stream);
 

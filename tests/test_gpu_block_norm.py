@@ -170,7 +170,7 @@ def test_in_place():
 def test_squares_past_fp32(K):
     # values whose squares overflow, or vanish: the norm is that of the scaled row
     c = Case(4, K, F32, F32, gate=None, scale=1.0, post="weight")
-    c.h = c.h * torch.tensor([1e30, 1e-30, 3e18, 1.0], device="cuda")[:, None]
+    c.h = c.h * torch.tensor([1e37, 1e-30, 3e18, 1.0], device="cuda")[:, None]
     c.x = (c.x.float() * torch.tensor([1.0, 1e-25, 1e25, 3e30], device="cuda")[:, None]).to(BF16)
     c.check_forward()
     c.h = c.h * torch.tensor([1.0, 1.0, 1e5, 1.0], device="cuda")[:, None]

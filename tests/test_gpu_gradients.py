@@ -121,9 +121,12 @@ def test_versions_and_refusals():
     for bad in ([], [g.cpu()], [g.half()], [g.view(8, 8).t()], [g, g.cpu()], [g.long()]):
         with pytest.raises(ValueError):
             nf4.grad_norm(bad)
-    for bad in ([None], ["g"], 3, g[0]):
+    for bad in ([None], ["g"], 3, g[0], g):
         with pytest.raises(TypeError):
             nf4.grad_norm(bad)
+    h = g.clone()
+    nf4.clip_grads(iter([h]), 1e-3)                                    # what can be walked along once serves
+    assert abs(float(h.norm()) - 1e-3) <= 1e-8
     for out in ([], [g[:5]], [g.bfloat16()], [g, g]):
         with pytest.raises((ValueError, nf4.NF4Error)):
             nf4.clip_grads([g], 1.0, out=out)

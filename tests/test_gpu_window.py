@@ -7,7 +7,7 @@ import torch
 
 import bit_nf4_quantized_09_amd as nf4
 import step_ref as ref
-from test_gpu_kv import Case, f64
+from test_gpu_kv import Case, dev, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -107,6 +107,21 @@ def test_long_sequences():
     for window, sinks in ((5000, 4), (30000, 100), (7, 0)):
         check(c, window, sinks, max_new=2, max_length=40001)
     check(c, 5000, 4)
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [3, 70]])
+def test_positions_near_the_end_of_the_table(counts):
+    # sequences that end 2^31 - 256 positions on, over a table that holds them: the answer of the same keys early on
+    page, pages, window, sinks = 256, (1 << 31) // 256 - 1, 300, 4
+    c = Case([800, 800], counts, page=page, kv=2, heads=8, dim=64, seed=5)
+    want = check(c, window, sinks, max_new=max(counts), max_length=1024)
+    far = (pages - 4) * page                                         # the last four pages: positions 0 .. 1023 moved by `far`
+    table = torch.full((2, pages), -1, dtype=torch.int32, device="cuda")
+    table[:, 0] = dev(c.table)[:, 0]
+    table[:, pages - 4:pages - 4 + c.table.shape[1]] = dev(c.table)
+    for longest in (1024, 2 ** 31 - 1):
+        got = nf4.kv_attention(c.cache, c.q, dev(c.starts), dev(c.lengths + far), table, max_new=max(counts), max_length=longest, window=window, sinks=sinks)
+        assert torch.all((got.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -10 * 8)
 
 
 def test_rows_that_see_nothing():

@@ -61,7 +61,7 @@ def test_block_norm_refusals():
     assert fwd(M=0) == OK
     assert fwd(M=-1) == UNSUPPORTED and fwd(M=1 << 31) == UNSUPPORTED and fwd(K=0) == UNSUPPORTED and fwd(K=32769) == UNSUPPORTED
     assert abi.library().qlora_block_norm_fwd(None, 4, 64, BF16, by(rows()), None, None, by(rows(MORE)), None) == ARG
-    for n in (norm(eps=0.0), norm(eps=float("inf")), norm(scale=float("nan")), norm(dtype=5), norm(pre=SOME, norm_pre=0), norm(post=SOME),
+    for n in (norm(eps=0.0), norm(eps=1e-39), norm(eps=float("inf")), norm(scale=float("nan")), norm(dtype=5), norm(pre=SOME, norm_pre=0), norm(post=SOME),
               norm(pre=4097), norm(gate=SOME, gate_rows=0), norm(gate=SOME, gate_rows=3), norm(gate=SOME, gate_rows=8)):
         assert fwd(n) == ARG and bwd(n) == ARG, why()
     assert fwd(dtype=9) == ARG and bwd(dtype=9) == ARG
