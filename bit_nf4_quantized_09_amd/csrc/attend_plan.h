@@ -61,9 +61,9 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // A window makes the sequences equally long, so that workgroups come in rounds: window_splits takes the chunks, all of one
 // size, for which an estimate is least: rounds of three workgroups on a compute unit (one with heads of 256), each as
 // long as a wave's steps take one after the other (1.1 us) or the round's bytes at 6 TB/s, and 5 us for a join.  24
-// sequences, window of 4096, 64 heads on 8: 39 us with one round of four chunks, 48 with one and a half of six; window of
-// 1024: 14 us with whole windows, 20 to 22 with two chunks.  (Eight waves to a workgroup instead of chunks: no faster, one
-// sequence, window of 1000: 13.3 us, 11.8 with chunks.)
+// sequences, window of 4096, 64 heads on 8: 39 us with whole windows, 42 with a round of four chunks, 48 with one and a half of
+// six; window of 1024: 14 us whole, 20 to 22 with two chunks; of 8192: 71 with four, 80 with nine.  (Eight waves to a
+// workgroup instead of chunks: no faster, one sequence, window of 1000: 13.3 us, 11.8 with chunks.)
 inline int64_t window_splits(const AttendShape& a, int64_t groups) {
     const int64_t most = a.max_length / (KV_WAVES * KV_STEP) < 64 ? a.max_length / (KV_WAVES * KV_STEP) : 64;
     const int64_t at_once = 256 * (a.dim == 256 ? 1 : 3);

@@ -31,6 +31,10 @@
 // behind up to 1100 cached, 32 heads of 128 (74 GFLOP): 137 us alone, 127 a call among others, whose blocks fill
 // that third (540 and 585 TFLOP/s); 1.5 of 2 waves resident, vector instructions issued 39% of the time, matrix
 // cores busy 22%.
+// With a window a token sees the last `window` keys and the first `sinks`: the steps of both follow each other, from whole
+// steps on, as if nothing lay between (Sight), and what a row does not see of them is hidden like what comes after it.
+// 24 sequences behind 40000 positions, window of 4096, 64 heads on 8 (202 MB): 39 us, 5.2 TB/s; 3 prompts of up to 1500
+// tokens, window of 1024, 32 heads on 8 (62 GFLOP): 112 us.
 #include "bufio.h"
 #include "paged.h"
 #include "attend_plan.h"

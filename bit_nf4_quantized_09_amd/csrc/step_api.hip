@@ -88,30 +88,36 @@ nf4_status gradients_of(const qlora_tensor* g, int64_t count, const char* name, 
 }
 
 // Whether a tensor that is written shares memory with another one, read or written (in[i] and out[i] may be the same).
+// Lists that ascend in memory, as most do, are not sorted.
 bool written_overlap(const std::vector<Gradient>& in, const std::vector<Gradient>& out) {
     struct Range {
         uintptr_t from, to;
-        bool written;
     };
-    std::vector<Range> all;
-    all.reserve(in.size() + out.size());
-    auto add = [&](const Gradient& g, bool written) {
+    std::vector<Range> written, read;
+    written.reserve(out.size());
+    auto add = [](std::vector<Range>& v, const Gradient& g) {
         const uintptr_t at = (uintptr_t)g.data;
-        if (g.n > 0) all.push_back(Range{at, at + (size_t)g.n * (g.bf16 ? 2 : 4), written});
+        if (g.n > 0) v.push_back(Range{at, at + (size_t)g.n * (g.bf16 ? 2 : 4)});
     };
     for (size_t i = 0; i < in.size(); ++i) {
-        add(out[i], true);
-        if (in[i].data != out[i].data) add(in[i], false);
+        add(written, out[i]);
+        if (in[i].data != out[i].data) add(read, in[i]);
     }
     auto before = [](const Range& a, const Range& b) { return a.from < b.from; };
-    if (!std::is_sorted(all.begin(), all.end(), before)) std::sort(all.begin(), all.end(), before);
-    uintptr_t any = 0, written = 0;       // the ends so far
-    for (const Range& r : all) {
-        if (r.from < (r.written ? any : written)) return true;
-        any = std::max(any, r.to);
-        if (r.written) written = std::max(written, r.to);
+    for (std::vector<Range>* v : {&written, &read})
+        if (!std::is_sorted(v->begin(), v->end(), before)) std::sort(v->begin(), v->end(), before);
+    uintptr_t any = 0, end = 0;           // where all so far end, and those that are written
+    size_t r = 0;
+    for (const Range& w : written) {
+        for (; r < read.size() && read[r].from <= w.from; ++r) {
+            if (read[r].from < end) return true;
+            any = std::max(any, read[r].to);
+        }
+        if (w.from < any) return true;
+        any = std::max(any, w.to);
+        end = std::max(end, w.to);
     }
-    return false;
+    return r < read.size() && read[r].from < end;
 }
 
 }  // namespace
