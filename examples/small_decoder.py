@@ -144,7 +144,7 @@ def train_loss(model, tokens, targets):
     return _Loss.apply(model.hidden(tokens, attend), model.head, targets)
 
 
-def train(model, tokens, targets, steps=20, lr=3e-3, max_norm=10.0, say=lambda *a: None):
+def train(model, tokens, targets, steps=20, lr=3e-3, max_norm=1.0, say=lambda *a: None):
     """Adapter steps on one sequence, the gradients clipped to a norm of max_norm; returns the losses."""
     linears = model.linears()
     opt = nf4.PagedAdamW([p for m in linears for p in (m.A, m.B)], lr=lr)

@@ -63,8 +63,8 @@ nf4_status qlora_block_norm_fwd(const qlora_block_norm* norm, int64_t M, int64_t
  *   dh_out  out: the gradient of the stream before the block, of the stream's type; may be dh itself
  *   dx      out, with x: bf16, the gradient of the block's output
  *   dpre, dpost, dgate   out: fp32 [K], [K], [gate_rows][K], or NULL: sums over the tokens in a fixed order
- *   workspace  qlora_block_norm_bwd_workspace_bytes of the same sizes, 256-byte aligned: fp32 sums of up to 4096
- *              workers, each as long as the outputs asked for (two gate rows each) */
+ *   workspace  qlora_block_norm_bwd_workspace_bytes of the same sizes, 256-byte aligned: fp32 sums of up to 2048
+ *              workers, each as long as the outputs asked for (of several gates two rows each) */
 size_t qlora_block_norm_bwd_workspace_bytes(int64_t M, int64_t K, int64_t gate_rows, int32_t need_dpre, int32_t need_dpost,
                                             int32_t need_dgate);
 nf4_status qlora_block_norm_bwd(const qlora_block_norm* norm, int64_t M, int64_t K, nf4_dtype stream_dtype,

@@ -193,6 +193,29 @@ def test_rows_of_nothing_and_of_the_non_finite():
     assert torch.equal(back["dh"][0], clean[1]["dh"][0]) and torch.equal(back["dx"][2], clean[1]["dx"][2])
 
 
+def test_offsets_past_32_bits():
+    # rows beyond 2^32 bytes of every operand, against the same rows alone
+    M, K = 140000, 16384
+    g = torch.Generator(device="cuda").manual_seed(1)
+    h = torch.empty((M, K), dtype=BF16, device="cuda")
+    for a in range(0, M, 10000):
+        h[a:a + 10000] = torch.randn((10000, K), generator=g, device="cuda")
+    gate = torch.rand((2, K), generator=g, device="cuda").to(BF16)
+    s, y = nf4.block_norm_fwd(h, h, gate=gate)
+    dh, dx, _, _, dgate = nf4.block_norm_bwd(s, y, None, h, gate=gate)
+    for row in (0, M // 2 - 1, M // 2, M - 1):
+        one = slice(row, row + 1)
+        own = gate[row // (M // 2)]
+        t, z = nf4.block_norm_fwd(h[one], h[one], gate=own)
+        assert torch.equal(s[one], t) and torch.equal(y[one], z)
+        back = nf4.block_norm_bwd(t, z, None, h[one], gate=own)
+        assert torch.equal(dh[one], back[0]) and torch.equal(dx[one], back[1])
+    # each half's gate has the sum of its own tokens: the two of one kind of rows, as large within its spread
+    assert torch.isfinite(dgate).all() and dgate.shape == (2, K)
+    part = sum((h[a:a + 10000].float() * dh[a:a + 10000].float()).double().sum(0) for a in range(0, M // 2, 10000))
+    assert float((dgate[0].double() - part).norm()) <= 0.02 * float(part.norm())
+
+
 def test_no_tokens():
     c = Case(0, 64, gate=1)
     new, y = c.forward()

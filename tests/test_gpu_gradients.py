@@ -63,6 +63,20 @@ def test_shapes_and_any_alignment():
     assert torch.equal(buf[~inside], keep[~inside]) and torch.equal(half[~of], kept[~of])      # what lies between is left
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_tensor_of_more_than_2_to_the_30_values(dtype):
+    n = (1 << 30) + 12345
+    big = torch.ones(n, dtype=dtype, device="cuda")
+    big[-1], big[1 << 30] = 3.0, 2.0
+    other = torch.full((777,), 2.0, device="cuda")
+    norm = math.sqrt(n - 2 + 9 + 4 + 4 * 777)
+    got = nf4.clip_grads([other, big], norm / 2)
+    assert abs(float(got) - norm) <= 2.0 ** -23 * norm
+    assert float(other.min()) == float(other.max()) and abs(float(other[0]) - 1.0) <= 2.0 ** -22
+    assert float(big[0]) == 0.5 and float(big[-1]) == 1.5 and float(big[1 << 30]) == 1.0 and float(big[(1 << 30) - 1]) == 0.5
+    assert bool((big[:-1] >= 0.4999).all())
+
+
 def test_many_tensors_and_repeats():
     gs = tensors([1 + 37 * i % 5000 for i in range(1300)], (F32, BF16), seed=3)
     a = nf4.grad_norm(gs)

@@ -99,6 +99,20 @@ def test_one_token_alone(width):
     assert got.tolist() == [[-1.0, -3.0, -1.0]]
 
 
+def test_offsets_past_32_bits():
+    R, V = 18000, 128256
+    z = torch.empty((R, V), dtype=BF16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for a in range(0, R, 2000):
+        z[a:a + 2000] = torch.randn((2000, V), generator=g, device="cuda")
+    history = torch.randint(0, V, (R, 20), generator=g, dtype=torch.int32, device="cuda")
+    got = nf4.shape_logits(z, history, presence=1.0, repetition=1.5)
+    for row in (0, R // 2, R - 1):
+        one = slice(row, row + 1)
+        assert torch.equal(got[one], nf4.shape_logits(z[one], history[one], presence=1.0, repetition=1.5))
+        assert int((got[one] != z[one]).sum()) >= 15
+
+
 def test_many_rows():
     z = torch.randn((70000, 3), device="cuda")
     history = torch.randint(0, 3, (70000, 2), dtype=torch.int32, device="cuda")

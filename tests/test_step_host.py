@@ -93,7 +93,7 @@ def test_block_norm_workspace():
         for K in (1, 64, 1000, 8192, 32768):
             assert bytes_of(M, K, 1, 0, 0, 0) == 0 and bytes_of(M, K, M, 0, 0, 1) == 0
             one = bytes_of(M, K, 1, 1, 0, 0)
-            assert one % 256 == 0 and one <= 4096 * K * 4 + 256 and bytes_of(M, K, 1, 1, 1, 1) <= 4 * one + 256
+            assert one % 256 == 0 and one <= 2048 * K * 4 + 256 and bytes_of(M, K, 1, 1, 1, 1) <= 4 * one + 256
             assert one <= bytes_of(M, K, 1, 1, 1, 0) <= bytes_of(M, K, 1, 1, 1, 1)
     assert bytes_of(-1, 64, 1, 1, 1, 1) == bytes_of(4, 0, 1, 1, 1, 1) == bytes_of(4, 40000, 1, 1, 1, 1) == 0
 
