@@ -582,7 +582,7 @@ class PagedAdamW:
         """One AdamW step for every parameter; grads are fp32 GPU tensors (dA, dB).  With max_norm the
         gradients count times min(1, max_norm / their global norm), without being written, and the
         norm is returned (a fp32 number on the GPU)."""
-        grads = list(grads)
+        grads = [g.contiguous().reshape(-1) for g in grads]
         if len(grads) != len(self.params):
             raise ValueError("one gradient per parameter")
         norm = factor = None
@@ -590,8 +590,7 @@ class PagedAdamW:
             norm, factor = _norm_and_factor(grads, float(max_norm))
         self.t += 1
         b1, b2 = self.betas
-        for q, g, st in zip(self.params, grads, self.state):
-            gq = g.reshape(-1)
+        for q, gq, st in zip(self.params, grads, self.state):
             if st["host"]:
                 if self._stage is None:
                     self._stage = _workspace(self._stage_bytes, q.device)

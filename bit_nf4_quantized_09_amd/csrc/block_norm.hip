@@ -17,8 +17,8 @@
 // of 512, else a workgroup of as many waves as it takes.  Workers (a wave or a workgroup) walk along a stretch of
 // rows: the next row's operands are loaded while one is computed, the weights stay in registers, and the sums over
 // tokens of dpre, dpost and dgate are kept there; the workers' sums are added up in a second launch, in a fixed
-// order.  4096 tokens of width 8192, all bf16: forward 46 us (268 MB, 5.8 TB/s), backward with all sums 84 us
-// (403 MB, 4.8 TB/s) and 5 for the join; 16 tokens of width 4096 3.5 us.
+// order.  4096 tokens of width 8192, all bf16: forward 44 us (268 MB, 6.1 TB/s), backward with all sums 77 us
+// (403 MB, 5.2 TB/s) and 5 for the join; 16 tokens of width 4096 3.5 us.
 #include "rows.h"
 #include "step.h"
 

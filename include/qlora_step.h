@@ -121,7 +121,7 @@ nf4_status qlora_kv_attention_window(const qlora_kv_cache* cache, const qlora_kv
  *   z - (frequency * count + presence)             where it is `count` > 0 times among those after the prompt
  *   z + bias                                       of the last entry of bias_ids that is v
  *   -inf                                           where bit v % 32 of word v / 32 of `allowed` is 0
- * Fields of NULL leave their step out.  What is [rows] or has a row stride may be one row for all (stride 0).
+ * Fields of NULL leave their step out.  What has a stride may be one row for all (a stride of 0).
  *   history       int32 [rows][history_width]: token i of a row counts for i < lengths[r] (NULL: all; held to
  *                 0 .. history_width), and as the prompt's for i < prompts[r] (NULL: none); tokens outside 0 .. V-1 are
  *                 passed over

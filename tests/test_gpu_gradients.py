@@ -194,3 +194,15 @@ def test_clipped_optimizer(budget):
         torch.cuda.synchronize()
         assert all(torch.equal(u, v) for u, v in zip(a, b))
     assert np.isfinite(float(norm))
+
+
+def test_clipped_optimizer_takes_the_gradients_that_step_takes():
+    # of any strides, from what can be walked along once
+    rand = lambda s, *shape: torch.randn(shape, generator=torch.Generator().manual_seed(s)).cuda()  # noqa: E731
+    dense = [rand(1, 40, 24), rand(2, 24, 40)]
+    strided = [dense[0].t().contiguous().t(), torch.stack([dense[1], dense[1]], -1)[..., 0]]
+    assert not any(g.is_contiguous() for g in strided)
+    a, b = [[rand(3, 40, 24).bfloat16(), rand(4, 24, 40).bfloat16()] for _ in range(2)]
+    one, two = nf4.PagedAdamW(a, lr=1e-2), nf4.PagedAdamW(b, lr=1e-2)
+    assert torch.equal(one.step(iter(strided), max_norm=0.3), two.step(dense, max_norm=0.3))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
