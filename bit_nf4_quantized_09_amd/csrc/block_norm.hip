@@ -17,7 +17,8 @@
 // of 512, else a workgroup of as many waves as it takes.  Workers (a wave or a workgroup) walk along a stretch of
 // rows: the next row's operands are loaded while one is computed, the weights stay in registers, and the sums over
 // tokens of dpre, dpost and dgate are kept there; the workers' sums are added up in a second launch, in a fixed
-// order.  4096 tokens of width 8192, all bf16: forward 44 us (268 MB, 6.1 TB/s), backward with all sums 77 us
+// order.  (Past a width of 8192 the sums lie in LDS, and the rows on their way and the weights do not stay.)  4096 tokens of
+// width 8192, all bf16: forward 44 us (268 MB, 6.1 TB/s), backward with all sums 77 us
 // (403 MB, 5.2 TB/s) and 5 for the join; 16 tokens of width 4096 3.5 us.
 #include "rows.h"
 #include "step.h"
@@ -47,13 +48,14 @@ struct RowOperands {
     Eight<S> dh[BACK ? NC : 1];
     Eight<uint16_t> x[NC];
     Eight<uint16_t> dy[BACK ? NC : 1];
-    Eight<W> gate[NC];
+    Eight<W> gate[BACK && NC > 1 ? 1 : NC];       // (else read where it is needed)
 };
 
 // The rows of a worker, and the thread's columns of them.
 template <typename S, typename W, bool GROUP, int NC, bool STREAM, bool BACK>
 struct RowOf {
     typedef RowOperands<S, W, NC, BACK> Operands;
+    static constexpr bool GATE = !BACK || NC == 1;        // the gate is among a row's operands
     const NormArgs& a;
     uint32_t t, threads;                  // thread among those of a row
     uint32_t worker, first, end;          // rows first .. end - 1
@@ -88,7 +90,9 @@ struct RowOf {
             const uint32_t c = column(i);
             if (!BACK || a.norm_pre) r.h[i] = start<STREAM>((const S*)a.h.data + row * a.h.stride, c);
             if (a.x.data) r.x[i] = start<STREAM>((const uint16_t*)a.x.data + row * a.x.stride, c);
-            if (a.gate) r.gate[i] = start((const W*)a.gate + (uint64_t)gate * a.K, c);
+            if constexpr (GATE) {
+                if (a.gate) r.gate[i] = start((const W*)a.gate + (uint64_t)gate * a.K, c);
+            }
             if constexpr (BACK) {
                 if (a.norm_pre) r.dy[i] = start<STREAM>((const uint16_t*)a.dy.data + row * a.dy.stride, c);
                 if (a.dh.data) r.dh[i] = start<STREAM>((const S*)a.dh.data + row * a.dh.stride, c);
@@ -106,7 +110,7 @@ struct RowOf {
         for (int i = 0; i < NC; ++i) {
             r.h[i] = {};
             r.x[i] = {};
-            r.gate[i] = pack_eight<W>(one);
+            if constexpr (GATE) r.gate[i] = pack_eight<W>(one);
             if constexpr (BACK) {
                 r.dy[i] = {};
                 r.dh[i] = {};
@@ -120,7 +124,9 @@ struct RowOf {
             const uint32_t c = column(i);
             if (!BACK || a.norm_pre) finish(r.h[i], c);
             if (a.x.data) finish(r.x[i], c);
-            if (a.gate) finish(r.gate[i], c);
+            if constexpr (GATE) {
+                if (a.gate) finish(r.gate[i], c);
+            }
             if constexpr (BACK) {
                 if (a.norm_pre) finish(r.dy[i], c);
                 if (a.dh.data) finish(r.dh[i], c);
@@ -156,6 +162,36 @@ struct Weights {
     }
 };
 
+// Sums over tokens of the thread's columns: in registers, or, of several vectors, in LDS (16 bytes a thread side by side; each
+// thread reads and writes its own places, so that no barrier is needed).  128 KB are both sums of two vectors a thread
+// (gradients of 2048 x 16384, bf16: 114 us, 322 with sums and rows on their way spilled), or one of four (1024 x 32768: 262
+// and 757; the other is spilled).
+template <int NC, bool LDS>
+struct TokenSums {
+    float v[NC][8] = {};
+    __device__ __forceinline__ explicit TokenSums(float4*) {}
+    template <typename F>
+    __device__ __forceinline__ void each(int i, F&& f) {
+        f(v[i]);
+    }
+};
+template <int NC>
+struct TokenSums<NC, true> {
+    float4* own;
+    __device__ __forceinline__ explicit TokenSums(float4* places) : own(places + threadIdx.x) {
+#pragma unroll
+        for (int i = 0; i < 2 * NC; ++i) own[i * 1024] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(int i, F&& f) {
+        const float4 a = own[2 * i * 1024], b = own[(2 * i + 1) * 1024];
+        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        f(v);
+        own[2 * i * 1024] = make_float4(v[0], v[1], v[2], v[3]);
+        own[(2 * i + 1) * 1024] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+
 // GROUP: a row is shared by the waves of a workgroup, else each of four waves has rows of its own.  STREAM: nontemporal
 // loads of what is read once.
 template <typename S, typename W, bool GROUP, int NC, bool STREAM>
@@ -171,9 +207,13 @@ void k_block_norm_fwd(NormArgs a) {
     typedef RowOf<S, W, GROUP, NC, STREAM, false> Of;
     Of of(a);
     if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
+    // (the next row on its way: up to two vectors a thread there are registers for it; 1024 x 32768 with four: 74 us, 122 with)
+    constexpr bool AHEAD = NC <= 2;
     typename Of::Operands next, now;
-    of.neutral(next);
-    of.load(next, of.first);
+    if constexpr (AHEAD) {
+        of.neutral(next);
+        of.load(next, of.first);
+    }
     const Weights<Of, W, NC> pre(of, a.pre), post(of, a.post);
     // 1 / the root of the mean square of a row
     auto factor = [&](const float (&v)[NC][8]) {
@@ -191,8 +231,13 @@ void k_block_norm_fwd(NormArgs a) {
         return __frsqrt_rn(squares(NORM_SHRINK) * a.per) * NORM_SHRINK;         // (infinities and NaN come here too)
     };
     for (uint32_t row = of.first; row < of.end; ++row) {
-        now = next;
-        if (row + 1 < of.end) of.load(next, row + 1);
+        if constexpr (AHEAD) {
+            now = next;
+            if (row + 1 < of.end) of.load(next, row + 1);
+        } else {
+            of.neutral(now);
+            of.load(now, row);
+        }
         of.settle_all(now);
         float h[NC][8];
 #pragma unroll
@@ -244,6 +289,7 @@ template <typename S, typename W, int THREADS, bool GROUP, int NC, bool STREAM, 
 __global__ __launch_bounds__(THREADS)
 void k_block_norm_bwd(NormArgs a) {
     __shared__ float4 shared[2 * 3 * 4];
+    __shared__ float4 places[LEARN && NC > 1 ? 8 * 1024 : 1];
     int turn = 0;
     const int waves = blockDim.x >> 6;
     if constexpr (GROUP) {
@@ -252,18 +298,24 @@ void k_block_norm_bwd(NormArgs a) {
     }
     typedef RowOf<S, W, GROUP, NC, STREAM, true> Of;
     Of of(a);
+    // The next row's operands are loaded while one is computed, but for several vectors a thread, whose registers the rows on
+    // their way would spill (gradient of 2048 x 16384, bf16: 91 us, 105 with them; fp32 129 and 178).
+    constexpr bool AHEAD = NC == 1;
     typename Of::Operands next, now;
     if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
-    of.neutral(next);
-    of.load(next, of.first);
+    if constexpr (AHEAD) {
+        of.neutral(next);
+        of.load(next, of.first);
+    }
     const Weights<Of, W, NC> pre(of, a.pre), post(of, a.post);
-    float spre[NC][8] = {}, sover[NC][8] = {};
+    TokenSums<LEARN ? NC : 1, LEARN && NC != 1> spre(places);
+    TokenSums<LEARN ? NC : 1, LEARN && NC == 2> sover(places + (LEARN && NC == 2 ? 4 * 1024 : 0));
     constexpr bool OWN = LEARN == 2;
     const bool one_gate = a.gate && a.gate_span == a.M;
     bool posted = false;                          // the worker's sum of dpost is partly in memory
-    auto put = [&](float* to, const float (&v)[NC][8]) {
+    auto put = [&](float* to, auto& sums) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) store_eight(to, of.column(i), a.K, pack_eight<float>(v[i]));
+        for (int i = 0; i < NC; ++i) sums.each(i, [&](float (&v)[8]) { store_eight(to, of.column(i), a.K, pack_eight<float>(v)); });
     };
     // one of the row sums in turn (the shared numbers are laid out for three)
     auto sum = [&](float v) {
@@ -272,25 +324,48 @@ void k_block_norm_bwd(NormArgs a) {
         return q[0];
     };
     uint32_t gate = of.first / a.gate_span, gate_first = gate * a.gate_span;        // of the row computed
+    auto gate_of = [&](int i, float (&v)[8]) {
+        if constexpr (Of::GATE) unpack_eight<W>(now.gate[i], v);
+        else unpack_eight<W>(of.weight(a.gate ? (const W*)a.gate + (uint64_t)gate * a.K : nullptr, i), v);
+    };
+    // (the block's output stays as it was read where a thread has several vectors of it)
+    constexpr bool KEPT = NC == 1;
+    float kept[KEPT ? NC : 1][8];
+    auto block = [&](int i, float factor, float (&v)[8]) {
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = kept[i][j] * factor;
+        } else {
+            unpack_eight<uint16_t>(now.x[i], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= factor;
+        }
+    };
     for (uint32_t row = of.first; row < of.end; ++row) {
-        now = next;
-        if (row + 1 < of.end) of.load(next, row + 1);
+        if constexpr (AHEAD) {
+            now = next;
+            if (row + 1 < of.end) of.load(next, row + 1);
+        } else {
+            of.neutral(now);
+            of.load(now, row);
+        }
         of.settle_all(now);
-        float d[NC][8], x[NC][8];
+        float d[NC][8];
         // ---- through the norm before the next block (without one, h' and dy are zero) ----
         float q[3] = {0.0f, 0.0f, 0.0f};          // squares of h', t h', squares of x
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            float h[8], t[8], w[8];
+            float h[8], t[8], w[8], x[8];
             unpack_eight<S>(now.h[i], h);
             unpack_eight<uint16_t>(now.dy[i], t);
             pre.get(i, w);
-            unpack_eight<uint16_t>(now.x[i], x[i]);
+            unpack_eight<uint16_t>(now.x[i], x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 q[0] = __fmaf_rn(h[j], h[j], q[0]);
                 q[1] = __fmaf_rn(t[j] * w[j], h[j], q[1]);
-                q[2] = __fmaf_rn(x[i][j], x[i][j], q[2]);
+                q[2] = __fmaf_rn(x[j], x[j], q[2]);
+                if constexpr (KEPT) kept[i][j] = x[j];
             }
         }
         row_sums<GROUP>(q, shared, turn, waves);
@@ -331,10 +406,14 @@ void k_block_norm_bwd(NormArgs a) {
             pre.get(i, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float n = h[j] * f;
-                if (LEARN) spre[i][j] = __fmaf_rn(t[j], n, spre[i][j]);
-                d[i][j] = __fmaf_rn(__fmaf_rn(t[j], w[j], -n * mean), f, d[i][j]);
+                h[j] *= f;
+                d[i][j] = __fmaf_rn(__fmaf_rn(t[j], w[j], -h[j] * mean), f, d[i][j]);
             }
+            if constexpr (LEARN != 0)
+                spre.each(i, [&](float (&s)[8]) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[j] = __fmaf_rn(t[j], h[j], s[j]);
+                });
             store_eight((S*)a.h_out.data + row * a.h_out.stride, of.column(i), a.K, pack_eight<S>(d[i]));
         }
         // ---- through the gate and the norm after the block ----
@@ -346,48 +425,63 @@ void k_block_norm_bwd(NormArgs a) {
                 } else {
                     float v = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i)
+                    for (int i = 0; i < NC; ++i) {
+                        float x[8];
+                        block(i, NORM_SHRINK, x);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v = __fmaf_rn(x[i][j] * NORM_SHRINK, x[i][j] * NORM_SHRINK, v);
+                        for (int j = 0; j < 8; ++j) v = __fmaf_rn(x[j], x[j], v);
+                    }
                     g = __frsqrt_rn(sum(v) * a.per) * NORM_SHRINK;
                 }
             }
             if constexpr (OWN) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    float w[8], e[8];
-                    unpack_eight<W>(now.gate[i], e);
+                    float w[8], e[8], x[8];
+                    gate_of(i, e);
                     post.get(i, w);
+                    block(i, g, x);
+                    sover.each(i, [&](float (&s)[8]) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float v = a.scale * d[i][j] * (x[i][j] * g);
-                        sover[i][j] = __fmaf_rn(v, e[j], sover[i][j]);
-                        w[j] *= v;
-                    }
+                        for (int j = 0; j < 8; ++j) {
+                            const float v = a.scale * d[i][j] * x[j];
+                            s[j] = __fmaf_rn(v, e[j], s[j]);
+                            w[j] *= v;
+                        }
+                    });
                     if (a.dgate) store_eight(a.dgate + (uint64_t)row * a.K, of.column(i), a.K, pack_eight<float>(w));
                 }
             }
             float over = 0.0f;                    // the sum of u b
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                float w[8], e[8];
-                unpack_eight<W>(now.gate[i], e);
+                float w[8], e[8], x[8];
+                gate_of(i, e);
                 post.get(i, w);
+                block(i, g, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] *= a.scale;
+                if constexpr (LEARN != 0 && !OWN)
+                    sover.each(i, [&](float (&s)[8]) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) s[j] = __fmaf_rn(d[i][j], x[j], s[j]);
+                    });
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    x[i][j] *= g;
-                    const float c = a.scale * d[i][j];
-                    if (LEARN && !OWN) sover[i][j] = __fmaf_rn(c, x[i][j], sover[i][j]);
-                    d[i][j] = c * e[j] * w[j];
-                    over = __fmaf_rn(d[i][j], x[i][j], over);
+                    d[i][j] = d[i][j] * e[j] * w[j];
+                    over = __fmaf_rn(d[i][j], x[j], over);
+                    if constexpr (KEPT) kept[i][j] = x[j];
                 }
             }
             if (a.norm_post) {
                 over = sum(over) * a.per;
 #pragma unroll
-                for (int i = 0; i < NC; ++i)
+                for (int i = 0; i < NC; ++i) {
+                    float x[8];
+                    block(i, KEPT ? 1.0f : g, x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[i][j] = __fmaf_rn(-x[i][j], over, d[i][j]) * g;
+                    for (int j = 0; j < 8; ++j) d[i][j] = __fmaf_rn(-x[j], over, d[i][j]) * g;
+                }
             }
 #pragma unroll
             for (int i = 0; i < NC; ++i) store_eight((uint16_t*)a.y.data + row * a.y.stride, of.column(i), a.K, pack_eight<uint16_t>(d[i]));
@@ -399,20 +493,26 @@ void k_block_norm_bwd(NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     float w[8], e[8], s[8], was[8] = {};
+                    float over[8];
                     post.get(i, w);
-                    unpack_eight<W>(now.gate[i], e);
+                    gate_of(i, e);
+                    sover.each(i, [&](float (&v)[8]) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[j] = sover[i][j] * w[j];
+                        for (int j = 0; j < 8; ++j) {
+                            over[j] = v[j];
+                            v[j] = 0.0f;
+                        }
+                    });
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[j] = over[j] * w[j];
                     if (a.dgate) store_eight(to, of.column(i), a.K, pack_eight<float>(s));
                     if (a.dpost) {
                         float* post_to = (a.part_post ? a.part_post + (uint64_t)of.worker * a.K : a.dpost);
                         if (posted) unpack_eight<float>(load_eight((const float*)post_to, of.column(i), a.K), was);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) was[j] = __fmaf_rn(sover[i][j], e[j], was[j]);
+                        for (int j = 0; j < 8; ++j) was[j] = __fmaf_rn(over[j], e[j], was[j]);
                         store_eight(post_to, of.column(i), a.K, pack_eight<float>(was));
                     }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sover[i][j] = 0.0f;
                 }
                 posted = true;
             }
@@ -427,14 +527,12 @@ void k_block_norm_bwd(NormArgs a) {
         if (!OWN && one_gate && !a.part_post) {   // one worker
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                float w[8], e[8];
+                float w[8], e[8], over[8];
+                sover.each(i, [&](float (&v)[8]) { __builtin_memcpy(over, v, sizeof(v)); });
                 post.get(i, w);
                 unpack_eight<W>(of.weight(a.gate, i), e);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    w[j] *= sover[i][j];
-                    e[j] *= sover[i][j];
-                }
+                for (int j = 0; j < 8; ++j) w[j] *= over[j], e[j] *= over[j];
                 if (a.dgate) store_eight(a.dgate, of.column(i), a.K, pack_eight<float>(w));
                 if (a.dpost) store_eight(a.dpost, of.column(i), a.K, pack_eight<float>(e));
             }
@@ -552,7 +650,9 @@ static void with_types(const BlockNorm& n, F&& f) {
 
 // 32 MB of a bf16 operand and more, in whole lines of 128 bytes: nontemporal loads (4096 x 8192: 47 us forward and 82 backward,
 // 55 and 92 without; rows that begin inside a line, which two workgroups read: 28.0 us backward of 1001 x 2501, 24.6 without).
-static bool streams(int64_t M, int64_t K, const NormShape& p) { return p.group() && p.chunks == 1 && M * K >= (int64_t)1 << 24 && K % 64 == 0; }
+// Past a width of 8192 from 64 MB on (backward with sums 2048 x 16384: 114 us, 121 without; forward 2048 x 8704 in fp32, 53
+// and 46).
+static bool streams(int64_t M, int64_t K, const NormShape& p) { return p.group() && M * K >= (int64_t)1 << (p.chunks == 1 ? 24 : 25) && K % 64 == 0; }
 
 static NormArgs norm_args(const BlockNorm& n, int64_t M, int64_t K, const NormShape& p) {
     NormArgs a{};
@@ -584,11 +684,14 @@ hipError_t launch_block_norm_fwd(const BlockNorm& n, int64_t M, int64_t K, const
             hipLaunchKernelGGL((k_block_norm_fwd<decltype(st), decltype(wt), decltype(group)::value, decltype(chunks)::value, decltype(stream)::value>),
                                p.grid(), p.block(), 0, s, a);
         };
+        auto group = [&](auto chunks) {
+            if (streams(M, K, p)) run(std::true_type{}, chunks, std::true_type{});
+            else run(std::true_type{}, chunks, std::false_type{});
+        };
         if (!p.group()) run(std::false_type{}, std::integral_constant<int, 1>{}, std::false_type{});
-        else if (streams(M, K, p)) run(std::true_type{}, std::integral_constant<int, 1>{}, std::true_type{});
-        else if (p.chunks == 1) run(std::true_type{}, std::integral_constant<int, 1>{}, std::false_type{});
-        else if (p.chunks == 2) run(std::true_type{}, std::integral_constant<int, 2>{}, std::false_type{});
-        else run(std::true_type{}, std::integral_constant<int, 4>{}, std::false_type{});
+        else if (p.chunks == 1) group(std::integral_constant<int, 1>{});
+        else if (p.chunks == 2) group(std::integral_constant<int, 2>{});
+        else group(std::integral_constant<int, 4>{});
     });
     return hipGetLastError();
 }
@@ -645,16 +748,16 @@ hipError_t launch_block_norm_bwd(const BlockNorm& n, int64_t M, int64_t K, const
                 else if (learn) with(k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, N, 1>);
                 else with(k_block_norm_bwd<decltype(st), decltype(wt), T, G, C, N, 0>);
             };
-            auto one_vector = [&](auto threads) {
-                if (streams(M, K, p)) run(threads, std::true_type{}, std::integral_constant<int, 1>{}, std::true_type{});
-                else run(threads, std::true_type{}, std::integral_constant<int, 1>{}, std::false_type{});
+            auto group = [&](auto threads, auto chunks) {
+                if (streams(M, K, p)) run(threads, std::true_type{}, chunks, std::true_type{});
+                else run(threads, std::true_type{}, chunks, std::false_type{});
             };
-            // (a workgroup of 1024 threads has 128 registers a thread: few spills with one vector, more beyond a width of 8192)
+            // (a workgroup of 1024 threads has 128 registers a thread: few spills up to a width of 16384, more beyond)
             if (!p.group()) run(std::integral_constant<int, 256>{}, std::false_type{}, std::integral_constant<int, 1>{}, std::false_type{});
-            else if (p.chunks == 1 && p.waves <= 8) one_vector(std::integral_constant<int, 512>{});
-            else if (p.chunks == 1) one_vector(std::integral_constant<int, 1024>{});
-            else if (p.chunks == 2) run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 2>{}, std::false_type{});
-            else run(std::integral_constant<int, 1024>{}, std::true_type{}, std::integral_constant<int, 4>{}, std::false_type{});
+            else if (p.chunks == 1 && p.waves <= 8) group(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+            else if (p.chunks == 1) group(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+            else if (p.chunks == 2) group(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+            else group(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
         });
     if (q.bytes > 0 || (M == 0 && learn)) {
         // (a token's own gate is never shared)

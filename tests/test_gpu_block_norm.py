@@ -128,6 +128,42 @@ def test_gates(K, M, gates):
     c.check_backward()
 
 
+@pytest.mark.parametrize("M,K,stream,weights", [(600, 8200, F32, F32), (600, 16384, BF16, BF16), (600, 9999, BF16, F32), (300, 20001, BF16, BF16),
+                                                (300, 24576, F32, F32)])
+def test_wide_rows_of_several_tokens_a_worker(M, K, stream, weights):
+    # past a width of 8192 the sums over tokens lie elsewhere: stretches of two and three rows, gates that begin and end inside them
+    for gate in (None, 1, 5, 100, M // 2, M):
+        c = Case(M, K, stream, weights, gate=gate)
+        c.check_backward()
+        if gate in (1, 5):
+            c.check_backward(need_weights=False)
+    c.check_forward()
+    c = Case(M, K, stream, weights, post=None, gate=M // 3)
+    c.check_backward()
+
+
+@pytest.mark.parametrize("stream", [F32, BF16])
+@pytest.mark.parametrize("M,K", [(2100, 16384), (1030, 32768)])
+def test_many_wide_rows_as_alone(M, K, stream):
+    c = Case(M, K, stream, BF16)
+    new, y = c.forward()
+    back = c.backward()
+    plain = c.backward(need_weights=False)
+    assert torch.equal(plain["dh"], back["dh"]) and torch.equal(plain["dx"], back["dx"])
+    for row in (0, 1, M // 2, M - 1):
+        one = slice(row, row + 1)
+        t, z = nf4.block_norm_fwd(c.h[one], c.x[one], **c.how)
+        assert torch.equal(new[one], t) and torch.equal(y[one], z)
+        got = nf4.block_norm_bwd(c.h[one], c.dy[one], c.dh[one], c.x[one], **c.how)
+        assert torch.equal(back["dh"][one], got[0]) and torch.equal(back["dx"][one], got[1])
+    want, size = 0, 0
+    for a in range(0, M, 100):
+        h, t = c.h[a:a + 100].double(), c.dy[a:a + 100].double()
+        term = t * h / (h.square().mean(1, keepdim=True) + c.how["eps"]).sqrt()
+        want, size = want + term.cumsum(0)[-1], size + term.abs().cumsum(0)[-1]
+    near(back["dpre"], want.cpu(), (UP + (M + 64) * 2.0 ** -24) * size.cpu() + 2.0 ** -24 * want.abs().cpu())
+
+
 def test_strides_and_alignment():
     for pad, first in ((0, 0), (3, 1), (8, 8)):
         c, d = (Case(11, 1003, BF16, F32, gate=11) for _ in range(2))
