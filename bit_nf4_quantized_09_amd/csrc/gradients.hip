@@ -7,7 +7,7 @@
 // tensor's type.  A norm of infinity makes the factor zero and one of NaN makes it NaN, as the formula says.
 //
 // Shape.  Bound by HBM: the norm reads each value once, the clipping reads and writes it once more.  The
-// tensors' addresses and sizes travel in the kernels' arguments (240 or 160 of them in a launch), so that
+// tensors' addresses and sizes travel in the kernels' arguments (240 of them in a launch, 160 with outputs apart), so that
 // nothing is copied to the device and a captured graph holds them itself.  A launch's values are cut into
 // spans of 8192, none across two tensors, and each workgroup walks along equally many neighbouring ones.  It leaves one
 // sum; they are added up in a fixed order: no atomics, the same call gives the same bits.  1120 tensors of 3.2 GB in
@@ -19,7 +19,7 @@
 
 namespace nf4 {
 
-// Tensors of a launch: 16 and 24 bytes each of 4 KiB of arguments; a list of up to 32 takes less (the arguments' way to
+// Tensors of a launch: 16 or (with outputs apart) 24 bytes each of 4 KiB of arguments; a list of up to 32 takes less (the arguments' way to
 // the GPU is part of a call: 28 tensors clipped in 9.6 us, 12.6 with 4 KiB).
 constexpr int NORM_TENSORS = 240, SCALE_TENSORS = 160, FEW_TENSORS = 32;
 constexpr uint32_t IS_BF16 = 0x80000000u;
@@ -36,9 +36,17 @@ struct TensorTable {
     int count;
     bool stream;              // more than the last-level cache keeps until it is read again
 };
-template <int MOST>
+template <int MOST, bool APART>
 struct ScaleTable : TensorTable<MOST> {
     void* out[MOST];
+    __host__ __device__ void put(int i, void* p) { out[i] = p; }
+    __device__ void* to(int i) const { return out[i]; }
+};
+// (all in place: an address each is enough, and fewer launches: 448 tensors 33 us, 38 with 160 a launch; 196 tensors 17 and 22)
+template <int MOST>
+struct ScaleTable<MOST, false> : TensorTable<MOST> {
+    __host__ __device__ void put(int, void*) {}
+    __device__ void* to(int i) const { return const_cast<void*>(this->in[i]); }
 };
 
 // The tensor of a span: the last one with span0 <= span.
@@ -163,9 +171,9 @@ __device__ __forceinline__ void scale_values(const T* in, T* out, uint32_t n, bo
 }
 
 // JOIN: the norm's sums are so few that every workgroup adds them up for itself, and one of each launch says what they give.
-template <int MOST, bool JOIN>
+template <int MOST, bool APART, bool JOIN>
 __global__ __launch_bounds__(256)
-void k_grad_scale(ScaleTable<MOST> t, const double* part, int parts, double max_norm, float* norm, const float* factor) {
+void k_grad_scale(ScaleTable<MOST, APART> t, const double* part, int parts, double max_norm, float* norm, const float* factor) {
     float f;
     if constexpr (JOIN) {
         double s = 0.0;
@@ -177,9 +185,9 @@ void k_grad_scale(ScaleTable<MOST> t, const double* part, int parts, double max_
         f = *factor;
     }
     for_values<MOST>(t, [&](int i, uint32_t first, uint32_t n) {
-        if (f == 1.0f && t.in[i] == t.out[i]) return;           // in place, and nothing to clip
-        if (t.size[i] & IS_BF16) scale_values((const uint16_t*)t.in[i] + first, (uint16_t*)t.out[i] + first, n, t.stream, f);
-        else scale_values((const float*)t.in[i] + first, (float*)t.out[i] + first, n, t.stream, f);
+        if (f == 1.0f && t.in[i] == t.to(i)) return;            // in place, and nothing to clip
+        if (t.size[i] & IS_BF16) scale_values((const uint16_t*)t.in[i] + first, (uint16_t*)t.to(i) + first, n, t.stream, f);
+        else scale_values((const float*)t.in[i] + first, (float*)t.to(i) + first, n, t.stream, f);
     });
 }
 
@@ -245,25 +253,28 @@ hipError_t launch_grad_norm(const Gradient* g, int64_t count, double max_norm, f
 }
 
 // The tensors read last are clipped first: the last-level cache still has them.
-template <int MOST>
+template <int MOST, bool APART>
 static void launch_scale(const Gradient* g, const Gradient* out, int64_t count, int parts, double max_norm, float* norm, float* factor, void* ws,
                          hipStream_t s) {
-    const auto tables = tables_of<MOST, ScaleTable<MOST>>(g, count, [&](ScaleTable<MOST>& t, int entry, int64_t i, int64_t at) {
-        t.out[entry] = (uint8_t*)out[i].data + at * (out[i].bf16 ? 2 : 4);
+    const auto tables = tables_of<MOST, ScaleTable<MOST, APART>>(g, count, [&](ScaleTable<MOST, APART>& t, int entry, int64_t i, int64_t at) {
+        t.put(entry, (uint8_t*)out[i].data + at * (out[i].bf16 ? 2 : 4));
     });
     // up to 1024 sums are added up by each workgroup (28 tensors of 0.3 million values in all: 12 us, 16 with a launch more)
     const bool join = !tables.empty() && parts <= 1024;
     if (!join) hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(1024), 0, s, (const double*)ws, parts, max_norm, norm, factor);
     for (auto t = tables.rbegin(); t != tables.rend(); ++t) {
-        if (join) hipLaunchKernelGGL((k_grad_scale<MOST, true>), dim3(grid_of(*t)), dim3(256), 0, s, *t, (const double*)ws, parts, max_norm, norm, (const float*)nullptr);
-        else hipLaunchKernelGGL((k_grad_scale<MOST, false>), dim3(grid_of(*t)), dim3(256), 0, s, *t, (const double*)nullptr, 0, 0.0, (float*)nullptr, (const float*)factor);
+        if (join) hipLaunchKernelGGL((k_grad_scale<MOST, APART, true>), dim3(grid_of(*t)), dim3(256), 0, s, *t, (const double*)ws, parts, max_norm, norm, (const float*)nullptr);
+        else hipLaunchKernelGGL((k_grad_scale<MOST, APART, false>), dim3(grid_of(*t)), dim3(256), 0, s, *t, (const double*)nullptr, 0, 0.0, (float*)nullptr, (const float*)factor);
     }
 }
 hipError_t launch_grad_clip(const Gradient* g, const Gradient* out, int64_t count, double max_norm, float* norm, float* factor,
                             void* ws, hipStream_t s) {
     const int parts = launch_squares(g, count, ws, s);
-    if (pieces_of(g, count) <= FEW_TENSORS) launch_scale<FEW_TENSORS>(g, out, count, parts, max_norm, norm, factor, ws, s);
-    else launch_scale<SCALE_TENSORS>(g, out, count, parts, max_norm, norm, factor, ws, s);
+    bool apart = false;
+    for (int64_t i = 0; i < count; ++i) apart = apart || g[i].data != out[i].data;
+    if (pieces_of(g, count) <= FEW_TENSORS) launch_scale<FEW_TENSORS, true>(g, out, count, parts, max_norm, norm, factor, ws, s);
+    else if (apart) launch_scale<SCALE_TENSORS, true>(g, out, count, parts, max_norm, norm, factor, ws, s);
+    else launch_scale<NORM_TENSORS, false>(g, out, count, parts, max_norm, norm, factor, ws, s);
     return hipGetLastError();
 }
 
