@@ -6,10 +6,12 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <string>
 #include <vector>
 
 #include "../../include/qlora_step.h"
+#include "overlap.h"
 #include "status.h"
 #include "step.h"
 
@@ -18,6 +20,7 @@ using nf4::BlockNorm;
 using nf4::fail;
 using nf4::Gradient;
 using nf4::hip_status;
+using nf4::Memory;
 using nf4::RowsView;
 
 namespace {
@@ -69,6 +72,13 @@ nf4_status check_norm(const qlora_block_norm* n, int64_t M, int64_t K, nf4_dtype
 }
 
 bool same_rows(const RowsView& a, const RowsView& b, int64_t M) { return a.data == b.data && (M <= 1 || a.stride == b.stride); }
+Memory memory_of(const RowsView& r, int64_t M, int64_t K, int elem) { return Memory(r.data, M, r.stride, K, elem); }
+// What is written may share memory with nothing else: other workgroups read or write that, whenever they come to it.
+nf4_status check_apart(const Memory& out, const char* name, std::initializer_list<Memory> others) {
+    for (const Memory& m : others)
+        if (share_memory(out, m)) return fail(NF4_ERR_ARG, std::string(name) + " shares memory with another operand");
+    return NF4_OK;
+}
 
 nf4_status gradients_of(const qlora_tensor* g, int64_t count, const char* name, std::vector<Gradient>& v) {
     const std::string n(name);
@@ -140,8 +150,11 @@ nf4_status qlora_block_norm_fwd(const qlora_block_norm* norm, int64_t M, int64_t
         if (nf4_status st = check_rows(h_out, "h_out", block, true, M, K, elem, ov)) return st;
         if (nf4_status st = check_rows(y, "y", n.norm_pre, true, M, K, 2, yv)) return st;
         if (ov.data && ov.data == hv.data && !same_rows(ov, hv, M)) return fail(NF4_ERR_ARG, "in place needs the same stride");
-        if ((ov.data && (ov.data == xv.data || ov.data == yv.data)) || (yv.data && (yv.data == hv.data || yv.data == xv.data)))
-            return fail(NF4_ERR_ARG, "h_out and y may not be another operand's memory");
+        const int welem = size_of(norm->dtype);
+        const Memory hm = memory_of(hv, M, K, elem), xm = memory_of(xv, M, K, 2), om = memory_of(ov, M, K, elem), ym = memory_of(yv, M, K, 2),
+                     pre(n.pre, 1, 0, K, welem), post(n.post, 1, 0, K, welem), gate(n.gate, n.gate_rows, K, K, welem);
+        if (nf4_status st = check_apart(om, "h_out", {ov.data == hv.data ? Memory() : hm, xm, ym, pre, post, gate})) return st;
+        if (nf4_status st = check_apart(ym, "y", {hm, xm, pre, post, gate})) return st;
         return hip_status(nf4::launch_block_norm_fwd(n, M, K, hv, xv, ov, yv, (hipStream_t)stream), "qlora_block_norm_fwd");
     });
 }
@@ -173,12 +186,20 @@ nf4_status qlora_block_norm_bwd(const qlora_block_norm* norm, int64_t M, int64_t
             if (nf4_status st = check_rows(dh_out, "dh_out", true, true, M, K, elem, ov)) return st;
             if (nf4_status st = check_rows(dx, "dx", block, true, M, K, 2, dxv)) return st;
             if (ov.data == dv.data && !same_rows(ov, dv, M)) return fail(NF4_ERR_ARG, "in place needs the same stride");
-            for (const RowsView& r : {hv, xv, yv})
-                if (r.data && (r.data == ov.data || r.data == dxv.data)) return fail(NF4_ERR_ARG, "dh_out and dx may not be another operand's memory");
-            if (dxv.data && (dxv.data == ov.data || dxv.data == dv.data)) return fail(NF4_ERR_ARG, "dh_out and dx may not be another operand's memory");
             const size_t need = nf4::block_norm_ws_bytes(M, K, n.gate_rows, dpre, dpost, dgate);
             if (need > 0 && (!workspace || workspace_bytes < need)) return fail(NF4_ERR_WORKSPACE, "workspace missing or too small");
             if (need > 0 && !aligned(workspace, 256)) return fail(NF4_ERR_ARG, "workspace must be 256-byte aligned");
+            const int welem = size_of(norm->dtype);
+            const Memory hm = memory_of(hv, M, K, elem), xm = memory_of(xv, M, K, 2), ym = memory_of(yv, M, K, 2), dm = memory_of(dv, M, K, elem),
+                         om = memory_of(ov, M, K, elem), dxm = memory_of(dxv, M, K, 2), pre(n.pre, 1, 0, K, welem), post(n.post, 1, 0, K, welem),
+                         gate(n.gate, n.gate_rows, K, K, welem), ws(workspace, need), wpre(dpre, 1, 0, K, 4), wpost(dpost, 1, 0, K, 4),
+                         wgate(dgate, n.gate_rows, K, K, 4);
+            if (nf4_status st = check_apart(om, "dh_out", {ov.data == dv.data ? Memory() : dm, hm, xm, ym, dxm, pre, post, gate, wpre, wpost, wgate, ws})) return st;
+            if (nf4_status st = check_apart(dxm, "dx", {dm, hm, xm, ym, pre, post, gate, wpre, wpost, wgate, ws})) return st;
+            if (nf4_status st = check_apart(wpre, "dpre", {dm, hm, xm, ym, pre, post, gate, wpost, wgate, ws})) return st;
+            if (nf4_status st = check_apart(wpost, "dpost", {dm, hm, xm, ym, pre, post, gate, wgate, ws})) return st;
+            if (nf4_status st = check_apart(wgate, "dgate", {dm, hm, xm, ym, pre, post, gate, ws})) return st;
+            if (nf4_status st = check_apart(ws, "workspace", {dm, hm, xm, ym, pre, post, gate})) return st;
         }
         return hip_status(nf4::launch_block_norm_bwd(n, M, K, hv, xv, yv, dv, ov, dxv, dpre, dpost, dgate, workspace, (hipStream_t)stream),
                           "qlora_block_norm_bwd");

@@ -202,7 +202,8 @@ def block_norm_fwd(h: torch.Tensor, x: Optional[torch.Tensor] = None, pre=True, 
       gate   [width], or [rows, width] where each row belongs to tokens / rows neighbouring tokens (a row for each
              sequence of a batch of equal lengths, or for each token); None: ones
     pre, post and gate are fp32 or bf16, all of one type.  h' is of the stream's type (h itself is written if `inplace`;
-    not of tensors that autograd records), and y, bf16, is the norm of h' as it was rounded."""
+    not of tensors that autograd records, nor where h shares memory with another operand), and y, bf16, is the norm of h'
+    as it was rounded."""
     return (_bound or _binding()).block_norm_fwd(h, x, pre, post, gate, scale, eps, inplace)
 
 

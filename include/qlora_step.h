@@ -50,7 +50,8 @@ typedef struct qlora_block_norm {
  *   x       bf16, the block's output; NULL: no block, and y = n(h) pre (norm_post, gate and h_out are then not given)
  *   h_out   with x: the stream after the block, of the stream's type; may be h itself (same pointer and stride)
  *   y       bf16, with norm_pre
- * Outputs may not overlap anything else.  Any strides and alignments of whole values. */
+ * Outputs may not share memory with anything else, which is refused (NF4_ERR_ARG); rows of several operands may lie side by
+ * side in one buffer.  Any strides and alignments of whole values. */
 nf4_status qlora_block_norm_fwd(const qlora_block_norm* norm, int64_t M, int64_t K, nf4_dtype stream_dtype,
                                 const qlora_rows* h, const qlora_rows* x, const qlora_rows* h_out, const qlora_rows* y,
                                 void* stream);
@@ -64,7 +65,8 @@ nf4_status qlora_block_norm_fwd(const qlora_block_norm* norm, int64_t M, int64_t
  *   dx      out, with x: bf16, the gradient of the block's output
  *   dpre, dpost, dgate   out: fp32 [K], [K], [gate_rows][K], or NULL: sums over the tokens in a fixed order
  *   workspace  qlora_block_norm_bwd_workspace_bytes of the same sizes, 256-byte aligned: fp32 sums of up to 2048
- *              workers, each as long as the outputs asked for (of several gates two rows each) */
+ *              workers, each as long as the outputs asked for (of several gates two rows each)
+ * Outputs and the workspace may not share memory with anything else, as in the forward call. */
 size_t qlora_block_norm_bwd_workspace_bytes(int64_t M, int64_t K, int64_t gate_rows, int32_t need_dpre, int32_t need_dpost,
                                             int32_t need_dgate);
 nf4_status qlora_block_norm_bwd(const qlora_block_norm* norm, int64_t M, int64_t K, nf4_dtype stream_dtype,

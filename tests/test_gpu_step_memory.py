@@ -1,0 +1,31 @@
+"""Calls in place beside operands of the same buffer: refused where they share memory, right where they lie side by side."""
+import pytest
+import torch
+
+import bit_nf4_quantized_09_amd as nf4
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def test_norms_in_place_beside_other_operands():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    M, K = 40, 600
+    buf = torch.randn((M + 1, 2 * K + 8), generator=g, device="cuda").to(BF16)
+    before = buf.clone()
+    # rows (or columns) that both operands have: the stream's are written while others still read the block's output
+    for h, x in ((buf[:M, :K], buf[1:, :K]), (buf[1:, :K], buf[:M, :K]), (buf[:M, :K], buf[:M, K - 1:2 * K - 1]), (buf[:M, 1:K + 1], buf[:M, :K]),
+                 (buf[:M, :K], buf[3:4, :K].expand(M, K))):
+        with pytest.raises(nf4.NF4Error, match="shares memory"):
+            nf4.block_norm_fwd(h, x, inplace=True)
+    with pytest.raises(nf4.NF4Error, match="shares memory"):
+        nf4.block_norm_fwd(buf[:M, :K], buf[:M, K:2 * K], pre=buf[2, 5:K + 5], inplace=True)
+    assert torch.equal(buf, before)
+    # side by side
+    for h, x in ((buf[:M, :K], buf[:M, K:2 * K]), (buf[:M, K + 8:], buf[:M, 8:K + 8]), (buf[:M, :K], buf[1:, K:2 * K])):
+        buf.copy_(before)
+        want, norm = nf4.block_norm_fwd(h.clone(), x.clone())
+        got, y = nf4.block_norm_fwd(h, x, inplace=True)
+        assert got.data_ptr() == h.data_ptr() and torch.equal(h, want) and torch.equal(y, norm)
+        h.copy_(before.as_strided(h.size(), h.stride(), h.storage_offset()))
+        assert torch.equal(buf, before)
