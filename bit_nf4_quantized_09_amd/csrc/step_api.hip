@@ -291,6 +291,13 @@ nf4_status qlora_logits_shape(const qlora_logit_rules* rules, int64_t rows, int6
         if (nf4_status st = check_rows(logits, "logits", true, false, rows, V, size_of(dtype), in)) return st;
         if (nf4_status st = check_rows(out, "out", true, true, rows, V, size_of(dtype), to)) return st;
         if (in.data == to.data && !same_rows(in, to, rows)) return fail(NF4_ERR_ARG, "in place needs the same stride");
+        const Memory om = memory_of(to, rows, V, size_of(dtype));
+        if (nf4_status st = check_apart(om, "out", {in.data == to.data ? Memory() : memory_of(in, rows, V, size_of(dtype)),
+                                                    Memory(q.history, rows, q.history_stride, q.history_width, 4), Memory(q.lengths, rows, 1, 1, 4),
+                                                    Memory(q.prompts, rows, 1, 1, 4), Memory(q.repetitions, rows, 1, 1, 4), Memory(q.presences, rows, 1, 1, 4),
+                                                    Memory(q.frequencies, rows, 1, 1, 4), Memory(q.bias_ids, rows, q.bias_ids_stride, q.biases, 4),
+                                                    Memory(q.bias, rows, q.bias_stride, q.biases, 4), Memory(q.allowed, rows, q.allowed_stride, (V + 31) / 32, 4)}))
+            return st;
         const nf4::LogitRules r{rows, q.history, q.lengths, q.prompts, q.history_stride, (int)q.history_width, q.repetition, q.presence, q.frequency,
                                 q.repetitions, q.presences, q.frequencies, q.bias_ids, q.bias, q.bias_ids_stride, q.bias_stride, (int)q.biases,
                                 q.allowed, q.allowed_stride};

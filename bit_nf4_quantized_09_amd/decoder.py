@@ -260,6 +260,6 @@ def shape_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = None, l
       bias_ids, bias   int32 and fp32 [rows, biases]; ids outside the vocabulary are unused
       allowed   int32 [rows, at least vocabulary / 32, rounded up]
     history, bias_ids, bias and allowed may have a single row for all.  Returns a new dense tensor, or the same one if
-    `inplace` (not of tensors that autograd records)."""
+    `inplace` (not of tensors that autograd records, nor of those that share memory with another operand)."""
     return (_bound or _binding()).shape_logits(logits, history, lengths, prompts, repetition, presence, frequency, bias_ids, bias,
                                                allowed, inplace)

@@ -151,7 +151,8 @@ typedef struct qlora_logit_rules {
     int64_t allowed_stride;
 } qlora_logit_rules;
 
-/* logits and out: fp32 or bf16 [rows][V], rounded once; out may be the logits themselves (same pointer and stride).
+/* logits and out: fp32 or bf16 [rows][V], rounded once; out may be the logits themselves (same pointer and stride),
+ * and may share memory with nothing else (NF4_ERR_ARG).
  * 0 <= rows < 2^24, 1 <= V < 2^28; history_width and biases up to 2^31 - 2.  A repetition must be positive; one given as a
  * number is checked. */
 nf4_status qlora_logits_shape(const qlora_logit_rules* rules, int64_t rows, int64_t V, nf4_dtype dtype,

@@ -29,3 +29,24 @@ def test_norms_in_place_beside_other_operands():
         assert got.data_ptr() == h.data_ptr() and torch.equal(h, want) and torch.equal(y, norm)
         h.copy_(before.as_strided(h.size(), h.stride(), h.storage_offset()))
         assert torch.equal(buf, before)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_logits_in_place_beside_other_operands(dtype):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    R, V = 20, 5000
+    buf = torch.randn((R, V + 40), generator=g, device="cuda").to(dtype)
+    before, z = buf.clone(), buf[:, :V]
+    raw = buf.view(torch.int32)                               # the same bytes
+    width = V * z.element_size() // 4
+    for kw in (dict(history=raw[:, width - 1:width + 2]), dict(allowed=raw[:, :V // 32 + 1]), dict(allowed=raw[3:4, width - 140:width + 20]),
+               dict(history=raw[5:6, :9]), dict(bias_ids=raw[:, width:width + 3], bias=raw[:, width - 3:width].view(torch.float32))):
+        with pytest.raises(nf4.NF4Error, match="shares memory"):
+            nf4.shape_logits(z, inplace=True, **kw)
+    assert torch.equal(buf, before)
+    # a history that lies behind each row's logits
+    raw[:, width:width + 4] = torch.tensor([1, 7, V - 1, 7], dtype=torch.int32, device="cuda")
+    history = raw[:, width:width + 4]
+    want = nf4.shape_logits(z.clone(), history.clone(), repetition=1.5, frequency=0.25)
+    got = nf4.shape_logits(z, history, repetition=1.5, frequency=0.25, inplace=True)
+    assert got is z and torch.equal(z, want) and not torch.equal(z, before[:, :V]) and history.tolist() == [[1, 7, V - 1, 7]] * R

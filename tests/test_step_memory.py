@@ -1,5 +1,6 @@
 """Operands of include/qlora_step.h that share memory with one that is written are refused on the host, before any HIP call,
 also where they begin at different addresses; operands side by side in one buffer do not share any."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -7,6 +8,7 @@ import subprocess
 import pytest
 
 import bit_nf4_quantized_09_amd as nf4
+import step_abi as abi
 from test_step_host import SOME, bwd, fwd, norm, rows, why
 
 ARG = nf4.NF4_ERR_ARG
@@ -68,3 +70,25 @@ def test_norms_weights_gradients_and_workspace():
     many = dict(M=4000, h=rows(1 << 27), x=rows(1 << 28), dy=rows(1 << 29), dh_out=rows(1 << 30), dx=rows(1 << 31))
     for where in (1 << 27, 1 << 28, 1 << 29, 1 << 30, 1 << 31, FAR, 2 * FAR):
         refused(bwd(n, **{**many, **at, "ws": where, "size": need}))
+
+
+def test_logits_and_their_rules():
+    rule = dict(history=None, history_stride=8, history_width=8, lengths=None, prompts=None, repetition=1.0, presence=0.0, frequency=0.0,
+                repetitions=None, presences=None, frequencies=None, bias_ids=None, bias_ids_stride=4, bias=None, bias_stride=4, biases=4,
+                allowed=None, allowed_stride=4)
+
+    def call(z, out, **kw):
+        r = abi.Rules(*{**rule, **kw}.values())
+        return abi.library().qlora_logits_shape(ctypes.byref(r), 3, 100, nf4.NF4_F32, ctypes.byref(z), ctypes.byref(out), None)
+    at = abi.Rows(FAR, 100)                                   # 1200 bytes
+    for shift in (-1196, -400, -4, 4, 400, 1196):
+        refused(call(abi.Rows(FAR + shift, 100), at))
+    refused(call(abi.Rows(FAR, 250), abi.Rows(FAR + 99 * 4, 250)))
+    refused(call(abi.Rows(FAR + 800, 0), at))                 # one row for all
+    # the rules' tables, which begin before the logits and end in them: in place
+    history = dict(history=2 * FAR)
+    for name, size, kw in (("history", 3 * 32, {}), ("lengths", 12, history), ("prompts", 12, history), ("repetitions", 12, history),
+                           ("presences", 12, history), ("frequencies", 12, history), ("bias_ids", 48, dict(bias=2 * FAR)),
+                           ("bias", 48, dict(bias_ids=2 * FAR)), ("allowed", 48, {})):
+        for where in (FAR - size + 4, FAR, FAR + 1196):
+            refused(call(at, at, **{**kw, name: where}))
