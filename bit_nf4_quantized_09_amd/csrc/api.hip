@@ -709,7 +709,9 @@ nf4_status adamw_step(float* p, const float* g, float* m, float* v, uint16_t* p_
         for (int j = i + 1; j < 4; ++j)
             if (overlaps(bufs[i], b4, bufs[j], b4)) return fail(NF4_ERR_ARG, "p, g, m and v must not overlap");
         if (overlaps(bufs[i], b4, p_bf16, b2)) return fail(NF4_ERR_ARG, "p_bf16 overlaps the state");
+        if (bufs[i] != g && overlaps(bufs[i], b4, factor, 4)) return fail(NF4_ERR_ARG, "factor lies in the state, which is written");
     }
+    if (overlaps(p_bf16, b2, factor, 4)) return fail(NF4_ERR_ARG, "factor lies in p_bf16, which is written");
     return hip_status(nf4::launch_adamw(p, g, m, v, p_bf16, n, k, factor, (hipStream_t)stream), name);
 }
 
@@ -727,6 +729,8 @@ nf4_status adamw_step_paged(float* p_host, const float* g, float* m_host, float*
     if (!aligned(p_bf16, 8)) return fail(NF4_ERR_ARG, "p_bf16 must be 8-byte aligned");
     if (!stage || !aligned(stage, 256)) return fail(NF4_ERR_ARG, "stage must be a 256-byte aligned buffer");
     if (stage_bytes < 1536) return fail(NF4_ERR_WORKSPACE, "stage must hold at least 1536 bytes");
+    if (overlaps(stage, stage_bytes, factor, 4) || overlaps(p_bf16, (size_t)n * 2, factor, 4))
+        return fail(NF4_ERR_ARG, "factor lies in stage or p_bf16, which are written");
     // two halves, each [p][m][v] of `chunk` parameters (a multiple of 64, so that every
     // staged vector stays 256-byte aligned): chunk c uses half c % 2
     const int64_t chunk = (int64_t)(stage_bytes / 1536) * 64;

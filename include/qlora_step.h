@@ -99,7 +99,8 @@ nf4_status qlora_grad_clip(const qlora_tensor* grads, const qlora_tensor* out, i
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* nf4_adamw_step and nf4_adamw_step_paged with the gradient times a factor (device fp32, of qlora_grad_norm), which is
- * rounded to fp32 before the step; with a factor of 1 they give the same bits as those. */
+ * rounded to fp32 before the step; with a factor of 1 they give the same bits as those.  The factor lies apart from all
+ * that is written (the state, p_bf16, the stage). */
 nf4_status qlora_adamw_step_scaled(float* p, const float* g, float* m, float* v, uint16_t* p_bf16, int64_t n,
                                    float lr, float beta1, float beta2, float eps, float weight_decay,
                                    int64_t step, const float* factor, void* stream);

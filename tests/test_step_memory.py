@@ -92,3 +92,15 @@ def test_logits_and_their_rules():
                            ("bias", 48, dict(bias_ids=2 * FAR)), ("allowed", 48, {})):
         for where in (FAR - size + 4, FAR, FAR + 1196):
             refused(call(at, at, **{**kw, name: where}))
+
+
+def test_the_factor_apart_from_what_the_step_writes():
+    # every workgroup reads the factor, whenever it begins
+    L = nf4.load_library()
+    vp = ctypes.c_void_p
+    p, g, m, v, half, stage = (i << 20 for i in range(1, 7))
+    how = (64, 1e-4, 0.9, 0.999, 1e-8, 0.0, 1)
+    for f in (p, p + 252, m, m + 128, v + 252, half, half + 124):
+        assert L.qlora_adamw_step_scaled(vp(p), vp(g), vp(m), vp(v), vp(half), *how, vp(f), None) == ARG and "factor" in why()
+    for f in (stage, stage + 4092, half + 124):
+        assert L.qlora_adamw_step_paged_scaled(vp(p), vp(g), vp(m), vp(v), vp(half), *how, vp(f), vp(stage), 4096, None) == ARG and "factor" in why()
