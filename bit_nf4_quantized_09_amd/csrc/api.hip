@@ -35,6 +35,12 @@ nf4_status nf4::hip_status(hipError_t e, const char* where) {
     return fail(NF4_ERR_HIP, std::string(where) + ": " + hipGetErrorString(e));
 }
 
+// (13 characters lie in the string itself: nothing is allocated)
+nf4_status nf4::out_of_memory() noexcept {
+    g_last_error = "out of memory";
+    return NF4_ERR_HIP;
+}
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -795,17 +801,21 @@ nf4_status nf4_adamw_step_paged(float* p_host, const float* g, float* m_host, fl
 nf4_status qlora_adamw_step_scaled(float* p, const float* g, float* m, float* v, uint16_t* p_bf16, int64_t n,
                                    float lr, float beta1, float beta2, float eps, float weight_decay,
                                    int64_t step, const float* factor, void* stream) {
-    if (nf4_status st = check_factor(factor)) return st;
-    return adamw_step(p, g, m, v, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, factor, stream, "qlora_adamw_step_scaled");
+    return nf4::guarded([&]() -> nf4_status {
+        if (nf4_status st = check_factor(factor)) return st;
+        return adamw_step(p, g, m, v, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, factor, stream, "qlora_adamw_step_scaled");
+    });
 }
 
 nf4_status qlora_adamw_step_paged_scaled(float* p_host, const float* g, float* m_host, float* v_host,
                                          uint16_t* p_bf16, int64_t n, float lr, float beta1, float beta2,
                                          float eps, float weight_decay, int64_t step, const float* factor, void* stage,
                                          size_t stage_bytes, void* stream) {
-    if (nf4_status st = check_factor(factor)) return st;
-    return adamw_step_paged(p_host, g, m_host, v_host, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, factor, stage,
-                            stage_bytes, stream, "qlora_adamw_step_paged_scaled");
+    return nf4::guarded([&]() -> nf4_status {
+        if (nf4_status st = check_factor(factor)) return st;
+        return adamw_step_paged(p_host, g, m_host, v_host, p_bf16, n, lr, beta1, beta2, eps, weight_decay, step, factor, stage,
+                                stage_bytes, stream, "qlora_adamw_step_paged_scaled");
+    });
 }
 
 }  // extern "C"

@@ -15,21 +15,12 @@ using nf4::aligned;
 using nf4::BatchView;
 using nf4::CacheView;
 using nf4::fail;
+using nf4::guarded;
 using nf4::HeadsView;
 using nf4::hip_status;
 using nf4::RopeView;
 
 namespace {
-
-// Nothing may leave a C entry point but a status.
-template <typename F>
-nf4_status guarded(F&& f) noexcept {
-    try {
-        return f();
-    } catch (...) {
-        return NF4_ERR_HIP;   // out of host memory, for a message
-    }
-}
 
 constexpr int64_t MAX_TOKENS = (int64_t)1 << 23;
 

@@ -14,6 +14,17 @@ namespace nf4 {
 
 nf4_status fail(nf4_status st, const std::string& msg);
 nf4_status hip_status(hipError_t e, const char* where);
+nf4_status out_of_memory() noexcept;      // NF4_ERR_HIP, and says so
+
+// Nothing may leave a C entry point but a status: what throws here is the host's memory.
+template <typename F>
+nf4_status guarded(F&& f) noexcept {
+    try {
+        return f();
+    } catch (...) {
+        return out_of_memory();
+    }
+}
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 

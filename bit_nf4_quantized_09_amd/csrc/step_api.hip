@@ -18,22 +18,13 @@
 using nf4::aligned;
 using nf4::BlockNorm;
 using nf4::fail;
+using nf4::guarded;
 using nf4::Gradient;
 using nf4::hip_status;
 using nf4::Memory;
 using nf4::RowsView;
 
 namespace {
-
-// Nothing may leave a C entry point but a status.
-template <typename F>
-nf4_status guarded(F&& f) noexcept {
-    try {
-        return f();
-    } catch (...) {
-        return NF4_ERR_HIP;   // out of host memory
-    }
-}
 
 int size_of(nf4_dtype t) { return t == NF4_BF16 ? 2 : 4; }
 bool known(nf4_dtype t) { return t == NF4_F32 || t == NF4_BF16; }
