@@ -144,8 +144,9 @@ def train_loss(model, tokens, targets):
     return _Loss.apply(model.hidden(tokens, attend), model.head, targets)
 
 
-def train(model, tokens, targets, steps=20, lr=3e-3, max_norm=1.0, say=lambda *a: None):
-    """Adapter steps on one sequence, the gradients clipped to a norm of max_norm; returns the losses."""
+def train(model, tokens, targets, steps=20, lr=3e-3, max_norm=1.0, say=None):
+    """Adapter steps on one sequence, the gradients clipped to a norm of max_norm (None: as they are); returns the
+    losses.  say gets a line for each step."""
     linears = model.linears()
     opt = nf4.PagedAdamW([p for m in linears for p in (m.A, m.B)], lr=lr)
     model.table.requires_grad_(True)                # so that the first layer's gradient is asked for, like the others'
@@ -155,7 +156,8 @@ def train(model, tokens, targets, steps=20, lr=3e-3, max_norm=1.0, say=lambda *a
         loss.backward()
         size = opt.step([d for m in linears for d in m.gradients], max_norm=max_norm)
         losses.append(float(loss.detach()))
-        say("step %2d  loss %.4f  gradients %.3f" % (i, losses[-1], float(size)))
+        if say is not None:
+            say("step %2d  loss %.4f%s" % (i, losses[-1], "" if size is None else "  gradients %.3f" % float(size)))
     model.table.requires_grad_(False)
     model.table.grad = None
     return losses
