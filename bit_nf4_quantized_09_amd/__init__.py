@@ -582,15 +582,17 @@ class PagedAdamW:
         """One AdamW step for every parameter; grads are fp32 GPU tensors (dA, dB).  With max_norm the
         gradients count times min(1, max_norm / their global norm), without being written, and the
         norm is returned (a fp32 number on the GPU)."""
-        grads = [g.contiguous().reshape(-1) for g in grads]
+        grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError("one gradient per parameter")
         norm = factor = None
         if max_norm is not None:
+            grads = [g.contiguous() for g in grads]       # (one dense copy for the norm and the step)
             norm, factor = _norm_and_factor(grads, float(max_norm))
         self.t += 1
         b1, b2 = self.betas
-        for q, gq, st in zip(self.params, grads, self.state):
+        for q, g, st in zip(self.params, grads, self.state):
+            gq = g.reshape(-1)
             if st["host"]:
                 if self._stage is None:
                     self._stage = _workspace(self._stage_bytes, q.device)
