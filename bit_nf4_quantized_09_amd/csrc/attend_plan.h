@@ -18,7 +18,7 @@ constexpr int KV_WHOLE = 1 << 30;         // the longest chunk (a longer sequenc
 struct AttendShape {
     int dim, kv_heads;
     int64_t seqs, tokens, heads, max_new, max_length;
-    bool window = false;                  // max_length is a window's keys, which most sequences fill
+    bool window = false;                  // max_length is a window's keys, which the sequences that it cuts fill
 };
 constexpr int64_t ATTEND_PAIRS = (int64_t)1 << 25;        // (sequence, kv head) pairs of a call at most: one wave each, of 2^32 threads
 
@@ -58,23 +58,31 @@ constexpr int block_rows(int dim) { return block_tiles(dim) * 16; }
 // each SIMD: of 128 keys a wave at least where most of the keys were there before (27 sequences of up to 494 keys
 // and 11 tokens: 15 us, 24 with 512), of 512 for prompts, whose early rows see few keys but are joined like the
 // others (one prompt of 252 behind 1370 keys, 8 heads of 256: 70 us with 128, 49 with 512).
-// A window makes the sequences equally long, so that workgroups come in rounds: window_splits takes the chunks, all of one
-// size, for which an estimate is least: rounds of three workgroups on a compute unit (one with heads of 256), each as
-// long as a wave's steps take one after the other (1.1 us) or the round's bytes at 6 TB/s, and 5 us for a join.  24
+// A window makes the sequences that it cuts equally long, so that workgroups come in rounds: window_splits takes the chunks,
+// all of one size, for which an estimate is least: rounds of three workgroups on a compute unit (one with heads of 256), each
+// as long as a wave's steps take one after the other (1.1 us) or the round's bytes at 6 TB/s, and 5 us for a join.  24
 // sequences, window of 4096, 64 heads on 8: 39 us with whole windows, 42 with a round of four chunks, 48 with one and a half of
-// six; window of 1024: 14 us whole, 20 to 22 with two chunks; of 8192: 71 with four, 80 with nine.  (Eight waves to a
+// six; window of 1024: 14 us whole, 20 to 22 with two chunks; of 8192: 72 whole, 80 with two.  (Eight waves to a
 // workgroup instead of chunks: no faster, one sequence, window of 1000: 13.3 us, 11.8 with chunks.)
+// Sequences that the window does not cut stay ragged, and then the call waits for a long chunk's few waves: chunks of
+// KV_SERIAL keys at most (80 us of a wave's steps), or of an eighth of the window where that is longer, and no more of
+// them than workgroups are wanted without a window, for most may find nothing to do.  48 sequences of 500 to 60000 keys,
+// 64 heads on 8, window of 50000: 347 us, 412 in the chunks of the estimate alone; one of 60000 and 47 of 200: 75 and
+// 345; 16 of 131072, which a window of 65536 cuts all: 343 and 316.
+constexpr int64_t KV_SERIAL = 72 * KV_WAVES * KV_STEP, KV_ROUNDS = 4096;
 inline int64_t window_splits(const AttendShape& a, int64_t groups) {
-    const int64_t most = a.max_length / (KV_WAVES * KV_STEP) < 64 ? a.max_length / (KV_WAVES * KV_STEP) : 64;
+    auto held = [](int64_t v, int64_t low, int64_t high) { return v < low ? low : v > high ? high : v; };
+    const int64_t first = held((a.max_length + KV_SERIAL - 1) / KV_SERIAL, 1, 8);
+    const int64_t most = held(held(a.max_length / (KV_WAVES * KV_STEP), 1, KV_ROUNDS / groups), first, 64);
     const int64_t at_once = 256 * (a.dim == 256 ? 1 : 3);
-    int64_t best = 1;
+    int64_t best = first;
     double least = 0;
-    for (int64_t s = 1; s <= most || s == 1; ++s) {
+    for (int64_t s = first; s <= most; ++s) {
         const int64_t steps = (a.max_length + s * KV_STEP - 1) / (s * KV_STEP), workgroups = groups * s;
         const double wave = 1.1 * (double)((steps + KV_WAVES - 1) / KV_WAVES);
         const double bytes = (double)(workgroups < at_once ? workgroups : at_once) * (double)steps * (KV_STEP * 2.0) * a.dim / 6e6;
         const double cost = (double)((workgroups + at_once - 1) / at_once) * (wave > bytes ? wave : bytes) + (s > 1 ? 5.0 : 0.0);
-        if (s == 1 || cost < least) best = s, least = cost;
+        if (s == first || cost < least) best = s, least = cost;
     }
     return best;
 }
@@ -122,6 +130,17 @@ inline AttendPlan attend_plan(const AttendShape& a) {
         else chunks(p.block, max_length * groups * waves / 1024, KV_STEP, (16 * max_new <= max_length ? 128 : 512) * waves, (size_t)(a.tokens * a.heads));
     }
     return p;
+}
+
+// The shape of a call with a window: its keys side by side are the sequence as far as the launches are concerned (a
+// block's rows and the window's start up to a whole step reach further).  A window that cuts no sequence of the stated
+// length is planned like none (48 sequences of 500 to 60000 keys, 64 heads on 8, window of 2^20: 325 us, none 317, as a window 450).
+inline int64_t sink_span(int64_t sinks) { return (sinks + KV_STEP - 1) / KV_STEP * KV_STEP; }
+inline AttendShape window_shape(AttendShape a, int64_t window, int64_t sinks) {
+    const int64_t most = sink_span(sinks) + window + block_rows(a.dim) + KV_STEP;
+    a.window = window + sinks < a.max_length;
+    if (most < a.max_length) a.max_length = most;
+    return a;
 }
 
 }  // namespace nf4

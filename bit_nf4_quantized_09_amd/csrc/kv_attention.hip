@@ -374,9 +374,12 @@ void k_attend_rows(AttendArgs a) {
     constexpr int TILES = D / 16;         // value dimension tiles of the output
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, quarter = lane >> 4;
-    const int split = blockIdx.x;
     const int head = blockIdx.y % a.c.heads, tile0 = blockIdx.y / a.c.heads;
     const int seq = blockIdx.z;
+    // (Behind a window most of a batch's chunks may be its sequences' first ones, and neighbouring workgroups run on XCDs in
+    // turn: were a chunk's place the same for all, eight of a row would leave the first ones to a single XCD: 48 sequences
+    // of 500 to 60000 keys, window of 50000: 514 us, 311 in turn.)
+    const int split = WINDOW ? (blockIdx.x + blockIdx.y + blockIdx.z) % (uint32_t)a.splits : blockIdx.x;
     const NewTokens fresh = new_tokens(a.b, scalar_load(a.b.starts + seq), scalar_load(a.b.starts + seq + 1));
     const int before = scalar_load(a.b.lengths + seq), begin = fresh.begin;
     const int rows = fresh.count * a.group;
@@ -864,26 +867,20 @@ void k_attend_join(AttendArgs a) {
     *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
 
-// A window's keys side by side are the sequence as far as the launch is concerned.
-static int64_t sink_span(const AttendWindow& w) { return (w.sinks + KV_STEP - 1) / KV_STEP * KV_STEP; }
-static AttendPlan plan_of(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length, const AttendWindow& w) {
-    if (w.on()) {
-        // (a block's rows and the window's start up to a whole step reach further)
-        const int64_t most = sink_span(w) + w.window + block_rows(c.dim) + KV_STEP;
-        max_length = max_length < most ? max_length : most;
-    }
-    return attend_plan(AttendShape{c.dim, c.heads, b.seqs, b.tokens, heads, max_new, max_length, w.on()});
+static AttendShape shape_of(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length, const AttendWindow& w) {
+    const AttendShape a{c.dim, c.heads, b.seqs, b.tokens, heads, max_new, max_length};
+    return w.on() ? window_shape(a, w.window, w.sinks) : a;
 }
 
 size_t kv_attention_ws_bytes(const CacheView& c, const BatchView& b, int heads, int64_t max_new, int64_t max_length,
                              const AttendWindow& w) {
-    const AttendPlan p = plan_of(c, b, heads, max_new, max_length, w);
+    const AttendPlan p = attend_plan(shape_of(c, b, heads, max_new, max_length, w));
     return p.rows.bytes + p.block.bytes;
 }
 
 hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const HeadsView& q, const HeadsView& out,
                                float scale, int64_t max_new, int64_t max_length, const AttendWindow& w, void* ws, hipStream_t s) {
-    const AttendPlan p = plan_of(c, b, q.heads, max_new, max_length, w);
+    const AttendPlan p = attend_plan(shape_of(c, b, q.heads, max_new, max_length, w));
     AttendArgs a{};
     a.c = c;
     a.b = b;
@@ -896,7 +893,7 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
     if (w.on()) {
         a.window = (int)w.window;
         a.sinks = (int)w.sinks;
-        a.sink_span = (int)sink_span(w);
+        a.sink_span = (int)sink_span(w.sinks);
     }
     auto part = [&](const AttendPart& q, void* at) {
         a.chunk = q.chunk;
@@ -914,9 +911,11 @@ hipError_t launch_kv_attention(const CacheView& c, const BatchView& b, const Hea
             const int64_t pairs = ((int64_t)b.seqs * c.heads + XCDS - 1) / XCDS * XCDS;
             const dim3 grid((uint32_t)(pairs * a.blocks), (uint32_t)a.splits);
             // more waves than the 2048 that run at once: those with most keys first, in whichever sequence (a pair for
-            // each lane; beyond some rounds the order of one sequence's blocks is enough, and behind a window nearly all
-            // see as many: 3 prompts of up to 1500 tokens, window of 1024: 124 us, 130 in order; of 256: 53 and 59)
-            a.ordered = !WINDOW && pairs <= 64 * XCDS && pairs * a.blocks * p.block.waves > 2048 && pairs * a.blocks * p.block.waves <= 8 * 2048;
+            // each lane; beyond some rounds the order of one sequence's blocks is enough, and behind a window much shorter
+            // than the sequences nearly all see as many: 3 prompts of up to 1500 tokens behind up to 3000 keys, window of
+            // 1024: 124 us, 130 in order; of 256: 53 and 59; but 3 of 1500, window of 2500: 254 and 218; of 4000: 293 and 253)
+            const bool even = WINDOW && 2 * (w.window + w.sinks) < max_length;
+            a.ordered = !even && pairs <= 64 * XCDS && pairs * a.blocks * p.block.waves > 2048 && pairs * a.blocks * p.block.waves <= 8 * 2048;
             // pages of 32 tokens and more hold a whole step: half the address work (3 prompts of up to 1500
             // tokens, 32 heads of 64: 74 us for 85)
             auto run = [&](auto wide, auto waves) {
