@@ -10,7 +10,7 @@
 //   u = q post,  dx = s(x) (u - b mean(u b)),   dpost = sum of q b,   dgate = sum of scale p dh'
 // and the stream's gradient is dh'.  Both factors s are computed again from h' and x, which have to be read
 // anyway: nothing but the operands is kept between the passes.  Sums and products are fp32, each output is
-// rounded once.  Squares that leave fp32 (values past 1.8e19) are summed again times 2^-160.
+// rounded once.  Squares that leave fp32 (values past 1.8e19), or an eps next to its end, are summed again times 2^-160.
 //
 // Shape.  Bound by HBM: each operand is read once and each output written once, so a row stays in the
 // registers of the threads that share it (8 values of 16 bytes a thread and operand), one wave up to a width
@@ -40,6 +40,13 @@ struct NormArgs {
 
 constexpr float NORM_LARGE = 3e38f;
 constexpr float NORM_SHRINK = 0x1p-80f;
+// 1 / the root of the mean square plus eps, from a row's sum of squares: whether that fits fp32, and from the squares times
+// 2^-160 where it does not (there eps counts too, where it is large itself).
+__device__ __forceinline__ bool fits(float squares, const NormArgs& a) { return squares + a.eps < NORM_LARGE; }
+__device__ __forceinline__ float inverse_root(float squares, const NormArgs& a) { return __frsqrt_rn(squares * a.per + a.eps); }
+__device__ __forceinline__ float inverse_root_shrunk(float squares, const NormArgs& a) {
+    return __frsqrt_rn(squares * a.per + a.eps * NORM_SHRINK * NORM_SHRINK) * NORM_SHRINK;
+}
 
 // One row's operands in a thread.
 template <typename S, typename W, int NC, bool BACK>
@@ -227,8 +234,8 @@ void k_block_norm_fwd(NormArgs a) {
             return q[0];
         };
         const float q = squares(1.0f);
-        if (__builtin_expect(q < NORM_LARGE, 1)) return __frsqrt_rn(q * a.per + a.eps);
-        return __frsqrt_rn(squares(NORM_SHRINK) * a.per) * NORM_SHRINK;         // (infinities and NaN come here too)
+        if (__builtin_expect(fits(q, a), 1)) return inverse_root(q, a);
+        return inverse_root_shrunk(squares(NORM_SHRINK), a);         // (infinities and NaN come here too)
     };
     for (uint32_t row = of.first; row < of.end; ++row) {
         if constexpr (AHEAD) {
@@ -370,8 +377,8 @@ void k_block_norm_bwd(NormArgs a) {
         }
         row_sums<GROUP>(q, shared, turn, waves);
         float f, mean;                            // s(h'); the mean of t a
-        if (__builtin_expect(q[0] < NORM_LARGE, 1)) {
-            f = __frsqrt_rn(q[0] * a.per + a.eps);
+        if (__builtin_expect(fits(q[0], a), 1)) {
+            f = inverse_root(q[0], a);
         } else {
             float v = 0.0f;
 #pragma unroll
@@ -381,7 +388,7 @@ void k_block_norm_bwd(NormArgs a) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v = __fmaf_rn(h[j] * NORM_SHRINK, h[j] * NORM_SHRINK, v);
             }
-            f = __frsqrt_rn(sum(v) * a.per) * NORM_SHRINK;
+            f = inverse_root_shrunk(sum(v), a);
         }
         mean = q[1] * f * a.per;
         if (__builtin_expect(!(fabsf(q[1]) < NORM_LARGE), 0)) {           // t h' left fp32: the sum of t a itself
@@ -420,8 +427,8 @@ void k_block_norm_bwd(NormArgs a) {
         if (a.y.data) {
             float g = 1.0f;                       // s(x)
             if (a.norm_post) {
-                if (__builtin_expect(q[2] < NORM_LARGE, 1)) {
-                    g = __frsqrt_rn(q[2] * a.per + a.eps);
+                if (__builtin_expect(fits(q[2], a), 1)) {
+                    g = inverse_root(q[2], a);
                 } else {
                     float v = 0.0f;
 #pragma unroll
@@ -431,7 +438,7 @@ void k_block_norm_bwd(NormArgs a) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v = __fmaf_rn(x[j], x[j], v);
                     }
-                    g = __frsqrt_rn(sum(v) * a.per) * NORM_SHRINK;
+                    g = inverse_root_shrunk(sum(v), a);
                 }
             }
             if constexpr (OWN) {
