@@ -40,6 +40,11 @@ struct NormArgs {
 
 constexpr float NORM_LARGE = 3e38f;
 constexpr float NORM_SHRINK = 0x1p-80f;
+// The mean of t a from the sum of t h': not where that leaves fp32, or where its terms may have lost their last bits below 2^-126
+// (by 2^-150 each) and s(h') > 2^12 brings them back: what s(h')^2 2^-150 adds to a gradient otherwise is itself below 2^-126.
+__device__ __forceinline__ bool product_fits(float sum, float factor) {
+    return fabsf(sum) < NORM_LARGE && !(factor > 0x1p12f && fabsf(sum) < 0x1p-100f);
+}
 // 1 / the root of the mean square plus eps, from a row's sum of squares: whether that fits fp32, and from the squares times
 // 2^-160 where it does not (there eps counts too, where it is large itself).
 __device__ __forceinline__ bool fits(float squares, const NormArgs& a) { return squares + a.eps < NORM_LARGE; }
@@ -391,7 +396,7 @@ void k_block_norm_bwd(NormArgs a) {
             f = inverse_root_shrunk(sum(v), a);
         }
         mean = q[1] * f * a.per;
-        if (__builtin_expect(!(fabsf(q[1]) < NORM_LARGE), 0)) {           // t h' left fp32: the sum of t a itself
+        if (__builtin_expect(!product_fits(q[1], f), 0)) {           // the sum of t a itself
             float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
