@@ -36,21 +36,20 @@ struct NormArgs {
     uint32_t K;
     bool norm_pre, norm_post;
     float scale, eps, per;    // per: 1 / K
+    float large, eps_shrunk;  // sums of squares from which eps and they leave fp32; eps times 2^-160
 };
 
 constexpr float NORM_LARGE = 3e38f;
 constexpr float NORM_SHRINK = 0x1p-80f;
-// The mean of t a from the sum of t h': not where that leaves fp32, or where its terms may have lost their last bits below 2^-126
-// (by 2^-150 each) and s(h') > 2^12 brings them back: what s(h')^2 2^-150 adds to a gradient otherwise is itself below 2^-126.
-__device__ __forceinline__ bool product_fits(float sum, float factor) {
-    return fabsf(sum) < NORM_LARGE && !(factor > 0x1p12f && fabsf(sum) < 0x1p-100f);
-}
+// t h' is summed times 2^80, for gradients and rows whose products lie below fp32's normal numbers although s(h') brings them
+// back; the sums that this takes past its end, like those that leave it by themselves, are summed again as t a.
+constexpr float NORM_RAISE = 0x1p80f;     // (1 / NORM_SHRINK)
 // 1 / the root of the mean square plus eps, from a row's sum of squares: whether that fits fp32, and from the squares times
 // 2^-160 where it does not (there eps counts too, where it is large itself).
-__device__ __forceinline__ bool fits(float squares, const NormArgs& a) { return squares + a.eps < NORM_LARGE; }
+__device__ __forceinline__ bool fits(float squares, const NormArgs& a) { return squares < a.large; }
 __device__ __forceinline__ float inverse_root(float squares, const NormArgs& a) { return __frsqrt_rn(squares * a.per + a.eps); }
 __device__ __forceinline__ float inverse_root_shrunk(float squares, const NormArgs& a) {
-    return __frsqrt_rn(squares * a.per + a.eps * NORM_SHRINK * NORM_SHRINK) * NORM_SHRINK;
+    return __frsqrt_rn(squares * a.per + a.eps_shrunk) * NORM_SHRINK;
 }
 
 // One row's operands in a thread.
@@ -219,6 +218,7 @@ void k_block_norm_fwd(NormArgs a) {
     typedef RowOf<S, W, GROUP, NC, STREAM, false> Of;
     Of of(a);
     if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
+    constexpr bool UNIFORM = NC <= 2;
     // (the next row on its way: up to two vectors a thread there are registers for it; 1024 x 32768 with four: 74 us, 122 with)
     constexpr bool AHEAD = NC <= 2;
     typename Of::Operands next, now;
@@ -235,7 +235,7 @@ void k_block_norm_fwd(NormArgs a) {
             for (int i = 0; i < NC; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q[0] = __fmaf_rn(v[i][j] * shrink, v[i][j] * shrink, q[0]);
-            row_sums<GROUP>(q, shared, turn, waves);
+            row_sums<GROUP, UNIFORM>(q, shared, turn, waves);
             return q[0];
         };
         const float q = squares(1.0f);
@@ -312,7 +312,7 @@ void k_block_norm_bwd(NormArgs a) {
     Of of(a);
     // The next row's operands are loaded while one is computed, but for several vectors a thread, whose registers the rows on
     // their way would spill (gradient of 2048 x 16384, bf16: 91 us, 105 with them; fp32 129 and 178).
-    constexpr bool AHEAD = NC == 1;
+    constexpr bool AHEAD = NC == 1, UNIFORM = NC <= 2;
     typename Of::Operands next, now;
     if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
     if constexpr (AHEAD) {
@@ -332,7 +332,7 @@ void k_block_norm_bwd(NormArgs a) {
     // one of the row sums in turn (the shared numbers are laid out for three)
     auto sum = [&](float v) {
         float q[3] = {v, 0.0f, 0.0f};
-        row_sums<GROUP>(q, shared, turn, waves);
+        row_sums<GROUP, UNIFORM>(q, shared, turn, waves);
         return q[0];
     };
     uint32_t gate = of.first / a.gate_span, gate_first = gate * a.gate_span;        // of the row computed
@@ -364,7 +364,7 @@ void k_block_norm_bwd(NormArgs a) {
         of.settle_all(now);
         float d[NC][8];
         // ---- through the norm before the next block (without one, h' and dy are zero) ----
-        float q[3] = {0.0f, 0.0f, 0.0f};          // squares of h', t h', squares of x
+        float q[3] = {0.0f, 0.0f, 0.0f};          // squares of h', t h' 2^80, squares of x
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float h[8], t[8], w[8], x[8];
@@ -375,12 +375,12 @@ void k_block_norm_bwd(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 q[0] = __fmaf_rn(h[j], h[j], q[0]);
-                q[1] = __fmaf_rn(t[j] * w[j], h[j], q[1]);
+                q[1] = __fmaf_rn(t[j] * w[j], h[j] * NORM_RAISE, q[1]);
                 q[2] = __fmaf_rn(x[j], x[j], q[2]);
                 if constexpr (KEPT) kept[i][j] = x[j];
             }
         }
-        row_sums<GROUP>(q, shared, turn, waves);
+        row_sums<GROUP, UNIFORM>(q, shared, turn, waves);
         float f, mean;                            // s(h'); the mean of t a
         if (__builtin_expect(fits(q[0], a), 1)) {
             f = inverse_root(q[0], a);
@@ -395,8 +395,8 @@ void k_block_norm_bwd(NormArgs a) {
             }
             f = inverse_root_shrunk(sum(v), a);
         }
-        mean = q[1] * f * a.per;
-        if (__builtin_expect(!product_fits(q[1], f), 0)) {           // the sum of t a itself
+        mean = (f > 1.0f ? q[1] * (f * NORM_SHRINK) : q[1] * NORM_SHRINK * f) * a.per;
+        if (__builtin_expect(!(fabsf(q[1]) < NORM_LARGE), 0)) {           // the sum of t a itself
             float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
@@ -679,6 +679,8 @@ static NormArgs norm_args(const BlockNorm& n, int64_t M, int64_t K, const NormSh
     a.norm_post = n.norm_post;
     a.scale = n.scale;
     a.eps = n.eps;
+    a.large = NORM_LARGE - n.eps;
+    a.eps_shrunk = n.eps * NORM_SHRINK * NORM_SHRINK;
     a.per = (float)(1.0 / (double)K);
     return a;
 }

@@ -151,8 +151,10 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // Sums of N numbers over the `waves` waves that share a row (16 at most; GROUP false: one, without a barrier), in all of
 // their threads.  `shared` has 2 N quadruples of four, zero at first; the halves take turns, so that one barrier per sum is
-// enough (a half is written again only after the barrier of the sum between).
-template <bool GROUP, int N>
+// enough (a half is written again only after the barrier of the sum between).  UNIFORM: the sums leave the vector registers
+// (gradients of 4096 x 8192, fp32 stream: 124 us, 128 without; where a thread has four vectors of a row, whose registers are
+// spilled either way, of 1024 x 32768: 365 and 325).
+template <bool GROUP, bool UNIFORM, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float4* shared, int& turn, int waves) {
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
@@ -171,6 +173,9 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float4* shared, int& tur
                 const float4 s = half[n * 4 + (w >> 2)];
                 v[n] += (s.x + s.y) + (s.z + s.w);
             }
+        if constexpr (UNIFORM)
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v[n])));
         turn ^= 1;
     }
 }
