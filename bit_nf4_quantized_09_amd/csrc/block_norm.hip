@@ -17,7 +17,8 @@
 // of 512, else a workgroup of as many waves as it takes.  Workers (a wave or a workgroup) walk along a stretch of
 // rows: the next row's operands are loaded while one is computed, the weights stay in registers, and the sums over
 // tokens of dpre, dpost and dgate are kept there; the workers' sums are added up in a second launch, in a fixed
-// order.  (Past a width of 8192 the sums lie in LDS, and the rows on their way and the weights do not stay.)  4096 tokens of
+// order.  (Gradients with sums past a width of 4096 spill 4 to 17 registers where the stream or the weights are fp32.  Past a
+// width of 8192 the sums lie in LDS, and the rows on their way and the weights do not stay.)  4096 tokens of
 // width 8192, all bf16: forward 44 us (268 MB, 6.1 TB/s), backward with all sums 77 us
 // (403 MB, 5.2 TB/s) and 5 for the join; 16 tokens of width 4096 3.5 us.
 #include "rows.h"
@@ -219,7 +220,8 @@ void k_block_norm_fwd(NormArgs a) {
     Of of(a);
     if (of.first >= of.end) return;       // (all threads of a barrier's workgroup together)
     constexpr bool UNIFORM = NC <= 2;
-    // (the next row on its way: up to two vectors a thread there are registers for it; 1024 x 32768 with four: 74 us, 122 with)
+    // (the next row on its way: up to two vectors a thread there are registers for it, but for 13 that an fp32 stream with fp32
+    // weights spills; 1024 x 32768 with four: 74 us, 122 with)
     constexpr bool AHEAD = NC <= 2;
     typename Of::Operands next, now;
     if constexpr (AHEAD) {
@@ -766,7 +768,8 @@ hipError_t launch_block_norm_bwd(const BlockNorm& n, int64_t M, int64_t K, const
                 if (streams(M, K, p)) run(threads, std::true_type{}, chunks, std::true_type{});
                 else run(threads, std::true_type{}, chunks, std::false_type{});
             };
-            // (a workgroup of 1024 threads has 128 registers a thread: few spills up to a width of 16384, more beyond)
+            // (a workgroup of 1024 threads has 128 registers a thread: of a row of one or two vectors a thread none is spilled in
+            // bf16 and up to 17 with fp32, of one of four 70 to 115 without sums and 186 to 270 with them)
             if (!p.group()) run(std::integral_constant<int, 256>{}, std::false_type{}, std::integral_constant<int, 1>{}, std::false_type{});
             else if (p.chunks == 1 && p.waves <= 8) group(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
             else if (p.chunks == 1) group(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});

@@ -20,7 +20,7 @@
 namespace nf4 {
 
 // Tensors of a launch: 16 or (with outputs apart) 24 bytes each of 4 KiB of arguments; a list of up to 32 takes less (the arguments' way to
-// the GPU is part of a call: 28 tensors clipped in 9.6 us, 12.6 with 4 KiB).
+// the GPU is part of a call: 28 tensors clipped into others in 10.8 us, 12.2 with 4 KiB).
 constexpr int NORM_TENSORS = 240, SCALE_TENSORS = 160, FEW_TENSORS = 32;
 constexpr uint32_t IS_BF16 = 0x80000000u;
 constexpr int SPAN_LOG2 = 13;                     // values of a span
@@ -259,7 +259,7 @@ static void launch_scale(const Gradient* g, const Gradient* out, int64_t count, 
     const auto tables = tables_of<MOST, ScaleTable<MOST, APART>>(g, count, [&](ScaleTable<MOST, APART>& t, int entry, int64_t i, int64_t at) {
         t.put(entry, (uint8_t*)out[i].data + at * (out[i].bf16 ? 2 : 4));
     });
-    // up to 1024 sums are added up by each workgroup (28 tensors of 0.3 million values in all: 12 us, 16 with a launch more)
+    // up to 1024 sums are added up by each workgroup (28 tensors of 0.3 million values in all: 10.8 us, 14.2 with a launch more)
     const bool join = !tables.empty() && parts <= 1024;
     if (!join) hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(1024), 0, s, (const double*)ws, parts, max_norm, norm, factor);
     for (auto t = tables.rbegin(); t != tables.rend(); ++t) {

@@ -29,7 +29,8 @@ struct LogitArgs {
     int V;
 };
 
-// A row's int32 values, four a thread and load: the first ones are on their way from `start` on, the others two loads at a time.
+// A row's int32 values, four a thread and load: the first ones are on their way from `start` on, and each time the next ones
+// while the last are taken.
 template <int THREADS>
 struct Tokens {
     typedef int32_t i4 __attribute__((ext_vector_type(4), aligned(4)));

@@ -113,6 +113,8 @@ nf4_status qlora_kv_append(const qlora_kv_cache* cache, const qlora_kv_batch* ba
  * Sums of queries times codes are held in fp32 before any scale is applied to them: queries up
  * to 2^110 in magnitude stay within it at any head size.
  * A query with a non-finite value that sees any key gives NaN.
+ * Scores, maxima, sums and accumulators are fp32; the weights of the softmax meet the values in fp16, with 11 significant bits
+ * down to 2^-24 of a row's largest.
  *   q, out      bf16 [tokens][heads][head_dim], rows 16-byte aligned; heads a multiple of kv_heads
  *   scale       of any sign, below 2^127 in magnitude (0: every key that is seen weighs the same)
  *   max_new     the most new tokens of one sequence (at least 1; more than `tokens` count as that), and

@@ -111,6 +111,11 @@ nf4_status qlora_adamw_step_paged_scaled(float* p_host, const float* g, float* m
 
 /* qlora_kv_attention where a token at position p sees the keys j of 0 .. p with j > p - window or j < sinks.
  * Pages that none of the batch's tokens sees are not read: their table entries may be -1, and the pages given to others.
+ * Precision, as for qlora_kv_attention: scores, maxima, sums and accumulators are fp32.  The weights of the softmax meet the
+ * values in fp16, with 11 significant bits down to 2^-24 of a row's largest (outputs of the same inputs with weights of 22
+ * bits differ by 7e-4 of their norm, most of it where the bf16 output rounds the other way).  Queries of sequences with many new
+ * rows and heads of 128 and 256 meet the keys as the sum of two E4M3 numbers, exact down to 2^-14 of a query's largest value
+ * and within 2^-23 of it below.
  *   window  1 .. 2^31 - 1;  sinks  0 .. 2^30;  everything else as for qlora_kv_attention (max_length is still the
  *           sequence's positions) */
 size_t qlora_kv_attention_window_workspace_bytes(const qlora_kv_cache* cache, const qlora_kv_batch* batch, int32_t heads,
