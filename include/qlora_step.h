@@ -82,7 +82,8 @@ typedef struct qlora_tensor {
 } qlora_tensor;
 
 /* norm = sqrt(sum of the squares of all values), and the factor that clips it to max_norm:
- * factor = max_norm / norm if norm > max_norm, else 1 (a norm of infinity gives 0, of NaN NaN).
+ * factor = max_norm / norm if norm > max_norm, else 1 (a norm of infinity gives 0, of NaN NaN).  It is a fp32 number: norms of
+ * more than 2^126 max_norm leave it fewer bits than a normal one has, and past 2^150 max_norm it is 0.
  * Squares are added in 64 bits in a fixed order.  A tensor given twice counts twice.
  *   norm, factor  device fp32; factor may be NULL (max_norm is not looked at then);  max_norm >= 0
  *   count         0 .. 2^24 (0: norm 0)
