@@ -10,16 +10,16 @@ namespace nf4 {
 // products need not fit 64.  (Rows one behind the other are one row, and so is a row that stands for all.)
 struct Memory {
     typedef __int128 Wide;
-    Wide at = 0, rows = 0, stride = 0, width = 0;
+    Wide at = 0, rows = 0, stride = 0, width = 0, end = 0;
     Memory() {}
     Memory(const void* p, int64_t n, int64_t step, int64_t row_width, int elem)
         : at((Wide)(uintptr_t)p), rows(p ? n : 0), stride((Wide)step * elem), width((Wide)row_width * elem) {
         if (rows > 1 && stride == width) width *= rows, rows = 1;
         if (rows > 1 && stride == 0) rows = 1;
+        end = at + (rows - 1) * stride + width;
     }
     Memory(const void* p, size_t bytes) : Memory(p, 1, 0, (int64_t)bytes, 1) {}
     bool empty() const { return rows < 1 || width < 1; }
-    Wide end() const { return at + (rows - 1) * stride + width; }
     // whether a row of them meets the bytes from .. to - 1: the first row that ends past `from` does, or none
     bool meets(Wide from, Wide to) const {
         const Wide row = from < at + width ? 0 : rows == 1 ? 1 : (from - at - width) / stride + 1;
@@ -30,9 +30,9 @@ struct Memory {
 // Operands that lie side by side in the rows of one buffer do not meet, although their ranges do.
 inline bool share_memory(const Memory& a, const Memory& b) {
     typedef Memory::Wide Wide;
-    if (a.empty() || b.empty() || a.end() <= b.at || b.end() <= a.at) return false;
-    if (a.rows == 1) return b.meets(a.at, a.end());
-    if (b.rows == 1) return a.meets(b.at, b.end());
+    if (a.end <= b.at || b.end <= a.at || a.empty() || b.empty()) return false;
+    if (a.rows == 1) return b.meets(a.at, a.end);
+    if (b.rows == 1) return a.meets(b.at, b.end);
     if (a.stride == b.stride && a.width <= a.stride && b.width <= b.stride) {
         // every row of b lies as far behind a row of a: only that one and the next can meet it
         const Memory& first = a.at <= b.at ? a : b;
